@@ -40,3 +40,15 @@ from .binding import (  # noqa: F401
     status_string,
     step_launches,
 )
+from .latent import (  # noqa: F401
+    latent_plan,
+    latent_prefill_attention,
+    paged_latent_append,
+    paged_latent_attention,
+    paged_latent_gather,
+)
+from .rope import (  # noqa: F401
+    PKV_ERRBIT_POSITION,
+    paged_qk_norm_rope_append,
+    paged_qk_norm_rope_append_fp8,
+)

@@ -1,0 +1,424 @@
+"""The latent cache's operators against their 64-bit statements: append,
+absorbed attention, gather, expanded attention, and a run of them together."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_213_gb300 as pkv
+from latent_util import (Paged, assert_attention, assert_once_rounded, attend64, norm64, table,
+                         turn64)
+from paged_kv_cache_213_gb300.blocks import paged_kv_copy_blocks
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    pkv.library()
+
+
+def _t(a):
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _err():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+# --- append ------------------------------------------------------------------
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,R,P,bs,norm", [
+    (1, 1, 512, 64, 16, True), (9, 16, 512, 64, 64, False), (21, 3, 256, 64, 16, True),
+    (5, 0, 512, 64, 32, True), (4, 33, 1024, 128, 16, True), (3, 5, 24, 16, 1, True),
+    (2, 2, 8, 48, 16, True), (70, 128, 512, 64, 128, True)])
+def test_latent_append(T, H, R, P, bs, norm, interleaved):
+    rng = np.random.default_rng(T + H + R)
+    wide = rng.standard_normal((T, R + P + 8)).astype(np.float16)
+    w = (1 + 0.2 * rng.standard_normal(R)).astype(np.float16) if norm else None
+    cs, pos = table(P, 300), rng.integers(0, 300, T).astype(np.int32)
+    NB = -(-T // bs) + 2
+    slots = rng.permutation(NB * bs)[:T].astype(np.int64)
+    cache = rng.standard_normal((NB, bs, R + P)).astype(np.float16)
+    q = rng.standard_normal((T, H, 40 + P)).astype(np.float16)
+    o = rng.standard_normal((T, H, R + P)).astype(np.float16)
+    c, qo, err = _t(cache), _t(o), _err()
+    pkv.paged_latent_append(_t(wide)[:, :R + P], _t(w), EPS, _t(cs), _t(pos), _t(slots), c,
+                            q_rope=_t(q)[..., 40:] if H else None,
+                            q_out=qo[..., R:] if H else None, interleaved=interleaved,
+                            err_word=err)
+    assert pkv.get_error(err) == 0
+    got = c.cpu().numpy()
+    n = norm64(wide[:, :R], w, EPS)
+    r, mag = turn64(wide[:, None, R:R + P].astype(np.float64), cs[pos], interleaved)
+    flat = got.reshape(-1, R + P)
+    assert_once_rounded(flat[slots, :R], n, np.abs(n), "latent")
+    assert_once_rounded(flat[slots, R:], r[:, 0], mag[:, 0], "rope")
+    others = np.setdiff1d(np.arange(NB * bs), slots)
+    assert np.array_equal(flat[others], cache.reshape(-1, R + P)[others])
+    if H:
+        y, mag = turn64(q[..., 40:].astype(np.float64), cs[pos], interleaved)
+        assert_once_rounded(qo.cpu().numpy()[..., R:], y, mag, "q")
+        assert np.array_equal(qo.cpu().numpy()[..., :R], o[..., :R])
+
+
+def test_latent_append_bad_tokens_and_in_place():
+    T, H, R, P, bs = 6, 4, 512, 64, 16
+    rng = np.random.default_rng(5)
+    kv = rng.standard_normal((T, R + P)).astype(np.float16)
+    cs = table(P, 50)
+    pos = np.array([0, 1, 50, 3, -1, 49], np.int32)
+    slots = np.array([3, -1, 5, 32, 7, 8], np.int64)
+    q = rng.standard_normal((T, H, P)).astype(np.float16)
+    qd, err = _t(q), _err()
+    c = torch.zeros(2, bs, R + P, dtype=torch.float16, device="cuda")
+    pkv.paged_latent_append(_t(kv), None, EPS, _t(cs), _t(pos), _t(slots), c, q_rope=qd, q_out=qd,
+                            err_word=err)
+    assert pkv.get_error(err) == pkv.PKV_ERRBIT_SLOT | pkv.PKV_ERRBIT_POSITION
+    flat = c.cpu().numpy().reshape(-1, R + P)
+    assert np.array_equal(flat[[3, 8], :R], kv[[0, 5], :R])
+    assert not np.any(np.delete(flat, [3, 8], 0))
+    y, mag = turn64(q.astype(np.float64), cs[np.clip(pos, 0, 49)], False)
+    got = qd.cpu().numpy()
+    assert_once_rounded(got[[0, 5]], y[[0, 5]], mag[[0, 5]], "q in place")
+    assert np.array_equal(got[1:5], q[1:5])
+
+
+# --- absorbed attention --------------------------------------------------------
+
+def _problem(lens, nq, H, R, bs, seed, spread=1.7):
+    p = Paged(lens, R, 64, bs, seed)
+    rng = np.random.default_rng(seed + 1)
+    qs = np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)
+    q = rng.standard_normal((int(qs[-1]), H, R + 64)).astype(np.float16)
+    return p, q, qs, spread / np.sqrt(R + 64)
+
+
+def _attend(p, q, qs, scale, nq, out=None, **kw):
+    err = _err()
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    if out is None:
+        out = torch.full((*q.shape[:2], p.R), 7.0, dtype=torch.float16, device="cuda")
+    pkv.paged_latent_attention(_t(q), _t(p.cache), _t(p.tables), _t(p.lens.astype(np.int32)),
+                               scale, p.R, query_start=None if qs is None else _t(qs),
+                               max_q_len=max(1, max(nq)), out=out, lse=lse, err_word=err,
+                               **{"max_context_len": int(max(1, p.lens.max())), **kw})
+    return out.cpu().numpy(), lse.cpu().numpy(), pkv.get_error(err)
+
+
+def _check(p, q, qs, scale, nq, what, got=None, skip=()):
+    out, lse, bits = _attend(p, q, qs, scale, nq) if got is None else got
+    if got is None:
+        assert bits == 0, what
+    for b, n in enumerate(nq):
+        if n == 0 or b in skip:
+            continue
+        L, r = int(p.lens[b]), slice(int(qs[b]), int(qs[b + 1]))
+        ref = attend64(q[r], p.rows[b], p.rows[b][:, :p.R], L - n + np.arange(n) + 1, scale)
+        assert_attention(out[r], lse[r], *ref, f"{what}: sequence {b}")
+
+
+@pytest.mark.parametrize("R", [256, 512])
+@pytest.mark.parametrize("bs", [16, 64, 256])
+@pytest.mark.parametrize("H", [1, 5, 16, 40, 128])
+def test_decode(H, bs, R):
+    lens = [1, 15, 16, 17, 63, 64, 65, 127, 200, 129]
+    p, q, qs, scale = _problem(lens, [1] * len(lens), H, R, bs, H + bs + R)
+    _check(p, q, qs, scale, [1] * len(lens), "decode")
+
+
+@pytest.mark.parametrize("H,nq", [(16, [1, 3, 0, 8, 2]), (7, [9, 1, 1, 0, 33]),
+                                  (128, [2, 1, 4, 1, 3]), (1, [100, 1, 0, 7, 65])])
+def test_several_tokens(H, nq):
+    lens = [150, 3, 70, 8, 333]
+    nq = [min(n, m) for n, m in zip(nq, lens)]
+    p, q, qs, scale = _problem(lens, nq, H, 512, 32, 40 + H)
+    _check(p, q, qs, scale, nq, "several tokens")
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_long_contexts_are_split_and_joined(H):
+    lens = [9000, 1, 4097, 20]
+    p, q, qs, scale = _problem(lens, [1] * 4, H, 512, 64, 50 + H)
+    _check(p, q, qs, scale, [1] * 4, "long")
+
+
+@pytest.mark.parametrize("B", [1, 40, 700])
+def test_many_and_few_sequences(B):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(1, 90, B)
+    p, q, qs, scale = _problem(lens, [1] * B, 8, 512, 16, 60 + B)
+    _check(p, q, qs, scale, [1] * B, "batch")
+
+
+@pytest.mark.parametrize("spread", [0.0, 60.0])
+def test_flat_and_peaked_weights(spread):
+    """All weights equal (scale 0), and one weight near 1 with logits far apart."""
+    lens = [300, 77, 1, 129]
+    p, q, qs, scale = _problem(lens, [1] * 4, 16, 512, 16, 70, spread)
+    _check(p, q, qs, scale, [1] * 4, "peaked")
+
+
+def test_rising_logits():
+    """Keys that grow along the sequence: the running maximum moves in every tile."""
+    lens = [900]
+    p, q, qs, scale = _problem(lens, [1], 16, 512, 16, 71)
+    grow = np.linspace(0.01, 3.0, 900)[:, None]
+    sign = np.sign(q[0, 0].astype(np.float64))
+    p.rows[0] = (grow * sign * np.abs(p.rows[0])).astype(np.float16)
+    t = np.arange(900)
+    p.cache[p.tables[0, t // 16], t % 16] = p.rows[0]
+    _check(p, q, qs, scale, [1], "rising")
+
+
+def test_decode_form_with_an_empty_sequence():
+    """Without query_start a context length of 0 gives out 0 and lse -inf."""
+    p, q, qs, scale = _problem([20, 0, 130], [1, 1, 1], 16, 512, 16, 80)
+    out, lse, bits = _attend(p, q, None, scale, [1])
+    assert bits == 0 and not np.any(out[1]) and np.all(np.isneginf(lse[1]))
+    _check(p, q, qs, scale, [1, 0, 1], "empty", (out, lse, bits))
+
+
+def test_all_sequences_empty():
+    p, q, qs, scale = _problem([0, 0], [1, 1], 16, 512, 16, 81)
+    out, lse, bits = _attend(p, q, None, scale, [1])
+    assert bits == 0 and not np.any(out) and np.all(np.isneginf(lse))
+
+
+def test_bad_sequences_are_flagged_and_left_unwritten():
+    """More tokens than cached, a length beyond the table, more tokens than
+    max_q_len: flagged, rows as they were; the other sequences are right."""
+    nq = [2, 1, 1, 3]
+    p, q, qs, scale = _problem([50, 30, 40, 64], nq, 16, 512, 16, 90)
+    keep = p.lens.copy()
+    p.lens = np.array([1, 30, p.MB * 16 + 1, 64])
+    out, lse, bits = _attend(p, q, qs, scale, [2], max_context_len=64)
+    assert bits == pkv.PKV_ERRBIT_CONTEXT
+    for r in (slice(0, 2), slice(3, 4), slice(4, 7)):
+        assert np.all(out[r] == 7.0) and np.all(lse[r] == 7.0)
+    p.lens = keep
+    _check(p, q, qs, scale, nq, "bad", (out, lse, bits), skip=(0, 2, 3))
+
+
+def test_a_bad_block_id_is_flagged():
+    p, q, qs, scale = _problem([100, 100], [1, 1], 16, 512, 16, 91)
+    p.tables[0, 3] = p.NB
+    out, lse, bits = _attend(p, q, qs, scale, [1, 1])
+    assert bits == pkv.PKV_ERRBIT_BLOCK_ID
+    _check(p, q, qs, scale, [1, 1], "bad id", (out, lse, bits), skip=(0,))
+
+
+def test_repeated_calls_are_bit_identical_and_graph_replay():
+    """One workspace over calls of other shapes; captured once and replayed on
+    changed lengths, with the maximum as the host's bound."""
+    p, q, qs, scale = _problem([700, 1300, 5, 90], [1] * 4, 32, 512, 32, 92)
+    one = _attend(p, q, qs, scale, [1])
+    ws = torch.randint(0, 256, (pkv.latent_plan(4, 4, 1, 32, 512, 64, 32, p.MB, 1300) + 4096,),
+                       dtype=torch.uint8, device="cuda")
+    two = _attend(p, q, qs, scale, [1], workspace=ws)
+    assert np.array_equal(one[0], two[0]) and np.array_equal(one[1], two[1])
+    args = [_t(x) for x in (q, p.cache, p.tables, p.lens.astype(np.int32))]
+    out = torch.zeros(4, 32, 512, dtype=torch.float16, device="cuda")
+    lse = torch.zeros(4, 32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.paged_latent_attention(*args, scale, 512, max_context_len=1300, out=out, lse=lse,
+                                   workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert np.array_equal(out.cpu().numpy(), one[0])
+    short = np.array([33, 1, 5, 64])
+    args[3].copy_(_t(short.astype(np.int32)))
+    g.replay()
+    torch.cuda.synchronize()
+    p.rows = [x[:n] for x, n in zip(p.rows, short)]
+    p.lens = short
+    _check(p, q, qs, scale, [1] * 4, "replayed", (out.cpu().numpy(), lse.cpu().numpy(), 0))
+
+
+# --- gather --------------------------------------------------------------------
+
+@pytest.mark.parametrize("R,P,bs", [(512, 64, 16), (256, 64, 64), (24, 8, 5)])
+def test_gather(R, P, bs):
+    lens = [1, 40, 0, 17, 129]
+    p = Paged(lens, R, P, bs, 7)
+    start = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    lat = torch.full((200, R), 5.0, dtype=torch.float16, device="cuda")
+    rop = torch.full((200, P), 5.0, dtype=torch.float16, device="cuda")
+    err = _err()
+    pkv.paged_latent_gather(_t(p.cache), _t(p.tables), _t(start), 200, R, latents=lat, ropes=rop,
+                            err_word=err)
+    assert pkv.get_error(err) == 0
+    rows = np.concatenate(p.rows)
+    assert np.array_equal(lat.cpu().numpy()[:187], rows[:, :R])
+    assert np.array_equal(rop.cpu().numpy()[:187], rows[:, R:])
+    assert torch.all(lat[187:] == 5.0) and torch.all(rop[187:] == 5.0)
+
+
+def test_gather_flags():
+    p = Paged([40, 20], 64, 16, 16, 8)
+    p.tables[0, 1] = -1
+    start = np.array([0, 40, 40 + 49], np.int32)   # 49 > 3 blocks of 16
+    lat = torch.full((89, 64), 5.0, dtype=torch.float16, device="cuda")
+    err = _err()
+    p.tables[1] = [p.tables[1, 0], p.tables[1, 1], 0]
+    got, _ = pkv.paged_latent_gather(_t(p.cache), _t(p.tables), _t(start), 89, 64, latents=lat,
+                                     err_word=err)
+    assert pkv.get_error(err) == pkv.PKV_ERRBIT_BLOCK_ID | pkv.PKV_ERRBIT_CONTEXT
+    got = got.cpu().numpy()
+    assert np.array_equal(got[:16], p.rows[0][:16, :64]) and np.all(got[16:32] == 5.0)
+    assert np.array_equal(got[40:60], p.rows[1][:, :64]) and np.all(got[88] == 5.0)
+
+
+# --- expanded attention ----------------------------------------------------------
+
+def _prefill_problem(nq, nk, H, d, seed):
+    rng = np.random.default_rng(seed)
+    TQ, TK = sum(nq), sum(nk)
+    qs = np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)
+    ks = np.concatenate([[0], np.cumsum(nk)]).astype(np.int32)
+    q = rng.standard_normal((TQ, H, d + 64)).astype(np.float16)
+    kv = rng.standard_normal((TK, H, 2 * d)).astype(np.float16)
+    kr = rng.standard_normal((TK, 64)).astype(np.float16)
+    return q, kv, kr, qs, ks
+
+
+def _prefill(q, kv, kr, qs, ks, scale, mq, mk):
+    err = _err()
+    d = q.shape[2] - 64
+    out = torch.full((q.shape[0], q.shape[1], d), 7.0, dtype=torch.float16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    pkv.latent_prefill_attention(_t(q), _t(kv), _t(kr), _t(qs), _t(ks), scale, mq, mk, out=out,
+                                 lse=lse, err_word=err)
+    return out.cpu().numpy(), lse.cpu().numpy(), pkv.get_error(err)
+
+
+def _check_prefill(q, kv, kr, qs, ks, scale, got, what, skip=()):
+    out, lse, _ = got
+    d, H = q.shape[2] - 64, q.shape[1]
+    for b in range(len(qs) - 1):
+        n, m = int(qs[b + 1] - qs[b]), int(ks[b + 1] - ks[b])
+        if n == 0 or b in skip:
+            continue
+        r, s = slice(int(qs[b]), int(qs[b + 1])), slice(int(ks[b]), int(ks[b + 1]))
+        k = np.concatenate([kv[s][..., :d], np.repeat(kr[s][:, None], H, 1)], -1)
+        ref = attend64(q[r], k, kv[s][..., d:], m - n + np.arange(n) + 1, scale)
+        assert_attention(out[r], lse[r], *ref, f"{what}: sequence {b}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,nk,H", [
+    ([1], [1], 1), ([1, 5, 0, 64], [1, 5, 3, 64], 3), ([128, 129, 127], [128, 129, 127], 2),
+    ([257], [257], 5), ([3, 100, 1], [200, 333, 1], 4), ([130], [1000], 2), ([600], [600], 1)])
+def test_prefill(nq, nk, H, d):
+    q, kv, kr, qs, ks = _prefill_problem(nq, nk, H, d, sum(nq) + d + H)
+    scale = 1.0 / np.sqrt(d + 64)
+    got = _prefill(q, kv, kr, qs, ks, scale, max(nq), max(nk))
+    assert got[2] == 0
+    _check_prefill(q, kv, kr, qs, ks, scale, got, "prefill")
+
+
+@pytest.mark.parametrize("factor", [0.0, 20.0])
+def test_prefill_flat_and_peaked(factor):
+    q, kv, kr, qs, ks = _prefill_problem([300, 40], [300, 200], 2, 128, 5)
+    scale = factor / np.sqrt(192)
+    _check_prefill(q, kv, kr, qs, ks, scale, _prefill(q, kv, kr, qs, ks, scale, 300, 300), "peaked")
+
+
+def test_prefill_neighbours_do_not_leak():
+    """NaN in the rows of another sequence and beyond the last one stays there."""
+    nq, nk = [70, 33, 200], [70, 150, 200]
+    q, kv, kr, qs, ks = _prefill_problem(nq, nk, 2, 128, 6)
+    kv = np.concatenate([kv, np.full((200, 2, 256), np.nan, np.float16)])
+    kr = np.concatenate([kr, np.full((200, 64), np.nan, np.float16)])
+    kv[ks[1]:ks[2]] = np.nan
+    out, lse, bits = _prefill(q, kv, kr, qs, ks, 0.07, 200, 200)
+    assert bits == 0
+    kv[ks[1]:ks[2]] = 0
+    _check_prefill(q, kv, kr, qs, ks, 0.07, (out, lse, 0), "neighbours", skip=(1,))
+
+
+def test_prefill_bad_sequences():
+    """More queries than keys, rows beyond the tensors, a longer sequence than the
+    host's bound: flagged and left unwritten."""
+    q, kv, kr, qs, ks = _prefill_problem([40, 30, 20, 10], [40, 30, 20, 10], 2, 128, 7)
+    ks2 = ks.copy()
+    ks2[2] = ks2[1] + 29        # 30 queries, 29 keys; the next sequence has 21 keys
+    ks2[4] = 101                # 11 keys, one beyond the tensor
+    out, lse, bits = _prefill(q, kv, kr, qs, ks2, 0.07, 39, 40)
+    assert bits == pkv.PKV_ERRBIT_CONTEXT
+    for b in (0, 1, 3):
+        assert np.all(out[qs[b]:qs[b + 1]] == 7.0) and np.all(lse[qs[b]:qs[b + 1]] == 7.0)
+    _check_prefill(q, kv, kr, qs, ks2, 0.07, (out, lse, 0), "bad", skip=(0, 1, 3))
+
+
+# --- together --------------------------------------------------------------------
+
+def test_prompt_then_decode_expanded_equals_absorbed():
+    """A layer's run over a latent cache: the prompt is appended, gathered and
+    attended in the expanded form; the next tokens are appended and attended in the
+    absorbed form; both against the 64-bit formula on the cache's values."""
+    H, d, R, P, bs, n, more = 4, 128, 512, 64, 16, 75, 3
+    g = torch.Generator().manual_seed(3)
+
+    def rnd(*s, f=1.0):
+        return (f * torch.randn(*s, generator=g)).half().cuda()
+
+    wk, wv = rnd(H, d, R, f=R ** -0.5), rnd(H, d, R, f=R ** -0.5)
+    kv, q, w = rnd(n + more, R + P), rnd(n + more, H, d + P), rnd(R, f=0.1) + 1
+    cs = torch.from_numpy(table(P, 200)).cuda()
+    pos = torch.arange(n + more, dtype=torch.int32, device="cuda")
+    bt = torch.tensor([[4, 1, 6, 0, 2]], dtype=torch.int32, device="cuda")
+    slots = bt[0, pos.long() // bs].long() * bs + pos.long() % bs
+    cache = torch.full((7, bs, R + P), float("nan"), dtype=torch.float16, device="cuda")
+    err, scale = _err(), (d + P) ** -0.5
+    qt = q.clone()
+    absorbed = torch.empty(more, H, R + P, dtype=torch.float16, device="cuda")
+    # the prompt
+    pkv.paged_latent_append(kv[:n], w, EPS, cs, pos[:n], slots[:n], cache, q_rope=qt[:n, :, d:],
+                            q_out=qt[:n, :, d:], err_word=err)
+    st = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    lat, rop = pkv.paged_latent_gather(cache, bt, st, n, R, err_word=err)
+    ex = torch.cat([torch.einsum("tr,hdr->thd", lat.float(), wk.float()),
+                    torch.einsum("tr,hdr->thd", lat.float(), wv.float())], -1).half()
+    out = pkv.latent_prefill_attention(qt[:n], ex, rop, st, st, scale, n, n, err_word=err)
+    # the next tokens
+    pkv.paged_latent_append(kv[n:], w, EPS, cs, pos[n:], slots[n:], cache, q_rope=q[n:, :, d:],
+                            q_out=absorbed[..., R:], err_word=err)
+    absorbed[..., :R] = torch.einsum("thd,hdr->thr", q[n:, :, :d].float(), wk.float()).half()
+    lens = torch.tensor([n + more], dtype=torch.int32, device="cuda")
+    o2 = pkv.paged_latent_attention(absorbed, cache, bt, lens, scale, R,
+                                    query_start=torch.tensor([0, more], dtype=torch.int32,
+                                                             device="cuda"),
+                                    max_q_len=more, max_context_len=n + more, err_word=err)
+    o2 = torch.einsum("thr,hdr->thd", o2.float(), wv.float())
+    assert pkv.get_error(err) == 0
+    # the formula in 64 bits on the cache's values
+    rows = cache.view(-1, R + P)[slots].double().cpu().numpy()
+    k = np.einsum("tr,hdr->thd", rows[:, :R], wk.double().cpu().numpy())
+    v = np.einsum("tr,hdr->thd", rows[:, :R], wv.double().cpu().numpy())
+    qr, _ = turn64(q[..., d:].double().cpu().numpy(), cs.cpu().numpy()[:n + more], False)
+    q64 = np.concatenate([q[..., :d].double().cpu().numpy(), qr], -1)
+    k = np.concatenate([k, np.repeat(rows[:, None, R:], H, 1)], -1)
+    ref, mag, _, _ = attend64(q64, k, v, np.arange(n + more) + 1, scale)
+    got = np.concatenate([out.double().cpu().numpy(), o2.double().cpu().numpy()])
+    # fp16 roundings of k, v, q' and the rotated queries (2^-11 each, on logits of
+    # size about 10: 0.02 of a weight at most), weights and results
+    assert np.max(np.abs(got - ref)) <= 0.02 * np.max(mag)
+    assert np.linalg.norm(got - ref) <= 2e-3 * np.linalg.norm(ref)
+
+
+def test_copy_on_write_of_a_latent_block():
+    """The block manager's copy on a latent cache, as one head of R + P entries."""
+    R, P, bs = 512, 64, 16
+    c = torch.randn(4, bs, R + P).half().cuda()
+    was = c.clone()
+    view = c.view(4, 1, bs, R + P)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    paged_kv_copy_blocks(view, view, torch.tensor([2], **i32), torch.tensor([0], **i32),
+                         torch.tensor([5], **i32))
+    assert torch.equal(c[0, :5], was[2, :5]) and torch.equal(c[0, 5:], was[0, 5:])
+    assert torch.equal(c[1:], was[1:])
