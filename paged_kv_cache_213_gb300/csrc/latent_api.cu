@@ -22,6 +22,17 @@ bool cache_block_ok(int bs) {
     return bs == 16 || bs == 32 || bs == 64 || bs == 128 || bs == 256;
 }
 
+bool scale_ok(float scale) {  // finite, in base 2 too
+    return std::isfinite(scale) && std::fabs(scale) < 1e38f;
+}
+
+// |scale| * log2(e).  A scale of 0 becomes 1e-30: the weights are equal all the
+// same, and a masked logit of -inf stays -inf.
+float scale_log2_of(float scale) {
+    const double s = std::fabs(static_cast<double>(scale)) * 1.4426950408889634;
+    return s < 1e-30 ? 1e-30f : static_cast<float>(s);
+}
+
 int status_of(cudaError_t e) {
     if (e == cudaErrorInvalidValue) return PKV_ERR_UNSUPPORTED;
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
@@ -224,7 +235,7 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
                            int latent_dim, int rope_dim, int block_size, int max_context_len,
                            void *workspace, size_t workspace_bytes, float *lse_out,
                            int32_t *err_word, void *cuda_stream) {
-    if (num_blocks <= 0 || !std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+    if (num_blocks <= 0 || !scale_ok(scale)) return PKV_ERR_INVALID_ARG;
     if (!query_start && (total_q != num_seqs || (num_seqs > 0 && max_q_len != 1)))
         return PKV_ERR_INVALID_ARG;
     LatentPlan plan{};
@@ -253,7 +264,8 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
     a.max_q_len = max_q_len;
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.num_blocks = num_blocks;
-    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.scale_log2 = scale_log2_of(scale);
+    a.negate = scale < 0.f;
     a.n_q_heads = n_q_heads;
     a.latent_dim = latent_dim;
     a.rope_dim = rope_dim;
@@ -293,7 +305,7 @@ int latent_prefill_attention(void *out, const void *q, const void *kv, const voi
                              float scale, int n_heads, int head_dim, int rope_dim,
                              float *lse_out, int32_t *err_word, void *cuda_stream) {
     if (num_seqs < 0 || total_q < 0 || total_kv < 0 || max_q_len < 0 || max_kv_len < 0 ||
-        n_heads <= 0 || head_dim <= 0 || rope_dim <= 0 || !std::isfinite(scale))
+        n_heads <= 0 || head_dim <= 0 || rope_dim <= 0 || !scale_ok(scale))
         return PKV_ERR_INVALID_ARG;
     if ((head_dim != 64 && head_dim != 128) || rope_dim != 64 || n_heads > 65535 ||
         num_seqs > 65535)
@@ -316,7 +328,8 @@ int latent_prefill_attention(void *out, const void *q, const void *kv, const voi
     a.total_kv = total_kv;
     a.max_q_len = max_q_len;
     a.max_kv_len = max_kv_len;
-    a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    a.scale_log2 = scale_log2_of(scale);
+    a.negate = scale < 0.f;
     a.n_heads = n_heads;
     a.head_dim = head_dim;
     a.rope_dim = rope_dim;

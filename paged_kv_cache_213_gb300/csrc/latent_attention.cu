@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(32 * kWarps) latent_attention_kernel(const Lat
             }
 #pragma unroll
             for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-            s *= a.scale_log2;
+            s *= a.negate ? -a.scale_log2 : a.scale_log2;
             const float mn = fmaxf(m, s);
             const float f = exp2f(m - mn), p = exp2f(s - mn);
             m = mn;

@@ -69,7 +69,8 @@ struct LatentAttentionArgs {
     const int32_t *block_tables, *context_lens, *query_start;
     int num_seqs, total_q, max_q_len, max_blocks_per_seq;
     long long num_blocks;
-    float scale_log2;  // scale * log2(e)
+    float scale_log2;  // |scale| * log2(e), at least 1e-30: a masked logit stays -inf
+    int negate;        // the scale is negative
     int n_q_heads, latent_dim, rope_dim, block_size, max_context_len;
     void *workspace;
     float *lse_out;
@@ -82,7 +83,8 @@ struct LatentPrefillArgs {
     const void *q, *kv, *k_rope;
     const int32_t *q_start, *kv_start;
     int num_seqs, total_q, total_kv, max_q_len, max_kv_len;
-    float scale_log2;
+    float scale_log2;  // |scale| * log2(e), at least 1e-30: a masked logit stays -inf
+    int negate;        // the scale is negative
     int n_heads, head_dim, rope_dim;
     float *lse_out;
     int32_t *err;
