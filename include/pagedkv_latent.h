@@ -101,7 +101,8 @@ int paged_latent_append(const void *kv, int64_t kv_stride, const void *weight, f
  * Logits, softmax and sums in fp32; the softmax weights are rounded to fp16
  * for the product with the values.  A sequence whose tokens, length or rows
  * are out of bounds sets PKV_ERRBIT_CONTEXT and its rows are left unwritten;
- * a bad block id sets PKV_ERRBIT_BLOCK_ID and that block is skipped.
+ * a bad block id sets PKV_ERRBIT_BLOCK_ID, and the results of the sequence
+ * that names it are unspecified.
  * At most 4096 sequences (PKV_ERR_UNSUPPORTED beyond).
  */
 int paged_latent_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int latent_dim,

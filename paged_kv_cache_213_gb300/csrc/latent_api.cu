@@ -3,6 +3,7 @@
 // caller's stream.  Allocates nothing.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -101,8 +102,25 @@ int qk_append(void *q_out, const void *q, const void *k, const void *v, int64_t 
     return status_of(pkv::launch_qk_append(a, fp8, static_cast<cudaStream_t>(cuda_stream)));
 }
 
+// SMs of the current device, looked up once per device.
+int sm_count(int *out) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> cached[kMaxDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    const bool keep = dev >= 0 && dev < kMaxDevices;
+    if (keep) n = cached[dev].load(std::memory_order_relaxed);
+    if (n <= 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+            return PKV_ERR_CUDA;
+        if (keep) cached[dev].store(n, std::memory_order_relaxed);
+    }
+    *out = n;
+    return PKV_OK;
+}
+
 struct LatentPlan {
-    int max_len;
+    int max_len, workers;
     size_t ws_bytes;
 };
 
@@ -121,7 +139,13 @@ int make_latent_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, in
     long long max_len = max_context_len <= 0 ? cap : max_context_len;
     if (max_len > cap) max_len = cap;
     plan->max_len = static_cast<int>(max_len);
-    plan->ws_bytes = 0;
+    if (num_seqs == 0 || total_q == 0 || max_q_len == 0) {  // nothing to launch
+        plan->workers = 0;
+        plan->ws_bytes = 0;
+        return PKV_OK;
+    }
+    if (sm_count(&plan->workers) != PKV_OK) return PKV_ERR_CUDA;
+    plan->ws_bytes = pkv::latent_workspace(max_q_len, n_q_heads, latent_dim, plan->workers);
     return PKV_OK;
 }
 
@@ -242,7 +266,7 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
     const int rc = make_latent_plan(num_seqs, total_q, max_q_len, n_q_heads, latent_dim, rope_dim,
                                     block_size, max_blocks_per_seq, max_context_len, &plan);
     if (rc != PKV_OK) return rc;
-    if (num_seqs == 0 || total_q == 0) return PKV_OK;
+    if (plan.workers == 0) return PKV_OK;
     if (!out || !q || !cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4) || (query_start && !aligned(query_start, 4)) ||
@@ -274,7 +298,7 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
     a.workspace = workspace;
     a.lse_out = lse_out;
     a.err = err_word;
-    return status_of(pkv::launch_latent_attention(a, static_cast<cudaStream_t>(cuda_stream)));
+    return status_of(pkv::launch_latent_attention(a, plan.workers, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int paged_latent_gather(void *latents, void *ropes, const void *cache,

@@ -76,7 +76,10 @@ struct LatentAttentionArgs {
     float *lse_out;
     int32_t *err;
 };
-cudaError_t launch_latent_attention(const LatentAttentionArgs &a, cudaStream_t stream);
+// workers: CTAs of the split (one per SM); the workspace holds what they cut.
+size_t latent_workspace(int max_q_len, int heads, int latent_dim, int workers);
+cudaError_t launch_latent_attention(const LatentAttentionArgs &a, int workers,
+                                    cudaStream_t stream);
 
 struct LatentPrefillArgs {
     void *out;
