@@ -4,11 +4,12 @@ CUDA kernels."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from .binding import _check, _need, _ptr, library
-from .rope import _launch, _need_cuda
+from .binding import _check, _need, library
+from .rope import _current_device, _launch, _need_cuda, _ptr
 
 _bound = None
 
@@ -104,13 +105,22 @@ def paged_latent_append(kv, weight, eps, cos_sin, positions, slot_mapping, cache
 
 def latent_plan(num_seqs, total_q, max_q_len, n_q_heads, latent_dim, rope_dim, block_size,
                 max_blocks_per_seq, max_context_len=0):
-    """Workspace bytes of paged_latent_attention."""
+    """Workspace bytes of paged_latent_attention on the current device."""
     W = ctypes.c_size_t(0)
     _check("paged_latent_plan",
            _lib().paged_latent_plan(num_seqs, total_q, max_q_len, n_q_heads, latent_dim, rope_dim,
                                     block_size, max_blocks_per_seq, max_context_len,
                                     ctypes.byref(W)))
     return W.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _plan_on(index, *sizes):
+    """latent_plan on device `index`: a function of the sizes alone."""
+    if _current_device() == index:
+        return latent_plan(*sizes)
+    with torch.cuda.device(index):
+        return latent_plan(*sizes)
 
 
 def paged_latent_attention(q, cache, block_tables, context_lens, scale, latent_dim,
@@ -158,11 +168,7 @@ def paged_latent_attention(q, cache, block_tables, context_lens, scale, latent_d
     if err_word is not None:
         _need(err_word, "err_word", torch.int32, dev)
     if workspace is None:
-        if torch.cuda.current_device() == dev.index:
-            ws = latent_plan(B, TQ, max_q_len, H, R, E - R, bs, MB, mcl)
-        else:
-            with torch.cuda.device(dev):
-                ws = latent_plan(B, TQ, max_q_len, H, R, E - R, bs, MB, mcl)
+        ws = _plan_on(dev.index, B, TQ, max_q_len, H, R, E - R, bs, MB, mcl)
         workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
     else:
         _need(workspace, "workspace", torch.uint8, dev)
