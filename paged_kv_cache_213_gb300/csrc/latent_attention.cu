@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 5) {
         // --- matrix products ---
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t ds = mma_desc(kTile, N, false, false);
             constexpr uint32_t dpv = mma_desc(128, N, true, true);
             const uint32_t kv = smem_addr(base), qa = smem_addr(q_smem), pa = smem_addr(p_smem);

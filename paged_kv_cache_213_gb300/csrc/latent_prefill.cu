@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // TMEM columns: S of tile t at 128 t (P in its first half), O at 256 + 128 t
 
     if (warp == 8) {
-        if (lane == 0) {
+        if (elect_one()) {
             prefetch_tmap(&mq);
             prefetch_tmap(&mkv);
             prefetch_tmap(&mr);
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t ds = mma_desc(kRows, kKeys, false, false);
             constexpr uint32_t dpv = mma_desc(kRows, D, false, true);
             const uint32_t q_addr = smem_addr(base), kv_addr = q_addr + C::Q_BYTES;

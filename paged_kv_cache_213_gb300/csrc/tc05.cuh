@@ -33,6 +33,18 @@ __device__ __forceinline__ bool warp_wait_or_stop(uint64_t *bar, uint32_t parity
     return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop));
 }
 
+// One lane of a converged warp.  The compiler knows that the branch on it has a
+// single thread, so that tcgen05 and TMA operands go to uniform registers at
+// once: a run of tcgen05.mma issues every 23 cycles behind it, every 47 behind
+// `lane == 0` (measured, M = 64, N = 16).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // 2^x by the special-function unit (results below the normal range flush to 0).
 __device__ __forceinline__ float ex2(float x) {
     float y;
