@@ -120,8 +120,9 @@ int sm_count(int *out) {
 }
 
 struct LatentPlan {
-    int max_len, workers;
-    size_t ws_bytes;
+    int max_len;
+    bool empty;  // nothing to launch
+    pkv::LatentSplit split;
 };
 
 int make_latent_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int latent_dim,
@@ -135,17 +136,20 @@ int make_latent_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, in
         return PKV_ERR_UNSUPPORTED;
     const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
     if (cap > (1LL << 30)) return PKV_ERR_INVALID_ARG;
-    if (static_cast<long long>(total_q) * n_q_heads > (1LL << 30)) return PKV_ERR_UNSUPPORTED;
+    if (static_cast<long long>(total_q) * n_q_heads > (1LL << 30) ||
+        static_cast<long long>(max_q_len) * n_q_heads > (1LL << 30))
+        return PKV_ERR_UNSUPPORTED;
     long long max_len = max_context_len <= 0 ? cap : max_context_len;
     if (max_len > cap) max_len = cap;
     plan->max_len = static_cast<int>(max_len);
-    if (num_seqs == 0 || total_q == 0 || max_q_len == 0) {  // nothing to launch
-        plan->workers = 0;
-        plan->ws_bytes = 0;
-        return PKV_OK;
-    }
-    if (sm_count(&plan->workers) != PKV_OK) return PKV_ERR_CUDA;
-    plan->ws_bytes = pkv::latent_workspace(max_q_len, n_q_heads, latent_dim, plan->workers);
+    plan->empty = num_seqs == 0 || total_q == 0 || max_q_len == 0;
+    plan->split.ws_bytes = 0;
+    if (plan->empty) return PKV_OK;
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    if (!pkv::latent_split(num_seqs, max_q_len, n_q_heads, latent_dim, plan->max_len, sms,
+                           &plan->split))
+        return PKV_ERR_UNSUPPORTED;
     return PKV_OK;
 }
 
@@ -248,7 +252,7 @@ int paged_latent_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, i
     LatentPlan plan{};
     const int rc = make_latent_plan(num_seqs, total_q, max_q_len, n_q_heads, latent_dim, rope_dim,
                                     block_size, max_blocks_per_seq, max_context_len, &plan);
-    if (rc == PKV_OK && workspace_bytes_out) *workspace_bytes_out = plan.ws_bytes;
+    if (rc == PKV_OK && workspace_bytes_out) *workspace_bytes_out = plan.split.ws_bytes;
     return rc;
 }
 
@@ -266,14 +270,13 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
     const int rc = make_latent_plan(num_seqs, total_q, max_q_len, n_q_heads, latent_dim, rope_dim,
                                     block_size, max_blocks_per_seq, max_context_len, &plan);
     if (rc != PKV_OK) return rc;
-    if (plan.workers == 0) return PKV_OK;
+    if (plan.empty) return PKV_OK;
     if (!out || !q || !cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(cache, 16) || !aligned(block_tables, 4) ||
         !aligned(context_lens, 4) || (query_start && !aligned(query_start, 4)) ||
         (lse_out && !aligned(lse_out, 4)) || (err_word && !aligned(err_word, 4)))
         return PKV_ERR_INVALID_ARG;
-    if (plan.ws_bytes > 0 &&
-        (!workspace || workspace_bytes < plan.ws_bytes || !aligned(workspace, 256)))
+    if (!workspace || workspace_bytes < plan.split.ws_bytes || !aligned(workspace, 256))
         return PKV_ERR_WORKSPACE;
     if (num_blocks * block_size >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;  // 32-bit rows
     pkv::LatentAttentionArgs a{};
@@ -298,7 +301,7 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
     a.workspace = workspace;
     a.lse_out = lse_out;
     a.err = err_word;
-    return status_of(pkv::launch_latent_attention(a, plan.workers, static_cast<cudaStream_t>(cuda_stream)));
+    return status_of(pkv::launch_latent_attention(a, plan.split, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 int paged_latent_gather(void *latents, void *ropes, const void *cache,

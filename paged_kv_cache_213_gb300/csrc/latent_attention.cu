@@ -30,15 +30,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 namespace {
 
-constexpr int kTile = 64;      // tokens
-constexpr int kThreads = 192;  // softmax warps 0-3, copy warp 4, MMA warp 5
+constexpr int kTile = 64;  // tokens
 // P holds 2^(s - r) with r kHead below the running maximum: weights up to
 // 2^kHead, and up to 2^(kHead + kLag) before r follows; fp16 ends at 2^16.
 constexpr float kHead = 6.f, kLag = 8.f;
 
-template <int R, int N>
+// CL: CTAs of a cluster, which share every token tile (each loads a part of it for
+// both) and have N query rows each.
+template <int R, int N, int CL>
 struct Cfg {
     static constexpr int E = R + 64, PL = E / 64, VT = R / 128;
+    static constexpr int ROWS = CL * N;  // query rows of a worker's row tile
     static constexpr int PLANE = kTile * 128, QPLANE = N * 128;
     static constexpr int STAGE = PL * PLANE;
     static constexpr int STAGES = R == 512 ? 2 : 4;
@@ -46,6 +48,11 @@ struct Cfg {
     static constexpr int SMEM = 1024 + STAGES * STAGE + Q_BYTES + P_BYTES;
     static constexpr int COLS = (VT + 2) * N;
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    // softmax warps, four a group; a group takes NG of the rows and VG of O^T's
+    // 16-column pieces
+    static constexpr int GROUPS = N == 64 ? 2 : 1, SW = 4 * GROUPS;
+    static constexpr int NG = N / GROUPS;
+    static constexpr int THREADS = 32 * (SW + 2);  // and the copy and the MMA warp
 };
 
 // One sequence's work: its query rows and how many of its tokens each attends.
@@ -70,73 +77,70 @@ __device__ __forceinline__ bool load_seq(const LatentAttentionArgs &a, int b, Se
 
 // Tokens that the rows of a row tile attend at most.
 __device__ __forceinline__ int tile_end(const Seq &s, int heads, int rows, int rt) {
-    const int last = min(static_cast<int>((static_cast<long long>(rt + 1) * rows - 1) / heads), s.n - 1);
-    return s.len > 0 ? s.len - s.n + last + 1 : 0;
+    if (s.n == 1) return s.len;
+    const int last = min(static_cast<int>((static_cast<unsigned>(rt + 1) * rows - 1) / heads), s.n - 1);
+    return s.len - s.n + last + 1;
 }
 
-__device__ __forceinline__ int row_tiles(const Seq &s, int heads, int rows) {
-    return static_cast<int>((static_cast<long long>(s.n) * heads + rows - 1) / rows);
+// Row tiles of n query tokens (total_q * heads is at most 2^30).
+__device__ __forceinline__ int row_tiles(int n, int heads, int rows) {
+    return (n * heads + rows - 1) / rows;
 }
 
 __device__ __forceinline__ int token_tiles(int end) {
     return end > 0 ? (end + kTile - 1) / kTile : 1;
 }
 
-// Units (token tiles) of a whole sequence.
-__device__ __forceinline__ long long seq_units(const LatentAttentionArgs &a, int b, int rows,
-                                               bool *good) {
+// Units (token tiles of a row tile) of a whole sequence; the host keeps the sum
+// over the batch below 2^31.
+__device__ __forceinline__ int seq_units(const LatentAttentionArgs &a, int b, int rows, bool *good) {
     Seq s;
     *good = load_seq(a, b, &s);
     if (!*good || s.n == 0) return 0;
-    if (s.n == 1) return static_cast<long long>(row_tiles(s, a.n_q_heads, rows)) * token_tiles(s.len);
-    long long u = 0;
-    for (int rt = row_tiles(s, a.n_q_heads, rows) - 1; rt >= 0; --rt)
+    int u = 0;
+    for (int rt = row_tiles(s.n, a.n_q_heads, rows) - 1; rt >= 0; --rt)
         u += token_tiles(tile_end(s, a.n_q_heads, rows, rt));
     return u;
 }
 
-// A CTA's place in the split: units [first, first + left) starting `skip` units
-// into sequence `b`.
-struct Range {
-    int b;
-    long long skip, left, first, total;
-    int workers;
+// The even split: worker c has the units [first(c), first(c + 1)).
+struct Split {
+    int each, more;  // units of a worker, workers with one more
+    __device__ int first(int c) const { return c * each + min(c, more); }
+    __device__ int worker_of(int unit) const {
+        const int big = more * (each + 1);
+        return unit < big ? unit / (each + 1) : more + (unit - big) / each;
+    }
 };
 
 // A run of token tiles of one (sequence, row tile).
 struct Piece {
     Seq s;
-    int b, rt, t0, tiles, end;  // end: tokens of the whole segment
-    int seg_tiles;
-    long long seg_first;        // unit at which the segment starts
+    int b, rt, t0, tiles;
+    int seg_tiles, seg_first;  // tiles of the whole segment, and its first unit
 };
 
+// A place in the list of units: `left` units from `skip` units behind the start of
+// row tile rt of sequence b, which is at `unit`.
 struct Walk {
-    int b, rt;
-    long long skip, left, unit;
+    int b, rt, skip, left, unit;
 };
-
-__device__ __forceinline__ Walk start_walk(const Range &r) {
-    return Walk{r.b, 0, r.skip, r.left, r.first - r.skip};
-}
 
 __device__ bool next_piece(const LatentAttentionArgs &a, int rows, Walk *w, Piece *p) {
     if (w->left <= 0) return false;
     while (w->b < a.num_seqs) {
         Seq s;
         if (load_seq(a, w->b, &s)) {
-            const int rts = row_tiles(s, a.n_q_heads, rows);
+            const int rts = row_tiles(s.n, a.n_q_heads, rows);
             for (; w->rt < rts; ++w->rt) {
-                const int end = tile_end(s, a.n_q_heads, rows, w->rt);
-                const int tiles = token_tiles(end);
+                const int tiles = token_tiles(tile_end(s, a.n_q_heads, rows, w->rt));
                 if (w->skip >= tiles) {
                     w->skip -= tiles;
                     w->unit += tiles;
                     continue;
                 }
-                const int t0 = static_cast<int>(w->skip);
-                const int take = static_cast<int>(min(static_cast<long long>(tiles - t0), w->left));
-                *p = Piece{s, w->b, w->rt, t0, take, end, tiles, w->unit};
+                const int take = min(tiles - w->skip, w->left);
+                *p = Piece{s, w->b, w->rt, w->skip, take, tiles, w->unit};
                 w->left -= take;
                 w->skip = 0;
                 w->unit += tiles;
@@ -150,91 +154,110 @@ __device__ bool next_piece(const LatentAttentionArgs &a, int rows, Walk *w, Piec
     return false;
 }
 
-// Workspace: a record per CTA {first output row, rows, last CTA of the segment or
-// -1, 0}, then per piece slot (two a CTA: 0 ends a segment or lies inside one, 1
-// starts one) N pairs (r, l) and N x R partial sums.
+// Workspace: `records` x CL records {first output row, rows, first and last worker
+// of the segment; no rows: nothing to join}, then per piece slot (two a worker: 0
+// ends a segment or lies inside one, 1 starts one) and CTA of the cluster N pairs
+// (r, l) and R x N partial sums, a column's N rows together.
 struct Layout {
     size_t ml, acc, total;
 };
 
-__host__ __device__ inline Layout layout(int workers, int rows, int R) {
+__host__ __device__ inline Layout layout(int records, int workers, int cl, int rows, int R) {
+    const size_t slots = static_cast<size_t>(2 * workers) * cl;
     Layout l;
-    l.ml = (static_cast<size_t>(workers) * 16 + 255) / 256 * 256;
-    l.acc = l.ml + static_cast<size_t>(2 * workers) * rows * 8;
-    l.total = l.acc + static_cast<size_t>(2 * workers) * rows * R * 4;
+    l.ml = (static_cast<size_t>(records) * cl * 16 + 255) / 256 * 256;
+    l.acc = l.ml + slots * rows * 8;
+    l.total = l.acc + slots * rows * R * 4;
     return l;
 }
 
 struct Shared {
-    uint64_t full[4], empty[4], s_full[2], p_ready, q_full, q_empty, o_full, o_free, drained;
+    uint64_t full[4], empty[4], s_full[2], p_ready, pv_done, q_full, q_empty, o_full, o_free, drained;
     uint32_t tmem;
     int stop;
-    Range range;
-    long long sums[kThreads / 32];
-    float warps[4][64];  // per row, of each softmax warp: a tile's maxima, a piece's sums
+    Split split;
+    Walk walk;
+    int sums[16];
+    float warps[4][64];  // per row, of each softmax warp of its group: a tile's maxima, a piece's sums
     float factor[64];    // what O^T's columns are multiplied with
     float ref[64];
 };
 
-__device__ __forceinline__ bool any_softmax(bool x) {  // over the four softmax warps
+// Over the softmax warps.
+template <int THREADS>
+__device__ __forceinline__ bool any_softmax(bool x) {
     uint32_t r;
     __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.aligned.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.aligned.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(static_cast<uint32_t>(x))
+        : "r"(static_cast<uint32_t>(x)), "n"(THREADS)
         : "memory");
     return r != 0;
 }
+template <int THREADS>
 __device__ __forceinline__ void sync_softmax() {
     __syncwarp();
-    asm volatile("barrier.cta.sync.aligned 1, 128;" ::: "memory");
+    asm volatile("barrier.cta.sync.aligned 1, %0;" ::"n"(THREADS) : "memory");
 }
 
 template <int N>
 __device__ __forceinline__ void load_scores(uint32_t (&x)[N / 2], uint32_t addr) {
-    if constexpr (N == 64) tmem_ld_m8(x, addr);
     if constexpr (N == 32) tmem_ld_m4(x, addr);
     if constexpr (N == 16) tmem_ld_m2(x, addr);
 }
 
 static_assert(sizeof(Shared) <= 2048, "beside the largest configuration's 225 KB");
 
-template <int R, int N>
-__global__ void __launch_bounds__(kThreads, 1)
-    latent_attention_kernel(const LatentAttentionArgs a, const __grid_constant__ CUtensorMap mq,
+template <int R, int N, int CL>
+__global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
+    latent_attention_kernel(const LatentAttentionArgs a, const LatentSplit sp,
+                            const __grid_constant__ CUtensorMap mq,
                             const __grid_constant__ CUtensorMap mc) {
-    using C = Cfg<R, N>;
+    using C = Cfg<R, N, CL>;
+    constexpr int kThreads = C::THREADS, kSoft = 32 * C::SW;
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
     unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     unsigned char *q_smem = base + C::STAGES * C::STAGE, *p_smem = q_smem + C::Q_BYTES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.n_q_heads;
+    const int worker = blockIdx.x / CL;
+    const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
+    int4 *records = static_cast<int4 *>(a.workspace);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], 1);
+            mbar_init(&sh.empty[s], CL);
         }
         mbar_init(&sh.s_full[0], 1);
         mbar_init(&sh.s_full[1], 1);
-        mbar_init(&sh.p_ready, 4);
+        mbar_init(&sh.p_ready, C::SW);
+        mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.o_full, 1);
-        mbar_init(&sh.o_free, 4);
+        mbar_init(&sh.o_free, C::SW);
         mbar_init(&sh.drained, 1);
         sh.stop = 0;
+        sh.walk.left = 0;
         fence_barrier_init();
     }
-    if (warp == 5) {
+    if (warp == C::SW + 1) {
         tmem_alloc(&sh.tmem, C::TMEM);
         if (lane == 0) {
             prefetch_tmap(&mq);
             prefetch_tmap(&mc);
         }
+    }
+    {
+        // the tables come to L2 while the kernel before drains (a prefetch reads
+        // nothing that could be stale)
+        const long long line = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+        if (line * 32 < static_cast<long long>(a.num_seqs) * a.max_blocks_per_seq)
+            prefetch_l2(a.block_tables + line * 32);
     }
     grid_dependency_wait();
     allow_dependent_launch();
@@ -244,66 +267,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int per = (a.num_seqs + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * per, a.num_seqs);
         const int b1 = min(b0 + per, a.num_seqs);
-        long long mine = 0;
+        int mine = 0;
         bool good;
         for (int b = b0; b < b1; ++b) {
-            mine += seq_units(a, b, N, &good);
-            if (!good && blockIdx.x == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+            const int u = seq_units(a, b, C::ROWS, &good);
+            mine += u;
+            if (blockIdx.x == 0 && !good) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+            if (blockIdx.x == 0 && u == 0 && sp.by_segment)
+                for (int i = 0; i < sp.row_tiles * CL; ++i)
+                    records[b * sp.row_tiles * CL + i] = make_int4(0, 0, 0, 0);
         }
         // inclusive scan: within the warp by shuffles, over the warps in shared memory
-        long long acc = mine;
+        int acc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, acc, o);
+            const int v = __shfl_up_sync(0xffffffffu, acc, o);
             if (lane >= o) acc += v;
         }
         if (lane == 31) sh.sums[warp] = acc;
-        if (threadIdx.x == 0) sh.range.left = 0;
         __syncthreads();
-        long long before = acc - mine, total = 0;
+        int before = acc - mine, total = 0;
+#pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += sh.sums[w];
             total += sh.sums[w];
         }
-        const int workers = static_cast<int>(min(total, static_cast<long long>(gridDim.x)));
-        if (static_cast<int>(blockIdx.x) < workers) {
-            const long long first = static_cast<long long>(blockIdx.x) * total / workers;
-            const long long last = static_cast<long long>(blockIdx.x + 1) * total / workers;
-            if (mine > 0 && before <= first && first < before + mine) {
-                int b = b0;
-                long long at = before;
-                for (; b < b1; ++b) {
-                    const long long u = seq_units(a, b, N, &good);
-                    if (first < at + u) break;
-                    at += u;
-                }
-                sh.range = Range{b, first - at, last - first, first, total, workers};
+        const int workers = min(total, sp.workers);
+        if (worker < workers) {
+            const Split split{total / workers, total % workers};
+            const int first = split.first(worker);
+            if (before <= first && first < before + mine) {
+                int b = b0, at = before;
+                if (per > 1)
+                    for (;; ++b) {
+                        const int u = seq_units(a, b, C::ROWS, &good);
+                        if (first < at + u) break;
+                        at += u;
+                    }
+                sh.split = split;
+                sh.walk = Walk{b, 0, first - at, split.first(worker + 1) - first, at};
             }
         }
     }
     tc_fence_before();
-    __syncthreads();
+    if (CL > 1) cluster_sync(); else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
-    const Range range = sh.range;
+    Walk w = sh.walk;
 
-    if (range.left <= 0) {
-        if (threadIdx.x == 0)
-            static_cast<int4 *>(a.workspace)[blockIdx.x] = make_int4(0, 0, -1, 0);
-    } else if (warp == 4) {
+    if (w.left <= 0) {
+        if (threadIdx.x == 0 && !sp.by_segment) records[blockIdx.x] = make_int4(0, 0, 0, 0);
+    } else if (warp == C::SW) {
         // --- copies ---
-        Walk w = start_walk(range);
         Piece p;
-        const int box = min(a.block_size, kTile), subs = kTile / box;
+        // this CTA loads the cluster's share `rank` of every tile: kTile / CL tokens
+        constexpr int kShare = kTile / CL;
+        const int box = min(a.block_size, kShare), subs = kTile / box, own = kShare / box;
         int g = 0, k = 0;  // tiles, pieces so far
         bool ok = true;
-        while (ok && next_piece(a, N, &w, &p)) {
+        while (ok && next_piece(a, C::ROWS, &w, &p)) {
             if (lane == 0) {
                 ok = wait_or_stop(&sh.q_empty, (k & 1) ^ 1, stop);
                 if (ok) {
                     mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
-                    const int row = p.s.q0 * H + p.rt * N;
+                    const int row = p.s.q0 * H + p.rt * C::ROWS + rank * N;
                     for (int x = 0; x < C::PL; ++x)
                         tma_load_2d(q_smem + x * C::QPLANE, &mq, 64 * x, row, &sh.q_full);
                 }
@@ -333,11 +361,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(&sh.full[s]);
                 }
                 __syncwarp();
-                if (id >= 0) {
+                if (id >= 0 && lane / own == rank) {
                     const int row = id * a.block_size + (t * kTile + lane * box) % a.block_size;
                     unsigned char *dst = base + s * C::STAGE + lane * box * 128;
                     for (int x = 0; x < C::PL; ++x)
-                        tma_load_2d(dst + x * C::PLANE, &mc, 64 * x, row, &sh.full[s]);
+                        if (CL > 1)
+                            tma_load_2d_multicast(dst + x * C::PLANE, &mc, 64 * x, row, &sh.full[s],
+                                                  (1 << CL) - 1);
+                        else
+                            tma_load_2d(dst + x * C::PLANE, &mc, 64 * x, row, &sh.full[s]);
                 }
                 id = next;
             }
@@ -349,17 +381,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = max(0, g - C::STAGES); i < g; ++i)
                 mbar_wait_bounded(&sh.full[i % C::STAGES], (i / C::STAGES) & 1);
         }
-    } else if (warp == 5) {
+    } else if (warp == C::SW + 1) {
         // --- matrix products ---
         if (elect_one()) {
             constexpr uint32_t ds = mma_desc(kTile, N, false, false);
             constexpr uint32_t dpv = mma_desc(128, N, true, true);
             const uint32_t kv = smem_addr(base), qa = smem_addr(q_smem), pa = smem_addr(p_smem);
-            Walk w = start_walk(range);
             Piece p;
             int g = 0, k = 0;
             bool ok = true;
-            while (ok && next_piece(a, N, &w, &p)) {
+            while (ok && next_piece(a, C::ROWS, &w, &p)) {
                 ok = wait_or_stop(&sh.q_full, k & 1, stop);
                 int sj = 0, pj = 0;
                 unsigned spins = 0;
@@ -393,7 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 mma_ss(tmem + v * N,
                                        smem_desc(va + 2 * v * C::PLANE + x * 2048, 1024, C::PLANE),
                                        smem_desc(pa + x * 2048, 1024, 0), dpv, pj > 0 || x > 0);
-                        mma_commit(&sh.empty[gp % C::STAGES]);
+                        if (CL > 1)
+                            mma_commit_multicast(&sh.empty[gp % C::STAGES], (1 << CL) - 1);
+                        else
+                            mma_commit(&sh.empty[gp % C::STAGES]);
+                        mma_commit(&sh.pv_done);
                         if (++pj == p.tiles) mma_commit(&sh.o_full);
                         spins = 0;
                     } else if ((++spins & 255u) == 0) {
@@ -414,38 +449,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // --- softmax, results ---
-        // scores: this thread holds tokens 16 warp + lane / 4 (+ 8) and rows
-        // 8 c + 2 (lane % 4) (+ 1), c < N / 8
-        constexpr int NC = N / 8;
-        const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
-        const int tok = 16 * warp + lane / 4, col = 2 * (lane & 3);
-        const Layout lay = layout(gridDim.x, N, R);
+        // scores: this thread holds tokens tok (+ 8) and rows row_of(c) (+ 1), c < NC
+        constexpr int NC = C::NG / 8;
+        const int group = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+        const int tok = 16 * quarter + lane / 4, col = C::NG * group + 2 * (lane & 3);
+        const Layout lay = layout(sp.records, sp.workers, CL, N, R);
         char *ws = static_cast<char *>(a.workspace);
         const float scale = a.scale_log2;
-        Walk w = start_walk(range);
         Piece p;
         int g = 0, k = 0;
         bool recorded = false;
-        while (next_piece(a, N, &w, &p)) {
+        while (next_piece(a, C::ROWS, &w, &p)) {
+            const int tile_row = p.rt * C::ROWS + rank * N;  // of the sequence's rows
             float ref[NC][2], sum[NC][2];
             int seen[NC][2];  // tokens that the row attends
 #pragma unroll
             for (int c = 0; c < NC; ++c)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int i = (p.rt * N + 8 * c + col + e) / H;
-                    seen[c][e] = p.s.n == 1 ? p.s.len : min(p.s.len - p.s.n + i + 1, p.s.len);
+                    seen[c][e] = p.s.len;
+                    if (p.s.n > 1)
+                        seen[c][e] = min(p.s.len - p.s.n + (tile_row + 8 * c + col + e) / H + 1, p.s.len);
                     ref[c][e] = sum[c][e] = 0.f;
                 }
             // tiles below this one need no mask
             const int first_masked =
-                (p.s.n == 1 ? p.s.len : p.s.len - p.s.n + (p.rt * N) / H + 1) / kTile;
+                (p.s.n == 1 ? p.s.len : p.s.len - p.s.n + min(tile_row / H + 1, p.s.n)) / kTile;
             for (int j = 0; j < p.tiles; ++j, ++g) {
                 const int t = p.t0 + j;
                 warp_wait_or_stop(&sh.s_full[g & 1], (g >> 1) & 1, stop);
                 tc_fence_after();
-                uint32_t xr[N / 2];
-                load_scores<N>(xr, tmem + (C::VT + (g & 1)) * N + lanes);
+                uint32_t xr[C::NG / 2];
+                load_scores<C::NG>(xr, tmem + (C::VT + (g & 1)) * N + C::NG * group + lanes);
                 tmem_wait_ld();
                 float x[NC][4];  // [c][2 * (second token) + (second row)]
 #pragma unroll
@@ -472,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         top[c][e] = fmaxf(x[c][e], x[c][2 + e]) * scale;
                         move |= top[c][e] - ref[c][e] > kHead + kLag;
                     }
-                if (any_softmax(move)) {
+                if (any_softmax<kSoft>(move)) {
                     // new references: the tile's maxima over all tokens
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
@@ -481,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int o = 4; o < 32; o <<= 1)
                                 top[c][e] = fmaxf(top[c][e], __shfl_xor_sync(0xffffffffu, top[c][e], o));
-                            if (lane < 4) sh.warps[warp][8 * c + col + e] = top[c][e];
+                            if (lane < 4) sh.warps[quarter][8 * c + col + e] = top[c][e];
                         }
-                    sync_softmax();
+                    sync_softmax<kSoft>();
 #pragma unroll
                     for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -499,16 +535,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float f = j == 0 ? 1.f : ex2(ref[c][e] - next);
                             sum[c][e] *= f;
                             ref[c][e] = next;
-                            if (warp == 0 && lane < 4) sh.factor[n] = f;
+                            if (quarter == 0 && lane < 4) sh.factor[n] = f;
                         }
-                    sync_softmax();
+                    sync_softmax<kSoft>();
                     if (j > 0) {
                         // O^T's columns follow, after the products into it
-                        warp_wait_or_stop(&sh.empty[(g - 1) % C::STAGES],
-                                          ((g - 1) / C::STAGES) & 1, stop);
+                        warp_wait_or_stop(&sh.pv_done, (g - 1) & 1, stop);
                         tc_fence_after();
 #pragma unroll 1
-                        for (int v = 0; v < C::VT * N; v += 16) {
+                        for (int v = 16 * group; v < C::VT * N; v += 16 * C::GROUPS) {
                             uint32_t o[16];
                             tmem_ld16(o, tmem + v + lanes);
                             tmem_wait_ld();
@@ -535,16 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     y[c][1] = pack_half2(p2, p3);
                 }
                 // the one P buffer is free when the products before are done
-                if (g > 0)
-                    warp_wait_or_stop(&sh.empty[(g - 1) % C::STAGES], ((g - 1) / C::STAGES) & 1,
-                                      stop);
+                if (g > 0) warp_wait_or_stop(&sh.pv_done, (g - 1) & 1, stop);
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = tok + 8 * e;
-                        *reinterpret_cast<uint32_t *>(p_smem + r * 128 + ((c ^ (r & 7)) << 4) +
-                                                      2 * col) = y[c][e];
+                        const int r = tok + 8 * e, piece = c + NC * group;
+                        *reinterpret_cast<uint32_t *>(p_smem + r * 128 + ((piece ^ (r & 7)) << 4) +
+                                                      4 * (lane & 3)) = y[c][e];
                     }
                 // values of rows past the sequence's end meet weights of 0: they must
                 // be finite
@@ -552,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (valid < kTile) {
                     unsigned char *v = base + (g % C::STAGES) * C::STAGE;
                     const int pieces = (kTile - valid) * 8;
-                    for (int e = threadIdx.x; e < pieces * (R / 64); e += 128)
+                    for (int e = threadIdx.x; e < pieces * (R / 64); e += kSoft)
                         *reinterpret_cast<uint4 *>(v + (e / pieces) * C::PLANE + valid * 128 +
                                                    (e % pieces) * 16) = make_uint4(0, 0, 0, 0);
                 }
@@ -568,128 +601,175 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1)
                         sum[c][e] += __shfl_xor_sync(0xffffffffu, sum[c][e], o);
-                    if (lane < 4) sh.warps[warp][8 * c + col + e] = sum[c][e];
-                    if (warp == 0 && lane < 4) sh.ref[8 * c + col + e] = ref[c][e];
+                    if (lane < 4) sh.warps[quarter][8 * c + col + e] = sum[c][e];
+                    if (quarter == 0 && lane < 4) sh.ref[8 * c + col + e] = ref[c][e];
                 }
             warp_wait_or_stop(&sh.o_full, k & 1, stop);
             tc_fence_after();
-            sync_softmax();
-            const int rows = min(N, p.s.n * H - p.rt * N);
-            const long long row0 = static_cast<long long>(p.s.q0) * H + p.rt * N;
+            sync_softmax<kSoft>();
+            const int rows = min(N, p.s.n * H - tile_row);  // this CTA's; none: padding
+            const int row0 = p.s.q0 * H + tile_row;
             const bool whole = p.t0 == 0 && p.tiles == p.seg_tiles;
-            const int slot = 2 * blockIdx.x + (p.t0 == 0 ? 1 : 0);
-            if (threadIdx.x < rows) {
+            const int slot = (2 * worker + (p.t0 == 0 ? 1 : 0)) * CL + rank;
+            if (static_cast<int>(threadIdx.x) < rows) {
                 const int n = threadIdx.x;
                 const float l = (sh.warps[0][n] + sh.warps[1][n]) + (sh.warps[2][n] + sh.warps[3][n]);
                 if (whole) {
-                    sh.factor[n] = l > 0.f || l != l ? 1.f / l : 0.f;
+                    sh.factor[n] = l == 0.f ? 0.f : 1.f / l;
                     if (a.lse_out)
                         a.lse_out[row0 + n] =
                             l == 0.f ? -INFINITY : (sh.ref[n] + log2f(l)) * 0.69314718055994531f;
                 } else {
-                    reinterpret_cast<float2 *>(ws + lay.ml)[slot * N + n] =
+                    reinterpret_cast<float2 *>(ws + lay.ml)[static_cast<size_t>(slot) * N + n] =
                         make_float2(l == 0.f ? -INFINITY : sh.ref[n], l);
                 }
             }
-            if (whole) sync_softmax();
-            float *acc = reinterpret_cast<float *>(ws + lay.acc) + static_cast<size_t>(slot) * N * R;
-            __half *out = static_cast<__half *>(a.out) + row0 * R;
+            if (whole) {
+                sync_softmax<kSoft>();
+                __half *out = static_cast<__half *>(a.out) + static_cast<long long>(row0) * R +
+                              32 * quarter + lane;
 #pragma unroll 1
-            for (int v = 0; v < C::VT * N; v += 16) {
-                uint32_t o[16];
-                tmem_ld16(o, tmem + v + lanes);
-                tmem_wait_ld();
-                const int d = 128 * (v / N) + 32 * warp + lane;
+                for (int v = 16 * group; v < C::VT * N; v += 16 * C::GROUPS) {
+                    const int n0 = v % N;
+                    if (n0 >= rows) continue;
+                    uint32_t o[16];
+                    tmem_ld16(o, tmem + v + lanes);
+                    tmem_wait_ld();
+                    __half *dst = out + n0 * R + 128 * (v / N);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int n = v % N + e;
-                    if (n >= rows) continue;
-                    const float f = __uint_as_float(o[e]);
-                    if (whole)
-                        out[static_cast<size_t>(n) * R + d] = __float2half_rn(f * sh.factor[n]);
-                    else
-                        acc[static_cast<size_t>(n) * R + d] = f;
+                    for (int e = 0; e < 16; ++e)
+                        if (n0 + e < rows)
+                            dst[e * R] = __float2half_rn(__uint_as_float(o[e]) * sh.factor[n0 + e]);
+                }
+            } else {
+                float *acc = reinterpret_cast<float *>(ws + lay.acc) +
+                             (static_cast<size_t>(slot) * R + 32 * quarter + lane) * N;
+#pragma unroll 2
+                for (int v = 16 * group; v < C::VT * N; v += 16 * C::GROUPS) {
+                    uint32_t o[16];
+                    tmem_ld16(o, tmem + v + lanes);
+                    tmem_wait_ld();
+                    uint4 *dst = reinterpret_cast<uint4 *>(acc + 128 * N * (v / N) + v % N);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
             tc_fence_before();
-            sync_softmax();  // sh.warps, sh.ref and sh.factor are free again
+            sync_softmax<kSoft>();  // sh.warps, sh.ref and sh.factor are free again
             if (lane == 0) mbar_arrive(&sh.o_free);
-            if (!whole && p.t0 == 0 && threadIdx.x == 0) {
-                // this CTA starts the segment: the join finds its last piece here
-                const long long last = p.seg_first + p.seg_tiles;
-                const int c1 = static_cast<int>((last * range.workers - 1) / range.total);
-                static_cast<int4 *>(a.workspace)[blockIdx.x] =
-                    make_int4(static_cast<int>(row0), rows, c1, 0);
+            if (p.t0 == 0) {
+                // the worker that starts a segment says where its last piece is
+                if (threadIdx.x == 0 && (!whole || sp.by_segment)) {
+                    const int at = sp.by_segment ? p.b * sp.row_tiles + p.rt : worker;
+                    const int last = whole ? worker : sh.split.worker_of(p.seg_first + p.seg_tiles - 1);
+                    records[at * CL + rank] = make_int4(row0, whole ? 0 : max(rows, 0), worker, last);
+                }
+                recorded |= !whole;
             }
-            recorded |= !whole && p.t0 == 0;
             ++k;
         }
-        if (!recorded && threadIdx.x == 0)
-            static_cast<int4 *>(a.workspace)[blockIdx.x] = make_int4(0, 0, -1, 0);
+        if (!recorded && threadIdx.x == 0 && !sp.by_segment) records[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
     tc_fence_before();
-    __syncthreads();
+    __syncwarp();
+    // a peer's copies and commits reach this CTA's memory until both are done
+    if (CL > 1) cluster_sync(); else __syncthreads();
     if (threadIdx.x == 0 && sh.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
     __syncwarp();
-    if (warp == 5) tmem_free(tmem, C::TMEM);
+    if (warp == C::SW + 1) tmem_free(tmem, C::TMEM);
 }
 
-// The pieces of each cut segment, joined: record blockIdx.x, rows blockIdx.y,
-// + gridDim.y, ...  Two halves of the block take every other piece.
-template <int R>
-__global__ void __launch_bounds__(R / 2)
-    latent_join_kernel(const LatentAttentionArgs a, int workers, int N) {
+// The pieces of each cut segment, joined.  A unit is four rows of one column (one
+// 16-byte load a piece); a block has 256 / G units and G threads a unit, each for
+// every G-th piece, and turns its columns to rows on the way out.
+constexpr int kJoinThreads = 256;
+
+template <int R, int N, int CL>
+__global__ void __launch_bounds__(kJoinThreads)
+    latent_join_kernel(const LatentAttentionArgs a, const LatentSplit sp) {
+    __shared__ float parts[kJoinThreads];
+    __shared__ float4 sums[kJoinThreads];
+    __shared__ float ref[N], inv[N];
+    __shared__ __align__(16) __half tile[kJoinThreads * 4];
     grid_dependency_wait();
     allow_dependent_launch();
-    constexpr int T = R / 4;  // threads of one half, 4 columns each
-    __shared__ float4 other[T];
     const int4 rec = static_cast<const int4 *>(a.workspace)[blockIdx.x];
-    if (rec.z < 0) return;
-    const Layout lay = layout(workers, N, R);
+    if (rec.y <= 0) return;
+    const Layout lay = layout(sp.records, sp.workers, CL, N, R);
     const char *ws = static_cast<const char *>(a.workspace);
     const float2 *ml = reinterpret_cast<const float2 *>(ws + lay.ml);
     const float4 *acc = reinterpret_cast<const float4 *>(ws + lay.acc);
-    const int pieces = rec.z - static_cast<int>(blockIdx.x) + 1;
-    const int half = threadIdx.x / T, x = threadIdx.x % T, lane = threadIdx.x & 31;
-    auto slot = [&](int k) { return 2 * (static_cast<int>(blockIdx.x) + k) + (k == 0 ? 1 : 0); };
-    for (int n = blockIdx.y; n < rec.y; n += gridDim.y) {
-        float m = -INFINITY;
-        for (int k = lane; k < pieces; k += 32) m = fmaxf(m, ml[slot(k) * N + n].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float m0 = m > -INFINITY ? m : 0.f;
-        float l = 0.f;
-        for (int k = lane; k < pieces; k += 32) {
-            const float2 v = ml[slot(k) * N + n];
-            l += v.y * ex2(v.x - m0);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = half; k < pieces; k += 2) {
-            const size_t at = static_cast<size_t>(slot(k)) * N + n;
-            const float f = ex2(ml[at].x - m0);
-            const float4 v = acc[at * (R / 4) + x];
-            s.x = fmaf(v.x, f, s.x);
-            s.y = fmaf(v.y, f, s.y);
-            s.z = fmaf(v.z, f, s.z);
-            s.w = fmaf(v.w, f, s.w);
-        }
-        if (half == 1) other[x] = s;
+    const int pieces = rec.w - rec.z + 1, rank = blockIdx.x % CL;
+    auto slot = [&](int k) { return static_cast<size_t>((2 * (rec.z + k) + (k == 0 ? 1 : 0)) * CL + rank); };
+    // the rows' references and sums over all pieces
+    {
+        constexpr int S = kJoinThreads / N;  // threads of a row
+        const int n = threadIdx.x % N, i = threadIdx.x / N;
+        float m = -INFINITY, l = 0.f;
+        for (int k = i; k < pieces; k += S) m = fmaxf(m, ml[slot(k) * N + n].x);
+        parts[threadIdx.x] = m;
         __syncthreads();
-        if (half == 0) {
-            const float4 v = other[x];
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-            const size_t row = static_cast<size_t>(rec.x) + n;
-            reinterpret_cast<uint2 *>(a.out)[row * (R / 4) + x] =
-                make_uint2(pack_half2((s.x + v.x) * inv, (s.y + v.y) * inv),
-                           pack_half2((s.z + v.z) * inv, (s.w + v.w) * inv));
-            if (a.lse_out && x == 0)
-                a.lse_out[row] = l == 0.f ? -INFINITY : (m0 + log2f(l)) * 0.69314718055994531f;
+#pragma unroll
+        for (int s = 0; s < S; ++s) m = fmaxf(m, parts[s * N + n]);
+        m = m > -INFINITY ? m : 0.f;
+        for (int k = i; k < pieces; k += S) {
+            const float2 v = ml[slot(k) * N + n];
+            l += v.y * ex2(v.x - m);
+        }
+        __syncthreads();
+        parts[threadIdx.x] = l;
+        __syncthreads();
+        if (i == 0) {
+#pragma unroll
+            for (int s = 1; s < S; ++s) l += parts[s * N + n];
+            ref[n] = m;
+            inv[n] = l == 0.f ? 0.f : 1.f / l;
+            if (a.lse_out && blockIdx.y == 0 && n < rec.y)
+                a.lse_out[rec.x + n] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         }
         __syncthreads();
     }
+    const int G = sp.join_threads, units = kJoinThreads / G;
+    const int u = threadIdx.x % units, i = threadIdx.x / units;
+    const int at = blockIdx.y * units + u, n0 = 4 * (at % (N / 4));
+    const float r0 = ref[n0], r1 = ref[n0 + 1], r2 = ref[n0 + 2], r3 = ref[n0 + 3];
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = i; k < pieces; k += G) {
+        const size_t sl = slot(k);
+        const float4 v = acc[sl * (R * N / 4) + at];
+        const float4 ma = *reinterpret_cast<const float4 *>(ml + sl * N + n0);
+        const float4 mb = *reinterpret_cast<const float4 *>(ml + sl * N + n0 + 2);
+        s.x = fmaf(v.x, ex2(ma.x - r0), s.x);
+        s.y = fmaf(v.y, ex2(ma.z - r1), s.y);
+        s.z = fmaf(v.z, ex2(mb.x - r2), s.z);
+        s.w = fmaf(v.w, ex2(mb.z - r3), s.w);
+    }
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    const int cols = units * 4 / N;  // of this block
+    if (i == 0) {
+        for (int k = 1; k < G; ++k) {
+            const float4 v = sums[k * units + u];
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        const int c = u / (N / 4);
+        tile[(n0 + 0) * cols + c] = __float2half_rn(s.x * inv[n0]);
+        tile[(n0 + 1) * cols + c] = __float2half_rn(s.y * inv[n0 + 1]);
+        tile[(n0 + 2) * cols + c] = __float2half_rn(s.z * inv[n0 + 2]);
+        tile[(n0 + 3) * cols + c] = __float2half_rn(s.w * inv[n0 + 3]);
+    }
+    __syncthreads();
+    const int words = cols / 2;
+    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__half *>(a.out) +
+                                                 static_cast<long long>(rec.x) * R + blockIdx.y * cols);
+    for (int x = threadIdx.x; x < min(rec.y, N) * words; x += kJoinThreads)
+        out[static_cast<size_t>(x / words) * (R / 2) + x % words] =
+            reinterpret_cast<const uint32_t *>(tile)[x];
 }
 
 bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t width,
@@ -703,48 +783,76 @@ bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t widt
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of a row tile: the smallest of 16, 32 and 64 that holds a sequence's rows.
-int tile_rows(int max_q_len, int heads) {
-    const long long rows = static_cast<long long>(max_q_len) * heads;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-}
-
-template <int R, int N>
-cudaError_t launch(const LatentAttentionArgs &a, int workers, cudaStream_t stream) {
-    using C = Cfg<R, N>;
+template <int R, int N, int CL>
+cudaError_t launch(const LatentAttentionArgs &a, const LatentSplit &sp, cudaStream_t stream) {
+    using C = Cfg<R, N, CL>;
     CUtensorMap mq, mc;
+    const int share = kTile / CL;
     if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E, N) ||
         !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E,
-                  a.block_size < kTile ? a.block_size : kTile))
+                  a.block_size < share ? a.block_size : share))
         return cudaErrorNotSupported;
-    auto kern = latent_attention_kernel<R, N>;
+    auto kern = latent_attention_kernel<R, N, CL>;
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [&] {
         attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (attr != cudaSuccess) return attr;
-    cudaError_t e = launch_pdl(kern, dim3(workers), dim3(kThreads), C::SMEM, stream, a, mq, mc);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sp.workers * CL);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CL;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, sp, mq, mc);
     if (e != cudaSuccess) return e;
-    return launch_pdl(latent_join_kernel<R>, dim3(workers, 16), dim3(R / 2), 0, stream, a, workers, N);
+    const dim3 grid(sp.records * CL, R * N / 4 * sp.join_threads / kJoinThreads);
+    return launch_pdl(latent_join_kernel<R, N, CL>, grid, dim3(kJoinThreads), 0, stream, a, sp);
 }
 
 }  // namespace
 
-size_t latent_workspace(int max_q_len, int heads, int latent_dim, int workers) {
-    return layout(workers, tile_rows(max_q_len, heads), latent_dim).total;
+bool latent_split(int num_seqs, int max_q_len, int heads, int latent_dim, int max_len, int sms,
+                  LatentSplit *sp) {
+    const long long rows = static_cast<long long>(max_q_len) * heads;
+    sp->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    sp->cluster = rows > 64 ? 2 : 1;
+    const int tile = sp->rows * sp->cluster;
+    const long long tiles = (rows + tile - 1) / tile;
+    const long long units = tiles * num_seqs * (max_len / kTile + 1);
+    if (units >= (1LL << 31)) return false;
+    sp->row_tiles = static_cast<int>(tiles);
+    sp->workers = sms / sp->cluster;
+    // one token a sequence: every sequence has the same row tiles, and its
+    // segments have fixed places; otherwise a worker records what it starts
+    sp->by_segment = max_q_len == 1 && tiles * num_seqs <= sp->workers;
+    sp->records = sp->by_segment ? static_cast<int>(tiles * num_seqs) : sp->workers;
+    // threads of the join over a segment's pieces: about workers / segments of them
+    const long long pieces = sp->workers / (tiles * num_seqs > 0 ? tiles * num_seqs : 1);
+    sp->join_threads = pieces >= 16 ? 8 : pieces >= 8 ? 4 : pieces >= 4 ? 2 : 1;
+    sp->ws_bytes = layout(sp->records, sp->workers, sp->cluster, sp->rows, latent_dim).total;
+    return true;
 }
 
-cudaError_t launch_latent_attention(const LatentAttentionArgs &a, int workers,
+cudaError_t launch_latent_attention(const LatentAttentionArgs &a, const LatentSplit &sp,
                                     cudaStream_t stream) {
-    const int rows = tile_rows(a.max_q_len, a.n_q_heads);
     if (a.latent_dim == 512)
-        return rows == 16   ? launch<512, 16>(a, workers, stream)
-               : rows == 32 ? launch<512, 32>(a, workers, stream)
-                            : launch<512, 64>(a, workers, stream);
-    return rows == 16   ? launch<256, 16>(a, workers, stream)
-           : rows == 32 ? launch<256, 32>(a, workers, stream)
-                        : launch<256, 64>(a, workers, stream);
+        return sp.cluster == 2 ? launch<512, 64, 2>(a, sp, stream)
+               : sp.rows == 16 ? launch<512, 16, 1>(a, sp, stream)
+               : sp.rows == 32 ? launch<512, 32, 1>(a, sp, stream)
+                               : launch<512, 64, 1>(a, sp, stream);
+    return sp.cluster == 2 ? launch<256, 64, 2>(a, sp, stream)
+           : sp.rows == 16 ? launch<256, 16, 1>(a, sp, stream)
+           : sp.rows == 32 ? launch<256, 32, 1>(a, sp, stream)
+                           : launch<256, 64, 1>(a, sp, stream);
 }
 
 }  // namespace pkv

@@ -76,9 +76,20 @@ struct LatentAttentionArgs {
     float *lse_out;
     int32_t *err;
 };
-// workers: CTAs of the split (one per SM); the workspace holds what they cut.
-size_t latent_workspace(int max_q_len, int heads, int latent_dim, int workers);
-cudaError_t launch_latent_attention(const LatentAttentionArgs &a, int workers,
+// How a call's work is split: `workers` clusters of `cluster` CTAs with `rows`
+// query rows each, one CTA per SM.
+struct LatentSplit {
+    int rows, cluster, workers;
+    int row_tiles;   // of a sequence of max_q_len tokens
+    int by_segment;  // the join's records: one per (sequence, row tile), else one per worker
+    int records;
+    int join_threads;
+    size_t ws_bytes;
+};
+// false: more than 2^31 units of work.
+bool latent_split(int num_seqs, int max_q_len, int heads, int latent_dim, int max_len, int sms,
+                  LatentSplit *sp);
+cudaError_t launch_latent_attention(const LatentAttentionArgs &a, const LatentSplit &sp,
                                     cudaStream_t stream);
 
 struct LatentPrefillArgs {
