@@ -31,6 +31,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 namespace {
 
 constexpr int kTile = 64;  // tokens
+constexpr int kAhead = 3;  // tiles that the copies into L2 run ahead of those into shared memory
 // P holds 2^(s - r) with r kHead below the running maximum: weights up to
 // 2^kHead, and up to 2^(kHead + kLag) before r follows; fp16 ends at 2^16.
 constexpr float kHead = 6.f, kLag = 8.f;
@@ -41,10 +42,12 @@ template <int R, int N, int CL>
 struct Cfg {
     static constexpr int E = R + 64, PL = E / 64, VT = R / 128;
     static constexpr int ROWS = CL * N;  // query rows of a worker's row tile
-    static constexpr int PLANE = kTile * 128, QPLANE = N * 128;
-    static constexpr int STAGE = PL * PLANE;
+    // shared memory holds rows in groups of 8: all 64-column planes of a group
+    // (1024 bytes each) together, so one copy brings 8 whole rows
+    static constexpr int GROUP = PL * 1024;
+    static constexpr int STAGE = kTile / 8 * GROUP;
     static constexpr int STAGES = R == 512 ? 2 : 4;
-    static constexpr int Q_BYTES = PL * QPLANE, P_BYTES = kTile * 128;
+    static constexpr int Q_BYTES = N / 8 * GROUP, P_BYTES = kTile * 128;
     static constexpr int SMEM = 1024 + STAGES * STAGE + Q_BYTES + P_BYTES;
     static constexpr int COLS = (VT + 2) * N;
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
@@ -321,9 +324,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
     } else if (warp == C::SW) {
         // --- copies ---
         Piece p;
-        // this CTA loads the cluster's share `rank` of every tile: kTile / CL tokens
-        constexpr int kShare = kTile / CL;
-        const int box = min(a.block_size, kShare), subs = kTile / box, own = kShare / box;
+        // a lane copies 8 tokens; the cluster's CTAs share a tile's lanes
+        constexpr int kLanes = kTile / 8;
+        const bool mine = lane < kLanes && lane / (kLanes / CL) == rank;
+        const char *cache = static_cast<const char *>(a.cache);
         int g = 0, k = 0;  // tiles, pieces so far
         bool ok = true;
         while (ok && next_piece(a, C::ROWS, &w, &p)) {
@@ -332,46 +336,53 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 if (ok) {
                     mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
                     const int row = p.s.q0 * H + p.rt * C::ROWS + rank * N;
-                    for (int x = 0; x < C::PL; ++x)
-                        tma_load_2d(q_smem + x * C::QPLANE, &mq, 64 * x, row, &sh.q_full);
+                    for (int x = 0; x < N / 8; ++x)
+                        tma_load_3d(q_smem + x * C::GROUP, &mq, 0, row + 8 * x, 0, &sh.q_full);
                 }
             }
             ++k;
             const int32_t *table = a.block_tables + static_cast<long long>(p.b) * a.max_blocks_per_seq;
-            auto block_of = [&](int t) {  // this lane's block of tile t, or -1
-                const int token = t * kTile + lane * box;
-                if (lane >= subs || token >= p.s.len || t >= p.t0 + p.tiles) return -1;
-                const int id = table[token / a.block_size];
-                if (id >= 0 && id < a.num_blocks) return id;
-                flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
-                return 0;  // some block of the pool: the sequence's result is unspecified
+            const int end = p.t0 + p.tiles;
+            auto row_of = [&](int t) {  // first cache row of this lane's tokens of tile t, or -1
+                const int token = t * kTile + lane * 8;
+                if (lane >= kLanes || token >= p.s.len || t >= end) return -1;
+                int id = table[token / a.block_size];
+                if (id < 0 || id >= a.num_blocks) {
+                    flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
+                    id = 0;  // some block of the pool: the sequence's result is unspecified
+                }
+                return id * a.block_size + token % a.block_size;
             };
-            int id = block_of(p.t0);
-            for (int t = p.t0; t < p.t0 + p.tiles; ++t, ++g) {
-                const int next = block_of(t + 1);
+            auto to_l2 = [&](int row) {
+                if (mine && row >= 0)
+                    bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), 8 * C::E * 2);
+            };
+            for (int d = 1; d < kAhead; ++d) to_l2(row_of(p.t0 + d));
+            int row = row_of(p.t0), far = row_of(p.t0 + kAhead);
+            for (int t = p.t0; t < end; ++t, ++g) {
+                const int next = row_of(t + 1), next_far = row_of(t + 1 + kAhead);
                 const int s = g % C::STAGES;
+                to_l2(far);
                 if (lane == 0) ok = ok && wait_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
-                const int live = __popc(__ballot_sync(0xffffffffu, id >= 0));
+                const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
                 if (lane == 0) {
                     if (live > 0)
-                        mbar_arrive_expect_tx(&sh.full[s], live * box * C::E * 2);
+                        mbar_arrive_expect_tx(&sh.full[s], live * C::GROUP);
                     else
                         mbar_arrive(&sh.full[s]);
                 }
                 __syncwarp();
-                if (id >= 0 && lane / own == rank) {
-                    const int row = id * a.block_size + (t * kTile + lane * box) % a.block_size;
-                    unsigned char *dst = base + s * C::STAGE + lane * box * 128;
-                    for (int x = 0; x < C::PL; ++x)
-                        if (CL > 1)
-                            tma_load_2d_multicast(dst + x * C::PLANE, &mc, 64 * x, row, &sh.full[s],
-                                                  (1 << CL) - 1);
-                        else
-                            tma_load_2d(dst + x * C::PLANE, &mc, 64 * x, row, &sh.full[s]);
+                if (mine && row >= 0) {
+                    unsigned char *dst = base + s * C::STAGE + lane * C::GROUP;
+                    if (CL > 1)
+                        tma_load_3d_multicast(dst, &mc, 0, row, 0, &sh.full[s], (1 << CL) - 1);
+                    else
+                        tma_load_3d(dst, &mc, 0, row, 0, &sh.full[s]);
                 }
-                id = next;
+                row = next;
+                far = next_far;
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
@@ -404,8 +415,8 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                         tc_fence_after();
 #pragma unroll
                         for (int x = 0; x < 4 * C::PL; ++x)
-                            mma_ss(d, smem_desc(ka + (x / 4) * C::PLANE + (x % 4) * 32, 1024, 0),
-                                   smem_desc(qa + (x / 4) * C::QPLANE + (x % 4) * 32, 1024, 0), ds,
+                            mma_ss(d, smem_desc(ka + (x / 4) * 1024 + (x % 4) * 32, C::GROUP, 0),
+                                   smem_desc(qa + (x / 4) * 1024 + (x % 4) * 32, C::GROUP, 0), ds,
                                    x > 0);
                         mma_commit(&sh.s_full[gs & 1]);
                         if (++sj == p.tiles) mma_commit(&sh.q_empty);
@@ -422,7 +433,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
 #pragma unroll
                             for (int x = 0; x < kTile / 16; ++x)
                                 mma_ss(tmem + v * N,
-                                       smem_desc(va + 2 * v * C::PLANE + x * 2048, 1024, C::PLANE),
+                                       smem_desc(va + 2 * v * 1024 + 2 * x * C::GROUP, C::GROUP, 1024),
                                        smem_desc(pa + x * 2048, 1024, 0), dpv, pj > 0 || x > 0);
                         if (CL > 1)
                             mma_commit_multicast(&sh.empty[gp % C::STAGES], (1 << CL) - 1);
@@ -584,10 +595,12 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 const int valid = p.s.len - t * kTile;
                 if (valid < kTile) {
                     unsigned char *v = base + (g % C::STAGES) * C::STAGE;
-                    const int pieces = (kTile - valid) * 8;
-                    for (int e = threadIdx.x; e < pieces * (R / 64); e += kSoft)
-                        *reinterpret_cast<uint4 *>(v + (e / pieces) * C::PLANE + valid * 128 +
-                                                   (e % pieces) * 16) = make_uint4(0, 0, 0, 0);
+                    for (int e = threadIdx.x; e < (kTile - valid) * (R / 8); e += kSoft) {
+                        const int r = valid + e / (R / 8), piece = e % (R / 8);
+                        *reinterpret_cast<uint4 *>(v + (r / 8) * C::GROUP + (piece / 8) * 1024 +
+                                                   (r % 8) * 128 + (piece % 8) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -772,12 +785,13 @@ __global__ void __launch_bounds__(kJoinThreads)
             reinterpret_cast<const uint32_t *>(tile)[x];
 }
 
-bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t width,
-              cuuint32_t box_rows) {
+// Rows of `width` fp16 values as [width / 64 planes][rows][64 columns]: a box is 8
+// rows of all planes, plane by plane, with the 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t width) {
     auto fn = encode_fn();
-    const cuuint64_t dims[2] = {width, rows}, strides[1] = {width * 2};
-    const cuuint32_t box[2] = {64, box_rows}, one[2] = {1, 1};
-    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(base), dims, strides,
+    const cuuint64_t dims[3] = {64, rows, width / 64}, strides[2] = {width * 2, 128};
+    const cuuint32_t box[3] = {64, 8, static_cast<cuuint32_t>(width / 64)}, one[3] = {1, 1, 1};
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides,
                     box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -787,10 +801,8 @@ template <int R, int N, int CL>
 cudaError_t launch(const LatentAttentionArgs &a, const LatentSplit &sp, cudaStream_t stream) {
     using C = Cfg<R, N, CL>;
     CUtensorMap mq, mc;
-    const int share = kTile / CL;
-    if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E, N) ||
-        !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E,
-                  a.block_size < share ? a.block_size : share))
+    if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E) ||
+        !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E))
         return cudaErrorNotSupported;
     auto kern = latent_attention_kernel<R, N, CL>;
     static std::once_flag once;

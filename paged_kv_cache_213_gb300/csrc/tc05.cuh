@@ -192,15 +192,21 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 2-D tiled TMA load to the same offset of every CTA of the mask, completion on
+// 3-D tiled TMA load to the same offset of every CTA of the mask, completion on
 // the barrier at this offset in each of them.
-__device__ __forceinline__ void tma_load_2d_multicast(void *dst, const void *tmap, int x, int y,
-                                                      uint64_t *bar, uint16_t mask) {
+__device__ __forceinline__ void tma_load_3d_multicast(void *dst, const void *tmap, int x, int y,
+                                                      int z, uint64_t *bar, uint16_t mask) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_addr(bar)), "h"(mask)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".multicast::cluster [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar)),
+        "h"(mask)
         : "memory");
+}
+
+// Brings bytes (a multiple of 16, from a 16-byte boundary) into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
 }  // namespace pkv
