@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRows = 16;
+constexpr int kSteps = 5;  // pieces a thread has in flight: 16 rows of 576 entries in one go
 
 __global__ void __launch_bounds__(kThreads) latent_gather_kernel(const LatentGatherArgs a) {
     allow_dependent_launch();
@@ -43,15 +44,26 @@ __global__ void __launch_bounds__(kThreads) latent_gather_kernel(const LatentGat
     }
     __syncthreads();
     const int rv = a.latent_dim / 8, pv = a.rope_dim / 8, w = rv + pv;
+    // i / w by the high half of a product: exact, since i * w < 2^20 < 2^32 / w
+    const unsigned inv = static_cast<unsigned>((0x100000000ull + w - 1) / w);
     const uint4 *cache = static_cast<const uint4 *>(a.cache);
     uint4 *latents = static_cast<uint4 *>(a.latents), *ropes = static_cast<uint4 *>(a.ropes);
-    for (int i = threadIdx.x; i < kRows * w; i += kThreads) {
-        const int k = i / w, c = i - k * w;
-        const long long row = src[k];
-        if (row < 0) continue;
-        const uint4 x = cache[row * w + c];
-        const long long r = first + k;
-        if (c < rv) latents[r * rv + c] = x; else ropes[r * pv + (c - rv)] = x;
+    for (int i0 = threadIdx.x; i0 < kRows * w; i0 += kSteps * kThreads) {
+        uint4 x[kSteps];
+        uint4 *dst[kSteps];
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            const int i = i0 + s * kThreads;
+            dst[s] = nullptr;
+            if (i >= kRows * w) continue;
+            const int k = __umulhi(i, inv), c = i - k * w;
+            if (src[k] < 0) continue;
+            x[s] = cache[src[k] * w + c];
+            dst[s] = c < rv ? latents + (first + k) * rv + c : ropes + (first + k) * pv + (c - rv);
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+            if (dst[s]) *dst[s] = x[s];
     }
 }
 

@@ -44,45 +44,64 @@ __device__ __forceinline__ uint2 quantize8(const float (&y)[8], float scale) {
     return make_uint2(w[0], w[1]);
 }
 
-// Rotates the 8 entries y (entries 8 j .. 8 j + 7 of a vector) by the table row
-// cs (cos, then sin, rot / 2 each).  Split halves: the partner entries are
-// rot / 16 lanes up or down; every lane of the warp calls this.
-__device__ __forceinline__ void rotate8(float (&y)[8], const float *cs, int j, int rot,
-                                        bool interleaved, bool active) {
+// The cosines and sines that entries 8 j .. 8 j + 7 of a vector need, from the
+// table row cs (cos, then sin, rot / 2 each): 8 pairs of split halves, or 4
+// interleaved ones.
+struct Turn {
+    float c[8], s[8];
+};
+
+__device__ __forceinline__ void load4(float *d, const float *p) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    d[0] = v.x;
+    d[1] = v.y;
+    d[2] = v.z;
+    d[3] = v.w;
+}
+
+__device__ __forceinline__ Turn load_turn(const float *cs, int j, int rot, bool interleaved) {
+    Turn t;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t.c[i] = 1.f, t.s[i] = 0.f;
+    if (8 * j >= rot) return t;
     const int half = rot / 2;
     if (interleaved) {
-        if (!active || 8 * j >= rot) return;
-        const float4 c = *reinterpret_cast<const float4 *>(cs + 4 * j);
-        const float4 s = *reinterpret_cast<const float4 *>(cs + half + 4 * j);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+        load4(t.c, cs + 4 * j);
+        load4(t.s, cs + half + 4 * j);
+    } else {
+        const int p = 8 * j < half ? 8 * j : 8 * j - half;
+        load4(t.c, cs + p);
+        load4(t.c + 4, cs + p + 4);
+        load4(t.s, cs + half + p);
+        load4(t.s + 4, cs + half + p + 4);
+    }
+    return t;
+}
+
+// Rotates the 8 entries y (entries 8 j .. of a vector) by t.  Split halves: the
+// partner entries are rot / 16 lanes up or down; every lane of the warp calls this.
+__device__ __forceinline__ void rotate8(float (&y)[8], const Turn &t, int j, int rot,
+                                        bool interleaved) {
+    if (interleaved) {
+        if (8 * j >= rot) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = y[2 * i], b = y[2 * i + 1];
-            y[2 * i] = a * cc[i] - b * ss[i];
-            y[2 * i + 1] = b * cc[i] + a * ss[i];
+            y[2 * i] = a * t.c[i] - b * t.s[i];
+            y[2 * i + 1] = b * t.c[i] + a * t.s[i];
         }
         return;
     }
-    const int h8 = half / 8;
-    const bool low = j < h8;
-    const bool turned = j < 2 * h8;
+    const int h8 = rot / 16;
+    const bool low = j < h8, turned = j < 2 * h8;
     const int lane = threadIdx.x & 31;
     const int src = turned ? (low ? lane + h8 : lane - h8) : lane;
-    float other[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) other[i] = __shfl_sync(0xffffffffu, y[i], src);
-    if (!active || !turned) return;
-    const int p = 8 * (low ? j : j - h8);
-    const float4 c0 = *reinterpret_cast<const float4 *>(cs + p);
-    const float4 c1 = *reinterpret_cast<const float4 *>(cs + p + 4);
-    const float4 s0 = *reinterpret_cast<const float4 *>(cs + half + p);
-    const float4 s1 = *reinterpret_cast<const float4 *>(cs + half + p + 4);
-    const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-    const float ss[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        // low half: a cos - b sin; high half: b cos + a sin
-        y[i] = low ? y[i] * cc[i] - other[i] * ss[i] : y[i] * cc[i] + other[i] * ss[i];
+    for (int i = 0; i < 8; ++i) {
+        const float other = __shfl_sync(0xffffffffu, y[i], src);
+        // low half: a cos - b sin; high half: b cos + a sin; beyond: cos 1, sin 0
+        y[i] = fmaf(other, low ? -t.s[i] : t.s[i], y[i] * t.c[i]);
+    }
 }
 
 // The slot and the rotation row of a token; false for a token that is skipped
@@ -103,76 +122,91 @@ __device__ __forceinline__ bool token_place(const int64_t *slots, const int32_t 
     return !bad_slot && !bad_pos;
 }
 
-// One group of `width` lanes per (token, head); heads 0 .. H-1 are queries,
-// then Hk keys, then Hk values.
-template <bool F8>
+// One warp per (token, heads): `width` lanes a head, 32 / width heads at once, U
+// steps of them, whose loads are all in flight together and which share the
+// token's slot and rotation row.  Heads 0 .. H-1 are queries, then Hk keys, then Hk
+// values.  U = 4 where the warps fill the GPU anyway: with one head a lane the
+// chain from position to rotation row leaves too few bytes in flight (8191 tokens x
+// 80 heads into E4M3: 125 us with U = 1).  U = 1 for fewer: more warps, a shorter
+// chain.
+template <bool F8, int U>
 __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs a) {
     allow_dependent_launch();  // the attention kernel may get scheduled meanwhile
-    const int heads = a.n_q_heads + 2 * a.n_kv_heads;
-    const unsigned unit = (blockIdx.x * kThreads + threadIdx.x) >> a.width_log2;
-    const int j = threadIdx.x & ((1 << a.width_log2) - 1);
-    const bool in_grid = unit < static_cast<unsigned>(a.num_tokens) * heads;
-    const int token = in_grid ? unit / heads : 0;
-    const int head = in_grid ? unit - token * heads : 0;
-    const bool is_q = head < a.n_q_heads;
-    const bool is_v = head >= a.n_q_heads + a.n_kv_heads;
-    const int kv_head = head - a.n_q_heads - (is_v ? a.n_kv_heads : 0);
-    const int d = a.head_dim;
-    bool active = in_grid && 8 * j < d;
-    const __half *x = static_cast<const __half *>(is_q ? a.q : is_v ? a.v : a.k) +
-                      token * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) +
-                      (is_q ? head : kv_head) * d + 8 * j;
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (active) raw = *reinterpret_cast<const uint4 *>(x);
-    long long slot = -1;
-    int position = 0;
-    const bool keep = token_place(a.slot_mapping, a.positions, a.num_slots, a.max_positions,
-                                  a.rot_dim, token, in_grid && head == 0 && j == 0, a.err, &slot,
-                                  &position);
-    active = active && keep;
-    if (!keep) position = 0;  // a row that exists: the lanes below load nothing of it
-    float y[8];
-    unpack8(raw, y);
-    const __half *w = static_cast<const __half *>(is_q ? a.q_weight : a.k_weight);
-    // the whole warp runs the shuffles; values pass through untouched
-    float sum = 0.f;
+    const int lane = threadIdx.x & 31, j = lane & ((1 << a.width_log2) - 1);
+    const int per = 32 >> a.width_log2;  // heads of a step
+    const unsigned job = (blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const unsigned token = job / a.jobs;
+    if (token >= static_cast<unsigned>(a.num_tokens)) return;
+    const int first = (job - token * a.jobs) * per * U + (lane >> a.width_log2);
+    const int H = a.n_q_heads, Hk = a.n_kv_heads, d = a.head_dim;
+    const bool inside = 8 * j < d;
+    const __half *q = static_cast<const __half *>(a.q) + token * a.q_stride + 8 * j;
+    const __half *k = static_cast<const __half *>(a.k) + token * a.k_stride + 8 * j;
+    const __half *v = static_cast<const __half *>(a.v) + token * a.v_stride + 8 * j;
+    uint4 raw[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum += y[i] * y[i];
-    for (int o = (1 << a.width_log2) / 2; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (!is_v && w && active) {
-        const float inv = 1.f / sqrtf(sum / static_cast<float>(d) + a.eps);
-        float wf[8];
-        unpack8(*reinterpret_cast<const uint4 *>(w + 8 * j), wf);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * wf[i];
+    for (int u = 0; u < U; ++u) {
+        const int h = first + u * per;
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (inside && h < H + 2 * Hk)
+            raw[u] = *reinterpret_cast<const uint4 *>(
+                h < H ? q + h * d : h < H + Hk ? k + (h - H) * d : v + (h - H - Hk) * d);
     }
-    if (a.rot_dim > 0) {
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = y[i];
-        rotate8(z, a.cos_sin + static_cast<long long>(position) * a.rot_dim, j, a.rot_dim,
-                a.interleaved, active && !is_v);
-        if (!is_v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = z[i];
-    }
-    if (!active) return;
-    if (is_q) {
-        __half *dst = static_cast<__half *>(a.q_out) +
-                      (static_cast<long long>(token) * a.n_q_heads + head) * d + 8 * j;
-        *reinterpret_cast<uint4 *>(dst) = pack8(y);
+    long long slot;
+    int position;
+    if (!token_place(a.slot_mapping, a.positions, a.num_slots, a.max_positions, a.rot_dim, token,
+                     lane == 0 && first == 0, a.err, &slot, &position))
         return;
-    }
+    Turn turn{};
+    if (a.rot_dim > 0)
+        turn = load_turn(a.cos_sin + static_cast<long long>(position) * a.rot_dim, j, a.rot_dim,
+                         a.interleaved);
     const long long block = slot / a.block_size;
     const long long row = slot - block * a.block_size;
-    const long long dst = ((block * a.n_kv_heads + kv_head) * a.block_size + row) * d + 8 * j;
-    if (F8) {
-        unsigned char *cache = static_cast<unsigned char *>(is_v ? a.v_cache : a.k_cache);
-        *reinterpret_cast<uint2 *>(cache + dst) = quantize8(y, is_v ? a.v_scale : a.k_scale);
-    } else {
-        __half *cache = static_cast<__half *>(is_v ? a.v_cache : a.k_cache);
-        *reinterpret_cast<uint4 *>(cache + dst) = is_v ? raw : pack8(y);
+    __half *out = static_cast<__half *>(a.q_out) + static_cast<long long>(token) * H * d + 8 * j;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int h = first + u * per;
+        const bool is_q = h < H, is_v = h >= H + Hk;
+        float y[8];
+        unpack8(raw[u], y);
+        const __half *w = static_cast<const __half *>(is_q ? a.q_weight : a.k_weight);
+        // the whole warp runs the shuffles; values pass through untouched
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+        for (int o = (1 << a.width_log2) / 2; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (!is_v && w && inside) {
+            const float inv = rsqrtf(fmaf(sum, 1.f / static_cast<float>(d), a.eps));
+            float wf[8];
+            unpack8(*reinterpret_cast<const uint4 *>(w + 8 * j), wf);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * wf[i];
+        }
+        if (a.rot_dim > 0) {
+            float z[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = y[i];
+            rotate8(z, turn, j, a.rot_dim, a.interleaved);
+            if (!is_v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = z[i];
+        }
+        if (!inside || h >= H + 2 * Hk) continue;
+        if (is_q) {
+            *reinterpret_cast<uint4 *>(out + h * d) = pack8(y);
+            continue;
+        }
+        const int kv_head = is_v ? h - H - Hk : h - H;
+        const long long dst = ((block * Hk + kv_head) * a.block_size + row) * d + 8 * j;
+        if (F8) {
+            unsigned char *cache = static_cast<unsigned char *>(is_v ? a.v_cache : a.k_cache);
+            *reinterpret_cast<uint2 *>(cache + dst) = quantize8(y, is_v ? a.v_scale : a.k_scale);
+        } else {
+            __half *cache = static_cast<__half *>(is_v ? a.v_cache : a.k_cache);
+            *reinterpret_cast<uint4 *>(cache + dst) = is_v ? raw[u] : pack8(y);
+        }
     }
 }
 
@@ -209,8 +243,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
         __half *row = static_cast<__half *>(a.cache) + slot * (R + P);
         float y[8];
         unpack8(rope, y);
-        rotate8(y, a.cos_sin + static_cast<long long>(position) * P, lane, P, a.interleaved,
-                8 * lane < P);
+        rotate8(y, load_turn(a.cos_sin + static_cast<long long>(position) * P, lane, P,
+                             a.interleaved), lane, P, a.interleaved);
         if (8 * lane < P) *reinterpret_cast<uint4 *>(row + R + 8 * lane) = pack8(y);
         const __half *w = static_cast<const __half *>(a.weight);
         if (!w) {
@@ -230,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float inv = 1.f / sqrtf(sum / static_cast<float>(R) + a.eps);
+        const float inv = rsqrtf(fmaf(sum, 1.f / static_cast<float>(R), a.eps));
 #pragma unroll
         for (int i = 0; i < kMaxLatentSteps; ++i) {
             const int e = 8 * (lane + 32 * i);
@@ -261,6 +295,8 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
     if (!token_place(a.slot_mapping, a.positions, a.num_slots, a.max_positions, P, token, false,
                      nullptr, &slot, &position))
         return;
+    const Turn turn =
+        load_turn(a.cos_sin + static_cast<long long>(position) * P, j, P, a.interleaved);
     __half *out = static_cast<__half *>(a.q_out) + token * a.out_token_stride + 8 * j;
 #pragma unroll
     for (int i = 0; i < kHeadSteps; ++i) {
@@ -268,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
         const bool active = h < a.n_q_heads && 8 * j < P;
         float y[8];
         unpack8(raw[i], y);
-        rotate8(y, a.cos_sin + static_cast<long long>(position) * P, j, P, a.interleaved, active);
+        rotate8(y, turn, j, P, a.interleaved);
         if (active) *reinterpret_cast<uint4 *>(out + h * a.out_head_stride) = pack8(y);
     }
 }
@@ -281,18 +317,30 @@ int log2_lanes(int entries) {  // lanes of 8 entries, rounded up to a power of t
 
 }  // namespace
 
+namespace {
+
+template <int U>
+cudaError_t launch_qk(QkAppendArgs a, bool fp8, cudaStream_t stream) {
+    const int per_job = U * (32 >> a.width_log2);
+    a.jobs = (a.n_q_heads + 2 * a.n_kv_heads + per_job - 1) / per_job;
+    const long long threads = static_cast<long long>(a.num_tokens) * a.jobs * 32;
+    if (threads > 0xffffffffLL - kThreads) return cudaErrorInvalidValue;
+    const unsigned blocks = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
+    if (fp8)
+        qk_append_kernel<true, U><<<blocks, kThreads, 0, stream>>>(a);
+    else
+        qk_append_kernel<false, U><<<blocks, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_qk_append(QkAppendArgs a, bool fp8, cudaStream_t stream) {
     a.width_log2 = log2_lanes(a.head_dim);
-    const long long units =
-        static_cast<long long>(a.num_tokens) * (a.n_q_heads + 2 * a.n_kv_heads);
-    const long long blocks = ((units << a.width_log2) + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffLL || (units << a.width_log2) > 0xffffffffLL)
-        return cudaErrorInvalidValue;
-    if (fp8)
-        qk_append_kernel<true><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-    else
-        qk_append_kernel<false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    const long long lanes =
+        (static_cast<long long>(a.num_tokens) * (a.n_q_heads + 2 * a.n_kv_heads)) << a.width_log2;
+    // twice the threads that the GPU holds at once
+    return lanes > 600000 ? launch_qk<4>(a, fp8, stream) : launch_qk<1>(a, fp8, stream);
 }
 
 cudaError_t launch_latent_append(LatentAppendArgs a, cudaStream_t stream) {
@@ -301,7 +349,7 @@ cudaError_t launch_latent_append(LatentAppendArgs a, cudaStream_t stream) {
     a.jobs = 1 + (a.n_q_heads + per_job - 1) / per_job;
     const long long threads = static_cast<long long>(a.num_tokens) * a.jobs * 32;
     const long long blocks = (threads + kThreads - 1) / kThreads;
-    if (threads > 0xffffffffLL) return cudaErrorInvalidValue;
+    if (threads > 0xffffffffLL - kThreads) return cudaErrorInvalidValue;
     latent_append_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }

@@ -23,7 +23,7 @@ struct QkAppendArgs {
     long long num_slots;
     float k_scale, v_scale;
     int32_t *err;
-    int width_log2;  // lanes per head, set by the launcher
+    int width_log2, jobs;  // lanes per head, warps per token: set by the launcher
 };
 // cudaErrorInvalidValue: more (token, head) pairs than the grid's 32-bit index.
 cudaError_t launch_qk_append(QkAppendArgs a, bool fp8, cudaStream_t stream);
