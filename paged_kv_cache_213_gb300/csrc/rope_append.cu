@@ -82,8 +82,7 @@ __device__ __forceinline__ Turn load_turn(const float *cs, int j, int rot, bool 
 // partner entries are rot / 16 lanes up or down; every lane of the warp calls this.
 __device__ __forceinline__ void rotate8(float (&y)[8], const Turn &t, int j, int rot,
                                         bool interleaved) {
-    if (interleaved) {
-        if (8 * j >= rot) return;
+    if (interleaved) {  // beyond rot: cos 1, sin 0
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float a = y[2 * i], b = y[2 * i + 1];
@@ -122,91 +121,107 @@ __device__ __forceinline__ bool token_place(const int64_t *slots, const int32_t 
     return !bad_slot && !bad_pos;
 }
 
-// One warp per (token, heads): `width` lanes a head, 32 / width heads at once, U
-// steps of them, whose loads are all in flight together and which share the
-// token's slot and rotation row.  Heads 0 .. H-1 are queries, then Hk keys, then Hk
-// values.  U = 4 where the warps fill the GPU anyway: with one head a lane the
-// chain from position to rotation row leaves too few bytes in flight (8191 tokens x
-// 80 heads into E4M3: 125 us with U = 1).  U = 1 for fewer: more warps, a shorter
-// chain.
-template <bool F8, int U>
+// One warp per job: U steps of 32 / width heads of a token and of one kind,
+// `width` lanes a head, whose loads are all in flight together and which share the
+// token's slot, rotation row and norm weights.  A token's first jobs take its
+// queries, the next its keys, the others its values, which only move.
+//  U = 4 where the warps fill the GPU anyway: with one head a lane too few bytes are
+// in flight behind the chain from position to rotation row.  U = 1 for fewer: more
+// warps, a shorter chain.
+//  D = 64 or 128 knows the head size: with sizes of the call and heads of all kinds
+// in a warp the kernel was bound by instruction issue (945 a warp; 8191 tokens x 80
+// heads into E4M3 took 108 us).  D = 0 is any other size.
+template <bool F8, int U, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs a) {
     allow_dependent_launch();  // the attention kernel may get scheduled meanwhile
-    const int lane = threadIdx.x & 31, j = lane & ((1 << a.width_log2) - 1);
-    const int per = 32 >> a.width_log2;  // heads of a step
+    const int width = D > 0 ? D / 8 : 1 << a.width_log2;
+    const int lane = threadIdx.x & 31, j = lane & (width - 1);
+    const int per = 32 / width;  // heads of a step
     const unsigned job = (blockIdx.x * kThreads + threadIdx.x) >> 5;
     const unsigned token = job / a.jobs;
     if (token >= static_cast<unsigned>(a.num_tokens)) return;
-    const int first = (job - token * a.jobs) * per * U + (lane >> a.width_log2);
-    const int H = a.n_q_heads, Hk = a.n_kv_heads, d = a.head_dim;
-    const bool inside = 8 * j < d;
-    const __half *q = static_cast<const __half *>(a.q) + token * a.q_stride + 8 * j;
-    const __half *k = static_cast<const __half *>(a.k) + token * a.k_stride + 8 * j;
-    const __half *v = static_cast<const __half *>(a.v) + token * a.v_stride + 8 * j;
+    int part = job - token * a.jobs;
+    const bool tell = part == 0 && lane == 0;
+    const int H = a.n_q_heads, Hk = a.n_kv_heads, d = D > 0 ? D : a.head_dim;
+    const bool inside = D > 0 || 8 * j < d;
+    // the kind of the job's heads
+    const bool is_q = part < a.q_jobs;
+    part -= is_q ? 0 : a.q_jobs;
+    const bool is_v = !is_q && part >= a.kv_jobs;
+    part -= is_v ? a.kv_jobs : 0;
+    const int heads = is_q ? H : Hk;
+    const int first = part * per * U + lane / width;
+    const __half *x = static_cast<const __half *>(is_q ? a.q : is_v ? a.v : a.k) +
+                      token * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + first * d + 8 * j;
     uint4 raw[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int h = first + u * per;
         raw[u] = make_uint4(0, 0, 0, 0);
-        if (inside && h < H + 2 * Hk)
-            raw[u] = *reinterpret_cast<const uint4 *>(
-                h < H ? q + h * d : h < H + Hk ? k + (h - H) * d : v + (h - H - Hk) * d);
+        if (inside && first + u * per < heads)
+            raw[u] = *reinterpret_cast<const uint4 *>(x + u * per * d);
     }
     long long slot;
     int position;
     if (!token_place(a.slot_mapping, a.positions, a.num_slots, a.max_positions, a.rot_dim, token,
-                     lane == 0 && first == 0, a.err, &slot, &position))
+                     tell, a.err, &slot, &position))
         return;
-    Turn turn{};
-    if (a.rot_dim > 0)
-        turn = load_turn(a.cos_sin + static_cast<long long>(position) * a.rot_dim, j, a.rot_dim,
-                         a.interleaved);
-    const long long block = slot / a.block_size;
+    // 32-bit division where it will do: the 64-bit one is some 70 instructions
+    const long long block = slot >> 32 ? slot / a.block_size
+                                       : static_cast<unsigned>(slot) / static_cast<unsigned>(a.block_size);
     const long long row = slot - block * a.block_size;
-    __half *out = static_cast<__half *>(a.q_out) + static_cast<long long>(token) * H * d + 8 * j;
+    // where the first head goes (in entries), and a head further
+    const long long dst =
+        is_q ? (static_cast<long long>(token) * H + first) * d + 8 * j
+             : ((block * Hk + first) * a.block_size + row) * d + 8 * j;
+    const int step = per * d * (is_q ? 1 : a.block_size);
+    unsigned char *cache = static_cast<unsigned char *>(is_v ? a.v_cache : a.k_cache);
+    if (is_v) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!inside || first + u * per >= heads) continue;
+            const long long at = dst + static_cast<long long>(u) * step;
+            if (F8) {
+                float y[8];
+                unpack8(raw[u], y);
+                *reinterpret_cast<uint2 *>(cache + at) = quantize8(y, a.v_scale);
+            } else {
+                *reinterpret_cast<uint4 *>(cache + 2 * at) = raw[u];
+            }
+        }
+        return;
+    }
+    const bool turns = a.rot_dim > 0;
+    Turn turn{};
+    if (turns)
+        turn = load_turn(a.cos_sin + static_cast<long long>(position) * a.rot_dim, j, a.rot_dim,
+                         INTERLEAVED);
+    const __half *w = static_cast<const __half *>(is_q ? a.q_weight : a.k_weight);
+    float wf[8];
+    if (w && inside) unpack8(*reinterpret_cast<const uint4 *>(w + 8 * j), wf);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int h = first + u * per;
-        const bool is_q = h < H, is_v = h >= H + Hk;
         float y[8];
         unpack8(raw[u], y);
-        const __half *w = static_cast<const __half *>(is_q ? a.q_weight : a.k_weight);
-        // the whole warp runs the shuffles; values pass through untouched
-        float sum = 0.f;
+        if (w) {
+            float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
-        for (int o = (1 << a.width_log2) / 2; o > 0; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (!is_v && w && inside) {
-            const float inv = rsqrtf(fmaf(sum, 1.f / static_cast<float>(d), a.eps));
-            float wf[8];
-            unpack8(*reinterpret_cast<const uint4 *>(w + 8 * j), wf);
+            for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                if (o < width) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * wf[i];
         }
-        if (a.rot_dim > 0) {
-            float z[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = y[i];
-            rotate8(z, turn, j, a.rot_dim, a.interleaved);
-            if (!is_v)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = z[i];
-        }
-        if (!inside || h >= H + 2 * Hk) continue;
-        if (is_q) {
-            *reinterpret_cast<uint4 *>(out + h * d) = pack8(y);
-            continue;
-        }
-        const int kv_head = is_v ? h - H - Hk : h - H;
-        const long long dst = ((block * Hk + kv_head) * a.block_size + row) * d + 8 * j;
-        if (F8) {
-            unsigned char *cache = static_cast<unsigned char *>(is_v ? a.v_cache : a.k_cache);
-            *reinterpret_cast<uint2 *>(cache + dst) = quantize8(y, is_v ? a.v_scale : a.k_scale);
-        } else {
-            __half *cache = static_cast<__half *>(is_v ? a.v_cache : a.k_cache);
-            *reinterpret_cast<uint4 *>(cache + dst) = is_v ? raw[u] : pack8(y);
-        }
+        if (turns) rotate8(y, turn, j, a.rot_dim, INTERLEAVED);
+        if (!inside || first + u * per >= heads) continue;
+        const long long at = dst + static_cast<long long>(u) * step;
+        if (is_q)
+            *reinterpret_cast<uint4 *>(static_cast<__half *>(a.q_out) + at) = pack8(y);
+        else if (F8)
+            *reinterpret_cast<uint2 *>(cache + at) = quantize8(y, a.k_scale);
+        else
+            *reinterpret_cast<uint4 *>(cache + 2 * at) = pack8(y);
     }
 }
 
@@ -319,18 +334,28 @@ int log2_lanes(int entries) {  // lanes of 8 entries, rounded up to a power of t
 
 namespace {
 
-template <int U>
-cudaError_t launch_qk(QkAppendArgs a, bool fp8, cudaStream_t stream) {
+template <bool F8, int U, int D>
+cudaError_t launch_qk(QkAppendArgs a, cudaStream_t stream) {
     const int per_job = U * (32 >> a.width_log2);
-    a.jobs = (a.n_q_heads + 2 * a.n_kv_heads + per_job - 1) / per_job;
+    a.q_jobs = (a.n_q_heads + per_job - 1) / per_job;
+    a.kv_jobs = (a.n_kv_heads + per_job - 1) / per_job;
+    a.jobs = a.q_jobs + 2 * a.kv_jobs;
+    a.inv_dim = 1.f / static_cast<float>(a.head_dim);
     const long long threads = static_cast<long long>(a.num_tokens) * a.jobs * 32;
     if (threads > 0xffffffffLL - kThreads) return cudaErrorInvalidValue;
     const unsigned blocks = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
-    if (fp8)
-        qk_append_kernel<true, U><<<blocks, kThreads, 0, stream>>>(a);
+    if (a.interleaved)
+        qk_append_kernel<F8, U, D, true><<<blocks, kThreads, 0, stream>>>(a);
     else
-        qk_append_kernel<false, U><<<blocks, kThreads, 0, stream>>>(a);
+        qk_append_kernel<F8, U, D, false><<<blocks, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+template <bool F8, int U>
+cudaError_t launch_qk_sized(const QkAppendArgs &a, cudaStream_t stream) {
+    return a.head_dim == 128  ? launch_qk<F8, U, 128>(a, stream)
+           : a.head_dim == 64 ? launch_qk<F8, U, 64>(a, stream)
+                              : launch_qk<F8, U, 0>(a, stream);
 }
 
 }  // namespace
@@ -340,7 +365,9 @@ cudaError_t launch_qk_append(QkAppendArgs a, bool fp8, cudaStream_t stream) {
     const long long lanes =
         (static_cast<long long>(a.num_tokens) * (a.n_q_heads + 2 * a.n_kv_heads)) << a.width_log2;
     // twice the threads that the GPU holds at once
-    return lanes > 600000 ? launch_qk<4>(a, fp8, stream) : launch_qk<1>(a, fp8, stream);
+    if (lanes > 600000)
+        return fp8 ? launch_qk_sized<true, 4>(a, stream) : launch_qk_sized<false, 4>(a, stream);
+    return fp8 ? launch_qk_sized<true, 1>(a, stream) : launch_qk_sized<false, 1>(a, stream);
 }
 
 cudaError_t launch_latent_append(LatentAppendArgs a, cudaStream_t stream) {

@@ -23,7 +23,10 @@ struct QkAppendArgs {
     long long num_slots;
     float k_scale, v_scale;
     int32_t *err;
-    int width_log2, jobs;  // lanes per head, warps per token: set by the launcher
+    // set by the launcher: lanes per head, warps per token, those for queries and for
+    // keys (or values), 1 / head_dim
+    int width_log2, jobs, q_jobs, kv_jobs;
+    float inv_dim;
 };
 // cudaErrorInvalidValue: more (token, head) pairs than the grid's 32-bit index.
 cudaError_t launch_qk_append(QkAppendArgs a, bool fp8, cudaStream_t stream);
