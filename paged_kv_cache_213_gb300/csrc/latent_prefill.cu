@@ -22,7 +22,9 @@ namespace {
 constexpr int kP = 64;          // rotated entries
 constexpr int kRows = 128;      // query rows of a tile
 constexpr int kKeys = 96;       // key rows of a step
-constexpr int kThreads = 320;   // two softmax warpgroups, the copy warp, the MMA warp
+constexpr int kThreads = 384;   // two softmax warpgroups; copy warp, MMA warp, two idle ones
+// Registers move from the third warpgroup to the softmax: 8 x 32 x 208 + 4 x 32 x 88
+// is the 12 x 32 x 168 of the launch.
 constexpr int kQPlane = kRows * 128, kKPlane = kKeys * 128;  // 64 columns of a tile, bytes
 // P holds 2^(s - r) with r kHead below the running maximum: weights up to
 // 2^kHead, and up to 2^(kHead + kLag) before r follows; fp16 ends at 2^16.
@@ -37,11 +39,70 @@ struct Cfg {
     static constexpr int SMEM = 1024 + Q_BYTES + STAGES * STAGE_BYTES;
 };
 
-struct Barriers {
-    uint64_t q_full[2], s_full[2], p_ready[2][2], o_done[2], drained;
-    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+struct Shared {
+    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_done[2], o_free[2];
+    uint64_t full[4], empty[4], asked[2], answered[2], turn[2], drained[2];
+    uint4 answer[2];
     uint32_t tmem;
     int stop;
+};
+
+// One CTA's worth of work: two neighbouring tiles of query rows of one head.
+struct Item {
+    int h, pair, q0, n, k0, m;
+    int steps[2], total;  // key steps of the tiles, and of both
+};
+
+// The work of CTA `cta`; false when it has none.
+__device__ __forceinline__ bool load_item(const LatentPrefillArgs &a, const uint3 &cta, bool tell,
+                                          Item *it) {
+    const int seq = cta.z;
+    it->h = cta.y;
+    it->pair = gridDim.x - 1 - cta.x;  // the longest rows first
+    it->q0 = a.q_start[seq];
+    it->n = a.q_start[seq + 1] - it->q0;
+    it->k0 = a.kv_start[seq];
+    it->m = a.kv_start[seq + 1] - it->k0;
+    if (it->n == 0) return false;
+    if (it->n < 0 || it->n > it->m || it->n > a.max_q_len || it->m > a.max_kv_len || it->q0 < 0 ||
+        it->k0 < 0 || it->n > a.total_q - it->q0 || it->m > a.total_kv - it->k0) {
+        if (tell) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+        return false;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int first = (2 * it->pair + t) * kRows;
+        const int last = min(first + kRows, it->n) - 1;
+        it->steps[t] = first < it->n ? (it->m - it->n + last + kKeys) / kKeys : 0;
+    }
+    it->total = max(it->steps[0], it->steps[1]);
+    return it->total > 0;
+}
+
+// Each role walks the same list of items: its own CTA's, then those that the copy
+// role takes over.
+struct Items {
+    uint3 cta;
+    int k;  // answers read
+
+    // The next item, or false at the end (or when the kernel gives up).
+    __device__ bool advance(const LatentPrefillArgs &a, Shared &sh, bool whole_warp, bool tell,
+                            Item *it) {
+        do {
+            volatile int *stop = &sh.stop;
+            const int s = k & 1;
+            const bool ok = whole_warp ? warp_wait_or_stop(&sh.answered[s], (k >> 1) & 1, stop)
+                                       : wait_or_stop(&sh.answered[s], (k >> 1) & 1, stop);
+            if (!ok) return false;
+            const bool more = next_cta(&sh.answer[s], &cta);
+            fence_proxy_async_smem();
+            ++k;
+            if (whole_warp) __syncwarp();
+            if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.asked[s]);
+            if (!more) return false;
+        } while (!load_item(a, cta, tell, it));
+        return true;
+    }
 };
 
 template <int D>
@@ -51,274 +112,367 @@ __global__ void __launch_bounds__(kThreads, 1)
                           const __grid_constant__ CUtensorMap mr) {
     using C = Cfg<D>;
     extern __shared__ unsigned char raw[];
-    __shared__ Barriers bar;
+    __shared__ __align__(16) Shared sh;
     unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int seq = blockIdx.z, h = blockIdx.y;
-    const int pair = gridDim.x - 1 - blockIdx.x;  // the longest rows first
-    grid_dependency_wait();
-    allow_dependent_launch();
-    const int q0 = a.q_start[seq], n = a.q_start[seq + 1] - q0;
-    const int k0 = a.kv_start[seq], m = a.kv_start[seq + 1] - k0;
-    if (n == 0) return;
-    if (n < 0 || n > m || n > a.max_q_len || m > a.max_kv_len || q0 < 0 || k0 < 0 ||
-        n > a.total_q - q0 || m > a.total_kv - k0) {
-        if (threadIdx.x == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
-        return;
-    }
-    if (pair * 2 * kRows >= n) return;
-    // key steps of the two row tiles
-    int steps[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int first = (2 * pair + t) * kRows;
-        const int last = min(first + kRows, n) - 1;
-        steps[t] = first < n ? (m - n + last + kKeys) / kKeys : 0;  // ceil((m - n + last + 1) / kKeys)
-    }
-    const int total = max(steps[0], steps[1]);
 
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&bar.q_full[t], 1);
-            mbar_init(&bar.s_full[t], 1);
-            mbar_init(&bar.p_ready[t][0], 4);
-            mbar_init(&bar.p_ready[t][1], 4);
-            mbar_init(&bar.o_done[t], 1);
+            mbar_init(&sh.q_full[t], 1);
+            mbar_init(&sh.q_empty[t], 1);
+            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.p_ready[t][0], 4);
+            mbar_init(&sh.p_ready[t][1], 4);
+            mbar_init(&sh.o_done[t], 1);
+            mbar_init(&sh.o_free[t], 4);
+            mbar_init(&sh.asked[t], 11);  // an answer is read by eight warps and three threads
+            mbar_init(&sh.answered[t], 1);
+            mbar_init(&sh.drained[t], 1);
+            mbar_init(&sh.turn[t], 1);
         }
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&bar.k_full[s], 1);
-            mbar_init(&bar.k_empty[s], 1);
-            mbar_init(&bar.v_full[s], 1);
-            mbar_init(&bar.v_empty[s], 1);
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 2);
         }
-        mbar_init(&bar.drained, 1);
-        bar.stop = 0;
+        sh.stop = 0;
         fence_barrier_init();
     }
-    if (warp == 9) tmem_alloc(&bar.tmem, 512);
+    if (warp == 9) tmem_alloc(&sh.tmem, 512);
+    if (warp == 8 && lane == 0) {
+        prefetch_tmap(&mq);
+        prefetch_tmap(&mkv);
+        prefetch_tmap(&mr);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bar.tmem;
-    volatile int *stop = &bar.stop;
+    grid_dependency_wait();
+    allow_dependent_launch();
+    const uint32_t tmem = sh.tmem;
+    volatile int *stop = &sh.stop;
+    Items items{blockIdx, 0};
+    Item it;
     // TMEM columns: S of tile t at 128 t (P in its first half), O at 256 + 128 t
 
+    if (warp >= 8) {
+    give_registers<88>();
     if (warp == 8) {
+        // --- copies ---
         if (elect_one()) {
-            prefetch_tmap(&mq);
-            prefetch_tmap(&mkv);
-            prefetch_tmap(&mr);
-            for (int t = 0; t < 2; ++t)
-                if (steps[t] > 0) {
-                    mbar_arrive_expect_tx(&bar.q_full[t], C::KP * kQPlane);
-                    for (int p = 0; p < C::KP; ++p)
-                        tma_load_3d(base + (t * C::KP + p) * kQPlane, &mq, 64 * p, h,
-                                    q0 + (2 * pair + t) * kRows, &bar.q_full[t]);
+            // Pair f of the ring is the keys of step f and the values of step f - 1:
+            // what the products between two softmax steps take, on one barrier.
+            // Steps count on over the items.
+            int f = 0;
+            int q[2] = {0, 0};  // query tiles so far
+            int asks = 0;
+            bool ok = true;
+            Item last;        // whose final values are still to come
+            auto ask = [&] {  // for the item after the one at hand
+                const int s = asks & 1;
+                ok = ok && wait_or_stop(&sh.asked[s], ((asks >> 1) & 1) ^ 1, stop);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&sh.answered[s], 16);
+                ask_next_cta(&sh.answer[s], &sh.answered[s]);
+                ++asks;
+            };
+            // the next pair: values of vi at step vj, keys of ki at step kj (either null)
+            auto copy_pair = [&](const Item *vi, int vj, const Item *ki, int kj) {
+                const int s = f % C::STAGES;
+                ok = wait_or_stop(&sh.empty[s], ((f / C::STAGES) & 1) ^ 1, stop);
+                if (!ok) return;
+                mbar_arrive_expect_tx(&sh.full[s], (ki ? C::KP * kKPlane : 0) + (vi ? C::VP * kKPlane : 0));
+                unsigned char *st = base + C::Q_BYTES;
+                if (vi)
+#pragma unroll 1
+                    for (int p = 0; p < C::VP; ++p)
+                        tma_load_3d(st + ((f - 1) % C::STAGES) * C::STAGE_BYTES + (C::KP + p) * kKPlane,
+                                    &mkv, D + 64 * p, vi->h, vi->k0 + vj * kKeys, &sh.full[s]);
+                if (ki) {
+#pragma unroll 1
+                    for (int p = 0; p < D / 64; ++p)
+                        tma_load_3d(st + s * C::STAGE_BYTES + p * kKPlane, &mkv, 64 * p, ki->h,
+                                    ki->k0 + kj * kKeys, &sh.full[s]);
+                    tma_load_2d(st + s * C::STAGE_BYTES + (D / 64) * kKPlane, &mr, 0,
+                                ki->k0 + kj * kKeys, &sh.full[s]);
                 }
-            int j = 0;
-            for (; j < total; ++j) {
-                const int s = j % C::STAGES;
-                const uint32_t par = ((j / C::STAGES) & 1) ^ 1;
-                unsigned char *st = base + C::Q_BYTES + s * C::STAGE_BYTES;
-                const int row = k0 + j * kKeys;
-                if (!wait_or_stop(&bar.k_empty[s], par, stop)) break;
-                mbar_arrive_expect_tx(&bar.k_full[s], C::KP * kKPlane);
-                for (int p = 0; p < D / 64; ++p)
-                    tma_load_3d(st + p * kKPlane, &mkv, 64 * p, h, row, &bar.k_full[s]);
-                tma_load_2d(st + (D / 64) * kKPlane, &mr, 0, row, &bar.k_full[s]);
-                if (!wait_or_stop(&bar.v_empty[s], par, stop)) break;
-                mbar_arrive_expect_tx(&bar.v_full[s], C::VP * kKPlane);
-                for (int p = 0; p < C::VP; ++p)
-                    tma_load_3d(st + (C::KP + p) * kKPlane, &mkv, D + 64 * p, h, row,
-                                &bar.v_full[s]);
+                ++f;
+            };
+            ask();
+            bool have = load_item(a, items.cta, false, &it);
+            while (ok) {
+                if (have) {
+#pragma unroll 1
+                    for (int j = 0; j < it.total && ok; ++j) {
+                        copy_pair(j > 0 ? &it : f > 0 ? &last : nullptr, j > 0 ? j - 1 : last.total - 1,
+                                  &it, j);
+                        if (j == 0)
+#pragma unroll 1
+                            for (int t = 0; t < 2 && ok; ++t)
+                                if (it.steps[t] > 0) {
+                                    ok = wait_or_stop(&sh.q_empty[t], (q[t] & 1) ^ 1, stop);
+                                    if (!ok) break;
+                                    ++q[t];
+                                    mbar_arrive_expect_tx(&sh.q_full[t], C::KP * kQPlane);
+                                    for (int p = 0; p < C::KP; ++p)
+                                        tma_load_3d(base + (t * C::KP + p) * kQPlane, &mq, 64 * p,
+                                                    it.h, it.q0 + (2 * it.pair + t) * kRows,
+                                                    &sh.q_full[t]);
+                                }
+                    }
+                    last = it;
+                }
+                // the answer asked for one item ago; ask again while it says yes
+                const int s = items.k & 1;
+                ok = ok && wait_or_stop(&sh.answered[s], (items.k >> 1) & 1, stop);
+                if (!ok) break;
+                const bool more = next_cta(&sh.answer[s], &items.cta);
+                fence_proxy_async_smem();
+                mbar_arrive(&sh.asked[s]);
+                ++items.k;
+                if (!more) {
+                    if (f > 0) copy_pair(&last, last.total - 1, nullptr, 0);
+                    break;
+                }
+                ask();
+                have = load_item(a, items.cta, false, &it);
             }
-            if (*stop) {
+            if (!ok) {
                 // every copy in flight lands before the CTA gives its memory back
                 for (int t = 0; t < 2; ++t)
-                    if (steps[t] > 0) mbar_wait_bounded(&bar.q_full[t], 0);
-                for (int i = max(0, j - C::STAGES + 1); i <= min(j, total - 1); ++i) {
-                    mbar_wait_bounded(&bar.k_full[i % C::STAGES], (i / C::STAGES) & 1);
-                    mbar_wait_bounded(&bar.v_full[i % C::STAGES], (i / C::STAGES) & 1);
-                }
+                    if (q[t] > 0) mbar_wait_bounded(&sh.q_full[t], (q[t] - 1) & 1);
+                for (int i = max(0, f - C::STAGES); i < f; ++i)
+                    mbar_wait_bounded(&sh.full[i % C::STAGES], (i / C::STAGES) & 1);
+                if (asks > items.k)
+                    mbar_wait_bounded(&sh.answered[(asks - 1) & 1], ((asks - 1) >> 1) & 1);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp < 11) {
+        // --- matrix products ---
+        // One warp a tile, in turns of the products between two of the tile's softmax
+        // steps: a warp's waits and commits pass while the other's products run, and
+        // one tile's softmax runs under the other's products.  (One thread for both
+        // tiles left the tensor core idle for 1240 of a step's 3400 cycles: it takes
+        // hardly more than the next product ahead of time.  Without turns the two
+        // tiles fall into step, and nothing runs under their softmax: 3600.)
         if (elect_one()) {
+            const int t = warp - 9;
             constexpr uint32_t ds = mma_desc(kRows, kKeys, false, false);
             constexpr uint32_t dpv = mma_desc(kRows, D, false, true);
-            const uint32_t q_addr = smem_addr(base), kv_addr = q_addr + C::Q_BYTES;
-            auto scores = [&](int t, int j) {
-                const uint32_t qa = q_addr + t * C::KP * kQPlane;
-                const uint32_t ka = kv_addr + (j % C::STAGES) * C::STAGE_BYTES;
-#pragma unroll
-                for (int k = 0; k < 4 * C::KP; ++k)
-                    mma_ss(tmem + 128 * t, smem_desc(qa + (k / 4) * kQPlane + (k % 4) * 32, 1024, 0),
-                           smem_desc(ka + (k / 4) * kKPlane + (k % 4) * 32, 1024, 0), ds, k > 0);
-                mma_commit(&bar.s_full[t]);
-            };
-            bool ok = wait_or_stop(&bar.k_full[0], 0, stop);
-            for (int t = 0; t < 2 && ok; ++t)
-                if (steps[t] > 0) {
-                    ok = wait_or_stop(&bar.q_full[t], 0, stop);
-                    if (ok) {
-                        tc_fence_after();
-                        scores(t, 0);
-                    }
+            const uint32_t kv_addr = smem_addr(base) + C::Q_BYTES, ts = tmem + 128 * t;
+            const uint64_t qd = smem_desc(smem_addr(base) + t * C::KP * kQPlane, 1024, 0);
+            int f = 0;       // key steps so far
+            int sc = 0, qc = 0;  // this tile's steps and items
+            int turns = 0;
+            bool ok = true;
+            bool more = load_item(a, items.cta, false, &it) ||
+                        items.advance(a, sh, false, false, &it);
+            int steps = 0, total = 0;  // of the item at hand
+            int j = -1;  // its step whose weights come next; -1: only the first scores
+            while (ok) {
+                // between the softmax of step j and that of the step after it, which is
+                // step j + 1 of the item or the first of the next one
+                const bool end = j + 1 == total;
+                if (end && j >= 0) more = items.advance(a, sh, false, false, &it);
+                if (j < 0 && !more) break;
+                const int pair = j < 0 ? f : f + 1;  // of copies; also the step of its keys
+                ok = wait_or_stop(&sh.full[pair % C::STAGES], (pair / C::STAGES) & 1, stop);
+                const bool weights = j >= 0 && j < steps;
+                if (ok && weights) {
+                    if (j == 0) ok = wait_or_stop(&sh.o_free[t], qc & 1, stop);
+                    ok = ok && wait_or_stop(&sh.p_ready[t][0], sc & 1, stop);
                 }
-            if (ok && total > C::STAGES) mma_commit(&bar.k_empty[0]);
-            for (int j = 0; j < total && ok; ++j) {
-                const int s = j % C::STAGES;
-                const uint32_t par = (j / C::STAGES) & 1;
-                const uint32_t va = kv_addr + s * C::STAGE_BYTES + C::KP * kKPlane;
-                if (j + 1 < total)
-                    ok = wait_or_stop(&bar.k_full[(j + 1) % C::STAGES], ((j + 1) / C::STAGES) & 1,
-                                      stop);
-                ok = ok && wait_or_stop(&bar.v_full[s], par, stop);
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j >= steps[t]) continue;
+                ok = ok && wait_or_stop(&sh.turn[t], (turns & 1) ^ (t ^ 1), stop);
+                if (!ok) break;
+                ++turns;
+                tc_fence_after();
+                if (weights) {
+                    const uint64_t vd = smem_desc(kv_addr + (f % C::STAGES) * C::STAGE_BYTES +
+                                                      C::KP * kKPlane, 1024, kKPlane);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        ok = ok && wait_or_stop(&bar.p_ready[t][half], j & 1, stop);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = half * 3; k < half * 3 + 3; ++k)
-                            mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k,
-                                   smem_desc(va + k * 2048, 1024, kKPlane), dpv, j > 0 || k > 0);
-                    }
+                    for (int k = 0; k < 3; ++k)
+                        mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
+                    ok = wait_or_stop(&sh.p_ready[t][1], sc & 1, stop);
                     if (!ok) break;
-                    if (j + 1 < steps[t])
-                        scores(t, j + 1);
-                    else
-                        mma_commit(&bar.o_done[t]);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 3; k < 6; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, true);
+                    ++sc;
+                    if (j + 1 == steps) mma_commit(&sh.o_done[t]);
                 }
-                if (ok && j + C::STAGES < total) mma_commit(&bar.v_empty[s]);
-                if (ok && j + 1 + C::STAGES < total) mma_commit(&bar.k_empty[(j + 1) % C::STAGES]);
+                const int next_steps = more ? it.steps[t] : 0;
+                const bool first = end && next_steps > 0;
+                if (j + 1 < steps || first) {
+                    if (first) {
+                        ok = wait_or_stop(&sh.q_full[t], qc & 1, stop);
+                        if (!ok) break;
+                        ++qc;
+                    }
+                    tc_fence_after();
+                    const uint64_t kd = smem_desc(kv_addr + (pair % C::STAGES) * C::STAGE_BYTES, 1024, 0);
+#pragma unroll
+                    for (int k = 0; k < 4 * C::KP; ++k)
+                        mma_ss(ts, qd + (k / 4) * (kQPlane / 16) + (k % 4) * 2,
+                               kd + (k / 4) * (kKPlane / 16) + (k % 4) * 2, ds, k > 0);
+                    mbar_arrive(&sh.turn[t ^ 1]);
+                    mma_commit(&sh.s_full[t]);
+                    if (first ? next_steps == 1 : j + 2 == steps) mma_commit(&sh.q_empty[t]);
+                } else {
+                    mbar_arrive(&sh.turn[t ^ 1]);
+                }
+                mma_commit(&sh.empty[pair % C::STAGES]);
+                if (j >= 0) ++f;
+                ++j;
+                if (end) {
+                    if (!more) break;
+                    steps = next_steps;
+                    total = it.total;
+                    j = 0;
+                }
             }
             // nothing of the tensor core is left in flight when TMEM is freed
-            mma_commit(&bar.drained);
-            mbar_wait_bounded(&bar.drained, 0);
+            mma_commit(&sh.drained[t]);
+            mbar_wait_bounded(&sh.drained[t], 0);
         }
+    }
     } else {
+        // --- softmax, results ---
+        take_registers<208>();
         const int t = warp >> 2;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 * (warp % 4) << 16
         const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
-        const int i = (2 * pair + t) * kRows + (threadIdx.x & 127);
-        const int seen = min(m - n + i + 1, m);  // keys this row attends
         const float scale = a.scale_log2;
-        float r = 0.f, l = 0.f;
+        int f = 0, sc = 0, mine = 0;  // key steps, this tile's, and its items so far
+        bool have = load_item(a, items.cta, threadIdx.x == 0, &it) ||
+                    items.advance(a, sh, true, threadIdx.x == 0, &it);
         bool ok = true;
-        for (int j = 0; j < steps[t]; ++j) {
-            ok = warp_wait_or_stop(&bar.s_full[t], j & 1, stop);
-            if (!ok) break;
-            tc_fence_after();
-            uint32_t sb[3][32];
-#pragma unroll
-            for (int c = 0; c < 3; ++c) tmem_ld32(sb[c], ts + 32 * c);
-            tmem_wait_ld();
-            float x[kKeys];
-#pragma unroll
-            for (int c = 0; c < kKeys; ++c) x[c] = __uint_as_float(sb[c / 32][c % 32]);
-            if (a.negate) {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) x[c] = -x[c];
-            }
-            const int left = seen - j * kKeys;
-            if (__any_sync(0xffffffffu, left < kKeys)) {
-#pragma unroll
-                for (int c = 0; c < kKeys; ++c) x[c] = c < left ? x[c] : -INFINITY;
-            }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-            if (j == 0) {
-                r = top > -INFINITY ? top - kHead : 0.f;
-            } else {
-                const bool move = top - r > kHead + kLag;
-                if (__any_sync(0xffffffffu, move)) {
-                    // O follows the new reference; S being full, every earlier
-                    // product into O is done
-                    const float next = move ? top - kHead : r;
-                    const float f = ex2(r - next);
-                    r = next;
-                    l *= f;
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o, to + c);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32(to + c, o);
-                    }
-                }
-            }
-            // values of rows beyond the sequence's keys meet weights of 0: they
-            // must be finite, so the last step's are cleared
-            const int valid = m - j * kKeys;
-            if (valid < kKeys) {
-                ok = warp_wait_or_stop(&bar.v_full[j % C::STAGES], (j / C::STAGES) & 1, stop);
+        while (have) {
+            const int i = (2 * it.pair + t) * kRows + (threadIdx.x & 127);
+            const int seen = min(it.m - it.n + i + 1, it.m);  // keys this row attends
+            float r = 0.f, l = 0.f;
+            for (int j = 0; j < it.steps[t]; ++j, ++sc) {
+                ok = warp_wait_or_stop(&sh.s_full[t], sc & 1, stop);
                 if (!ok) break;
-                unsigned char *v = base + C::Q_BYTES + (j % C::STAGES) * C::STAGE_BYTES +
-                                   C::KP * kKPlane;
-                const int pieces = (kKeys - valid) * 8;
-                for (int e = threadIdx.x & 127; e < pieces * C::VP; e += 128)
-                    *reinterpret_cast<uint4 *>(v + (e / pieces) * kKPlane + valid * 128 +
-                                               (e % pieces) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_smem();
-            }
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                tc_fence_after();
+                uint32_t sb[3][32];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t p16[16], p8[8];
-#pragma unroll
-                for (int c = 0; c < 24; ++c) {
-                    const float y0 = ex2(fmaf(x[half * 48 + 2 * c], scale, -r));
-                    const float y1 = ex2(fmaf(x[half * 48 + 2 * c + 1], scale, -r));
-                    sum[(2 * c) & 3] += y0;
-                    sum[(2 * c + 1) & 3] += y1;
-                    if (c < 16) p16[c] = pack_half2(y0, y1); else p8[c - 16] = pack_half2(y0, y1);
-                }
-                tmem_st16(ts + half * 24, p16);
-                tmem_st8(ts + half * 24 + 16, p8);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_ready[t][half]);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        }
-        if (ok && steps[t] > 0) ok = warp_wait_or_stop(&bar.o_done[t], 0, stop);
-        if (ok && steps[t] > 0) {
-            tc_fence_after();
-            const float inv = 1.f / l;
-            const long long row = static_cast<long long>(q0 + i) * a.n_heads + h;
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + row * D);
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(o, to + c);
+                for (int c = 0; c < 3; ++c) tmem_ld32(sb[c], ts + 32 * c);
                 tmem_wait_ld();
-                if (i < n) {
+                float x[kKeys];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
+                for (int c = 0; c < kKeys; ++c) x[c] = __uint_as_float(sb[c / 32][c % 32]);
+                if (a.negate) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                              __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-                        out[c / 8 + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int c = 0; c < kKeys; ++c) x[c] = -x[c];
+                }
+                const int left = seen - j * kKeys;
+                if (__any_sync(0xffffffffu, left < kKeys)) {
+#pragma unroll
+                    for (int c = 0; c < kKeys; ++c) x[c] = c < left ? x[c] : -INFINITY;
+                }
+                float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                if (j == 0) {
+                    r = top > -INFINITY ? top - kHead : 0.f;
+                } else {
+                    const bool move = top - r > kHead + kLag;
+                    if (__any_sync(0xffffffffu, move)) {
+                        // O follows the new reference; S being full, every earlier
+                        // product into O is done
+                        const float next = move ? top - kHead : r;
+                        const float fac = ex2(r - next);
+                        r = next;
+                        l *= fac;
+#pragma unroll
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(o, to + c);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
+                            tmem_st32(to + c, o);
+                        }
                     }
                 }
+                // values of rows beyond the sequence's keys meet weights of 0: they
+                // must be finite, so the last step's are cleared
+                const int valid = it.m - j * kKeys;
+                if (valid < kKeys) {
+                    const int s = (f + j) % C::STAGES, pair = f + j + 1;
+                    ok = warp_wait_or_stop(&sh.full[pair % C::STAGES], (pair / C::STAGES) & 1, stop);
+                    if (!ok) break;
+                    unsigned char *v = base + C::Q_BYTES + s * C::STAGE_BYTES + C::KP * kKPlane;
+                    const int pieces = (kKeys - valid) * 8;
+                    for (int e = threadIdx.x & 127; e < pieces * C::VP; e += 128)
+                        *reinterpret_cast<uint4 *>(v + (e / pieces) * kKPlane + valid * 128 +
+                                                   (e % pieces) * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p16[16], p8[8];
+#pragma unroll
+                    for (int c = 0; c < 24; ++c) {
+                        const float y0 = ex2(fmaf(x[half * 48 + 2 * c], scale, -r));
+                        const float y1 = ex2(fmaf(x[half * 48 + 2 * c + 1], scale, -r));
+                        sum[(2 * c) & 3] += y0;
+                        sum[(2 * c + 1) & 3] += y1;
+                        if (c < 16) p16[c] = pack_half2(y0, y1); else p8[c - 16] = pack_half2(y0, y1);
+                    }
+                    tmem_st16(ts + half * 24, p16);
+                    tmem_st8(ts + half * 24 + 16, p8);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_ready[t][half]);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             }
-            if (a.lse_out && i < n) a.lse_out[row] = (r + log2f(l)) * 0.69314718055994531f;
+            if (!ok) break;
+            if (it.steps[t] > 0) {
+                ok = warp_wait_or_stop(&sh.o_done[t], mine & 1, stop);
+                if (!ok) break;
+                ++mine;
+                tc_fence_after();
+                const float inv = 1.f / l;
+                const long long row = static_cast<long long>(it.q0 + i) * a.n_heads + it.h;
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + row * D);
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(o, to + c);
+                    tmem_wait_ld();
+                    if (c + 32 == D) {
+                        // the next item's products may write O
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.o_free[t]);
+                    }
+                    if (i < it.n) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                                  __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                            out[c / 8 + e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (a.lse_out && i < it.n) a.lse_out[row] = (r + log2f(l)) * 0.69314718055994531f;
+            }
+            f += it.total;
+            have = items.advance(a, sh, true, threadIdx.x == 0, &it);
         }
     }
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
-    if (threadIdx.x == 0 && bar.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+    if (threadIdx.x == 0 && sh.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
     __syncwarp();
     if (warp == 9) tmem_free(tmem, 512);
 }

@@ -45,6 +45,17 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A warpgroup's registers per thread, down or up (all four warps call it; the sum
+// over the block stays within what it was launched with).
+template <int N>
+__device__ __forceinline__ void give_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void take_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 2^x by the special-function unit (results below the normal range flush to 0).
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -207,6 +218,36 @@ __device__ __forceinline__ void tma_load_3d_multicast(void *dst, const void *tma
 // Brings bytes (a multiple of 16, from a 16-byte boundary) into L2.
 __device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// --- taking the work of CTAs not launched yet ------------------------------------
+
+// Asks for the next CTA of the grid: 16 bytes of answer to shared memory, counted on
+// the barrier.  Not to be asked again once an answer was no.
+__device__ __forceinline__ void ask_next_cta(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 "
+        "[%0], [%1];" ::"r"(smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+// The answer: false when every CTA of the grid has been launched or taken.
+__device__ __forceinline__ bool next_cta(const void *answer, uint3 *cta) {
+    uint32_t yes, x, y, z;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "ld.shared.b128 r, [%4];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %3, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, %1, %2, _}, r;\n\t}"
+        : "=&r"(x), "=&r"(y), "=&r"(z), "=&r"(yes)
+        : "r"(smem_addr(answer))
+        : "memory");
+    cta->x = x;
+    cta->y = y;
+    cta->z = z;
+    return yes != 0;
 }
 
 }  // namespace pkv
