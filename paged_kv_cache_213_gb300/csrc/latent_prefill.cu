@@ -371,8 +371,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-                for (int c = 4; c < kKeys; ++c) mx[c & 3] = fmaxf(mx[c & 3], x[c]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+                for (int c = 4; c + 1 < kKeys; c += 2)
+                    mx[(c / 2) & 3] = max3(mx[(c / 2) & 3], x[c], x[c + 1]);
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * scale;
                 if (j == 0) {
                     r = top > -INFINITY ? top - kHead : 0.f;
                 } else {
@@ -410,16 +411,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                    (e % pieces) * 16) = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t p16[16], p8[8];
 #pragma unroll
                     for (int c = 0; c < 24; ++c) {
-                        const float y0 = ex2(fmaf(x[half * 48 + 2 * c], scale, -r));
-                        const float y1 = ex2(fmaf(x[half * 48 + 2 * c + 1], scale, -r));
-                        sum[(2 * c) & 3] += y0;
-                        sum[(2 * c + 1) & 3] += y1;
+                        const float2 e = fma2(make_float2(x[half * 48 + 2 * c], x[half * 48 + 2 * c + 1]),
+                                              scale, -r);
+                        const float y0 = ex2(e.x), y1 = ex2(e.y);
+                        sum[c & 1] = add2(sum[c & 1], make_float2(y0, y1));
                         if (c < 16) p16[c] = pack_half2(y0, y1); else p8[c - 16] = pack_half2(y0, y1);
                     }
                     tmem_st16(ts + half * 24, p16);
@@ -429,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.p_ready[t][half]);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
             }
             if (!ok) break;
             if (it.steps[t] > 0) {
