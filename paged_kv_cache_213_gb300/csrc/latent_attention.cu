@@ -47,8 +47,11 @@ struct Cfg {
     static constexpr int GROUP = PL * 1024;
     static constexpr int STAGE = kTile / 8 * GROUP;
     static constexpr int STAGES = R == 512 ? 2 : 4;
-    static constexpr int Q_BYTES = N / 8 * GROUP, P_BYTES = kTile * 128;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + Q_BYTES + P_BYTES;
+    static constexpr int Q_BYTES = N / 8 * GROUP;
+    // P^T takes the place of the tile's last plane (the rotated key part), which
+    // nothing reads after the scores: 128 bytes a token
+    static constexpr int P_AT = (PL - 1) * 1024;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + Q_BYTES;
     static constexpr int COLS = (VT + 2) * N;
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     // softmax warps, four a group; a group takes NG of the rows and VG of O^T's
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
     unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    unsigned char *q_smem = base + C::STAGES * C::STAGE, *p_smem = q_smem + C::Q_BYTES;
+    unsigned char *q_smem = base + C::STAGES * C::STAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.n_q_heads;
     const int worker = blockIdx.x / CL;
@@ -261,6 +264,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const long long line = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
         if (line * 32 < static_cast<long long>(a.num_seqs) * a.max_blocks_per_seq)
             prefetch_l2(a.block_tables + line * 32);
+        if (blockIdx.x == 0 && line * 32 <= a.num_seqs) {
+            if (line * 32 < a.num_seqs) prefetch_l2(a.context_lens + line * 32);
+            if (a.query_start) prefetch_l2(a.query_start + line * 32);
+        }
     }
     grid_dependency_wait();
     allow_dependent_launch();
@@ -357,12 +364,12 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 if (mine && row >= 0)
                     bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), 8 * C::E * 2);
             };
-            for (int d = 1; d < kAhead; ++d) to_l2(row_of(p.t0 + d));
-            int row = row_of(p.t0), far = row_of(p.t0 + kAhead);
+            int row = row_of(p.t0), next = row_of(p.t0 + 1);
+            int far[kAhead - 1];  // what only the copies into L2 take at the start
+#pragma unroll
+            for (int d = 0; d < kAhead - 1; ++d) far[d] = row_of(p.t0 + 2 + d);
             for (int t = p.t0; t < end; ++t, ++g) {
-                const int next = row_of(t + 1), next_far = row_of(t + 1 + kAhead);
                 const int s = g % C::STAGES;
-                to_l2(far);
                 if (lane == 0) ok = ok && wait_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
@@ -381,8 +388,15 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     else
                         tma_load_3d(dst, &mc, 0, row, 0, &sh.full[s]);
                 }
+                if (t == p.t0) {
+                    to_l2(next);
+#pragma unroll
+                    for (int d = 0; d < kAhead - 1; ++d) to_l2(far[d]);
+                } else {
+                    to_l2(row_of(t + kAhead));
+                }
                 row = next;
-                far = next_far;
+                next = row_of(t + 2);
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
@@ -397,7 +411,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         if (elect_one()) {
             constexpr uint32_t ds = mma_desc(kTile, N, false, false);
             constexpr uint32_t dpv = mma_desc(128, N, true, true);
-            const uint32_t kv = smem_addr(base), qa = smem_addr(q_smem), pa = smem_addr(p_smem);
+            const uint32_t kv = smem_addr(base), qa = smem_addr(q_smem);
             Piece p;
             int g = 0, k = 0;
             bool ok = true;
@@ -434,7 +448,8 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                             for (int x = 0; x < kTile / 16; ++x)
                                 mma_ss(tmem + v * N,
                                        smem_desc(va + 2 * v * 1024 + 2 * x * C::GROUP, C::GROUP, 1024),
-                                       smem_desc(pa + x * 2048, 1024, 0), dpv, pj > 0 || x > 0);
+                                       smem_desc(va + C::P_AT + 2 * x * C::GROUP, C::GROUP, 0), dpv,
+                                       pj > 0 || x > 0);
                         if (CL > 1)
                             mma_commit_multicast(&sh.empty[gp % C::STAGES], (1 << CL) - 1);
                         else
@@ -571,33 +586,31 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 uint32_t y[NC][2];
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const float p0 = ex2(fmaf(x[c][0], scale, -ref[c][0]));
-                    const float p1 = ex2(fmaf(x[c][1], scale, -ref[c][1]));
-                    const float p2 = ex2(fmaf(x[c][2], scale, -ref[c][0]));
-                    const float p3 = ex2(fmaf(x[c][3], scale, -ref[c][1]));
+                    const float2 u = fma2(make_float2(x[c][0], x[c][2]), scale, -ref[c][0]);
+                    const float2 v = fma2(make_float2(x[c][1], x[c][3]), scale, -ref[c][1]);
+                    const float p0 = ex2(u.x), p1 = ex2(v.x), p2 = ex2(u.y), p3 = ex2(v.y);
                     sum[c][0] += p0 + p2;
                     sum[c][1] += p1 + p3;
                     y[c][0] = pack_half2(p0, p1);
                     y[c][1] = pack_half2(p2, p3);
                 }
-                // the one P buffer is free when the products before are done
-                if (g > 0) warp_wait_or_stop(&sh.pv_done, (g - 1) & 1, stop);
+                unsigned char *tile = base + (g % C::STAGES) * C::STAGE;
 #pragma unroll
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = tok + 8 * e, piece = c + NC * group;
-                        *reinterpret_cast<uint32_t *>(p_smem + r * 128 + ((piece ^ (r & 7)) << 4) +
+                        *reinterpret_cast<uint32_t *>(tile + (r / 8) * C::GROUP + C::P_AT +
+                                                      (r % 8) * 128 + ((piece ^ (r & 7)) << 4) +
                                                       4 * (lane & 3)) = y[c][e];
                     }
                 // values of rows past the sequence's end meet weights of 0: they must
                 // be finite
                 const int valid = p.s.len - t * kTile;
                 if (valid < kTile) {
-                    unsigned char *v = base + (g % C::STAGES) * C::STAGE;
                     for (int e = threadIdx.x; e < (kTile - valid) * (R / 8); e += kSoft) {
                         const int r = valid + e / (R / 8), piece = e % (R / 8);
-                        *reinterpret_cast<uint4 *>(v + (r / 8) * C::GROUP + (piece / 8) * 1024 +
+                        *reinterpret_cast<uint4 *>(tile + (r / 8) * C::GROUP + (piece / 8) * 1024 +
                                                    (r % 8) * 128 + (piece % 8) * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
