@@ -58,7 +58,7 @@ struct Cfg {
     // 16-column pieces
     static constexpr int GROUPS = N == 64 ? 2 : 1, SW = 4 * GROUPS;
     static constexpr int NG = N / GROUPS;
-    static constexpr int THREADS = 32 * (SW + 2);  // and the copy and the MMA warp
+    static constexpr int THREADS = 32 * (SW + 3);  // and the copy warp and two for the products
 };
 
 // One sequence's work: its query rows and how many of its tokens each attends.
@@ -163,7 +163,7 @@ __device__ bool next_piece(const LatentAttentionArgs &a, int rows, Walk *w, Piec
 // Workspace: `records` x CL records {first output row, rows, first and last worker
 // of the segment; no rows: nothing to join}, then per piece slot (two a worker: 0
 // ends a segment or lies inside one, 1 starts one) and CTA of the cluster N pairs
-// (r, l) and R x N partial sums, a column's N rows together.
+// (r, l) and N x R partial sums, four rows of a column together, then the columns.
 struct Layout {
     size_t ml, acc, total;
 };
@@ -178,7 +178,7 @@ __host__ __device__ inline Layout layout(int records, int workers, int cl, int r
 }
 
 struct Shared {
-    uint64_t full[4], empty[4], s_full[2], p_ready, pv_done, q_full, q_empty, o_full, o_free, drained;
+    uint64_t full[4], empty[4], s_full[2], p_ready[2], pv_done, q_full, q_empty, o_full, o_free, drained[2];
     uint32_t tmem;
     int stop;
     Split split;
@@ -240,13 +240,15 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         }
         mbar_init(&sh.s_full[0], 1);
         mbar_init(&sh.s_full[1], 1);
-        mbar_init(&sh.p_ready, C::SW);
+        mbar_init(&sh.p_ready[0], C::SW);
+        mbar_init(&sh.p_ready[1], C::SW);
         mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.o_full, 1);
         mbar_init(&sh.o_free, C::SW);
-        mbar_init(&sh.drained, 1);
+        mbar_init(&sh.drained[0], 1);
+        mbar_init(&sh.drained[1], 1);
         sh.stop = 0;
         sh.walk.left = 0;
         fence_barrier_init();
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             for (int d = 0; d < kAhead - 1; ++d) far[d] = row_of(p.t0 + 2 + d);
             for (int t = p.t0; t < end; ++t, ++g) {
                 const int s = g % C::STAGES;
-                if (lane == 0) ok = ok && wait_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop);
+                if (lane == 0) ok = ok && poll_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
@@ -407,71 +409,75 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 mbar_wait_bounded(&sh.full[i % C::STAGES], (i / C::STAGES) & 1);
         }
     } else if (warp == C::SW + 1) {
-        // --- matrix products ---
+        // --- scores ---
+        // One warp issues them, the next one the outputs' products: neither's waits
+        // and commits keep the tensor core from the other's work.
         if (elect_one()) {
             constexpr uint32_t ds = mma_desc(kTile, N, false, false);
-            constexpr uint32_t dpv = mma_desc(128, N, true, true);
-            const uint32_t kv = smem_addr(base), qa = smem_addr(q_smem);
+            const uint32_t kv = smem_addr(base);
+            const uint64_t qd = smem_desc(smem_addr(q_smem), C::GROUP, 0);
             Piece p;
             int g = 0, k = 0;
             bool ok = true;
             while (ok && next_piece(a, C::ROWS, &w, &p)) {
                 ok = wait_or_stop(&sh.q_full, k & 1, stop);
-                int sj = 0, pj = 0;
-                unsigned spins = 0;
-                unsigned long long t0 = 0;
-                while (ok && pj < p.tiles) {
-                    const int gs = g + sj, gp = g + pj;
-                    if (sj < p.tiles && sj < pj + 2 &&
-                        mbar_test_wait(&sh.full[gs % C::STAGES], (gs / C::STAGES) & 1)) {
-                        const uint32_t ka = kv + (gs % C::STAGES) * C::STAGE;
-                        const uint32_t d = tmem + (C::VT + (gs & 1)) * N;
-                        tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < p.tiles && ok; ++j, ++g) {
+                    // the scores' place is free when the weights before last are made
+                    if (g > 1) ok = wait_or_stop(&sh.p_ready[g & 1], ((g >> 1) & 1) ^ 1, stop);
+                    ok = ok && poll_or_stop(&sh.full[g % C::STAGES], (g / C::STAGES) & 1, stop);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t kd = smem_desc(kv + (g % C::STAGES) * C::STAGE, C::GROUP, 0);
+                    const uint32_t d = tmem + (C::VT + (g & 1)) * N;
 #pragma unroll
-                        for (int x = 0; x < 4 * C::PL; ++x)
-                            mma_ss(d, smem_desc(ka + (x / 4) * 1024 + (x % 4) * 32, C::GROUP, 0),
-                                   smem_desc(qa + (x / 4) * 1024 + (x % 4) * 32, C::GROUP, 0), ds,
-                                   x > 0);
-                        mma_commit(&sh.s_full[gs & 1]);
-                        if (++sj == p.tiles) mma_commit(&sh.q_empty);
-                        spins = 0;
-                    } else if (pj < sj && mbar_test_wait(&sh.p_ready, gp & 1)) {
-                        if (pj == 0) {
-                            ok = wait_or_stop(&sh.o_free, (k & 1) ^ 1, stop);
-                            if (!ok) break;
-                        }
-                        const uint32_t va = kv + (gp % C::STAGES) * C::STAGE;
-                        tc_fence_after();
-#pragma unroll
-                        for (int v = 0; v < C::VT; ++v)
-#pragma unroll
-                            for (int x = 0; x < kTile / 16; ++x)
-                                mma_ss(tmem + v * N,
-                                       smem_desc(va + 2 * v * 1024 + 2 * x * C::GROUP, C::GROUP, 1024),
-                                       smem_desc(va + C::P_AT + 2 * x * C::GROUP, C::GROUP, 0), dpv,
-                                       pj > 0 || x > 0);
-                        if (CL > 1)
-                            mma_commit_multicast(&sh.empty[gp % C::STAGES], (1 << CL) - 1);
-                        else
-                            mma_commit(&sh.empty[gp % C::STAGES]);
-                        mma_commit(&sh.pv_done);
-                        if (++pj == p.tiles) mma_commit(&sh.o_full);
-                        spins = 0;
-                    } else if ((++spins & 255u) == 0) {
-                        if (spins == 256) t0 = global_timer_ns();
-                        if (*stop || spins > kWaitLimitIters ||
-                            global_timer_ns() - t0 > kWaitLimitNs) {
-                            *stop = 1;
-                            ok = false;
-                        }
-                    }
+                    for (int x = 0; x < 4 * C::PL; ++x)
+                        mma_ss(d, kd + (x / 4) * 64 + (x % 4) * 2, qd + (x / 4) * 64 + (x % 4) * 2, ds,
+                               x > 0);
+                    mma_commit(&sh.s_full[g & 1]);
                 }
-                g += p.tiles;
+                if (ok) mma_commit(&sh.q_empty);
                 ++k;
             }
             // nothing of the tensor core is left in flight when TMEM is freed
-            mma_commit(&sh.drained);
-            mbar_wait_bounded(&sh.drained, 0);
+            mma_commit(&sh.drained[0]);
+            mbar_wait_bounded(&sh.drained[0], 0);
+        }
+    } else if (warp == C::SW + 2) {
+        // --- outputs' products ---
+        if (elect_one()) {
+            constexpr uint32_t dpv = mma_desc(128, N, true, true);
+            const uint32_t kv = smem_addr(base);
+            Piece p;
+            int g = 0, k = 0;
+            bool ok = true;
+            while (ok && next_piece(a, C::ROWS, &w, &p)) {
+                ok = wait_or_stop(&sh.o_free, (k & 1) ^ 1, stop);
+#pragma unroll 1
+                for (int j = 0; j < p.tiles && ok; ++j, ++g) {
+                    ok = poll_or_stop(&sh.p_ready[g & 1], (g >> 1) & 1, stop);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t va = kv + (g % C::STAGES) * C::STAGE;
+                    const uint64_t vd = smem_desc(va, C::GROUP, 1024);
+                    const uint64_t pd = smem_desc(va + C::P_AT, C::GROUP, 0);
+#pragma unroll
+                    for (int v = 0; v < C::VT; ++v)
+#pragma unroll
+                        for (int x = 0; x < kTile / 16; ++x)
+                            mma_ss(tmem + v * N, vd + (2 * v * 1024 + 2 * x * C::GROUP) / 16,
+                                   pd + 2 * x * C::GROUP / 16, dpv, j > 0 || x > 0);
+                    if (CL > 1)
+                        mma_commit_multicast(&sh.empty[g % C::STAGES], (1 << CL) - 1);
+                    else
+                        mma_commit(&sh.empty[g % C::STAGES]);
+                    mma_commit(&sh.pv_done);
+                }
+                if (ok) mma_commit(&sh.o_full);
+                ++k;
+            }
+            mma_commit(&sh.drained[1]);
+            mbar_wait_bounded(&sh.drained[1], 0);
         }
     } else {
         // --- softmax, results ---
@@ -617,7 +623,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready);
+                if (lane == 0) mbar_arrive(&sh.p_ready[g & 1]);
             }
             // the row sums, over the tokens of all threads
 #pragma unroll
@@ -668,17 +674,17 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                             dst[e * R] = __float2half_rn(__uint_as_float(o[e]) * sh.factor[n0 + e]);
                 }
             } else {
-                float *acc = reinterpret_cast<float *>(ws + lay.acc) +
-                             (static_cast<size_t>(slot) * R + 32 * quarter + lane) * N;
+                uint4 *acc = reinterpret_cast<uint4 *>(ws + lay.acc) +
+                             static_cast<size_t>(slot) * (N / 4 * R) + 32 * quarter + lane;
 #pragma unroll 2
                 for (int v = 16 * group; v < C::VT * N; v += 16 * C::GROUPS) {
                     uint32_t o[16];
                     tmem_ld16(o, tmem + v + lanes);
                     tmem_wait_ld();
-                    uint4 *dst = reinterpret_cast<uint4 *>(acc + 128 * N * (v / N) + v % N);
+                    uint4 *dst = acc + (v % N) / 4 * R + 128 * (v / N);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        dst[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        dst[e * R] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                 }
             }
             tc_fence_before();
@@ -707,75 +713,84 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
 }
 
 // The pieces of each cut segment, joined.  A unit is four rows of one column (one
-// 16-byte load a piece); a block has 256 / G units and G threads a unit, each for
-// every G-th piece, and turns its columns to rows on the way out.
+// 16-byte load a piece); a block has 256 / G neighbouring columns of four rows and G
+// threads a unit, each for every G-th piece.
 constexpr int kJoinThreads = 256;
 
 template <int R, int N, int CL>
 __global__ void __launch_bounds__(kJoinThreads)
     latent_join_kernel(const LatentAttentionArgs a, const LatentSplit sp) {
-    __shared__ float parts[kJoinThreads];
+    __shared__ float parts[kJoinThreads / 32][4];
     __shared__ float4 sums[kJoinThreads];
-    __shared__ float ref[N], inv[N];
-    __shared__ __align__(16) __half tile[kJoinThreads * 4];
     grid_dependency_wait();
     allow_dependent_launch();
     const int4 rec = static_cast<const int4 *>(a.workspace)[blockIdx.x];
-    if (rec.y <= 0) return;
+    const int G = sp.join_threads, units = kJoinThreads / G;
+    const int n0 = static_cast<int>(blockIdx.y) * units / R * 4;  // the block's rows
+    if (n0 >= rec.y) return;
     const Layout lay = layout(sp.records, sp.workers, CL, N, R);
     const char *ws = static_cast<const char *>(a.workspace);
-    const float2 *ml = reinterpret_cast<const float2 *>(ws + lay.ml);
+    const float2 *ml = reinterpret_cast<const float2 *>(ws + lay.ml) + n0;
     const float4 *acc = reinterpret_cast<const float4 *>(ws + lay.acc);
     const int pieces = rec.w - rec.z + 1, rank = blockIdx.x % CL;
     auto slot = [&](int k) { return static_cast<size_t>((2 * (rec.z + k) + (k == 0 ? 1 : 0)) * CL + rank); };
-    // the rows' references and sums over all pieces
-    {
-        constexpr int S = kJoinThreads / N;  // threads of a row
-        const int n = threadIdx.x % N, i = threadIdx.x / N;
-        float m = -INFINITY, l = 0.f;
-        for (int k = i; k < pieces; k += S) m = fmaxf(m, ml[slot(k) * N + n].x);
-        parts[threadIdx.x] = m;
-        __syncthreads();
-#pragma unroll
-        for (int s = 0; s < S; ++s) m = fmaxf(m, parts[s * N + n]);
-        m = m > -INFINITY ? m : 0.f;
-        for (int k = i; k < pieces; k += S) {
-            const float2 v = ml[slot(k) * N + n];
-            l += v.y * ex2(v.x - m);
-        }
-        __syncthreads();
-        parts[threadIdx.x] = l;
-        __syncthreads();
-        if (i == 0) {
-#pragma unroll
-            for (int s = 1; s < S; ++s) l += parts[s * N + n];
-            ref[n] = m;
-            inv[n] = l == 0.f ? 0.f : 1.f / l;
-            if (a.lse_out && blockIdx.y == 0 && n < rec.y)
-                a.lse_out[rec.x + n] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-        }
-        __syncthreads();
-    }
-    const int G = sp.join_threads, units = kJoinThreads / G;
+    // this block's first loads of partial sums need nothing of the rows' statistics
     const int u = threadIdx.x % units, i = threadIdx.x / units;
-    const int at = blockIdx.y * units + u, n0 = 4 * (at % (N / 4));
-    const float r0 = ref[n0], r1 = ref[n0 + 1], r2 = ref[n0 + 2], r3 = ref[n0 + 3];
+    const size_t at = static_cast<size_t>(blockIdx.y) * units + u;
+    const float4 first = i < pieces ? acc[slot(i) * (N / 4 * R) + at] : make_float4(0.f, 0.f, 0.f, 0.f);
+    // the rows' references and sums over all pieces: thread x takes row x % 4 of every
+    // 64th piece
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float m = -INFINITY, l = 0.f;
+    for (int k = threadIdx.x / 4; k < pieces; k += kJoinThreads / 4) {
+        const float2 v = ml[slot(k) * N + threadIdx.x % 4];
+        const float next = fmaxf(m, v.x);
+        if (next > -INFINITY) l = l * ex2(m - next) + v.y * ex2(v.x - next);
+        m = next;
+    }
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+        const float next = fmaxf(m, m2);
+        if (next > -INFINITY) l = l * ex2(m - next) + l2 * ex2(m2 - next);
+        m = next;
+    }
+    __shared__ float warp_l[kJoinThreads / 32][4];
+    if (lane < 4) {
+        parts[warp][lane] = m;
+        warp_l[warp][lane] = l;
+    }
+    __syncthreads();
+    float ref[4], inv[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float r = -INFINITY, t = 0.f;
+#pragma unroll
+        for (int x = 0; x < kJoinThreads / 32; ++x) r = fmaxf(r, parts[x][e]);
+        r = r > -INFINITY ? r : 0.f;
+#pragma unroll
+        for (int x = 0; x < kJoinThreads / 32; ++x) t += warp_l[x][e] * ex2(parts[x][e] - r);
+        ref[e] = r;
+        inv[e] = t == 0.f ? 0.f : 1.f / t;
+        if (a.lse_out && static_cast<int>(blockIdx.y) * units % R == 0 && threadIdx.x == e && n0 + e < rec.y)
+            a.lse_out[rec.x + n0 + e] = t == 0.f ? -INFINITY : (r + log2f(t)) * 0.69314718055994531f;
+    }
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = i; k < pieces; k += G) {
         const size_t sl = slot(k);
-        const float4 v = acc[sl * (R * N / 4) + at];
-        const float4 ma = *reinterpret_cast<const float4 *>(ml + sl * N + n0);
-        const float4 mb = *reinterpret_cast<const float4 *>(ml + sl * N + n0 + 2);
-        s.x = fmaf(v.x, ex2(ma.x - r0), s.x);
-        s.y = fmaf(v.y, ex2(ma.z - r1), s.y);
-        s.z = fmaf(v.z, ex2(mb.x - r2), s.z);
-        s.w = fmaf(v.w, ex2(mb.z - r3), s.w);
+        const float4 v = k == i ? first : acc[sl * (N / 4 * R) + at];
+        const float4 ma = *reinterpret_cast<const float4 *>(ml + sl * N);
+        const float4 mb = *reinterpret_cast<const float4 *>(ml + sl * N + 2);
+        s.x = fmaf(v.x, ex2(ma.x - ref[0]), s.x);
+        s.y = fmaf(v.y, ex2(ma.z - ref[1]), s.y);
+        s.z = fmaf(v.z, ex2(mb.x - ref[2]), s.z);
+        s.w = fmaf(v.w, ex2(mb.z - ref[3]), s.w);
     }
-    sums[threadIdx.x] = s;
-    __syncthreads();
-    const int cols = units * 4 / N;  // of this block
-    if (i == 0) {
+    if (G > 1) {
+        sums[threadIdx.x] = s;
+        __syncthreads();
+        if (i > 0) return;
         for (int k = 1; k < G; ++k) {
             const float4 v = sums[k * units + u];
             s.x += v.x;
@@ -783,19 +798,12 @@ __global__ void __launch_bounds__(kJoinThreads)
             s.z += v.z;
             s.w += v.w;
         }
-        const int c = u / (N / 4);
-        tile[(n0 + 0) * cols + c] = __float2half_rn(s.x * inv[n0]);
-        tile[(n0 + 1) * cols + c] = __float2half_rn(s.y * inv[n0 + 1]);
-        tile[(n0 + 2) * cols + c] = __float2half_rn(s.z * inv[n0 + 2]);
-        tile[(n0 + 3) * cols + c] = __float2half_rn(s.w * inv[n0 + 3]);
     }
-    __syncthreads();
-    const int words = cols / 2;
-    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__half *>(a.out) +
-                                                 static_cast<long long>(rec.x) * R + blockIdx.y * cols);
-    for (int x = threadIdx.x; x < min(rec.y, N) * words; x += kJoinThreads)
-        out[static_cast<size_t>(x / words) * (R / 2) + x % words] =
-            reinterpret_cast<const uint32_t *>(tile)[x];
+    __half *out = static_cast<__half *>(a.out) + (static_cast<long long>(rec.x) + n0) * R + at % R;
+    const float y[4] = {s.x * inv[0], s.y * inv[1], s.z * inv[2], s.w * inv[3]};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (n0 + e < rec.y) out[e * R] = __float2half_rn(y[e]);
 }
 
 // Rows of `width` fp16 values as [width / 64 planes][rows][64 columns]: a box is 8

@@ -27,6 +27,22 @@ __device__ __forceinline__ bool wait_or_stop(uint64_t *bar, uint32_t parity, vol
     return false;
 }
 
+// The same by polling, for single threads: one that try_wait has put to sleep starts
+// again some 100 cycles late.
+__device__ __forceinline__ bool poll_or_stop(uint64_t *bar, uint32_t parity, volatile int *stop) {
+    unsigned long long t0 = 0;
+    for (unsigned it = 1; it < kWaitLimitIters; ++it) {
+        if (mbar_test_wait(bar, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (*stop) return false;
+            if (it == 256u) t0 = global_timer_ns();
+            if (global_timer_ns() - t0 > kWaitLimitNs) break;
+        }
+    }
+    *stop = 1;
+    return false;
+}
+
 // The same by all lanes of a warp: one answer for the whole warp.
 __device__ __forceinline__ bool warp_wait_or_stop(uint64_t *bar, uint32_t parity,
                                                   volatile int *stop) {
