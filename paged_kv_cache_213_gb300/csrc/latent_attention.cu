@@ -99,13 +99,10 @@ __device__ __forceinline__ int token_tiles(int end) {
 
 // Units (token tiles of a row tile) of a whole sequence; the host keeps the sum
 // over the batch below 2^31.
-__device__ __forceinline__ int seq_units(const LatentAttentionArgs &a, int b, int rows, bool *good) {
-    Seq s;
-    *good = load_seq(a, b, &s);
-    if (!*good || s.n == 0) return 0;
+__device__ __forceinline__ int seq_units(const Seq &s, int heads, int rows) {
     int u = 0;
-    for (int rt = row_tiles(s.n, a.n_q_heads, rows) - 1; rt >= 0; --rt)
-        u += token_tiles(tile_end(s, a.n_q_heads, rows, rt));
+    for (int rt = row_tiles(s.n, heads, rows) - 1; rt >= 0; --rt)
+        u += token_tiles(tile_end(s, heads, rows, rt));
     return u;
 }
 
@@ -132,28 +129,32 @@ struct Walk {
     int b, rt, skip, left, unit;
 };
 
-__device__ bool next_piece(const LatentAttentionArgs &a, int rows, Walk *w, Piece *p) {
+// The piece of sequence w->b (which is s) that w stands at, if there is one.
+__device__ __forceinline__ bool piece_of(const Seq &s, int heads, int rows, Walk *w, Piece *p) {
+    const int rts = row_tiles(s.n, heads, rows);
+    for (; w->rt < rts; ++w->rt) {
+        const int tiles = token_tiles(tile_end(s, heads, rows, w->rt));
+        if (w->skip >= tiles) {
+            w->skip -= tiles;
+            w->unit += tiles;
+            continue;
+        }
+        const int take = min(tiles - w->skip, w->left);
+        *p = Piece{s, w->b, w->rt, w->skip, take, tiles, w->unit};
+        w->left -= take;
+        w->skip = 0;
+        w->unit += tiles;
+        ++w->rt;
+        return true;
+    }
+    return false;
+}
+
+__device__ __forceinline__ bool next_piece(const LatentAttentionArgs &a, int rows, Walk *w, Piece *p) {
     if (w->left <= 0) return false;
     while (w->b < a.num_seqs) {
         Seq s;
-        if (load_seq(a, w->b, &s)) {
-            const int rts = row_tiles(s.n, a.n_q_heads, rows);
-            for (; w->rt < rts; ++w->rt) {
-                const int tiles = token_tiles(tile_end(s, a.n_q_heads, rows, w->rt));
-                if (w->skip >= tiles) {
-                    w->skip -= tiles;
-                    w->unit += tiles;
-                    continue;
-                }
-                const int take = min(tiles - w->skip, w->left);
-                *p = Piece{s, w->b, w->rt, w->skip, take, tiles, w->unit};
-                w->left -= take;
-                w->skip = 0;
-                w->unit += tiles;
-                ++w->rt;
-                return true;
-            }
-        }
+        if (load_seq(a, w->b, &s) && piece_of(s, a.n_q_heads, rows, w, p)) return true;
         ++w->b;
         w->rt = 0;
     }
@@ -182,7 +183,8 @@ struct Shared {
     uint32_t tmem;
     int stop;
     Split split;
-    Walk walk;
+    Walk walk;    // behind the first piece
+    Piece first;
     int sums[16];
     float warps[4][64];  // per row, of each softmax warp of its group: a tile's maxima, a piece's sums
     float factor[64];    // what O^T's columns are multiplied with
@@ -250,7 +252,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         mbar_init(&sh.drained[0], 1);
         mbar_init(&sh.drained[1], 1);
         sh.stop = 0;
-        sh.walk.left = 0;
+        sh.first.tiles = 0;
         fence_barrier_init();
     }
     if (warp == C::SW + 1) {
@@ -280,9 +282,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const int b0 = min(static_cast<int>(threadIdx.x) * per, a.num_seqs);
         const int b1 = min(b0 + per, a.num_seqs);
         int mine = 0;
-        bool good;
+        Seq seq;  // the thread's only sequence, where it has one
         for (int b = b0; b < b1; ++b) {
-            const int u = seq_units(a, b, C::ROWS, &good);
+            const bool good = load_seq(a, b, &seq);
+            const int u = good ? seq_units(seq, a.n_q_heads, C::ROWS) : 0;
             mine += u;
             if (blockIdx.x == 0 && !good) flag_error(a.err, PKV_ERRBIT_CONTEXT);
             if (blockIdx.x == 0 && u == 0 && sp.by_segment)
@@ -312,12 +315,17 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 int b = b0, at = before;
                 if (per > 1)
                     for (;; ++b) {
-                        const int u = seq_units(a, b, C::ROWS, &good);
+                        const int u = load_seq(a, b, &seq) ? seq_units(seq, a.n_q_heads, C::ROWS) : 0;
                         if (first < at + u) break;
                         at += u;
                     }
+                // the first piece, for all roles at once
+                Walk w{b, 0, first - at, split.first(worker + 1) - first, at};
+                Piece p;
+                piece_of(seq, a.n_q_heads, C::ROWS, &w, &p);
                 sh.split = split;
-                sh.walk = Walk{b, 0, first - at, split.first(worker + 1) - first, at};
+                sh.walk = w;
+                sh.first = p;
             }
         }
     }
@@ -327,19 +335,40 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
     Walk w = sh.walk;
+    Piece p = sh.first;
 
-    if (w.left <= 0) {
+    if (p.tiles == 0) {
         if (threadIdx.x == 0 && !sp.by_segment) records[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else if (warp == C::SW) {
         // --- copies ---
-        Piece p;
         // a lane copies 8 tokens; the cluster's CTAs share a tile's lanes
         constexpr int kLanes = kTile / 8;
         const bool mine = lane < kLanes && lane / (kLanes / CL) == rank;
         const char *cache = static_cast<const char *>(a.cache);
+        const int block_log2 = 31 - __clz(a.block_size);
         int g = 0, k = 0;  // tiles, pieces so far
         bool ok = true;
-        while (ok && next_piece(a, C::ROWS, &w, &p)) {
+        do {
+            const int32_t *table = a.block_tables + static_cast<long long>(p.b) * a.max_blocks_per_seq;
+            const int end = p.t0 + p.tiles;
+            auto row_of = [&](int t) {  // first cache row of this lane's tokens of tile t, or -1
+                const int token = t * kTile + lane * 8;
+                if (lane >= kLanes || token >= p.s.len || t >= end) return -1;
+                int id = table[token >> block_log2];
+                if (id < 0 || id >= a.num_blocks) {
+                    flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
+                    id = 0;  // some block of the pool: the sequence's result is unspecified
+                }
+                return (id << block_log2) + (token & (a.block_size - 1));
+            };
+            auto to_l2 = [&](int row) {
+                if (mine && row >= 0)
+                    bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), 8 * C::E * 2);
+            };
+            int row = row_of(p.t0), next = row_of(p.t0 + 1);
+            int far[kAhead - 1];  // what only the copies into L2 take at the start
+#pragma unroll
+            for (int d = 0; d < kAhead - 1; ++d) far[d] = row_of(p.t0 + 2 + d);
             if (lane == 0) {
                 ok = wait_or_stop(&sh.q_empty, (k & 1) ^ 1, stop);
                 if (ok) {
@@ -350,26 +379,6 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 }
             }
             ++k;
-            const int32_t *table = a.block_tables + static_cast<long long>(p.b) * a.max_blocks_per_seq;
-            const int end = p.t0 + p.tiles;
-            auto row_of = [&](int t) {  // first cache row of this lane's tokens of tile t, or -1
-                const int token = t * kTile + lane * 8;
-                if (lane >= kLanes || token >= p.s.len || t >= end) return -1;
-                int id = table[token / a.block_size];
-                if (id < 0 || id >= a.num_blocks) {
-                    flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
-                    id = 0;  // some block of the pool: the sequence's result is unspecified
-                }
-                return id * a.block_size + token % a.block_size;
-            };
-            auto to_l2 = [&](int row) {
-                if (mine && row >= 0)
-                    bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), 8 * C::E * 2);
-            };
-            int row = row_of(p.t0), next = row_of(p.t0 + 1);
-            int far[kAhead - 1];  // what only the copies into L2 take at the start
-#pragma unroll
-            for (int d = 0; d < kAhead - 1; ++d) far[d] = row_of(p.t0 + 2 + d);
             for (int t = p.t0; t < end; ++t, ++g) {
                 const int s = g % C::STAGES;
                 if (lane == 0) ok = ok && poll_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop);
@@ -401,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 next = row_of(t + 2);
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
-        }
+        } while (ok && next_piece(a, C::ROWS, &w, &p));
         if (!ok && lane == 0) {
             // every copy in flight lands before the CTA gives its memory back
             mbar_wait_bounded(&sh.q_full, (k - 1) & 1);
@@ -416,10 +425,9 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             constexpr uint32_t ds = mma_desc(kTile, N, false, false);
             const uint32_t kv = smem_addr(base);
             const uint64_t qd = smem_desc(smem_addr(q_smem), C::GROUP, 0);
-            Piece p;
             int g = 0, k = 0;
             bool ok = true;
-            while (ok && next_piece(a, C::ROWS, &w, &p)) {
+            do {
                 ok = wait_or_stop(&sh.q_full, k & 1, stop);
 #pragma unroll 1
                 for (int j = 0; j < p.tiles && ok; ++j, ++g) {
@@ -438,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 }
                 if (ok) mma_commit(&sh.q_empty);
                 ++k;
-            }
+            } while (ok && next_piece(a, C::ROWS, &w, &p));
             // nothing of the tensor core is left in flight when TMEM is freed
             mma_commit(&sh.drained[0]);
             mbar_wait_bounded(&sh.drained[0], 0);
@@ -448,10 +456,9 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         if (elect_one()) {
             constexpr uint32_t dpv = mma_desc(128, N, true, true);
             const uint32_t kv = smem_addr(base);
-            Piece p;
             int g = 0, k = 0;
             bool ok = true;
-            while (ok && next_piece(a, C::ROWS, &w, &p)) {
+            do {
                 ok = wait_or_stop(&sh.o_free, (k & 1) ^ 1, stop);
 #pragma unroll 1
                 for (int j = 0; j < p.tiles && ok; ++j, ++g) {
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 }
                 if (ok) mma_commit(&sh.o_full);
                 ++k;
-            }
+            } while (ok && next_piece(a, C::ROWS, &w, &p));
             mma_commit(&sh.drained[1]);
             mbar_wait_bounded(&sh.drained[1], 0);
         }
@@ -489,10 +496,9 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const Layout lay = layout(sp.records, sp.workers, CL, N, R);
         char *ws = static_cast<char *>(a.workspace);
         const float scale = a.scale_log2;
-        Piece p;
         int g = 0, k = 0;
         bool recorded = false;
-        while (next_piece(a, C::ROWS, &w, &p)) {
+        do {
             const int tile_row = p.rt * C::ROWS + rank * N;  // of the sequence's rows
             float ref[NC][2], sum[NC][2];
             int seen[NC][2];  // tokens that the row attends
@@ -700,7 +706,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 recorded |= !whole;
             }
             ++k;
-        }
+        } while (next_piece(a, C::ROWS, &w, &p));
         if (!recorded && threadIdx.x == 0 && !sp.by_segment) records[blockIdx.x] = make_int4(0, 0, 0, 0);
     }
     tc_fence_before();
@@ -718,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
 constexpr int kJoinThreads = 256;
 
 template <int R, int N, int CL>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 4)
     latent_join_kernel(const LatentAttentionArgs a, const LatentSplit sp) {
     __shared__ float parts[kJoinThreads / 32][4];
     __shared__ float4 sums[kJoinThreads];
