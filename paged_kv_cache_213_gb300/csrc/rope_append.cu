@@ -12,7 +12,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
-#include "e4m3_quant.cuh"
+#include "f32x2.cuh"
 #include "pagedkv_rope.h"
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -23,30 +23,52 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
-    return make_uint4(pack_half2(y[0], y[1]), pack_half2(y[2], y[3]), pack_half2(y[4], y[5]),
-                      pack_half2(y[6], y[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&y)[4]) {
+    return make_uint4(pack_half2(y[0].x, y[0].y), pack_half2(y[1].x, y[1].y),
+                      pack_half2(y[2].x, y[2].y), pack_half2(y[3].x, y[3].y));
 }
 
-// 8 fp32 values to 8 E4M3 codes of y / scale (the rounding of quantize16).
-__device__ __forceinline__ uint2 quantize8(const float (&y)[8], float scale) {
-    uint32_t w[2];
+__device__ __forceinline__ void unpack8(const uint4 &v, float2 (&f)[4]) {
+    const __half2 *h = reinterpret_cast<const __half2 *>(&v);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const __nv_fp8x2_storage_t a = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(y[4 * i], scale), __fdiv_rn(y[4 * i + 1], scale)),
-            __NV_SATFINITE, __NV_E4M3);
-        const __nv_fp8x2_storage_t b = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(y[4 * i + 2], scale), __fdiv_rn(y[4 * i + 3], scale)),
-            __NV_SATFINITE, __NV_E4M3);
-        w[i] = static_cast<uint32_t>(a) | (static_cast<uint32_t>(b) << 16);
+    for (int i = 0; i < 4; ++i) f[i] = __half22float2(h[i]);
+}
+
+// x / scale, correctly rounded: the quotient by the reciprocal inv = RN(1 / scale),
+// then twice corrected by its exact residual (Markstein: with a correctly rounded
+// reciprocal and a quotient within one unit in the last place, one such correction
+// gives the rounded quotient; the first brings it there).  Exact where the residual is
+// a normal number, which holds for |x / scale| >= 2^-11 (smaller ones become code 0)
+// and scales in [2^-60, 2^60]; a quotient that is not finite stays as it is, and the
+// sign is that of x (a residual of 0 would turn -0 into 0).
+__device__ __forceinline__ float2 divide2(float2 x, float scale, float inv) {
+    const float2 s = make_float2(-scale, -scale), y = make_float2(inv, inv);
+    const float2 q0 = mul2(x, y);
+    const float2 q1 = fma2(fma2(s, q0, x), y, q0);
+    const float2 q2 = fma2(fma2(s, q1, x), y, q1);
+    return make_float2(fabsf(q0.x) < 1e30f ? copysignf(q2.x, q0.x) : q0.x,
+                       fabsf(q0.y) < 1e30f ? copysignf(q2.y, q0.y) : q0.y);
+}
+
+// 8 fp32 values to 8 E4M3 codes of y / scale, to the codes that paged_kv_append_fp8
+// stores.  inv = RN(1 / scale), or 0 for a scale that divide2 does not take.
+__device__ __forceinline__ uint2 quantize8(const float2 (&y)[4], float scale, float inv) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 q;
+        if (inv != 0.f)
+            q = divide2(y[i], scale, inv);
+        else
+            q = make_float2(__fdiv_rn(y[i].x, scale), __fdiv_rn(y[i].y, scale));
+        w[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
     }
-    return make_uint2(w[0], w[1]);
+    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
 // The cosines and sines that entries 8 j .. 8 j + 7 of a vector need, from the
 // table row cs (cos, then sin, rot / 2 each): 8 pairs of split halves, or 4
-// interleaved ones.
+// interleaved ones.  Beyond rot: cos 1, sin 0.
 struct Turn {
     float c[8], s[8];
 };
@@ -69,38 +91,52 @@ __device__ __forceinline__ Turn load_turn(const float *cs, int j, int rot, bool 
         load4(t.c, cs + 4 * j);
         load4(t.s, cs + half + 4 * j);
     } else {
-        const int p = 8 * j < half ? 8 * j : 8 * j - half;
+        const bool low = 8 * j < half;
+        const int p = low ? 8 * j : 8 * j - half;
         load4(t.c, cs + p);
         load4(t.c + 4, cs + p + 4);
         load4(t.s, cs + half + p);
         load4(t.s + 4, cs + half + p + 4);
+        // low half: a cos - b sin; high half: b cos + a sin
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t.s[i] = low ? -t.s[i] : t.s[i];
     }
     return t;
 }
 
 // Rotates the 8 entries y (entries 8 j .. of a vector) by t.  Split halves: the
 // partner entries are rot / 16 lanes up or down; every lane of the warp calls this.
-__device__ __forceinline__ void rotate8(float (&y)[8], const Turn &t, int j, int rot,
+__device__ __forceinline__ void rotate8(float2 (&y)[4], const Turn &t, int j, int rot,
                                         bool interleaved) {
-    if (interleaved) {  // beyond rot: cos 1, sin 0
+    if (interleaved) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = y[2 * i], b = y[2 * i + 1];
-            y[2 * i] = a * t.c[i] - b * t.s[i];
-            y[2 * i + 1] = b * t.c[i] + a * t.s[i];
-        }
+        for (int i = 0; i < 4; ++i)  // (a cos - b sin, b cos + a sin)
+            y[i] = fma2(y[i], make_float2(t.c[i], t.c[i]),
+                        mul2(make_float2(y[i].y, y[i].x), make_float2(-t.s[i], t.s[i])));
         return;
     }
     const int h8 = rot / 16;
-    const bool low = j < h8, turned = j < 2 * h8;
     const int lane = threadIdx.x & 31;
-    const int src = turned ? (low ? lane + h8 : lane - h8) : lane;
+    const int src = j < h8 ? lane + h8 : j < 2 * h8 ? lane - h8 : lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_sync(0xffffffffu, y[i], src);
-        // low half: a cos - b sin; high half: b cos + a sin; beyond: cos 1, sin 0
-        y[i] = fmaf(other, low ? -t.s[i] : t.s[i], y[i] * t.c[i]);
+    for (int i = 0; i < 4; ++i) {
+        const float2 other = make_float2(__shfl_sync(0xffffffffu, y[i].x, src),
+                                         __shfl_sync(0xffffffffu, y[i].y, src));
+        y[i] = fma2(other, make_float2(t.s[2 * i], t.s[2 * i + 1]),
+                    mul2(y[i], make_float2(t.c[2 * i], t.c[2 * i + 1])));
     }
+}
+
+// y * inv * w, and the sum of squares.
+__device__ __forceinline__ void scale8(float2 (&y)[4], float inv, const float2 (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(y[i], make_float2(inv, inv)), w[i]);
+}
+__device__ __forceinline__ float squares8(const float2 (&y)[4]) {
+    float2 s = mul2(y[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = fma2(y[i], y[i], s);
+    return s.x + s.y;
 }
 
 // The slot and the rotation row of a token; false for a token that is skipped
@@ -181,9 +217,9 @@ __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs 
             if (!inside || first + u * per >= heads) continue;
             const long long at = dst + static_cast<long long>(u) * step;
             if (F8) {
-                float y[8];
+                float2 y[4];
                 unpack8(raw[u], y);
-                *reinterpret_cast<uint2 *>(cache + at) = quantize8(y, a.v_scale);
+                *reinterpret_cast<uint2 *>(cache + at) = quantize8(y, a.v_scale, a.v_inv);
             } else {
                 *reinterpret_cast<uint4 *>(cache + 2 * at) = raw[u];
             }
@@ -196,22 +232,18 @@ __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs 
         turn = load_turn(a.cos_sin + static_cast<long long>(position) * a.rot_dim, j, a.rot_dim,
                          INTERLEAVED);
     const __half *w = static_cast<const __half *>(is_q ? a.q_weight : a.k_weight);
-    float wf[8];
+    float2 wf[4];
     if (w && inside) unpack8(*reinterpret_cast<const uint4 *>(w + 8 * j), wf);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float y[8];
+        float2 y[4];
         unpack8(raw[u], y);
         if (w) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+            float sum = squares8(y);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 if (o < width) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            const float inv = rsqrtf(fmaf(sum, a.inv_dim, a.eps));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = y[i] * inv * wf[i];
+            scale8(y, rsqrtf(fmaf(sum, a.inv_dim, a.eps)), wf);
         }
         if (turns) rotate8(y, turn, j, a.rot_dim, INTERLEAVED);
         if (!inside || first + u * per >= heads) continue;
@@ -219,7 +251,7 @@ __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs 
         if (is_q)
             *reinterpret_cast<uint4 *>(static_cast<__half *>(a.q_out) + at) = pack8(y);
         else if (F8)
-            *reinterpret_cast<uint2 *>(cache + at) = quantize8(y, a.k_scale);
+            *reinterpret_cast<uint2 *>(cache + at) = quantize8(y, a.k_scale, a.k_inv);
         else
             *reinterpret_cast<uint4 *>(cache + 2 * at) = pack8(y);
     }
@@ -256,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
                          lane == 0, a.err, &slot, &position))
             return;
         __half *row = static_cast<__half *>(a.cache) + slot * (R + P);
-        float y[8];
+        float2 y[4];
         unpack8(rope, y);
         rotate8(y, load_turn(a.cos_sin + static_cast<long long>(position) * P, lane, P,
                              a.interleaved), lane, P, a.interleaved);
@@ -274,8 +306,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
 #pragma unroll
         for (int i = 0; i < kMaxLatentSteps; ++i) {
             unpack8(raw[i], y);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += y[k] * y[k];
+            sum += squares8(y);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -284,11 +315,10 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
         for (int i = 0; i < kMaxLatentSteps; ++i) {
             const int e = 8 * (lane + 32 * i);
             if (e < R) {
-                float wf[8];
+                float2 wf[4];
                 unpack8(*reinterpret_cast<const uint4 *>(w + e), wf);
                 unpack8(raw[i], y);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = y[k] * inv * wf[k];
+                scale8(y, inv, wf);
                 *reinterpret_cast<uint4 *>(row + e) = pack8(y);
             }
         }
@@ -317,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentApp
     for (int i = 0; i < kHeadSteps; ++i) {
         const int h = first + i * per_step;
         const bool active = h < a.n_q_heads && 8 * j < P;
-        float y[8];
+        float2 y[4];
         unpack8(raw[i], y);
         rotate8(y, turn, j, P, a.interleaved);
         if (active) *reinterpret_cast<uint4 *>(out + h * a.out_head_stride) = pack8(y);
@@ -341,6 +371,9 @@ cudaError_t launch_qk(QkAppendArgs a, cudaStream_t stream) {
     a.kv_jobs = (a.n_kv_heads + per_job - 1) / per_job;
     a.jobs = a.q_jobs + 2 * a.kv_jobs;
     a.inv_dim = 1.f / static_cast<float>(a.head_dim);
+    auto inverse = [](float s) { return s >= 0x1p-60f && s <= 0x1p60f ? 1.f / s : 0.f; };
+    a.k_inv = inverse(a.k_scale);
+    a.v_inv = inverse(a.v_scale);
     const long long threads = static_cast<long long>(a.num_tokens) * a.jobs * 32;
     if (threads > 0xffffffffLL - kThreads) return cudaErrorInvalidValue;
     const unsigned blocks = static_cast<unsigned>((threads + kThreads - 1) / kThreads);

@@ -24,9 +24,9 @@ struct QkAppendArgs {
     float k_scale, v_scale;
     int32_t *err;
     // set by the launcher: lanes per head, warps per token, those for queries and for
-    // keys (or values), 1 / head_dim
+    // keys (or values)
     int width_log2, jobs, q_jobs, kv_jobs;
-    float inv_dim;
+    float inv_dim, k_inv, v_inv;  // 1 / head_dim; 1 / scale, or 0: divide instead
 };
 // cudaErrorInvalidValue: more (token, head) pairs than the grid's 32-bit index.
 cudaError_t launch_qk_append(QkAppendArgs a, bool fp8, cudaStream_t stream);

@@ -153,6 +153,19 @@ def test_e4m3(d, rot):
     assert np.array_equal(v2.cpu().numpy(), vc)
 
 
+@pytest.mark.parametrize("scale", [0.0125, 1.0, 0.3333, 3e-5, 1e-20, 1e30, 5e-39, 117.25])
+def test_e4m3_values_are_the_appends_for_every_fp16(scale):
+    """V is divided by a corrected reciprocal: the codes of all fp16 patterns
+    (infinities and NaN among them) are those of paged_kv_append_fp8."""
+    bits = np.arange(65536, dtype=np.uint16).view(np.float16).reshape(64, 8, 128)
+    v, slots = _t(bits), torch.arange(64, device="cuda")
+    caches = [torch.zeros(4, 8, 16, 128, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    pkv.paged_kv_append_fp8(v, v, slots, caches[0], caches[1], scale, scale)
+    pkv.paged_qk_norm_rope_append_fp8(v, v, v, None, None, 0.0, None, None, slots, caches[2],
+                                      caches[3], scale, scale)
+    assert torch.equal(caches[1], caches[3]) and torch.equal(caches[0], caches[2])
+
+
 def test_padding_and_bad_tokens():
     """Negative slots are skipped; a slot beyond the pool and a position outside
     the table are flagged; the other tokens land, and skipped rows of q_out stay."""
