@@ -99,7 +99,10 @@ int paged_latent_append(const void *kv, int64_t kv_stride, const void *weight, f
  *                 256-byte aligned; needs no zero-fill; calls that overlap in
  *                 time need separate workspaces
  * Logits, softmax and sums in fp32; the softmax weights are rounded to fp16
- * for the product with the values.  A sequence whose tokens, length or rows
+ * for the product with the values.  Rows behind a sequence's length are never
+ * read into a result, whatever they hold; a cached row that is not finite
+ * reaches every query of its sequence in whose last 64-token tile it lies, those
+ * before it included (their weight for it is 0, and 0 times infinity is NaN).  A sequence whose tokens, length or rows
  * are out of bounds sets PKV_ERRBIT_CONTEXT and its rows are left unwritten;
  * a bad block id sets PKV_ERRBIT_BLOCK_ID, and the results of the sequence
  * that names it are unspecified.
@@ -159,7 +162,9 @@ int paged_latent_gather(void *latents, void *ropes, const void *cache,
  *  out            device fp16 [total_q][n_heads][head_dim];  lse_out fp32
  *                 [total_q][n_heads], may be NULL
  *  head_dim       64 or 128;  rope_dim 64
- * Needs no workspace.  Rounding as for paged_latent_attention.
+ * Needs no workspace.  Rounding as for paged_latent_attention, and so with keys
+ * and values that are not finite: rows of other sequences never reach a result,
+ * those of the same sequence may within a tile of 128 queries.
  */
 int latent_prefill_attention(void *out, const void *q, const void *kv, const void *k_rope,
                              const int32_t *q_start, const int32_t *kv_start, int num_seqs,

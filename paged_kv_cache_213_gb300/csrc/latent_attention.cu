@@ -16,8 +16,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
-#include <mutex>
 
 #include "pagedkv_latent.h"
 #include "pkv_internal.h"
@@ -381,10 +381,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             ++k;
             for (int t = p.t0; t < end; ++t, ++g) {
                 const int s = g % C::STAGES;
-                if (lane == 0) ok = ok && poll_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
                 const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                ok = __all_sync(0xffffffffu,
+                                ok && poll_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop));
+                if (!ok) break;
                 if (lane == 0) {
                     if (live > 0)
                         mbar_arrive_expect_tx(&sh.full[s], live * C::GROUP);
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 row = next;
                 next = row_of(t + 2);
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = __all_sync(0xffffffffu, ok);
         } while (ok && next_piece(a, C::ROWS, &w, &p));
         if (!ok && lane == 0) {
             // every copy in flight lands before the CTA gives its memory back
@@ -495,12 +495,12 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const int tok = 16 * quarter + lane / 4, col = C::NG * group + 2 * (lane & 3);
         const Layout lay = layout(sp.records, sp.workers, CL, N, R);
         char *ws = static_cast<char *>(a.workspace);
-        const float scale = a.scale_log2;
+        const float scale = a.scale_log2, unscale = 1.f / scale;
         int g = 0, k = 0;
         bool recorded = false;
         do {
             const int tile_row = p.rt * C::ROWS + rank * N;  // of the sequence's rows
-            float ref[NC][2], sum[NC][2];
+            float ref[NC][2], sum[NC][2], most[NC][2];  // most: scores above it move ref
             int seen[NC][2];  // tokens that the row attends
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     seen[c][e] = p.s.len;
                     if (p.s.n > 1)
                         seen[c][e] = min(p.s.len - p.s.n + (tile_row + 8 * c + col + e) / H + 1, p.s.len);
-                    ref[c][e] = sum[c][e] = 0.f;
+                    ref[c][e] = sum[c][e] = most[c][e] = 0.f;
                 }
             // tiles below this one need no mask
             const int first_masked =
@@ -543,8 +543,8 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 for (int c = 0; c < NC; ++c)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        top[c][e] = fmaxf(x[c][e], x[c][2 + e]) * scale;
-                        move |= top[c][e] - ref[c][e] > kHead + kLag;
+                        top[c][e] = fmaxf(x[c][e], x[c][2 + e]);
+                        move |= top[c][e] > most[c][e];
                     }
                 if (any_softmax<kSoft>(move)) {
                     // new references: the tile's maxima over all tokens
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                         for (int e = 0; e < 2; ++e) {
                             const int n = 8 * c + col + e;
                             const float m = fmaxf(fmaxf(sh.warps[0][n], sh.warps[1][n]),
-                                                  fmaxf(sh.warps[2][n], sh.warps[3][n]));
+                                                  fmaxf(sh.warps[2][n], sh.warps[3][n])) * scale;
                             float next = ref[c][e];
                             if (j == 0)
                                 next = m > -INFINITY ? m - kHead : 0.f;
@@ -573,6 +573,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                             const float f = j == 0 ? 1.f : ex2(ref[c][e] - next);
                             sum[c][e] *= f;
                             ref[c][e] = next;
+                            most[c][e] = (next + kHead + kLag) * unscale;
                             if (quarter == 0 && lane < 4) sh.factor[n] = f;
                         }
                     sync_softmax<kSoft>();
@@ -832,11 +833,8 @@ cudaError_t launch(const LatentAttentionArgs &a, const LatentSplit &sp, cudaStre
         !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E))
         return cudaErrorNotSupported;
     auto kern = latent_attention_kernel<R, N, CL>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [&] {
-        attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    });
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t attr = allow_smem(kern, C::SMEM, done);
     if (attr != cudaSuccess) return attr;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(sp.workers * CL);

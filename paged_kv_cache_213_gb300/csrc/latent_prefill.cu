@@ -5,8 +5,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <cmath>
-#include <mutex>
 
 #include "pagedkv_latent.h"
 #include "pkv_internal.h"
@@ -41,8 +41,9 @@ struct Cfg {
 
 struct Shared {
     uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_done[2], o_free[2];
-    uint64_t full[4], empty[4], asked[2], answered[2], turn[2], drained[2];
-    uint4 answer[2];
+    uint64_t full[4], empty[4], item_full[2], item_free[2], answered, turn[2], drained[2];
+    uint4 answer;   // of the hardware, to the copy role
+    uint4 item[2];  // of the copy role, to the others: a CTA's coordinates, 1; or 0 at the end
     uint32_t tmem;
     int stop;
 };
@@ -79,29 +80,24 @@ __device__ __forceinline__ bool load_item(const LatentPrefillArgs &a, const uint
     return it->total > 0;
 }
 
-// Each role walks the same list of items: its own CTA's, then those that the copy
-// role takes over.
+// The copy role finds the items that have work: its own CTA's, then those of CTAs
+// not launched yet, which it takes over.  It hands them to the other roles through two
+// places; a place is free again when all ten readers have read it.
 struct Items {
-    uint3 cta;
-    int k;  // answers read
+    int k;  // items read
 
     // The next item, or false at the end (or when the kernel gives up).
-    __device__ bool advance(const LatentPrefillArgs &a, Shared &sh, bool whole_warp, bool tell,
-                            Item *it) {
-        do {
-            volatile int *stop = &sh.stop;
-            const int s = k & 1;
-            const bool ok = whole_warp ? warp_wait_or_stop(&sh.answered[s], (k >> 1) & 1, stop)
-                                       : wait_or_stop(&sh.answered[s], (k >> 1) & 1, stop);
-            if (!ok) return false;
-            const bool more = next_cta(&sh.answer[s], &cta);
-            fence_proxy_async_smem();
-            ++k;
-            if (whole_warp) __syncwarp();
-            if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.asked[s]);
-            if (!more) return false;
-        } while (!load_item(a, cta, tell, it));
-        return true;
+    __device__ bool advance(const LatentPrefillArgs &a, Shared &sh, bool whole_warp, Item *it) {
+        volatile int *stop = &sh.stop;
+        const int s = k & 1;
+        const bool ok = whole_warp ? warp_wait_or_stop(&sh.item_full[s], (k >> 1) & 1, stop)
+                                   : wait_or_stop(&sh.item_full[s], (k >> 1) & 1, stop);
+        if (!ok) return false;
+        const uint4 c = sh.item[s];
+        ++k;
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.item_free[s]);
+        return c.w != 0 && load_item(a, make_uint3(c.x, c.y, c.z), false, it);
     }
 };
 
@@ -125,8 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.p_ready[t][1], 4);
             mbar_init(&sh.o_done[t], 1);
             mbar_init(&sh.o_free[t], 4);
-            mbar_init(&sh.asked[t], 11);  // an answer is read by eight warps and three threads
-            mbar_init(&sh.answered[t], 1);
+            mbar_init(&sh.item_full[t], 1);
+            mbar_init(&sh.item_free[t], 10);  // eight warps and two threads
             mbar_init(&sh.drained[t], 1);
             mbar_init(&sh.turn[t], 1);
         }
@@ -134,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.full[s], 1);
             mbar_init(&sh.empty[s], 2);
         }
+        mbar_init(&sh.answered, 1);
         sh.stop = 0;
         fence_barrier_init();
     }
@@ -150,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     allow_dependent_launch();
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
-    Items items{blockIdx, 0};
+    Items items{0};
     Item it;
     // TMEM columns: S of tile t at 128 t (P in its first half), O at 256 + 128 t
 
@@ -164,16 +161,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Steps count on over the items.
             int f = 0;
             int q[2] = {0, 0};  // query tiles so far
-            int asks = 0;
-            bool ok = true;
+            bool ok = true, open = true;  // open: the hardware may have more CTAs
+            int answers = 0, handed = 0;
             Item last;        // whose final values are still to come
-            auto ask = [&] {  // for the item after the one at hand
-                const int s = asks & 1;
-                ok = ok && wait_or_stop(&sh.asked[s], ((asks >> 1) & 1) ^ 1, stop);
-                if (!ok) return;
-                mbar_arrive_expect_tx(&sh.answered[s], 16);
-                ask_next_cta(&sh.answer[s], &sh.answered[s]);
-                ++asks;
+            auto ask = [&] {  // for the CTA after the one at hand
+                mbar_arrive_expect_tx(&sh.answered, 16);
+                ask_next_cta(&sh.answer, &sh.answered);
+            };
+            uint3 cta = blockIdx;
+            // hands on the item of `cta`, or of the first CTA after it that has one;
+            // the next answer is then under way
+            auto hand_on = [&] {
+                bool have = load_item(a, cta, true, &it);
+                while (ok && !have && open) {
+                    ok = wait_or_stop(&sh.answered, answers & 1, stop);
+                    if (!ok) break;
+                    ++answers;
+                    open = next_cta(&sh.answer, &cta);
+                    fence_proxy_async_smem();
+                    if (open) {
+                        ask();
+                        have = load_item(a, cta, true, &it);
+                    }
+                }
+                const int s = handed & 1;
+                ok = ok && wait_or_stop(&sh.item_free[s], ((handed >> 1) & 1) ^ 1, stop);
+                if (!ok) return false;
+                sh.item[s] = make_uint4(cta.x, cta.y, cta.z, have ? 1 : 0);
+                mbar_arrive(&sh.item_full[s]);
+                ++handed;
+                return have;
             };
             // the next pair: values of vi at step vj, keys of ki at step kj (either null)
             auto copy_pair = [&](const Item *vi, int vj, const Item *ki, int kj) {
@@ -198,52 +215,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++f;
             };
             ask();
-            bool have = load_item(a, items.cta, false, &it);
-            while (ok) {
-                if (have) {
+            bool have = hand_on();
+            while (ok && have) {
 #pragma unroll 1
-                    for (int j = 0; j < it.total && ok; ++j) {
-                        copy_pair(j > 0 ? &it : f > 0 ? &last : nullptr, j > 0 ? j - 1 : last.total - 1,
-                                  &it, j);
-                        if (j == 0)
+                for (int j = 0; j < it.total && ok; ++j) {
+                    copy_pair(j > 0 ? &it : f > 0 ? &last : nullptr, j > 0 ? j - 1 : last.total - 1,
+                              &it, j);
+                    if (j == 0)
 #pragma unroll 1
-                            for (int t = 0; t < 2 && ok; ++t)
-                                if (it.steps[t] > 0) {
-                                    ok = wait_or_stop(&sh.q_empty[t], (q[t] & 1) ^ 1, stop);
-                                    if (!ok) break;
-                                    ++q[t];
-                                    mbar_arrive_expect_tx(&sh.q_full[t], C::KP * kQPlane);
-                                    for (int p = 0; p < C::KP; ++p)
-                                        tma_load_3d(base + (t * C::KP + p) * kQPlane, &mq, 64 * p,
-                                                    it.h, it.q0 + (2 * it.pair + t) * kRows,
-                                                    &sh.q_full[t]);
-                                }
-                    }
-                    last = it;
+                        for (int t = 0; t < 2 && ok; ++t)
+                            if (it.steps[t] > 0) {
+                                ok = wait_or_stop(&sh.q_empty[t], (q[t] & 1) ^ 1, stop);
+                                if (!ok) break;
+                                ++q[t];
+                                mbar_arrive_expect_tx(&sh.q_full[t], C::KP * kQPlane);
+                                for (int p = 0; p < C::KP; ++p)
+                                    tma_load_3d(base + (t * C::KP + p) * kQPlane, &mq, 64 * p,
+                                                it.h, it.q0 + (2 * it.pair + t) * kRows,
+                                                &sh.q_full[t]);
+                            }
                 }
-                // the answer asked for one item ago; ask again while it says yes
-                const int s = items.k & 1;
-                ok = ok && wait_or_stop(&sh.answered[s], (items.k >> 1) & 1, stop);
                 if (!ok) break;
-                const bool more = next_cta(&sh.answer[s], &items.cta);
-                fence_proxy_async_smem();
-                mbar_arrive(&sh.asked[s]);
-                ++items.k;
-                if (!more) {
-                    if (f > 0) copy_pair(&last, last.total - 1, nullptr, 0);
-                    break;
+                last = it;
+                if (open) {
+                    // the answer asked for while this item's copies were issued
+                    ok = wait_or_stop(&sh.answered, answers & 1, stop);
+                    if (!ok) break;
+                    ++answers;
+                    open = next_cta(&sh.answer, &cta);
+                    fence_proxy_async_smem();
+                    if (open) ask();
                 }
-                ask();
-                have = load_item(a, items.cta, false, &it);
+                if (open) {
+                    have = hand_on();
+                } else {
+                    have = false;
+                    const int s = handed & 1;
+                    ok = wait_or_stop(&sh.item_free[s], ((handed >> 1) & 1) ^ 1, stop);
+                    if (!ok) break;
+                    sh.item[s] = make_uint4(0, 0, 0, 0);
+                    mbar_arrive(&sh.item_full[s]);
+                    ++handed;
+                }
             }
+            if (ok && f > 0) copy_pair(&last, last.total - 1, nullptr, 0);
             if (!ok) {
                 // every copy in flight lands before the CTA gives its memory back
                 for (int t = 0; t < 2; ++t)
                     if (q[t] > 0) mbar_wait_bounded(&sh.q_full[t], (q[t] - 1) & 1);
                 for (int i = max(0, f - C::STAGES); i < f; ++i)
                     mbar_wait_bounded(&sh.full[i % C::STAGES], (i / C::STAGES) & 1);
-                if (asks > items.k)
-                    mbar_wait_bounded(&sh.answered[(asks - 1) & 1], ((asks - 1) >> 1) & 1);
+                if (open) mbar_wait_bounded(&sh.answered, answers & 1);
             }
         }
     } else if (warp < 11) {
@@ -264,15 +286,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             int sc = 0, qc = 0;  // this tile's steps and items
             int turns = 0;
             bool ok = true;
-            bool more = load_item(a, items.cta, false, &it) ||
-                        items.advance(a, sh, false, false, &it);
+            bool more = items.advance(a, sh, false, &it);
             int steps = 0, total = 0;  // of the item at hand
             int j = -1;  // its step whose weights come next; -1: only the first scores
             while (ok) {
                 // between the softmax of step j and that of the step after it, which is
                 // step j + 1 of the item or the first of the next one
                 const bool end = j + 1 == total;
-                if (end && j >= 0) more = items.advance(a, sh, false, false, &it);
+                if (end && j >= 0) more = items.advance(a, sh, false, &it);
                 if (j < 0 && !more) break;
                 const int pair = j < 0 ? f : f + 1;  // of copies; also the step of its keys
                 ok = wait_or_stop(&sh.full[pair % C::STAGES], (pair / C::STAGES) & 1, stop);
@@ -342,8 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
         const float scale = a.scale_log2;
         int f = 0, sc = 0, mine = 0;  // key steps, this tile's, and its items so far
-        bool have = load_item(a, items.cta, threadIdx.x == 0, &it) ||
-                    items.advance(a, sh, true, threadIdx.x == 0, &it);
+        bool have = items.advance(a, sh, true, &it);
         bool ok = true;
         while (have) {
             const int i = (2 * it.pair + t) * kRows + (threadIdx.x & 127);
@@ -468,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (a.lse_out && i < it.n) a.lse_out[row] = (r + log2f(l)) * 0.69314718055994531f;
             }
             f += it.total;
-            have = items.advance(a, sh, true, threadIdx.x == 0, &it);
+            have = items.advance(a, sh, true, &it);
         }
     }
     tc_fence_before();
@@ -509,11 +529,8 @@ cudaError_t launch(const LatentPrefillArgs &a, cudaStream_t stream) {
         !make_map(&mr, a.k_rope, 2, dr, sr, br))
         return cudaErrorNotSupported;
     auto kern = latent_prefill_kernel<D>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [&] {
-        attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    });
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t attr = allow_smem(kern, C::SMEM, done);
     if (attr != cudaSuccess) return attr;
     const dim3 grid((a.max_q_len + 2 * kRows - 1) / (2 * kRows), a.n_heads, a.num_seqs);
     return launch_pdl(kern, grid, dim3(kThreads), C::SMEM, stream, a, mq, mkv, mr);

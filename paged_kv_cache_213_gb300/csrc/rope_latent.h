@@ -2,11 +2,26 @@
 // latent attention kernels (rope_append.cu, latent_*.cu).  Not public.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
 
 namespace pkv {
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device, once a
+// device (`done`: a bit per device, one variable a kernel).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t a = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (a == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return a;
+}
 
 struct QkAppendArgs {
     void *q_out;

@@ -123,7 +123,7 @@ def _check(p, q, qs, scale, nq, what, got=None, skip=()):
 
 @pytest.mark.parametrize("R", [256, 512])
 @pytest.mark.parametrize("bs", [16, 64, 256])
-@pytest.mark.parametrize("H", [1, 5, 16, 40, 128])
+@pytest.mark.parametrize("H", [1, 5, 16, 20, 40, 72, 128])
 def test_decode(H, bs, R):
     lens = [1, 15, 16, 17, 63, 64, 65, 127, 200, 129]
     p, q, qs, scale = _problem(lens, [1] * len(lens), H, R, bs, H + bs + R)
@@ -154,18 +154,20 @@ def test_many_and_few_sequences(B):
     _check(p, q, qs, scale, [1] * B, "batch")
 
 
-@pytest.mark.parametrize("spread", [0.0, 60.0])
+@pytest.mark.parametrize("spread", [0.0, 60.0, -1.7, -40.0])
 def test_flat_and_peaked_weights(spread):
-    """All weights equal (scale 0), and one weight near 1 with logits far apart."""
+    """All weights equal (scale 0), one weight near 1 with logits far apart, and
+    negative scales."""
     lens = [300, 77, 1, 129]
     p, q, qs, scale = _problem(lens, [1] * 4, 16, 512, 16, 70, spread)
     _check(p, q, qs, scale, [1] * 4, "peaked")
 
 
-def test_rising_logits():
+@pytest.mark.parametrize("H", [16, 32, 64, 128])
+def test_rising_logits(H):
     """Keys that grow along the sequence: the running maximum moves in every tile."""
     lens = [900]
-    p, q, qs, scale = _problem(lens, [1], 16, 512, 16, 71)
+    p, q, qs, scale = _problem(lens, [1], H, 512, 16, 71)
     grow = np.linspace(0.01, 3.0, 900)[:, None]
     sign = np.sign(q[0, 0].astype(np.float64))
     p.rows[0] = (grow * sign * np.abs(p.rows[0])).astype(np.float16)
@@ -237,6 +239,69 @@ def test_repeated_calls_are_bit_identical_and_graph_replay():
     p.rows = [x[:n] for x, n in zip(p.rows, short)]
     p.lens = short
     _check(p, q, qs, scale, [1] * 4, "replayed", (out.cpu().numpy(), lse.cpu().numpy(), 0))
+
+
+def test_two_streams_at_once_and_other_than_the_inputs():
+    """Two calls in flight on two streams, each with its own workspace, on tensors
+    that a third stream made."""
+    a = _problem([3000, 40], [1, 1], 16, 512, 16, 95)
+    b = _problem([2000, 900], [1, 1], 128, 512, 64, 96)
+    outs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    made = []
+    for p, q, qs, scale in (a, b):
+        made.append([_t(x) for x in (q, p.cache, p.tables, p.lens.astype(np.int32))])
+    torch.cuda.synchronize()
+    for rep in range(3):
+        outs = []
+        for (p, q, qs, scale), t, s in zip((a, b), made, streams):
+            with torch.cuda.stream(s):
+                lse = torch.empty(q.shape[:2], device="cuda")
+                outs.append((pkv.paged_latent_attention(*t, scale, 512, lse=lse), lse))
+    torch.cuda.synchronize()
+    for (p, q, qs, scale), (o, l) in zip((a, b), outs):
+        _check(p, q, qs, scale, [1, 1], "streams", (o.cpu().numpy(), l.cpu().numpy(), 0))
+
+
+def test_shared_blocks_and_one_block_twice():
+    """Two sequences that share leading blocks, and one whose table names a block
+    twice."""
+    p, q, qs, scale = _problem([64, 50, 48], [1, 1, 1], 16, 512, 16, 97)
+    p.tables[1, :2] = p.tables[0, :2]
+    p.rows[1] = np.concatenate([p.rows[0][:32], p.rows[1][32:]])
+    p.tables[2, 1] = p.tables[2, 0]
+    p.rows[2] = np.concatenate([p.rows[2][:16], p.rows[2][:16], p.rows[2][32:]])
+    _check(p, q, qs, scale, [1, 1, 1], "shared")
+
+
+def test_caches_beyond_32_bit_offsets():
+    """A pool of more than 2^32 bytes and 2^31 values: append, gather and attention on
+    its last blocks."""
+    R, P, bs, NB = 512, 64, 64, 60000
+    E = R + P
+    assert NB * bs * E > 2 ** 31
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    cache = torch.empty(NB, bs, E, dtype=torch.float16, device="cuda")
+    n, H = 130, 16
+    rng = np.random.default_rng(12)
+    rows = rng.standard_normal((n, E)).astype(np.float16)
+    bt = torch.tensor([[NB - 1, 0, NB - 2]], dtype=torch.int32, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    slots = bt[0, pos.long() // bs].long() * bs + pos.long() % bs
+    cs = torch.cat([torch.ones(200, 32), torch.zeros(200, 32)], 1).cuda()   # no turn
+    err = _err()
+    pkv.paged_latent_append(_t(rows), None, EPS, cs, pos, slots, cache, err_word=err)
+    st = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    lat, rop = pkv.paged_latent_gather(cache, bt, st, n, R, err_word=err)
+    assert np.array_equal(lat.cpu().numpy(), rows[:, :R])
+    assert np.array_equal(rop.cpu().numpy(), rows[:, R:])
+    q = rng.standard_normal((1, H, E)).astype(np.float16)
+    lse = torch.empty(1, H, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = pkv.paged_latent_attention(_t(q), cache, bt, lens, 0.07, R, lse=lse, err_word=err)
+    assert pkv.get_error(err) == 0
+    ref = attend64(q, rows, rows[:, :R], [n], 0.07)
+    assert_attention(out.cpu().numpy(), lse.cpu().numpy(), *ref, "far blocks")
 
 
 # --- gather --------------------------------------------------------------------
@@ -321,11 +386,55 @@ def test_prefill(nq, nk, H, d):
     _check_prefill(q, kv, kr, qs, ks, scale, got, "prefill")
 
 
-@pytest.mark.parametrize("factor", [0.0, 20.0])
+@pytest.mark.parametrize("factor", [0.0, 20.0, -1.0, -20.0])
 def test_prefill_flat_and_peaked(factor):
     q, kv, kr, qs, ks = _prefill_problem([300, 40], [300, 200], 2, 128, 5)
     scale = factor / np.sqrt(192)
     _check_prefill(q, kv, kr, qs, ks, scale, _prefill(q, kv, kr, qs, ks, scale, 300, 300), "peaked")
+
+
+def test_prefill_rising_logits():
+    """Keys that grow along the sequence: O follows the reference in every step."""
+    q, kv, kr, qs, ks = _prefill_problem([700], [700], 2, 128, 8)
+    grow = np.linspace(0.01, 4.0, 700)[:, None, None]
+    sign = np.sign(q[600, :, :128].astype(np.float64))
+    kv[..., :128] = (grow * sign * np.abs(kv[..., :128].astype(np.float64))).astype(np.float16)
+    _check_prefill(q, kv, kr, qs, ks, 0.07, _prefill(q, kv, kr, qs, ks, 0.07, 700, 700), "rising")
+
+
+def test_prefill_many_items():
+    """More work than CTAs: each takes over several (sequence, head, rows) items,
+    some of them empty."""
+    nq = [300, 0, 17, 513, 1, 256]
+    nk = [300, 9, 17, 600, 700, 300]
+    q, kv, kr, qs, ks = _prefill_problem(nq, nk, 61, 64, 9)
+    got = _prefill(q, kv, kr, qs, ks, 0.09, 1024, 1024)
+    assert got[2] == 0
+    _check_prefill(q, kv, kr, qs, ks, 0.09, got, "many items")
+
+
+def test_prefill_captured_and_replayed():
+    """Captured with the largest lengths as bounds, replayed on shorter ones, after a
+    kernel on the same stream that writes its inputs."""
+    q, kv, kr, qs, ks = _prefill_problem([200, 130], [260, 130], 3, 128, 10)
+    dev = [_t(x) for x in (q, kv, kr, qs, ks)]
+    src = dev[0].clone()
+    out = torch.zeros(330, 3, 128, dtype=torch.float16, device="cuda")
+    lse = torch.zeros(330, 3, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dev[0].copy_(src)
+        pkv.latent_prefill_attention(*dev, 0.07, 330, 390, out=out, lse=lse)
+    dev[0].zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    _check_prefill(q, kv, kr, qs, ks, 0.07, (out.cpu().numpy(), lse.cpu().numpy(), 0), "replay")
+    qs2, ks2 = np.array([0, 30, 330], np.int32), np.array([0, 30, 390], np.int32)
+    dev[3].copy_(_t(qs2))
+    dev[4].copy_(_t(ks2))
+    g.replay()
+    torch.cuda.synchronize()
+    _check_prefill(q, kv, kr, qs2, ks2, 0.07, (out.cpu().numpy(), lse.cpu().numpy(), 0), "replay 2")
 
 
 def test_prefill_neighbours_do_not_leak():
