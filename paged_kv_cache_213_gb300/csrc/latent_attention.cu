@@ -120,13 +120,13 @@ struct Split {
 struct Piece {
     Seq s;
     int b, rt, t0, tiles;
-    int seg_tiles, seg_first;  // tiles of the whole segment, and its first unit
+    int seg, seg_tiles, seg_first;  // the segment's number, tiles and first unit
 };
 
 // A place in the list of units: `left` units from `skip` units behind the start of
-// row tile rt of sequence b, which is at `unit`.
+// row tile rt of sequence b, segment `seg` of the batch, which is at `unit`.
 struct Walk {
-    int b, rt, skip, left, unit;
+    int b, rt, skip, left, unit, seg;
 };
 
 // The piece of sequence w->b (which is s) that w stands at, if there is one.
@@ -137,13 +137,15 @@ __device__ __forceinline__ bool piece_of(const Seq &s, int heads, int rows, Walk
         if (w->skip >= tiles) {
             w->skip -= tiles;
             w->unit += tiles;
+            ++w->seg;
             continue;
         }
         const int take = min(tiles - w->skip, w->left);
-        *p = Piece{s, w->b, w->rt, w->skip, take, tiles, w->unit};
+        *p = Piece{s, w->b, w->rt, w->skip, take, w->seg, tiles, w->unit};
         w->left -= take;
         w->skip = 0;
         w->unit += tiles;
+        ++w->seg;
         ++w->rt;
         return true;
     }
@@ -185,7 +187,7 @@ struct Shared {
     Split split;
     Walk walk;    // behind the first piece
     Piece first;
-    int sums[16];
+    int2 sums[16];
     float warps[4][64];  // per row, of each softmax warp of its group: a tile's maxima, a piece's sums
     float factor[64];    // what O^T's columns are multiplied with
     float ref[64];
@@ -281,46 +283,58 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const int per = (a.num_seqs + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * per, a.num_seqs);
         const int b1 = min(b0 + per, a.num_seqs);
-        int mine = 0;
+        int2 mine = make_int2(0, 0);  // units, segments
         Seq seq;  // the thread's only sequence, where it has one
         for (int b = b0; b < b1; ++b) {
-            const bool good = load_seq(a, b, &seq);
-            const int u = good ? seq_units(seq, a.n_q_heads, C::ROWS) : 0;
-            mine += u;
-            if (blockIdx.x == 0 && !good) flag_error(a.err, PKV_ERRBIT_CONTEXT);
-            if (blockIdx.x == 0 && u == 0 && sp.by_segment)
-                for (int i = 0; i < sp.row_tiles * CL; ++i)
-                    records[b * sp.row_tiles * CL + i] = make_int4(0, 0, 0, 0);
+            if (load_seq(a, b, &seq)) {
+                mine.x += seq_units(seq, a.n_q_heads, C::ROWS);
+                mine.y += row_tiles(seq.n, a.n_q_heads, C::ROWS);
+            } else if (blockIdx.x == 0) {
+                flag_error(a.err, PKV_ERRBIT_CONTEXT);
+            }
         }
         // inclusive scan: within the warp by shuffles, over the warps in shared memory
-        int acc = mine;
+        int2 acc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, acc, o);
-            if (lane >= o) acc += v;
+            const int x = __shfl_up_sync(0xffffffffu, acc.x, o), y = __shfl_up_sync(0xffffffffu, acc.y, o);
+            if (lane >= o) {
+                acc.x += x;
+                acc.y += y;
+            }
         }
         if (lane == 31) sh.sums[warp] = acc;
         __syncthreads();
-        int before = acc - mine, total = 0;
+        int before = acc.x - mine.x, total = 0, seg = acc.y - mine.y, segs = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sh.sums[w];
-            total += sh.sums[w];
+            const int2 v = sh.sums[w];
+            if (w < warp) {
+                before += v.x;
+                seg += v.y;
+            }
+            total += v.x;
+            segs += v.y;
         }
+        if (blockIdx.x == 0 && sp.by_segment)  // places that no segment has
+            for (int i = segs * CL + threadIdx.x; i < sp.records * CL; i += kThreads)
+                records[i] = make_int4(0, 0, 0, 0);
         const int workers = min(total, sp.workers);
         if (worker < workers) {
             const Split split{total / workers, total % workers};
             const int first = split.first(worker);
-            if (before <= first && first < before + mine) {
+            if (before <= first && first < before + mine.x) {
                 int b = b0, at = before;
                 if (per > 1)
                     for (;; ++b) {
-                        const int u = load_seq(a, b, &seq) ? seq_units(seq, a.n_q_heads, C::ROWS) : 0;
+                        if (!load_seq(a, b, &seq)) continue;
+                        const int u = seq_units(seq, a.n_q_heads, C::ROWS);
                         if (first < at + u) break;
                         at += u;
+                        seg += row_tiles(seq.n, a.n_q_heads, C::ROWS);
                     }
                 // the first piece, for all roles at once
-                Walk w{b, 0, first - at, split.first(worker + 1) - first, at};
+                Walk w{b, 0, first - at, split.first(worker + 1) - first, at, seg};
                 Piece p;
                 piece_of(seq, a.n_q_heads, C::ROWS, &w, &p);
                 sh.split = split;
@@ -700,7 +714,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             if (p.t0 == 0) {
                 // the worker that starts a segment says where its last piece is
                 if (threadIdx.x == 0 && (!whole || sp.by_segment)) {
-                    const int at = sp.by_segment ? p.b * sp.row_tiles + p.rt : worker;
+                    const int at = sp.by_segment ? p.seg : worker;
                     const int last = whole ? worker : sh.split.worker_of(p.seg_first + p.seg_tiles - 1);
                     records[at * CL + rank] = make_int4(row0, whole ? 0 : max(rows, 0), worker, last);
                 }
@@ -720,20 +734,21 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
 }
 
 // The pieces of each cut segment, joined.  A unit is four rows of one column (one
-// 16-byte load a piece); a block has 256 / G neighbouring columns of four rows and G
-// threads a unit, each for every G-th piece.
+// 16-byte load a piece).  A block has 256 / G * U neighbouring columns of four rows,
+// U a thread, and G threads for each of them, which take every G-th piece.
 constexpr int kJoinThreads = 256;
 
-template <int R, int N, int CL>
+template <int R, int N, int CL, int U>
 __global__ void __launch_bounds__(kJoinThreads, 4)
     latent_join_kernel(const LatentAttentionArgs a, const LatentSplit sp) {
     __shared__ float parts[kJoinThreads / 32][4];
-    __shared__ float4 sums[kJoinThreads];
+    __shared__ float4 sums[U][kJoinThreads];
     grid_dependency_wait();
     allow_dependent_launch();
     const int4 rec = static_cast<const int4 *>(a.workspace)[blockIdx.x];
     const int G = sp.join_threads, units = kJoinThreads / G;
-    const int n0 = static_cast<int>(blockIdx.y) * units / R * 4;  // the block's rows
+    const int at0 = static_cast<int>(blockIdx.y) * units * U;  // the block's first unit
+    const int n0 = at0 / R * 4;  // the block's rows
     if (n0 >= rec.y) return;
     const Layout lay = layout(sp.records, sp.workers, CL, N, R);
     const char *ws = static_cast<const char *>(a.workspace);
@@ -743,8 +758,11 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     auto slot = [&](int k) { return static_cast<size_t>((2 * (rec.z + k) + (k == 0 ? 1 : 0)) * CL + rank); };
     // this block's first loads of partial sums need nothing of the rows' statistics
     const int u = threadIdx.x % units, i = threadIdx.x / units;
-    const size_t at = static_cast<size_t>(blockIdx.y) * units + u;
-    const float4 first = i < pieces ? acc[slot(i) * (N / 4 * R) + at] : make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 first[U];
+#pragma unroll
+    for (int c = 0; c < U; ++c)
+        first[c] = i < pieces ? acc[slot(i) * (N / 4 * R) + at0 + c * units + u]
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
     // the rows' references and sums over all pieces: thread x takes row x % 4 of every
     // 64th piece
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -779,38 +797,53 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
         for (int x = 0; x < kJoinThreads / 32; ++x) t += warp_l[x][e] * ex2(parts[x][e] - r);
         ref[e] = r;
         inv[e] = t == 0.f ? 0.f : 1.f / t;
-        if (a.lse_out && static_cast<int>(blockIdx.y) * units % R == 0 && threadIdx.x == e && n0 + e < rec.y)
+        if (a.lse_out && at0 % R == 0 && threadIdx.x == e && n0 + e < rec.y)
             a.lse_out[rec.x + n0 + e] = t == 0.f ? -INFINITY : (r + log2f(t)) * 0.69314718055994531f;
     }
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    float4 s[U];
+#pragma unroll
+    for (int c = 0; c < U; ++c) s[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(U > 1 ? 1 : 4)
     for (int k = i; k < pieces; k += G) {
         const size_t sl = slot(k);
-        const float4 v = k == i ? first : acc[sl * (N / 4 * R) + at];
+        float4 v[U];
+#pragma unroll
+        for (int c = 0; c < U; ++c) v[c] = k == i ? first[c] : acc[sl * (N / 4 * R) + at0 + c * units + u];
         const float4 ma = *reinterpret_cast<const float4 *>(ml + sl * N);
         const float4 mb = *reinterpret_cast<const float4 *>(ml + sl * N + 2);
-        s.x = fmaf(v.x, ex2(ma.x - ref[0]), s.x);
-        s.y = fmaf(v.y, ex2(ma.z - ref[1]), s.y);
-        s.z = fmaf(v.z, ex2(mb.x - ref[2]), s.z);
-        s.w = fmaf(v.w, ex2(mb.z - ref[3]), s.w);
-    }
-    if (G > 1) {
-        sums[threadIdx.x] = s;
-        __syncthreads();
-        if (i > 0) return;
-        for (int k = 1; k < G; ++k) {
-            const float4 v = sums[k * units + u];
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
+        const float f0 = ex2(ma.x - ref[0]), f1 = ex2(ma.z - ref[1]);
+        const float f2 = ex2(mb.x - ref[2]), f3 = ex2(mb.z - ref[3]);
+#pragma unroll
+        for (int c = 0; c < U; ++c) {
+            s[c].x = fmaf(v[c].x, f0, s[c].x);
+            s[c].y = fmaf(v[c].y, f1, s[c].y);
+            s[c].z = fmaf(v[c].z, f2, s[c].z);
+            s[c].w = fmaf(v[c].w, f3, s[c].w);
         }
     }
-    __half *out = static_cast<__half *>(a.out) + (static_cast<long long>(rec.x) + n0) * R + at % R;
-    const float y[4] = {s.x * inv[0], s.y * inv[1], s.z * inv[2], s.w * inv[3]};
+    if (G > 1) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (n0 + e < rec.y) out[e * R] = __float2half_rn(y[e]);
+        for (int c = 0; c < U; ++c) sums[c][threadIdx.x] = s[c];
+        __syncthreads();
+        if (i > 0) return;
+#pragma unroll
+        for (int c = 0; c < U; ++c)
+            for (int k = 1; k < G; ++k) {
+                const float4 v = sums[c][k * units + u];
+                s[c].x += v.x;
+                s[c].y += v.y;
+                s[c].z += v.z;
+                s[c].w += v.w;
+            }
+    }
+    __half *out = static_cast<__half *>(a.out) + (static_cast<long long>(rec.x) + n0) * R + at0 % R + u;
+#pragma unroll
+    for (int c = 0; c < U; ++c) {
+        const float y[4] = {s[c].x * inv[0], s[c].y * inv[1], s[c].z * inv[2], s[c].w * inv[3]};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n0 + e < rec.y) out[e * R + c * units] = __float2half_rn(y[e]);
+    }
 }
 
 // Rows of `width` fp16 values as [width / 64 planes][rows][64 columns]: a box is 8
@@ -851,8 +884,10 @@ cudaError_t launch(const LatentAttentionArgs &a, const LatentSplit &sp, cudaStre
     cfg.numAttrs = CL > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, sp, mq, mc);
     if (e != cudaSuccess) return e;
-    const dim3 grid(sp.records * CL, R * N / 4 * sp.join_threads / kJoinThreads);
-    return launch_pdl(latent_join_kernel<R, N, CL>, grid, dim3(kJoinThreads), 0, stream, a, sp);
+    // more columns a thread where the rows are many: fewer, longer blocks
+    constexpr int U = N == 64 ? R / 256 : 1;
+    const dim3 grid(sp.records * CL, R * N / 4 * sp.join_threads / (kJoinThreads * U));
+    return launch_pdl(latent_join_kernel<R, N, CL, U>, grid, dim3(kJoinThreads), 0, stream, a, sp);
 }
 
 }  // namespace
@@ -866,11 +901,9 @@ bool latent_split(int num_seqs, int max_q_len, int heads, int latent_dim, int ma
     const long long tiles = (rows + tile - 1) / tile;
     const long long units = tiles * num_seqs * (max_len / kTile + 1);
     if (units >= (1LL << 31)) return false;
-    sp->row_tiles = static_cast<int>(tiles);
     sp->workers = sms / sp->cluster;
-    // one token a sequence: every sequence has the same row tiles, and its
-    // segments have fixed places; otherwise a worker records what it starts
-    sp->by_segment = max_q_len == 1 && tiles * num_seqs <= sp->workers;
+    // few segments: a record each; more than workers: one for what each worker starts
+    sp->by_segment = tiles * num_seqs <= sp->workers;
     sp->records = sp->by_segment ? static_cast<int>(tiles * num_seqs) : sp->workers;
     // threads of the join over a segment's pieces: about workers / segments of them
     const long long pieces = sp->workers / (tiles * num_seqs > 0 ? tiles * num_seqs : 1);

@@ -98,8 +98,7 @@ struct LatentAttentionArgs {
 // query rows each, one CTA per SM.
 struct LatentSplit {
     int rows, cluster, workers;
-    int row_tiles;   // of a sequence of max_q_len tokens
-    int by_segment;  // the join's records: one per (sequence, row tile), else one per worker
+    int by_segment;  // the join's records: one per segment (sequence and row tile), else one per worker
     int records;
     int join_threads;
     size_t ws_bytes;
