@@ -380,9 +380,11 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), 8 * C::E * 2);
             };
             int row = row_of(p.t0), next = row_of(p.t0 + 1);
-            int far[kAhead - 1];  // what only the copies into L2 take at the start
+            // rows are looked up an iteration before they are used: a lookup takes as
+            // long as half a tile
+            int far[kAhead];  // for the copies into L2: tiles t + 2 .. t + 1 + kAhead
 #pragma unroll
-            for (int d = 0; d < kAhead - 1; ++d) far[d] = row_of(p.t0 + 2 + d);
+            for (int d = 0; d < kAhead; ++d) far[d] = row_of(p.t0 + 2 + d);
             if (lane == 0) {
                 ok = wait_or_stop(&sh.q_empty, (k & 1) ^ 1, stop);
                 if (ok) {
@@ -416,12 +418,14 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 if (t == p.t0) {
                     to_l2(next);
 #pragma unroll
-                    for (int d = 0; d < kAhead - 1; ++d) to_l2(far[d]);
-                } else {
-                    to_l2(row_of(t + kAhead));
+                    for (int d = 0; d < kAhead - 2; ++d) to_l2(far[d]);
                 }
+                to_l2(far[kAhead - 2]);
                 row = next;
-                next = row_of(t + 2);
+                next = far[0];
+#pragma unroll
+                for (int d = 0; d < kAhead - 1; ++d) far[d] = far[d + 1];
+                far[kAhead - 1] = row_of(t + 2 + kAhead);
             }
             ok = __all_sync(0xffffffffu, ok);
         } while (ok && next_piece(a, C::ROWS, &w, &p));
