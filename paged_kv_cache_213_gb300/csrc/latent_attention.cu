@@ -46,6 +46,15 @@ struct Cfg {
     // (1024 bytes each) together, so one copy brings 8 whole rows
     static constexpr int GROUP = PL * 1024;
     static constexpr int STAGE = kTile / 8 * GROUP;
+    // A tile comes and goes in parts of PP planes, each with barriers of its own: the
+    // scores start on the first part while the others are on their way, and the next
+    // tile's first part follows once the products that read this one's are done.
+    static constexpr int PARTS = PL % 3 == 0 ? 3 : 1, PP = PL / PARTS, PART = PP * 1024;
+    // the last of the VT output tiles that reads a part (tile v reads planes 2 v and
+    // 2 v + 1; the last part holds P^T too)
+    static constexpr int last_reader(int part) {
+        return part == PARTS - 1 ? VT - 1 : ((part + 1) * PP - 1) / 2;
+    }
     static constexpr int STAGES = R == 512 ? 2 : 4;
     static constexpr int Q_BYTES = N / 8 * GROUP;
     // P^T takes the place of the tile's last plane (the rotated key part), which
@@ -181,7 +190,7 @@ __host__ __device__ inline Layout layout(int records, int workers, int cl, int r
 }
 
 struct Shared {
-    uint64_t full[4], empty[4], s_full[2], p_ready[2], pv_done, q_full, q_empty, o_full, o_free, drained[2];
+    uint64_t full[4][3], empty[4][3], s_full[2], p_ready[2], pv_done, q_full, q_empty, o_full, o_free, drained[2];
     uint32_t tmem;
     int stop;
     Split split;
@@ -239,8 +248,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(&sh.full[s], 1);
-            mbar_init(&sh.empty[s], CL);
+            for (int x = 0; x < C::PARTS; ++x) {
+                mbar_init(&sh.full[s][x], 1);
+                mbar_init(&sh.empty[s][x], CL);
+            }
         }
         mbar_init(&sh.s_full[0], 1);
         mbar_init(&sh.s_full[1], 1);
@@ -361,6 +372,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const char *cache = static_cast<const char *>(a.cache);
         const int block_log2 = 31 - __clz(a.block_size);
         int g = 0, k = 0;  // tiles, pieces so far
+        int begun = 0;     // parts of tiles so far
         bool ok = true;
         do {
             const int32_t *table = a.block_tables + static_cast<long long>(p.b) * a.max_blocks_per_seq;
@@ -398,23 +410,29 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             for (int t = p.t0; t < end; ++t, ++g) {
                 const int s = g % C::STAGES;
                 const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
-                ok = __all_sync(0xffffffffu,
-                                ok && poll_or_stop(&sh.empty[s], ((g / C::STAGES) & 1) ^ 1, stop));
+#pragma unroll 1
+                for (int x = 0; x < C::PARTS; ++x) {
+                    ok = __all_sync(0xffffffffu, ok && poll_or_stop(&sh.empty[s][x],
+                                                                    ((g / C::STAGES) & 1) ^ 1, stop));
+                    if (!ok) break;
+                    uint64_t *full = &sh.full[s][x];
+                    if (lane == 0) {
+                        if (live > 0)
+                            mbar_arrive_expect_tx(full, live * C::PART);
+                        else
+                            mbar_arrive(full);
+                    }
+                    __syncwarp();
+                    if (mine && row >= 0) {
+                        unsigned char *dst = base + s * C::STAGE + lane * C::GROUP + x * C::PART;
+                        if (CL > 1)
+                            tma_load_3d_multicast(dst, &mc, 0, row, x * C::PP, full, (1 << CL) - 1);
+                        else
+                            tma_load_3d(dst, &mc, 0, row, x * C::PP, full);
+                    }
+                    begun = C::PARTS * g + x + 1;
+                }
                 if (!ok) break;
-                if (lane == 0) {
-                    if (live > 0)
-                        mbar_arrive_expect_tx(&sh.full[s], live * C::GROUP);
-                    else
-                        mbar_arrive(&sh.full[s]);
-                }
-                __syncwarp();
-                if (mine && row >= 0) {
-                    unsigned char *dst = base + s * C::STAGE + lane * C::GROUP;
-                    if (CL > 1)
-                        tma_load_3d_multicast(dst, &mc, 0, row, 0, &sh.full[s], (1 << CL) - 1);
-                    else
-                        tma_load_3d(dst, &mc, 0, row, 0, &sh.full[s]);
-                }
                 if (t == p.t0) {
                     to_l2(next);
 #pragma unroll
@@ -432,8 +450,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         if (!ok && lane == 0) {
             // every copy in flight lands before the CTA gives its memory back
             mbar_wait_bounded(&sh.q_full, (k - 1) & 1);
-            for (int i = max(0, g - C::STAGES); i < g; ++i)
-                mbar_wait_bounded(&sh.full[i % C::STAGES], (i / C::STAGES) & 1);
+            for (int i = max(0, begun - C::PARTS * C::STAGES); i < begun; ++i) {
+                const int t = i / C::PARTS;
+                mbar_wait_bounded(&sh.full[t % C::STAGES][i % C::PARTS], (t / C::STAGES) & 1);
+            }
         }
     } else if (warp == C::SW + 1) {
         // --- scores ---
@@ -451,15 +471,20 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 for (int j = 0; j < p.tiles && ok; ++j, ++g) {
                     // the scores' place is free when the weights before last are made
                     if (g > 1) ok = wait_or_stop(&sh.p_ready[g & 1], ((g >> 1) & 1) ^ 1, stop);
-                    ok = ok && poll_or_stop(&sh.full[g % C::STAGES], (g / C::STAGES) & 1, stop);
                     if (!ok) break;
-                    tc_fence_after();
                     const uint64_t kd = smem_desc(kv + (g % C::STAGES) * C::STAGE, C::GROUP, 0);
                     const uint32_t d = tmem + (C::VT + (g & 1)) * N;
 #pragma unroll
-                    for (int x = 0; x < 4 * C::PL; ++x)
-                        mma_ss(d, kd + (x / 4) * 64 + (x % 4) * 2, qd + (x / 4) * 64 + (x % 4) * 2, ds,
-                               x > 0);
+                    for (int part = 0; part < C::PARTS; ++part) {
+                        ok = ok && poll_or_stop(&sh.full[g % C::STAGES][part], (g / C::STAGES) & 1, stop);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = 4 * C::PP * part; x < 4 * C::PP * (part + 1); ++x)
+                            mma_ss(d, kd + (x / 4) * 64 + (x % 4) * 2, qd + (x / 4) * 64 + (x % 4) * 2,
+                                   ds, x > 0);
+                    }
+                    if (!ok) break;
                     mma_commit(&sh.s_full[g & 1]);
                 }
                 if (ok) mma_commit(&sh.q_empty);
@@ -487,15 +512,20 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     const uint64_t vd = smem_desc(va, C::GROUP, 1024);
                     const uint64_t pd = smem_desc(va + C::P_AT, C::GROUP, 0);
 #pragma unroll
-                    for (int v = 0; v < C::VT; ++v)
+                    for (int v = 0; v < C::VT; ++v) {
 #pragma unroll
                         for (int x = 0; x < kTile / 16; ++x)
                             mma_ss(tmem + v * N, vd + (2 * v * 1024 + 2 * x * C::GROUP) / 16,
                                    pd + 2 * x * C::GROUP / 16, dpv, j > 0 || x > 0);
-                    if (CL > 1)
-                        mma_commit_multicast(&sh.empty[g % C::STAGES], (1 << CL) - 1);
-                    else
-                        mma_commit(&sh.empty[g % C::STAGES]);
+#pragma unroll
+                        for (int part = 0; part < C::PARTS; ++part) {
+                            if (C::last_reader(part) != v) continue;
+                            if (CL > 1)
+                                mma_commit_multicast(&sh.empty[g % C::STAGES][part], (1 << CL) - 1);
+                            else
+                                mma_commit(&sh.empty[g % C::STAGES][part]);
+                        }
+                    }
                     mma_commit(&sh.pv_done);
                 }
                 if (ok) mma_commit(&sh.o_full);
@@ -851,11 +881,11 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
 }
 
 // Rows of `width` fp16 values as [width / 64 planes][rows][64 columns]: a box is 8
-// rows of all planes, plane by plane, with the 128-byte swizzle.
-bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t width) {
+// rows of `planes` planes, plane by plane, with the 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t width, cuuint32_t planes) {
     auto fn = encode_fn();
     const cuuint64_t dims[3] = {64, rows, width / 64}, strides[2] = {width * 2, 128};
-    const cuuint32_t box[3] = {64, 8, static_cast<cuuint32_t>(width / 64)}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 8, planes}, one[3] = {1, 1, 1};
     return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides,
                     box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -866,8 +896,8 @@ template <int R, int N, int CL>
 cudaError_t launch(const LatentAttentionArgs &a, const LatentSplit &sp, cudaStream_t stream) {
     using C = Cfg<R, N, CL>;
     CUtensorMap mq, mc;
-    if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E) ||
-        !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E))
+    if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E, C::PL) ||
+        !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E, C::PP))
         return cudaErrorNotSupported;
     auto kern = latent_attention_kernel<R, N, CL>;
     static std::atomic<uint64_t> done{0};
