@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
     } else if (warp == C::SW) {
         // --- copies ---
         // a lane copies 8 tokens; the cluster's CTAs share a tile's lanes
-        constexpr int kLanes = kTile / 8;
-        const bool mine = lane < kLanes && lane / (kLanes / CL) == rank;
+        constexpr int kLanes = kTile / 8, kOwn = kLanes / CL;
+        const bool mine = lane < kLanes && lane / kOwn == rank;
         const char *cache = static_cast<const char *>(a.cache);
         const int block_log2 = 31 - __clz(a.block_size);
         int g = 0, k = 0;  // tiles, pieces so far
@@ -410,28 +410,36 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             for (int t = p.t0; t < end; ++t, ++g) {
                 const int s = g % C::STAGES;
                 const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                // one lane issues: a copy issued by several lanes costs some 100 cycles a lane
+                int rows[kOwn];
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i)
+                    rows[i] = __shfl_sync(0xffffffffu, row, rank * kOwn + i);
+                if (elect_one()) {
+                    unsigned char *dst = base + s * C::STAGE + rank * kOwn * C::GROUP;
 #pragma unroll 1
-                for (int x = 0; x < C::PARTS; ++x) {
-                    ok = __all_sync(0xffffffffu, ok && poll_or_stop(&sh.empty[s][x],
-                                                                    ((g / C::STAGES) & 1) ^ 1, stop));
-                    if (!ok) break;
-                    uint64_t *full = &sh.full[s][x];
-                    if (lane == 0) {
+                    for (int x = 0; x < C::PARTS; ++x) {
+                        ok = poll_or_stop(&sh.empty[s][x], ((g / C::STAGES) & 1) ^ 1, stop);
+                        if (!ok) break;
+                        uint64_t *full = &sh.full[s][x];
                         if (live > 0)
                             mbar_arrive_expect_tx(full, live * C::PART);
                         else
                             mbar_arrive(full);
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i) {
+                            if (rows[i] < 0) continue;
+                            if (CL > 1)
+                                tma_load_3d_multicast(dst + i * C::GROUP + x * C::PART, &mc, 0, rows[i],
+                                                      x * C::PP, full, (1 << CL) - 1);
+                            else
+                                tma_load_3d(dst + i * C::GROUP + x * C::PART, &mc, 0, rows[i],
+                                            x * C::PP, full);
+                        }
+                        begun = C::PARTS * g + x + 1;
                     }
-                    __syncwarp();
-                    if (mine && row >= 0) {
-                        unsigned char *dst = base + s * C::STAGE + lane * C::GROUP + x * C::PART;
-                        if (CL > 1)
-                            tma_load_3d_multicast(dst, &mc, 0, row, x * C::PP, full, (1 << CL) - 1);
-                        else
-                            tma_load_3d(dst, &mc, 0, row, x * C::PP, full);
-                    }
-                    begun = C::PARTS * g + x + 1;
                 }
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if (t == p.t0) {
                     to_l2(next);
@@ -447,6 +455,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             }
             ok = __all_sync(0xffffffffu, ok);
         } while (ok && next_piece(a, C::ROWS, &w, &p));
+        begun = __reduce_max_sync(0xffffffffu, begun);
         if (!ok && lane == 0) {
             // every copy in flight lands before the CTA gives its memory back
             mbar_wait_bounded(&sh.q_full, (k - 1) & 1);
