@@ -42,24 +42,24 @@ template <int R, int N, int CL>
 struct Cfg {
     static constexpr int E = R + 64, PL = E / 64, VT = R / 128;
     static constexpr int ROWS = CL * N;  // query rows of a worker's row tile
-    // shared memory holds rows in groups of 8: all 64-column planes of a group
-    // (1024 bytes each) together, so one copy brings 8 whole rows
-    static constexpr int GROUP = PL * 1024;
-    static constexpr int STAGE = kTile / 8 * GROUP;
-    // A tile comes and goes in parts of PP planes, each with barriers of its own: the
-    // scores start on the first part while the others are on their way, and the next
-    // tile's first part follows once the products that read this one's are done.
-    static constexpr int PARTS = PL % 3 == 0 ? 3 : 1, PP = PL / PARTS, PART = PP * 1024;
+    // A tile comes and goes in parts of PP 64-column planes, each with barriers of its
+    // own: the scores start on the first part while the others are on their way, and
+    // the next tile's first part follows once the products that read this one's are
+    // done.  In shared memory a part is 8 groups of 8 tokens, a group PP planes of
+    // 1024 bytes (what one 4-D copy of a block's rows writes).
+    static constexpr int PARTS = PL % 3 == 0 ? 3 : 1, PP = PL / PARTS;
+    static constexpr int GROUP = PP * 1024, PART = kTile / 8 * GROUP, STAGE = PARTS * PART;
+    static constexpr int plane(int x) { return x / PP * PART + x % PP * 1024; }  // its offset
     // the last of the VT output tiles that reads a part (tile v reads planes 2 v and
     // 2 v + 1; the last part holds P^T too)
     static constexpr int last_reader(int part) {
         return part == PARTS - 1 ? VT - 1 : ((part + 1) * PP - 1) / 2;
     }
     static constexpr int STAGES = R == 512 ? 2 : 4;
-    static constexpr int Q_BYTES = N / 8 * GROUP;
+    static constexpr int Q_GROUP = PL * 1024, Q_BYTES = N / 8 * Q_GROUP;  // groups of all planes
     // P^T takes the place of the tile's last plane (the rotated key part), which
     // nothing reads after the scores: 128 bytes a token
-    static constexpr int P_AT = (PL - 1) * 1024;
+    static constexpr int P_AT = plane(PL - 1);
     static constexpr int SMEM = 1024 + STAGES * STAGE + Q_BYTES;
     static constexpr int COLS = (VT + 2) * N;
     static constexpr int TMEM = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
@@ -366,9 +366,11 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         if (threadIdx.x == 0 && !sp.by_segment) records[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else if (warp == C::SW) {
         // --- copies ---
-        // a lane copies 8 tokens; the cluster's CTAs share a tile's lanes
-        constexpr int kLanes = kTile / 8, kOwn = kLanes / CL;
-        const bool mine = lane < kLanes && lane / kOwn == rank;
+        // a lane looks up `box` tokens of a tile, which one block holds; the cluster's
+        // CTAs share a tile's boxes
+        constexpr int kMost = kTile / CL / 16;  // boxes of this CTA, at most
+        const int box = min(a.block_size, kTile / CL), boxes = kTile / box, own = boxes / CL;
+        const bool mine = lane / own == rank;
         const char *cache = static_cast<const char *>(a.cache);
         const int block_log2 = 31 - __clz(a.block_size);
         int g = 0, k = 0;  // tiles, pieces so far
@@ -378,8 +380,8 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             const int32_t *table = a.block_tables + static_cast<long long>(p.b) * a.max_blocks_per_seq;
             const int end = p.t0 + p.tiles;
             auto row_of = [&](int t) {  // first cache row of this lane's tokens of tile t, or -1
-                const int token = t * kTile + lane * 8;
-                if (lane >= kLanes || token >= p.s.len || t >= end) return -1;
+                const int token = t * kTile + lane * box;
+                if (lane >= boxes || token >= p.s.len || t >= end) return -1;
                 int id = table[token >> block_log2];
                 if (id < 0 || id >= a.num_blocks) {
                     flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             };
             auto to_l2 = [&](int row) {
                 if (mine && row >= 0)
-                    bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), 8 * C::E * 2);
+                    bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), box * C::E * 2);
             };
             int row = row_of(p.t0), next = row_of(p.t0 + 1);
             // rows are looked up an iteration before they are used: a lookup takes as
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
                     const int row = p.s.q0 * H + p.rt * C::ROWS + rank * N;
                     for (int x = 0; x < N / 8; ++x)
-                        tma_load_3d(q_smem + x * C::GROUP, &mq, 0, row + 8 * x, 0, &sh.q_full);
+                        tma_load_3d(q_smem + x * C::Q_GROUP, &mq, 0, row + 8 * x, 0, &sh.q_full);
                 }
             }
             ++k;
@@ -411,30 +413,32 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 const int s = g % C::STAGES;
                 const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
                 // one lane issues: a copy issued by several lanes costs some 100 cycles a lane
-                int rows[kOwn];
+                int groups[kMost];  // of 8 cache rows, or -1
 #pragma unroll
-                for (int i = 0; i < kOwn; ++i)
-                    rows[i] = __shfl_sync(0xffffffffu, row, rank * kOwn + i);
+                for (int i = 0; i < kMost; ++i) {
+                    const int r = __shfl_sync(0xffffffffu, row, rank * own + i);
+                    groups[i] = i < own && r >= 0 ? r / 8 : -1;
+                }
                 if (elect_one()) {
-                    unsigned char *dst = base + s * C::STAGE + rank * kOwn * C::GROUP;
+                    unsigned char *dst = base + s * C::STAGE + rank * (kTile / 8 / CL) * C::GROUP;
 #pragma unroll 1
                     for (int x = 0; x < C::PARTS; ++x) {
                         ok = poll_or_stop(&sh.empty[s][x], ((g / C::STAGES) & 1) ^ 1, stop);
                         if (!ok) break;
                         uint64_t *full = &sh.full[s][x];
                         if (live > 0)
-                            mbar_arrive_expect_tx(full, live * C::PART);
+                            mbar_arrive_expect_tx(full, live * (box / 8) * C::GROUP);
                         else
                             mbar_arrive(full);
 #pragma unroll
-                        for (int i = 0; i < kOwn; ++i) {
-                            if (rows[i] < 0) continue;
+                        for (int i = 0; i < kMost; ++i) {
+                            if (groups[i] < 0) continue;
+                            unsigned char *to = dst + x * C::PART + i * (box / 8) * C::GROUP;
                             if (CL > 1)
-                                tma_load_3d_multicast(dst + i * C::GROUP + x * C::PART, &mc, 0, rows[i],
-                                                      x * C::PP, full, (1 << CL) - 1);
+                                tma_load_4d_multicast(to, &mc, 0, 0, x * C::PP, groups[i], full,
+                                                      (1 << CL) - 1);
                             else
-                                tma_load_3d(dst + i * C::GROUP + x * C::PART, &mc, 0, rows[i],
-                                            x * C::PP, full);
+                                tma_load_4d(to, &mc, 0, 0, x * C::PP, groups[i], full);
                         }
                         begun = C::PARTS * g + x + 1;
                     }
@@ -471,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         if (elect_one()) {
             constexpr uint32_t ds = mma_desc(kTile, N, false, false);
             const uint32_t kv = smem_addr(base);
-            const uint64_t qd = smem_desc(smem_addr(q_smem), C::GROUP, 0);
+            const uint64_t qd = smem_desc(smem_addr(q_smem), C::Q_GROUP, 0);
             int g = 0, k = 0;
             bool ok = true;
             do {
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                         tc_fence_after();
 #pragma unroll
                         for (int x = 4 * C::PP * part; x < 4 * C::PP * (part + 1); ++x)
-                            mma_ss(d, kd + (x / 4) * 64 + (x % 4) * 2, qd + (x / 4) * 64 + (x % 4) * 2,
+                            mma_ss(d, kd + C::plane(x / 4) / 16 + (x % 4) * 2, qd + (x / 4) * 64 + (x % 4) * 2,
                                    ds, x > 0);
                     }
                     if (!ok) break;
@@ -518,13 +522,14 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t va = kv + (g % C::STAGES) * C::STAGE;
-                    const uint64_t vd = smem_desc(va, C::GROUP, 1024);
                     const uint64_t pd = smem_desc(va + C::P_AT, C::GROUP, 0);
 #pragma unroll
                     for (int v = 0; v < C::VT; ++v) {
+                        const uint64_t vd = smem_desc(va + C::plane(2 * v), C::GROUP,
+                                                      C::plane(2 * v + 1) - C::plane(2 * v));
 #pragma unroll
                         for (int x = 0; x < kTile / 16; ++x)
-                            mma_ss(tmem + v * N, vd + (2 * v * 1024 + 2 * x * C::GROUP) / 16,
+                            mma_ss(tmem + v * N, vd + 2 * x * C::GROUP / 16,
                                    pd + 2 * x * C::GROUP / 16, dpv, j > 0 || x > 0);
 #pragma unroll
                         for (int part = 0; part < C::PARTS; ++part) {
@@ -680,7 +685,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 if (valid < kTile) {
                     for (int e = threadIdx.x; e < (kTile - valid) * (R / 8); e += kSoft) {
                         const int r = valid + e / (R / 8), piece = e % (R / 8);
-                        *reinterpret_cast<uint4 *>(tile + (r / 8) * C::GROUP + (piece / 8) * 1024 +
+                        *reinterpret_cast<uint4 *>(tile + C::plane(piece / 8) + (r / 8) * C::GROUP +
                                                    (r % 8) * 128 + (piece % 8) * 16) =
                             make_uint4(0, 0, 0, 0);
                     }
@@ -889,14 +894,17 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
     }
 }
 
-// Rows of `width` fp16 values as [width / 64 planes][rows][64 columns]: a box is 8
-// rows of `planes` planes, plane by plane, with the 128-byte swizzle.
-bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t width, cuuint32_t planes) {
+// Rows of `width` fp16 values, as 64 columns x 8 rows x planes (x groups of 8 rows,
+// where the rows are a multiple of 8 and copied from such a row on): a box is 8 rows of
+// `planes` planes, plane by plane, `groups` times over, with the 128-byte swizzle.
+bool make_map(CUtensorMap *m, const void *base, cuuint64_t rows, cuuint64_t width, cuuint32_t planes,
+              cuuint32_t groups) {
     auto fn = encode_fn();
-    const cuuint64_t dims[3] = {64, rows, width / 64}, strides[2] = {width * 2, 128};
-    const cuuint32_t box[3] = {64, 8, planes}, one[3] = {1, 1, 1};
-    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides,
-                    box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint64_t dims[4] = {64, groups ? 8 : rows, width / 64, rows / 8};
+    const cuuint64_t strides[3] = {width * 2, 128, width * 16};
+    const cuuint32_t box[4] = {64, 8, planes, groups}, one[4] = {1, 1, 1, 1};
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, groups ? 4 : 3, const_cast<void *>(base), dims,
+                    strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -905,8 +913,9 @@ template <int R, int N, int CL>
 cudaError_t launch(const LatentAttentionArgs &a, const LatentSplit &sp, cudaStream_t stream) {
     using C = Cfg<R, N, CL>;
     CUtensorMap mq, mc;
-    if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E, C::PL) ||
-        !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E, C::PP))
+    if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E, C::PL, 0) ||
+        !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E, C::PP,
+                  (a.block_size < kTile / CL ? a.block_size : kTile / CL) / 8))
         return cudaErrorNotSupported;
     auto kern = latent_attention_kernel<R, N, CL>;
     static std::atomic<uint64_t> done{0};
