@@ -31,7 +31,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 namespace {
 
 constexpr int kTile = 64;  // tokens
-constexpr int kAhead = 3;  // tiles that the copies into L2 run ahead of those into shared memory
+constexpr int kAhead = 2;  // tiles that the copies into L2 run ahead of those into shared memory
 // P holds 2^(s - r) with r kHead below the running maximum: weights up to
 // 2^kHead, and up to 2^(kHead + kLag) before r follows; fp16 ends at 2^16.
 constexpr float kHead = 6.f, kLag = 8.f;
