@@ -957,8 +957,12 @@ bool latent_split(int num_seqs, int max_q_len, int heads, int latent_dim, int ma
     // few segments: a record each; more than workers: one for what each worker starts
     sp->by_segment = tiles * num_seqs <= sp->workers;
     sp->records = sp->by_segment ? static_cast<int>(tiles * num_seqs) : sp->workers;
-    // threads of the join over a segment's pieces: about workers / segments of them
-    const long long pieces = sp->workers / (tiles * num_seqs > 0 ? tiles * num_seqs : 1);
+    // threads of the join over a segment's pieces, about workers / segments of them: a
+    // quarter to a half of the pieces; with 64 rows half of that, as its blocks are many
+    // anyway (measured: 16 x 4 tokens x 32 heads 44.3 us with 2 threads, 42.6 with 1; 32
+    // sequences x 16 heads 20.5 with 2, 21.0 with 1)
+    const long long segments = tiles * num_seqs > 0 ? tiles * num_seqs : 1;
+    const long long pieces = sp->workers / segments / (sp->rows == 64 ? 2 : 1);
     sp->join_threads = pieces >= 16 ? 8 : pieces >= 8 ? 4 : pieces >= 4 ? 2 : 1;
     sp->ws_bytes = layout(sp->records, sp->workers, sp->cluster, sp->rows, latent_dim).total;
     return true;
