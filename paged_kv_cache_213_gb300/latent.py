@@ -9,7 +9,7 @@ import functools
 import torch
 
 from .binding import _check, _need, library
-from .rope import _current_device, _launch, _need_cuda, _ptr
+from .rope import _F16, _F32, _I32, _I64, _U8, _at, _at_strided, _current_device, _launch
 
 _bound = None
 
@@ -37,19 +37,22 @@ def _lib():
     return _bound
 
 
-def _need_cache(cache):
-    _need(cache, "cache", torch.float16)
-    if cache.dim() != 3:
+def _cache(cache):
+    """(device, address, blocks, block size, entries of a row) of a latent cache."""
+    _need(cache, "cache", _F16)
+    shape = cache.shape
+    if len(shape) != 3:
         raise ValueError("cache must be [num_blocks, block_size, latent_dim + rope_dim]")
+    return (cache.device, cache.data_ptr(), *shape)
 
 
-def _strides(t, name, per):
+def _strides(t, name, T, H, P):
     """(token stride, head stride) of t [T, H, P] with contiguous entries."""
-    T, H, P = t.shape
     st, sh, se = t.stride()
-    if P > 1 and se != 1:
+    if se != 1 and P > 1:
         raise ValueError(f"{name}: the entries of a head must be contiguous")
-    sh = sh if H > 1 else per
+    if H == 1:
+        sh = P
     return (st if T > 1 else H * sh), sh
 
 
@@ -62,44 +65,42 @@ def paged_latent_append(kv, weight, eps, cos_sin, positions, slot_mapping, cache
     With q_rope [T, H, P] the position part of the queries is rotated into
     q_out [T, H, P] (both any strides between tokens and heads, e.g.
     q[..., d:] and absorbed[..., R:]; q_out may be q_rope)."""
-    _need_cache(cache)
-    dev = cache.device
-    NB, bs, E = cache.shape
-    _need_cuda(kv, "kv", torch.float16, dev)
-    if kv.dim() != 2 or kv.shape[1] != E or (E > 1 and kv.stride(1) != 1):
+    dev, cp, NB, bs, E = _cache(cache)
+    kp = _at_strided(kv, "kv", _F16, dev)
+    shape = kv.shape
+    if len(shape) != 2 or shape[1] != E or (E > 1 and kv.stride(1) != 1):
         raise ValueError("kv must be [num_tokens, latent_dim + rope_dim], entries contiguous")
-    T = kv.shape[0]
-    _need(cos_sin, "cos_sin", torch.float32, dev)
-    _need(positions, "positions", torch.int32, dev)
-    _need(slot_mapping, "slot_mapping", torch.int64, dev)
-    if cos_sin.dim() != 2 or positions.shape != (T,) or slot_mapping.shape != (T,):
+    T = shape[0]
+    cs = _at(cos_sin, "cos_sin", _F32, dev)
+    pos = _at(positions, "positions", _I32, dev)
+    slots = _at(slot_mapping, "slot_mapping", _I64, dev)
+    shape = cos_sin.shape
+    if len(shape) != 2 or positions.shape != (T,) or slot_mapping.shape != (T,):
         raise ValueError("cos_sin must be [max_positions, rope_dim], positions and slot_mapping [T]")
-    table, P = cos_sin.shape
+    table, P = shape
     R = E - P
     if R <= 0:
         raise ValueError("cos_sin is as wide as the cache rows: no latent entries")
+    wp = None
     if weight is not None:
-        _need(weight, "weight", torch.float16, dev)
+        wp = _at(weight, "weight", _F16, dev)
         if weight.shape != (R,):
             raise ValueError("weight must be [latent_dim]")
-    if (q_rope is None) != (q_out is None):
+    H, qs, os, qp, op = 0, (0, 0), (0, 0), None, None
+    if q_rope is not None and q_out is not None:
+        qp = _at_strided(q_rope, "q_rope", _F16, dev)
+        op = _at_strided(q_out, "q_out", _F16, dev)
+        shape = q_rope.shape
+        if len(shape) != 3 or shape[0] != T or shape[2] != P or q_out.shape != shape:
+            raise ValueError("q_rope and q_out must be [num_tokens, n_q_heads, rope_dim]")
+        H = shape[1]
+        qs, os = _strides(q_rope, "q_rope", T, H, P), _strides(q_out, "q_out", T, H, P)
+    elif q_rope is not None or q_out is not None:
         raise ValueError("q_rope and q_out go together")
-    H, qs, os = 0, (0, 0), (0, 0)
-    if q_rope is not None:
-        for t, name in ((q_rope, "q_rope"), (q_out, "q_out")):
-            _need_cuda(t, name, torch.float16, dev)
-            if t.dim() != 3 or t.shape[0] != T or t.shape[2] != P:
-                raise ValueError(f"{name} must be [num_tokens, n_q_heads, rope_dim]")
-        if q_rope.shape != q_out.shape:
-            raise ValueError("q_out must have q_rope's shape")
-        H = q_rope.shape[1]
-        qs, os = _strides(q_rope, "q_rope", P), _strides(q_out, "q_out", P)
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
-    rc = _launch(dev, _lib().paged_latent_append, _ptr(kv), kv.stride(0) if T > 1 else E,
-                 _ptr(weight), float(eps), _ptr(cos_sin), _ptr(positions), table,
-                 int(bool(interleaved)), _ptr(slot_mapping), _ptr(cache), _ptr(q_rope), *qs,
-                 _ptr(q_out), *os, H, T, R, P, bs, NB, _ptr(err_word))
+    err = None if err_word is None else _at(err_word, "err_word", _I32, dev)
+    rc = _launch(dev, _lib().paged_latent_append, kp, kv.stride(0) if T > 1 else E, wp,
+                 float(eps), cs, pos, table, 1 if interleaved else 0, slots, cp, qp, *qs, op, *os, H, T, R, P, bs,
+                 NB, err)
     _check("paged_latent_append", rc)
 
 
@@ -133,49 +134,52 @@ def paged_latent_attention(q, cache, block_tables, context_lens, scale, latent_d
     sequence b owns the rows [query_start[b], query_start[b + 1]), its newest
     tokens (causal; max_q_len bounds their number); None: one token a sequence.
     Returns out [total_q, H, R] fp16: the weighted latents of every head."""
-    _need_cache(cache)
-    dev = cache.device
-    NB, bs, E = cache.shape
-    _need(q, "q", torch.float16, dev)
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _need(context_lens, "context_lens", torch.int32, dev)
-    if q.dim() != 3 or q.shape[2] != E:
+    dev, cp, NB, bs, E = _cache(cache)
+    qp = _at(q, "q", _F16, dev)
+    tables = _at(block_tables, "block_tables", _I32, dev)
+    lens = _at(context_lens, "context_lens", _I32, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != E:
         raise ValueError("q must be [total_q, n_q_heads, latent_dim + rope_dim]")
-    TQ, H = q.shape[:2]
+    TQ, H, _ = shape
     R = int(latent_dim)
     if not 0 < R < E:
         raise ValueError("latent_dim must be positive and smaller than the cache rows")
-    if block_tables.dim() != 2 or context_lens.shape != (block_tables.shape[0],):
+    shape = block_tables.shape
+    if len(shape) != 2 or context_lens.shape != (shape[0],):
         raise ValueError("block_tables must be [B, MB], context_lens [B]")
-    B, MB = block_tables.shape
+    B, MB = shape
+    start = None
     if query_start is not None:
-        _need(query_start, "query_start", torch.int32, dev)
+        start = _at(query_start, "query_start", _I32, dev)
         if query_start.shape != (B + 1,):
             raise ValueError("query_start must be [B + 1]")
     elif TQ != B or max_q_len != 1:
         raise ValueError("without query_start, q holds one token a sequence")
     mcl = 0 if max_context_len is None else int(max_context_len)
+    max_q_len = int(max_q_len)
     if out is None:
-        out = torch.empty((TQ, H, R), dtype=torch.float16, device=dev)
+        out = torch.empty((TQ, H, R), dtype=_F16, device=dev)
+        op = out.data_ptr()
     else:
-        _need(out, "out", torch.float16, dev)
+        op = _at(out, "out", _F16, dev)
         if out.shape != (TQ, H, R):
             raise ValueError("out must be [total_q, n_q_heads, latent_dim]")
+    lp = None
     if lse is not None:
-        _need(lse, "lse", torch.float32, dev)
+        lp = _at(lse, "lse", _F32, dev)
         if lse.shape != (TQ, H):
             raise ValueError("lse must be [total_q, n_q_heads]")
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
+    err = None if err_word is None else _at(err_word, "err_word", _I32, dev)
     if workspace is None:
-        ws = _plan_on(dev.index, B, TQ, max_q_len, H, R, E - R, bs, MB, mcl)
-        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+        size = _plan_on(dev.index, B, TQ, max_q_len, H, R, E - R, bs, MB, mcl)
+        workspace = torch.empty(size, dtype=_U8, device=dev)
+        wp = workspace.data_ptr()
     else:
-        _need(workspace, "workspace", torch.uint8, dev)
-    rc = _launch(dev, _lib().paged_latent_attention, _ptr(out), _ptr(q), _ptr(cache),
-                 _ptr(block_tables), _ptr(context_lens), _ptr(query_start), B, TQ, int(max_q_len),
-                 MB, NB, float(scale), H, R, E - R, bs, mcl, _ptr(workspace), workspace.numel(),
-                 _ptr(lse), _ptr(err_word))
+        wp = _at(workspace, "workspace", _U8, dev)
+        size = workspace.numel()
+    rc = _launch(dev, _lib().paged_latent_attention, op, qp, cp, tables, lens, start, B, TQ,
+                 max_q_len, MB, NB, float(scale), H, R, E - R, bs, mcl, wp, size, lp, err)
     _check("paged_latent_attention", rc)
     return out
 
@@ -186,30 +190,29 @@ def paged_latent_gather(cache, block_tables, start, total, latent_dim, latents=N
     are the first tokens of sequence b.  cache [NB, bs, R + P] fp16,
     block_tables [B, MB] and start [B + 1] int32, total: rows of the results.
     Returns (latents [total, R], ropes [total, P]) fp16."""
-    _need_cache(cache)
-    dev = cache.device
-    NB, bs, E = cache.shape
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _need(start, "start", torch.int32, dev)
+    dev, cp, NB, bs, E = _cache(cache)
+    tables = _at(block_tables, "block_tables", _I32, dev)
+    first = _at(start, "start", _I32, dev)
     R = int(latent_dim)
     if not 0 < R < E:
         raise ValueError("latent_dim must be positive and smaller than the cache rows")
-    if block_tables.dim() != 2 or start.shape != (block_tables.shape[0] + 1,):
+    shape = block_tables.shape
+    if len(shape) != 2 or start.shape != (shape[0] + 1,):
         raise ValueError("block_tables must be [B, MB], start [B + 1]")
-    B, MB = block_tables.shape
+    B, MB = shape
     total = int(total)
     if latents is None:
-        latents = torch.empty((total, R), dtype=torch.float16, device=dev)
+        latents = torch.empty((total, R), dtype=_F16, device=dev)
+    elif latents.shape != (total, R):
+        raise ValueError("latents must be [total, latent_dim]")
     if ropes is None:
-        ropes = torch.empty((total, E - R), dtype=torch.float16, device=dev)
-    for t, name, w in ((latents, "latents", R), (ropes, "ropes", E - R)):
-        _need(t, name, torch.float16, dev)
-        if t.shape != (total, w):
-            raise ValueError(f"{name} must be [total, {w}]")
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
-    rc = _launch(dev, _lib().paged_latent_gather, _ptr(latents), _ptr(ropes), _ptr(cache),
-                 _ptr(block_tables), _ptr(start), B, total, MB, NB, R, E - R, bs, _ptr(err_word))
+        ropes = torch.empty((total, E - R), dtype=_F16, device=dev)
+    elif ropes.shape != (total, E - R):
+        raise ValueError("ropes must be [total, rope_dim]")
+    err = None if err_word is None else _at(err_word, "err_word", _I32, dev)
+    rc = _launch(dev, _lib().paged_latent_gather, _at(latents, "latents", _F16, dev),
+                 _at(ropes, "ropes", _F16, dev), cp, tables, first, B, total, MB, NB, R, E - R, bs,
+                 err)
     _check("paged_latent_gather", rc)
     return latents, ropes
 
@@ -222,34 +225,32 @@ def latent_prefill_attention(q, kv, k_rope, q_start, kv_start, scale, max_q_len,
     [total_kv, P], fp16; q_start, kv_start [B + 1] int32: each sequence's query
     rows and key rows (its queries are the newest tokens of its keys).
     max_q_len, max_kv_len: host bounds.  Returns out [total_q, H, d] fp16."""
+    _need(q, "q", _F16)
     dev = q.device
-    _need(q, "q", torch.float16)
-    _need(kv, "kv", torch.float16, dev)
-    _need(k_rope, "k_rope", torch.float16, dev)
-    _need(q_start, "q_start", torch.int32, dev)
-    _need(kv_start, "kv_start", torch.int32, dev)
+    kp = _at(kv, "kv", _F16, dev)
+    rp = _at(k_rope, "k_rope", _F16, dev)
+    qs = _at(q_start, "q_start", _I32, dev)
+    ks = _at(kv_start, "kv_start", _I32, dev)
     if q.dim() != 3 or kv.dim() != 3 or k_rope.dim() != 2 or kv.shape[1] != q.shape[1] or \
             kv.shape[0] != k_rope.shape[0] or kv.shape[2] != 2 * (q.shape[2] - k_rope.shape[1]):
         raise ValueError("q must be [total_q, H, d + P], kv [total_kv, H, 2 d], k_rope [total_kv, P]")
-    TQ, H = q.shape[:2]
+    TQ, H, E = q.shape
     TK, P = k_rope.shape
-    d = q.shape[2] - P
+    d = E - P
     if q_start.dim() != 1 or q_start.numel() < 1 or kv_start.shape != q_start.shape:
         raise ValueError("q_start and kv_start must be [B + 1]")
     if out is None:
-        out = torch.empty((TQ, H, d), dtype=torch.float16, device=dev)
-    else:
-        _need(out, "out", torch.float16, dev)
-        if out.shape != (TQ, H, d):
-            raise ValueError("out must be [total_q, H, d]")
+        out = torch.empty((TQ, H, d), dtype=_F16, device=dev)
+    elif out.shape != (TQ, H, d):
+        raise ValueError("out must be [total_q, H, d]")
+    lp = None
     if lse is not None:
-        _need(lse, "lse", torch.float32, dev)
+        lp = _at(lse, "lse", _F32, dev)
         if lse.shape != (TQ, H):
             raise ValueError("lse must be [total_q, H]")
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
-    rc = _launch(dev, _lib().latent_prefill_attention, _ptr(out), _ptr(q), _ptr(kv), _ptr(k_rope),
-                 _ptr(q_start), _ptr(kv_start), q_start.numel() - 1, TQ, TK, int(max_q_len),
-                 int(max_kv_len), float(scale), H, d, P, _ptr(lse), _ptr(err_word))
+    err = None if err_word is None else _at(err_word, "err_word", _I32, dev)
+    rc = _launch(dev, _lib().latent_prefill_attention, _at(out, "out", _F16, dev), q.data_ptr(), kp,
+                 rp, qs, ks, q_start.numel() - 1, TQ, TK, int(max_q_len),
+                 int(max_kv_len), float(scale), H, d, P, lp, err)
     _check("latent_prefill_attention", rc)
     return out

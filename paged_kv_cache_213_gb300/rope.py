@@ -29,14 +29,39 @@ def _lib():
     return _bound
 
 
-# the current device and its current stream's handle as plain integers: the
-# wrapper objects of torch.cuda cost 2 us a call, a sixth of a small call's time
+# Small calls take as long as the host needs for them, so the marshalling below is
+# spare: each tensor is looked at once (the full checks of _need run where that look
+# fails, for the message), and device, stream and pointers are plain integers (the
+# wrapper objects of torch.cuda cost 2 us a call).
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
+_F16, _F32, _I32, _I64, _U8 = (torch.float16, torch.float32, torch.int32, torch.int64,
+                               torch.uint8)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _at(t, name, dtype, dev):
+    """t's address; t must be a contiguous tensor of this type on the CUDA device dev."""
+    try:
+        if t.dtype is dtype and t.device == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, dev)
+    raise ValueError(f"{name} must be on {dev}")
+
+
+def _at_strided(t, name, dtype, dev):
+    """t's address; the caller checks the strides."""
+    try:
+        if t.dtype is dtype and t.device == dev:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
 def _launch(dev, fn, *args):
@@ -48,23 +73,10 @@ def _launch(dev, fn, *args):
         return fn(*args, _current_stream(index))
 
 
-def _need_cuda(t, name, dtype, dev):
-    """_need without the contiguity check: the caller checks the strides."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device (no CPU path)")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-
-
-def _token_stride(t, name):
-    """Elements between tokens of t [T, heads, d], whose heads are contiguous."""
-    T, H, d = t.shape
+def _token_stride(t, name, T, H, d):
+    """Elements between tokens of t [T, H, d], whose heads are contiguous."""
     st, sh, se = t.stride()
-    if (d > 1 and se != 1) or (H > 1 and sh != d):
+    if (se != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     return st if T > 1 else H * d
 
@@ -72,54 +84,62 @@ def _token_stride(t, name):
 def _append(scales, q, k, v, q_weight, k_weight, eps, cos_sin, positions, slot_mapping, k_cache,
             v_cache, interleaved, q_out, err_word):
     fp8 = scales is not None
-    dev = k_cache.device
-    kind = torch.uint8 if fp8 else torch.float16
+    kind = _U8 if fp8 else _F16
     _need(k_cache, "k_cache", kind)
-    _need(v_cache, "v_cache", kind, dev)
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    dev = k_cache.device
+    vc = _at(v_cache, "v_cache", kind, dev)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache/v_cache must both be [num_blocks, n_kv_heads, block_size, head_dim]")
-    NB, Hk, bs, d = k_cache.shape
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _need_cuda(t, name, torch.float16, dev)
-    if q.dim() != 3 or q.shape[2] != d:
+    NB, Hk, bs, d = shape
+    qp = _at_strided(q, "q", _F16, dev)
+    kp = _at_strided(k, "k", _F16, dev)
+    vp = _at_strided(v, "v", _F16, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
         raise ValueError("q must be [num_tokens, n_q_heads, head_dim]")
-    T, H = q.shape[:2]
+    T, H, _ = shape
     if k.shape != (T, Hk, d) or v.shape != (T, Hk, d):
         raise ValueError("k/v must be [num_tokens, n_kv_heads, head_dim]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, torch.float16, dev)
-            if w.shape != (d,):
-                raise ValueError(f"{name} must be [head_dim]")
-    _need(slot_mapping, "slot_mapping", torch.int64, dev)
+    qw = kw = None
+    if q_weight is not None:
+        qw = _at(q_weight, "q_weight", _F16, dev)
+        if q_weight.shape != (d,):
+            raise ValueError("q_weight must be [head_dim]")
+    if k_weight is not None:
+        kw = _at(k_weight, "k_weight", _F16, dev)
+        if k_weight.shape != (d,):
+            raise ValueError("k_weight must be [head_dim]")
+    slots = _at(slot_mapping, "slot_mapping", _I64, dev)
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [num_tokens]")
-    table, rot = 0, 0
+    table = rot = 0
+    cs = pos = None
     if cos_sin is not None:
-        _need(cos_sin, "cos_sin", torch.float32, dev)
-        _need(positions, "positions", torch.int32, dev)
-        if cos_sin.dim() != 2 or positions.shape != (T,):
+        cs = _at(cos_sin, "cos_sin", _F32, dev)
+        pos = _at(positions, "positions", _I32, dev)
+        shape = cos_sin.shape
+        if len(shape) != 2 or positions.shape != (T,):
             raise ValueError("cos_sin must be [max_positions, rot_dim], positions [num_tokens]")
-        table, rot = cos_sin.shape
+        table, rot = shape
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=torch.float16, device=dev)
+        q_out = torch.empty((T, H, d), dtype=_F16, device=dev)
+        op = q_out.data_ptr()
     else:
-        _need(q_out, "q_out", torch.float16, dev)
+        op = _at(q_out, "q_out", _F16, dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
-    if err_word is not None:
-        _need(err_word, "err_word", torch.int32, dev)
+    err = None if err_word is None else _at(err_word, "err_word", _I32, dev)
     lib = _lib()
-    args = (_ptr(q_out), _ptr(q), _ptr(k), _ptr(v), _token_stride(q, "q"), _token_stride(k, "k"),
-            _token_stride(v, "v"), _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(cos_sin),
-            _ptr(positions) if rot else None, table, rot, int(bool(interleaved)),
-            _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), T, H, Hk, d, bs, NB)
+    args = (op, qp, kp, vp, _token_stride(q, "q", T, H, d), _token_stride(k, "k", T, Hk, d),
+            _token_stride(v, "v", T, Hk, d), qw, kw, float(eps), cs, pos, table, rot,
+            1 if interleaved else 0, slots, k_cache.data_ptr(), vc, T, H, Hk, d, bs, NB)
     if fp8:
         rc = _launch(dev, lib.paged_qk_norm_rope_append_fp8, *args, float(scales[0]),
-                     float(scales[1]), _ptr(err_word))
+                     float(scales[1]), err)
         _check("paged_qk_norm_rope_append_fp8", rc)
     else:
-        rc = _launch(dev, lib.paged_qk_norm_rope_append, *args, _ptr(err_word))
+        rc = _launch(dev, lib.paged_qk_norm_rope_append, *args, err)
         _check("paged_qk_norm_rope_append", rc)
     return q_out
 

@@ -531,3 +531,40 @@ def test_copy_on_write_of_a_latent_block():
                          torch.tensor([5], **i32))
     assert torch.equal(c[0, :5], was[2, :5]) and torch.equal(c[0, 5:], was[0, 5:])
     assert torch.equal(c[1:], was[1:])
+
+
+def test_python_calls_refuse_what_does_not_fit():
+    """Types, shapes, strides and devices that the calls do not take."""
+    p, q, qs, scale = _problem([20, 30], [1, 1], 4, 512, 16, 98)
+    q, c, bt, cl = (_t(x) for x in (q, p.cache, p.tables, p.lens.astype(np.int32)))
+
+    def bad(error, f, *a, **k):
+        with pytest.raises(error):
+            f(*a, **k)
+
+    f = pkv.paged_latent_attention
+    bad(TypeError, f, q.float(), c, bt, cl, scale, 512)
+    bad(TypeError, f, q, c, bt.long(), cl, scale, 512)
+    bad(TypeError, f, None, c, bt, cl, scale, 512)
+    bad(ValueError, f, q, c, bt.cpu(), cl, scale, 512)
+    bad(ValueError, f, q, c, bt.t().contiguous().t(), cl, scale, 512)   # not contiguous
+    bad(ValueError, f, q[:1], c, bt, cl, scale, 512)
+    bad(ValueError, f, q, c, bt, cl, scale, 576)
+    bad(ValueError, f, q, c, bt, cl, scale, 512, max_q_len=2)
+    bad(ValueError, f, q, c, bt, cl, scale, 512, lse=torch.empty(2, 5, device="cuda"))
+    bad(ValueError, f, q, c, bt, cl, scale, 512, out=torch.empty_like(q))
+    bad(pkv.PagedKVError, f, q, c, bt, cl, scale, 512,
+        workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    bad(pkv.PagedKVError, f, q, c, bt, cl, float("inf"), 512)
+    bad(pkv.PagedKVError, f, q, c, bt, cl, scale, 500)
+    st = torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda")
+    bad(ValueError, pkv.paged_latent_gather, c, bt, st[:2], 50, 512)
+    bad(ValueError, pkv.paged_latent_gather, c, bt, st, 50, 512, latents=q)
+    h = torch.zeros(3, 2, 192, dtype=torch.float16, device="cuda")
+    bad(ValueError, pkv.latent_prefill_attention, h, h, h[:, 0, :64].contiguous(), st, st, 1.0, 3, 3)
+    cs = torch.zeros(9, 64, device="cuda")
+    i = torch.zeros(2, dtype=torch.int32, device="cuda")
+    kv = torch.zeros(2, 576, dtype=torch.float16, device="cuda")
+    bad(ValueError, pkv.paged_latent_append, kv, None, EPS, cs, i, i.long(), c, q_rope=q[..., :64])
+    bad(ValueError, pkv.paged_latent_append, kv[:, ::2], None, EPS, cs, i, i.long(), c)
+    bad(TypeError, pkv.paged_latent_append, kv, None, EPS, cs, i.long(), i.long(), c)
