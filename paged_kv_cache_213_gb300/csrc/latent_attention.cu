@@ -11,7 +11,18 @@
 // Tokens are the M side of the first product and the value columns that of the
 // second: with few rows (N = 16 .. 64) no tensor-core row is padding, O^T takes
 // only N TMEM columns a tile, and both operands of the second product are the
-// bytes already in shared memory, read along their other axis.
+// bytes already in shared memory, read along their other axis.  Above 64 rows two
+// CTAs of a cluster have 64 each and share every tile (multicast copies).
+//
+// A token's row is 1152 bytes at R = 512 and costs 2 (R + E) flops a row: with 128
+// rows the copy rate and the product rate of the SMs meet.  What bounds the kernel:
+//  few rows    the copies: 32 sequences of 128 .. 2048 tokens x 16 rows 20.8 us, of
+//              which 6 are the bytes at the copy rate and the rest the start (every
+//              SM's first tiles at once, 4 us), one tile's chain and the join;
+//  64 rows     two tiles in flight: Q and a tile take 74 KB of shared memory each, and
+//              a tile lives 5500 cycles (copy 1100 .. 1800, scores 1200, softmax 1200,
+//              products 1000, release 700) for 1870 cycles of products.  64 sequences
+//              of 3000 .. 5000 tokens x 128 rows: 101 us, 3.1 TB/s, 708 TFLOP/s.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>

@@ -1,6 +1,26 @@
 // latent_prefill.cu -- expanded latent attention of prompts
 // (latent_prefill_attention): causal attention with keys [k, k_rope] of D + 64
 // entries and values of D.
+//
+// For a tile of 128 query rows and a step of 96 keys
+//   S [128 x 96] = Q [k, k_rope]^T         12 products of 16 entries (D = 128)
+//   P = 2^(S scale - r), r per row; O (+)= P V    6 products of 16 keys
+// with S, O and P in TMEM: P (fp16) takes the place of its own S and is the first
+// operand of the second product, so it never passes through shared memory.  r is the
+// running maximum, less kHead, and moves only when a score is far above it; O is then
+// rescaled in TMEM by the thread that owns the row.
+//
+// A CTA has two neighbouring tiles, which share the keys and values that TMA copies
+// bring: one tile's softmax (a warpgroup, a row a thread) runs under the other's
+// products.  Bound by the chain of one tile: products 1070 cycles (57 per 96-wide
+// score product: its operands' shared-memory reads, 64 per output product), signal
+// and wait 430, softmax 1100; a step of both tiles takes about 2500 cycles, of which
+// 2140 are products.  4096 tokens x 128 heads: 509 us, 1352 TFLOP/s (70 % of what a
+// large bf16 matrix product reaches).
+//
+// Why 96 keys a step: two steps of keys and values (2 x 60 KB) fit beside the two
+// tiles' queries (96 KB); with 128 there is room for one and a half, and the values
+// of a step would come a copy's latency late.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
