@@ -800,7 +800,8 @@ constexpr int kJoinThreads = 256;
 template <int R, int N, int CL, int U>
 __global__ void __launch_bounds__(kJoinThreads, 4)
     latent_join_kernel(const LatentAttentionArgs a, const LatentSplit sp) {
-    __shared__ float parts[kJoinThreads / 32][4];
+    __shared__ float parts[kJoinThreads / 32][4], warp_l[kJoinThreads / 32][4];
+    __shared__ float row_ref[4], row_inv[4];
     __shared__ float4 sums[U][kJoinThreads];
     grid_dependency_wait();
     allow_dependent_launch();
@@ -839,25 +840,31 @@ __global__ void __launch_bounds__(kJoinThreads, 4)
         if (next > -INFINITY) l = l * ex2(m - next) + l2 * ex2(m2 - next);
         m = next;
     }
-    __shared__ float warp_l[kJoinThreads / 32][4];
     if (lane < 4) {
         parts[warp][lane] = m;
         warp_l[warp][lane] = l;
     }
     __syncthreads();
+    if (threadIdx.x < 4) {
+        float r = -INFINITY, t = 0.f;
+#pragma unroll
+        for (int x = 0; x < kJoinThreads / 32; ++x) r = fmaxf(r, parts[x][threadIdx.x]);
+        r = r > -INFINITY ? r : 0.f;
+#pragma unroll
+        for (int x = 0; x < kJoinThreads / 32; ++x)
+            t += warp_l[x][threadIdx.x] * ex2(parts[x][threadIdx.x] - r);
+        row_ref[threadIdx.x] = r;
+        row_inv[threadIdx.x] = t == 0.f ? 0.f : 1.f / t;
+        const int n = n0 + threadIdx.x;
+        if (a.lse_out && at0 % R == 0 && n < rec.y)
+            a.lse_out[rec.x + n] = t == 0.f ? -INFINITY : (r + log2f(t)) * 0.69314718055994531f;
+    }
+    __syncthreads();
     float ref[4], inv[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        float r = -INFINITY, t = 0.f;
-#pragma unroll
-        for (int x = 0; x < kJoinThreads / 32; ++x) r = fmaxf(r, parts[x][e]);
-        r = r > -INFINITY ? r : 0.f;
-#pragma unroll
-        for (int x = 0; x < kJoinThreads / 32; ++x) t += warp_l[x][e] * ex2(parts[x][e] - r);
-        ref[e] = r;
-        inv[e] = t == 0.f ? 0.f : 1.f / t;
-        if (a.lse_out && at0 % R == 0 && threadIdx.x == e && n0 + e < rec.y)
-            a.lse_out[rec.x + n0 + e] = t == 0.f ? -INFINITY : (r + log2f(t)) * 0.69314718055994531f;
+        ref[e] = row_ref[e];
+        inv[e] = row_inv[e];
     }
     float4 s[U];
 #pragma unroll
