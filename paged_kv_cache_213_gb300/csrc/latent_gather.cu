@@ -3,7 +3,8 @@
 // rows: one thread a row finds the row's sequence (binary search over start)
 // and its cache row, then all threads move 16-byte pieces, coalesced on both
 // sides (a row is one contiguous piece of the cache).  72000 rows of 576 entries:
-// 29.2 us, 5.7 TB/s read and written, 84 % of the copy rate.
+// 26.8 us, 6.2 TB/s read and written, 91 % of the copy rate (28.4 with
+// the default cache policies: nothing here is used twice).
 #include "pagedkv_latent.h"
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -59,12 +60,12 @@ __global__ void __launch_bounds__(kThreads) latent_gather_kernel(const LatentGat
             if (i >= kRows * w) continue;
             const int k = __umulhi(i, inv), c = i - k * w;
             if (src[k] < 0) continue;
-            x[s] = cache[src[k] * w + c];
+            x[s] = __ldcs(cache + src[k] * w + c);
             dst[s] = c < rv ? latents + (first + k) * rv + c : ropes + (first + k) * pv + (c - rv);
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
-            if (dst[s]) *dst[s] = x[s];
+            if (dst[s]) __stcs(dst[s], x[s]);
     }
 }
 
