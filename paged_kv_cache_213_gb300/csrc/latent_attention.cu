@@ -384,6 +384,9 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const bool mine = lane / own == rank;
         const char *cache = static_cast<const char *>(a.cache);
         const int block_log2 = 31 - __clz(a.block_size);
+        // a single CTA's tiles are read once: first to leave L2 (32 sequences x 16 heads
+        // 19.7 -> 18.8 us; with clusters it costs 2 %)
+        const uint64_t policy = l2_policy_evict_first();
         int g = 0, k = 0;  // tiles, pieces so far
         int begun = 0;     // parts of tiles so far
         bool ok = true;
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                                 tma_load_4d_multicast(to, &mc, 0, 0, x * C::PP, groups[i], full,
                                                       (1 << CL) - 1);
                             else
-                                tma_load_4d(to, &mc, 0, 0, x * C::PP, groups[i], full);
+                                tma_load_4d(to, &mc, 0, 0, x * C::PP, groups[i], full, policy);
                         }
                         begun = C::PARTS * g + x + 1;
                     }

@@ -220,16 +220,17 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 4-D tiled TMA load; x = innermost coordinate.
+// 4-D tiled TMA load with an L2 eviction policy; x = innermost coordinate.
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w,
-                                            uint64_t *bar) {
+                                            uint64_t *bar, uint64_t policy) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)),
+        "l"(policy)
         : "memory");
 }
-// The same to this offset of every CTA of the mask, completion on the barrier at this
+// A 4-D load with the default policy, to this offset of every CTA of the mask, completion on the barrier at this
 // offset in each of them.
 __device__ __forceinline__ void tma_load_4d_multicast(void *dst, const void *tmap, int x, int y,
                                                       int z, int w, uint64_t *bar, uint16_t mask) {
