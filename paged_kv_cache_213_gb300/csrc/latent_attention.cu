@@ -28,6 +28,7 @@
 #include <cuda_fp16.h>
 
 #include <atomic>
+#include <climits>
 #include <cmath>
 
 #include "pagedkv_latent.h"
@@ -393,26 +394,28 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         do {
             const int32_t *table = a.block_tables + static_cast<long long>(p.b) * a.max_blocks_per_seq;
             const int end = p.t0 + p.tiles;
-            auto row_of = [&](int t) {  // first cache row of this lane's tokens of tile t, or -1
+            constexpr int kNone = INT_MIN;
+            auto block_of = [&](int t) {  // this lane's entry of the table for tile t
                 const int token = t * kTile + lane * box;
-                if (lane >= boxes || token >= p.s.len || t >= end) return -1;
-                int id = table[token >> block_log2];
+                return lane >= boxes || token >= p.s.len || t >= end ? kNone : table[token >> block_log2];
+            };
+            auto row_of = [&](int t, int id) {  // its first cache row, or -1
+                if (id == kNone) return -1;
                 if (id < 0 || id >= a.num_blocks) {
                     flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
                     id = 0;  // some block of the pool: the sequence's result is unspecified
                 }
-                return (id << block_log2) + (token & (a.block_size - 1));
+                return (id << block_log2) + ((t * kTile + lane * box) & (a.block_size - 1));
             };
             auto to_l2 = [&](int row) {
                 if (mine && row >= 0)
                     bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), box * C::E * 2);
             };
-            int row = row_of(p.t0), next = row_of(p.t0 + 1);
-            // rows are looked up an iteration before they are used: a lookup takes as
-            // long as half a tile
-            int far[kAhead];  // for the copies into L2: tiles t + 2 .. t + 1 + kAhead
+            // entries are looked up an iteration before they are used (a lookup takes as
+            // long as half a tile), and at the start all at once, before any is checked
+            int ahead[kAhead + 2];  // tiles t .. t + 1 + kAhead
 #pragma unroll
-            for (int d = 0; d < kAhead; ++d) far[d] = row_of(p.t0 + 2 + d);
+            for (int d = 0; d < kAhead + 2; ++d) ahead[d] = block_of(p.t0 + d);
             if (lane == 0) {
                 ok = wait_or_stop(&sh.q_empty, (k & 1) ^ 1, stop);
                 if (ok) {
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             }
             ++k;
             for (int t = p.t0; t < end; ++t, ++g) {
-                const int s = g % C::STAGES;
+                const int s = g % C::STAGES, row = row_of(t, ahead[0]);
                 const int live = __popc(__ballot_sync(0xffffffffu, row >= 0));
                 // one lane issues: a copy issued by several lanes costs some 100 cycles a lane
                 int groups[kMost];  // of 8 cache rows, or -1
@@ -459,17 +462,13 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 }
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (t == p.t0) {
-                    to_l2(next);
+                if (t == p.t0)
 #pragma unroll
-                    for (int d = 0; d < kAhead - 2; ++d) to_l2(far[d]);
-                }
-                to_l2(far[kAhead - 2]);
-                row = next;
-                next = far[0];
+                    for (int d = 1; d < kAhead; ++d) to_l2(row_of(t + d, ahead[d]));
+                to_l2(row_of(t + kAhead, ahead[kAhead]));
 #pragma unroll
-                for (int d = 0; d < kAhead - 1; ++d) far[d] = far[d + 1];
-                far[kAhead - 1] = row_of(t + 2 + kAhead);
+                for (int d = 0; d < kAhead + 1; ++d) ahead[d] = ahead[d + 1];
+                ahead[kAhead + 1] = block_of(t + 2 + kAhead);
             }
             ok = __all_sync(0xffffffffu, ok);
         } while (ok && next_piece(a, C::ROWS, &w, &p));
