@@ -104,11 +104,14 @@ __device__ __forceinline__ Turn load_turn(const float *cs, int j, int rot, bool 
     return t;
 }
 
-// Rotates the 8 entries y (entries 8 j .. of a vector) by t.  Split halves: the
-// partner entries are rot / 16 lanes up or down; every lane of the warp calls this.
+// Rotates the 8 entries y (entries 8 j .. of a vector) by t; those beyond rot stay bit
+// for bit (cos 1 and sin 0 would make NaN of an infinity and 0 of -0).  Split halves:
+// the partner entries are rot / 16 lanes up or down; every lane of the warp calls this.
 __device__ __forceinline__ void rotate8(float2 (&y)[4], const Turn &t, int j, int rot,
                                         bool interleaved) {
+    const bool turns = 8 * j < rot;
     if (interleaved) {
+        if (!turns) return;
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // (a cos - b sin, b cos + a sin)
             y[i] = fma2(y[i], make_float2(t.c[i], t.c[i]),
@@ -122,8 +125,9 @@ __device__ __forceinline__ void rotate8(float2 (&y)[4], const Turn &t, int j, in
     for (int i = 0; i < 4; ++i) {
         const float2 other = make_float2(__shfl_sync(0xffffffffu, y[i].x, src),
                                          __shfl_sync(0xffffffffu, y[i].y, src));
-        y[i] = fma2(other, make_float2(t.s[2 * i], t.s[2 * i + 1]),
-                    mul2(y[i], make_float2(t.c[2 * i], t.c[2 * i + 1])));
+        if (turns)
+            y[i] = fma2(other, make_float2(t.s[2 * i], t.s[2 * i + 1]),
+                        mul2(y[i], make_float2(t.c[2 * i], t.c[2 * i + 1])));
     }
 }
 
@@ -211,13 +215,13 @@ __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs 
     const long long dst =
         is_q ? (static_cast<long long>(token) * H + first) * d + 8 * j
              : ((block * Hk + first) * a.block_size + row) * d + 8 * j;
-    const int step = per * d * (is_q ? 1 : a.block_size);
+    const long long step = static_cast<long long>(per * d) * (is_q ? 1 : a.block_size);
     unsigned char *cache = static_cast<unsigned char *>(is_v ? a.v_cache : a.k_cache);
     if (is_v) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (!inside || first + u * per >= heads) continue;
-            const long long at = dst + static_cast<long long>(u) * step;
+            const long long at = dst + u * step;
             if (F8) {
                 float2 y[4];
                 unpack8(raw[u], y);
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs 
         }
         if (turns) rotate8(y, turn, j, a.rot_dim, INTERLEAVED);
         if (!inside || first + u * per >= heads) continue;
-        const long long at = dst + static_cast<long long>(u) * step;
+        const long long at = dst + u * step;
         if (is_q)
             __stcs(reinterpret_cast<uint4 *>(static_cast<__half *>(a.q_out) + at), pack8(y));
         else if (F8)

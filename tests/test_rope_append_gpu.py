@@ -180,6 +180,25 @@ def test_padding_and_bad_tokens():
     _check(p, False, res, keep, np.full((12, 4, 64), 9.0, np.float16))
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d, rot", [(64, 32), (128, 16), (80, 48), (128, 0)])
+def test_entries_beyond_the_rotation_stay_bit_for_bit(d, rot, interleaved):
+    """Without a norm, the entries that no rotation reaches are the input's bits:
+    infinities, negative zeros and subnormals among them."""
+    p = Problem(40, 4, 2, d, rot, 16, 31, norm=False)
+    odd = np.array([np.inf, -np.inf, -0.0, 0.0, 2.0 ** -24, 65504.0], np.float16)
+    for x in (p.q, p.k):
+        x[..., rot:] = np.random.default_rng(3).choice(odd, x[..., rot:].shape)
+    q, k, v = (_t(x) for x in (p.q, p.k, p.v))
+    kc, vc = _t(p.kc), _t(p.vc)
+    out = pkv.paged_qk_norm_rope_append(q, k, v, None, None, EPS, _t(p.cs),
+                                        _t(p.pos) if rot else None, _t(p.slots), kc, vc,
+                                        interleaved=interleaved).cpu().numpy()
+    kc = kc.cpu().numpy()[p.slots // 16, :, p.slots % 16]
+    assert np.array_equal(out[..., rot:].view(np.uint16), p.q[..., rot:].view(np.uint16))
+    assert np.array_equal(kc[..., rot:].view(np.uint16), p.k[..., rot:].view(np.uint16))
+
+
 def test_no_tokens():
     p = Problem(1, 4, 2, 64, 64, 16, 9)
     e = torch.empty(0, 4, 64, dtype=torch.float16, device="cuda")
