@@ -266,6 +266,8 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
     if (num_blocks <= 0 || !scale_ok(scale)) return PKV_ERR_INVALID_ARG;
     if (!query_start && (total_q != num_seqs || (num_seqs > 0 && max_q_len != 1)))
         return PKV_ERR_INVALID_ARG;
+    if (block_size > 0 && num_blocks > INT32_MAX / block_size)  // rows are numbered in 32 bits
+        return PKV_ERR_UNSUPPORTED;
     LatentPlan plan{};
     const int rc = make_latent_plan(num_seqs, total_q, max_q_len, n_q_heads, latent_dim, rope_dim,
                                     block_size, max_blocks_per_seq, max_context_len, &plan);
@@ -278,7 +280,6 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
         return PKV_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < plan.split.ws_bytes || !aligned(workspace, 256))
         return PKV_ERR_WORKSPACE;
-    if (num_blocks * block_size >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;  // 32-bit rows
     pkv::LatentAttentionArgs a{};
     a.out = out;
     a.q = q;
@@ -353,7 +354,7 @@ int latent_prefill_attention(void *out, const void *q, const void *kv, const voi
     a.num_seqs = num_seqs;
     a.total_q = total_q;
     a.total_kv = total_kv;
-    a.max_q_len = max_q_len;
+    a.max_q_len = max_q_len < total_q ? max_q_len : total_q;  // CTAs for no more rows than there are
     a.max_kv_len = max_kv_len;
     a.scale_log2 = scale_log2_of(scale);
     a.negate = scale < 0.f;

@@ -437,6 +437,13 @@ def test_prefill_captured_and_replayed():
     _check_prefill(q, kv, kr, qs2, ks2, 0.07, (out.cpu().numpy(), lse.cpu().numpy(), 0), "replay 2")
 
 
+def test_prefill_with_the_largest_bounds():
+    """Host bounds far above the lengths, up to the largest int."""
+    q, kv, kr, qs, ks = _prefill_problem([130, 1], [200, 90], 2, 64, 12)
+    top = 2 ** 31 - 1
+    _check_prefill(q, kv, kr, qs, ks, 0.09, _prefill(q, kv, kr, qs, ks, 0.09, top, top), "bounds")
+
+
 def test_prefill_neighbours_do_not_leak():
     """NaN in the rows of another sequence and beyond the last one stays there."""
     nq, nk = [70, 33, 200], [70, 150, 200]

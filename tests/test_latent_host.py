@@ -105,6 +105,13 @@ def test_latent_attention_refusals(lib):
         assert _call(fn, AT, **change) == UNSUPPORTED, change
 
 
+def test_latent_attention_refuses_pools_beyond_32_bit_rows(lib):
+    """Cache rows are numbered in 32 bits: refused before the workspace is looked at."""
+    one = dict(AT, num_seqs=1, total_q=1)
+    for blocks in (1 << 27, 1 << 60, (1 << 63) - 1):
+        assert _call(lib.paged_latent_attention, one, NB=blocks) == UNSUPPORTED
+
+
 GA = dict(latents=P, ropes=P, cache=P, tables=P, start=P, num_seqs=2, total=0, MB=8, NB=64, R=512,
           P=64, bs=16, err=0, stream=0)
 
