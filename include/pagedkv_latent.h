@@ -56,8 +56,9 @@ extern "C" {
  *  q_rope, q_out  device fp16, may both be NULL (no queries): entry (i, h) of
  *                 rope_dim values at element i * token_stride + h *
  *                 head_stride; q_out may be q_rope with the same strides, and
- *                 is otherwise disjoint from it.  Strides: multiples of 8;
- *                 head strides at least rope_dim.
+ *                 is otherwise disjoint from it.  Strides: multiples of 8,
+ *                 head strides at least rope_dim, token strides at least
+ *                 (n_q_heads - 1) * head_stride + rope_dim.
  *  latent_dim     a multiple of 8, at most 1024; rope_dim a multiple of 16, at
  *                 most 256
  * Padding tokens (negative slots), bad slots and positions: as for
@@ -101,12 +102,14 @@ int paged_latent_append(const void *kv, int64_t kv_stride, const void *weight, f
  * Logits, softmax and sums in fp32; the softmax weights are rounded to fp16
  * for the product with the values.  Rows behind a sequence's length are never
  * read into a result, whatever they hold; a cached row that is not finite
- * reaches every query of its sequence in whose last 64-token tile it lies, those
- * before it included (their weight for it is 0, and 0 times infinity is NaN).  A sequence whose tokens, length or rows
- * are out of bounds sets PKV_ERRBIT_CONTEXT and its rows are left unwritten;
- * a bad block id sets PKV_ERRBIT_BLOCK_ID, and the results of the sequence
- * that names it are unspecified.
- * At most 4096 sequences (PKV_ERR_UNSUPPORTED beyond).
+ * may reach every query of its sequence whose attended rows end in the same
+ * 64-token tile or behind it, those before it included (their weight for it is
+ * 0, and 0 times infinity is NaN).
+ * A sequence whose tokens, length or rows are out of bounds sets
+ * PKV_ERRBIT_CONTEXT and its rows are left unwritten; a bad block id sets
+ * PKV_ERRBIT_BLOCK_ID, and the results of the sequence that names it are
+ * unspecified.  At most 4096 sequences and fewer than 2^31 cache rows
+ * (PKV_ERR_UNSUPPORTED beyond).
  */
 int paged_latent_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int latent_dim,
                       int rope_dim, int block_size, int max_blocks_per_seq, int max_context_len,

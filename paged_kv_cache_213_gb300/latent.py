@@ -63,8 +63,8 @@ def paged_latent_append(kv, weight, eps, cos_sin, positions, slot_mapping, cache
     kv[:, R:] (cos_sin [max_positions, P] fp32, positions [T] int32) go to
     slot_mapping [T] int64.  kv [T, R + P] fp16, any stride between tokens.
     With q_rope [T, H, P] the position part of the queries is rotated into
-    q_out [T, H, P] (both any strides between tokens and heads, e.g.
-    q[..., d:] and absorbed[..., R:]; q_out may be q_rope)."""
+    q_out [T, H, P] (both with gaps between heads and tokens if need be, tokens
+    outermost: q[..., d:] and absorbed[..., R:]; q_out may be q_rope)."""
     dev, cp, NB, bs, E = _cache(cache)
     kp = _at_strided(kv, "kv", _F16, dev)
     shape = kv.shape
