@@ -363,7 +363,9 @@ int latent_prefill_attention(void *out, const void *q, const void *kv, const voi
     a.rope_dim = rope_dim;
     a.lse_out = lse_out;
     a.err = err_word;
-    return status_of(pkv::launch_latent_prefill(a, static_cast<cudaStream_t>(cuda_stream)));
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    return status_of(pkv::launch_latent_prefill(a, sms, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 }  // extern "C"

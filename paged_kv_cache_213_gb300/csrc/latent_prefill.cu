@@ -18,6 +18,9 @@
 // 2140 are products.  4096 tokens x 128 heads: 509 us, 1352 TFLOP/s (70 % of what a
 // large bf16 matrix product reaches).
 //
+// Where there are few items, a cluster of two or four CTAs has one, each a part of its
+// keys, and joins the parts through shared memory.
+//
 // Why 96 keys a step: two steps of keys and values (2 x 60 KB) fit beside the two
 // tiles' queries (96 KB); with 128 there is room for one and a half, and the values
 // of a step would come a copy's latency late.
@@ -68,18 +71,22 @@ struct Shared {
     int stop;
 };
 
-// One CTA's worth of work: two neighbouring tiles of query rows of one head.
+// One CTA's worth of work: two neighbouring tiles of query rows of one head and, in a
+// cluster of CL CTAs, this CTA's part of their key steps.
 struct Item {
     int h, pair, q0, n, k0, m;
     int steps[2], total;  // key steps of the tiles, and of both
+    int whole, first;     // those of the whole cluster; the first key of this CTA's
 };
 
 // The work of CTA `cta`; false when it has none.
+template <int CL>
 __device__ __forceinline__ bool load_item(const LatentPrefillArgs &a, const uint3 &cta, bool tell,
                                           Item *it) {
     const int seq = cta.z;
     it->h = cta.y;
-    it->pair = gridDim.x - 1 - cta.x;  // the longest rows first
+    it->pair = (gridDim.x - 1 - cta.x) / CL;  // the longest rows first
+    it->whole = it->first = 0;
     it->q0 = a.q_start[seq];
     it->n = a.q_start[seq + 1] - it->q0;
     it->k0 = a.kv_start[seq];
@@ -96,7 +103,14 @@ __device__ __forceinline__ bool load_item(const LatentPrefillArgs &a, const uint
         const int last = min(first + kRows, it->n) - 1;
         it->steps[t] = first < it->n ? (it->m - it->n + last + kKeys) / kKeys : 0;
     }
-    it->total = max(it->steps[0], it->steps[1]);
+    it->whole = it->total = max(it->steps[0], it->steps[1]);
+    if (CL > 1) {
+        const int rank = cta.x % CL, from = it->whole * rank / CL;
+        it->total = it->whole * (rank + 1) / CL - from;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) it->steps[t] = min(max(it->steps[t] - from, 0), it->total);
+        it->first = from * kKeys;
+    }
     return it->total > 0;
 }
 
@@ -107,6 +121,7 @@ struct Items {
     int k;  // items read
 
     // The next item, or false at the end (or when the kernel gives up).
+    template <int CL>
     __device__ bool advance(const LatentPrefillArgs &a, Shared &sh, bool whole_warp, Item *it) {
         volatile int *stop = &sh.stop;
         const int s = k & 1;
@@ -117,11 +132,102 @@ struct Items {
         ++k;
         if (whole_warp) __syncwarp();
         if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(&sh.item_free[s]);
-        return c.w != 0 && load_item(a, make_uint3(c.x, c.y, c.z), false, it);
+        return c.w != 0 && load_item<CL>(a, make_uint3(c.x, c.y, c.z), false, it);
     }
 };
 
-template <int D>
+// The CTAs of a cluster have attended a part of the keys each; CTA c finishes the columns
+// [c D / CL, (c + 1) D / CL) of both tiles.  Every CTA sends the others its rows'
+// references and sums and their columns of O, into the memory of the ring (whose copies
+// and products are over at the first barrier); `part`: this warp's tile had a step.
+template <int D, int CL>
+__device__ __forceinline__ void join_parts(const LatentPrefillArgs &a, const Item &it,
+                                           unsigned char *ring, uint32_t to, bool part, float r,
+                                           float l) {
+    constexpr int W = D / CL;  // columns of a CTA
+    static_assert(CL * 2048 + (CL - 1) * W * 1024 <= Cfg<D>::STAGES * Cfg<D>::STAGE_BYTES, "in the ring");
+    const uint32_t rank = cluster_rank();
+    const int row = threadIdx.x;  // of the 256 of both tiles
+    const bool some = part && l != 0.f;
+    const uint32_t stats = smem_addr(ring), parts = stats + CL * 2048;
+    __syncwarp();
+    cluster_sync();
+    if (it.whole > 0) {
+#pragma unroll
+        for (int x = 1; x <= CL; ++x) {
+            const uint32_t c = (rank + x) % CL;
+            store_peer2(peer_addr(stats + (rank * 256 + row) * 8, c), some ? r : -INFINITY,
+                        part ? l : 0.f);
+            if (x == CL || !part) continue;
+            // CTA c finds this one's columns in place x - 1
+            const uint32_t dst = peer_addr(parts + ((x - 1) * (W / 4) * 256 + row) * 16, c);
+#pragma unroll
+            for (int v = 0; v < W; v += 16) {
+                uint32_t o[16];
+                tmem_ld16(o, to + c * W + v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) store_peer4(dst + (v / 4 + e) * 4096, o + 4 * e);
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    const int i = 2 * kRows * it.pair + row;  // of the sequence's queries
+    if (it.whole == 0) return;
+    float2 st[CL];  // of the CTAs rank, rank - 1, rank - 2 ..
+    float top = -INFINITY, sum = 0.f, f[CL];
+#pragma unroll
+    for (int x = 0; x < CL; ++x) {
+        st[x] = *reinterpret_cast<const float2 *>(ring + (((rank + CL - x) % CL) * 256 + row) * 8);
+        top = fmaxf(top, st[x].x);
+    }
+#pragma unroll
+    for (int x = 0; x < CL; ++x) {
+        f[x] = st[x].y == 0.f ? 0.f : ex2(st[x].x - top);
+        sum += st[x].y * f[x];
+    }
+    const float inv = 1.f / sum;
+    const long long at = static_cast<long long>(it.q0 + i) * a.n_heads + it.h;
+    uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + at * D + rank * W);
+    const float4 *others = reinterpret_cast<const float4 *>(ring + CL * 2048) + row;
+#pragma unroll
+    for (int v = 0; v < W; v += 16) {
+        float y[16];
+        uint32_t o[16];
+        if (part) {
+            tmem_ld16(o, to + rank * W + v);
+            tmem_wait_ld();
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = f[0] != 0.f ? __uint_as_float(o[e]) * f[0] : 0.f;
+#pragma unroll
+        for (int x = 1; x < CL; ++x) {
+            if (f[x] == 0.f) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 z = others[((x - 1) * (W / 4) + v / 4 + e) * 256];
+                y[4 * e] += z.x * f[x];
+                y[4 * e + 1] += z.y * f[x];
+                y[4 * e + 2] += z.z * f[x];
+                y[4 * e + 3] += z.w * f[x];
+            }
+        }
+        if (i < it.n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[k] = pack_half2(y[8 * e + 2 * k] * inv, y[8 * e + 2 * k + 1] * inv);
+                out[v / 8 + e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    if (rank == 0 && a.lse_out && i < it.n) a.lse_out[at] = (top + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <int D, int CL>
 __global__ void __launch_bounds__(kThreads, 1)
     latent_prefill_kernel(const LatentPrefillArgs a, const __grid_constant__ CUtensorMap mq,
                           const __grid_constant__ CUtensorMap mkv,
@@ -181,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Steps count on over the items.
             int f = 0;
             int q[2] = {0, 0};  // query tiles so far
-            bool ok = true, open = true;  // open: the hardware may have more CTAs
+            bool ok = true, open = CL == 1;  // open: the hardware may have more CTAs
             int answers = 0, handed = 0;
             Item last;        // whose final values are still to come
             auto ask = [&] {  // for the CTA after the one at hand
@@ -192,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // hands on the item of `cta`, or of the first CTA after it that has one;
             // the next answer is then under way
             auto hand_on = [&] {
-                bool have = load_item(a, cta, true, &it);
+                bool have = load_item<CL>(a, cta, true, &it);
                 while (ok && !have && open) {
                     ok = wait_or_stop(&sh.answered, answers & 1, stop);
                     if (!ok) break;
@@ -201,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     if (open) {
                         ask();
-                        have = load_item(a, cta, true, &it);
+                        have = load_item<CL>(a, cta, true, &it);
                     }
                 }
                 const int s = handed & 1;
@@ -223,18 +329,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int p = 0; p < C::VP; ++p)
                         tma_load_3d(st + ((f - 1) % C::STAGES) * C::STAGE_BYTES + (C::KP + p) * kKPlane,
-                                    &mkv, D + 64 * p, vi->h, vi->k0 + vj * kKeys, &sh.full[s]);
+                                    &mkv, D + 64 * p, vi->h, vi->k0 + vi->first + vj * kKeys, &sh.full[s]);
                 if (ki) {
 #pragma unroll 1
                     for (int p = 0; p < D / 64; ++p)
                         tma_load_3d(st + s * C::STAGE_BYTES + p * kKPlane, &mkv, 64 * p, ki->h,
-                                    ki->k0 + kj * kKeys, &sh.full[s]);
+                                    ki->k0 + ki->first + kj * kKeys, &sh.full[s]);
                     tma_load_2d(st + s * C::STAGE_BYTES + (D / 64) * kKPlane, &mr, 0,
-                                ki->k0 + kj * kKeys, &sh.full[s]);
+                                ki->k0 + ki->first + kj * kKeys, &sh.full[s]);
                 }
                 ++f;
             };
-            ask();
+            if (open) ask();
             bool have = hand_on();
             while (ok && have) {
 #pragma unroll 1
@@ -306,14 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             int sc = 0, qc = 0;  // this tile's steps and items
             int turns = 0;
             bool ok = true;
-            bool more = items.advance(a, sh, false, &it);
+            bool more = items.advance<CL>(a, sh, false, &it);
             int steps = 0, total = 0;  // of the item at hand
             int j = -1;  // its step whose weights come next; -1: only the first scores
             while (ok) {
                 // between the softmax of step j and that of the step after it, which is
                 // step j + 1 of the item or the first of the next one
                 const bool end = j + 1 == total;
-                if (end && j >= 0) more = items.advance(a, sh, false, &it);
+                if (end && j >= 0) more = items.advance<CL>(a, sh, false, &it);
                 if (j < 0 && !more) break;
                 const int pair = j < 0 ? f : f + 1;  // of copies; also the step of its keys
                 ok = wait_or_stop(&sh.full[pair % C::STAGES], (pair / C::STAGES) & 1, stop);
@@ -383,12 +489,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
         const float scale = a.scale_log2;
         int f = 0, sc = 0, mine = 0;  // key steps, this tile's, and its items so far
-        bool have = items.advance(a, sh, true, &it);
+        bool have = items.advance<CL>(a, sh, true, &it);
         bool ok = true;
+        float r = 0.f, l = 0.f;
         while (have) {
             const int i = (2 * it.pair + t) * kRows + (threadIdx.x & 127);
             const int seen = min(it.m - it.n + i + 1, it.m);  // keys this row attends
-            float r = 0.f, l = 0.f;
+            r = l = 0.f;
             for (int j = 0; j < it.steps[t]; ++j, ++sc) {
                 ok = warp_wait_or_stop(&sh.s_full[t], sc & 1, stop);
                 if (!ok) break;
@@ -404,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kKeys; ++c) x[c] = -x[c];
                 }
-                const int left = seen - j * kKeys;
+                const int left = seen - it.first - j * kKeys;
                 if (__any_sync(0xffffffffu, left < kKeys)) {
 #pragma unroll
                     for (int c = 0; c < kKeys; ++c) x[c] = c < left ? x[c] : -INFINITY;
@@ -439,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // values of rows beyond the sequence's keys meet weights of 0: they
                 // must be finite, so the last step's are cleared
-                const int valid = it.m - j * kKeys;
+                const int valid = it.m - it.first - j * kKeys;
                 if (valid < kKeys) {
                     const int s = (f + j) % C::STAGES, pair = f + j + 1;
                     ok = warp_wait_or_stop(&sh.full[pair % C::STAGES], (pair / C::STAGES) & 1, stop);
@@ -479,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 ++mine;
                 tc_fence_after();
+                if (CL > 1) break;  // the parts are joined below
                 const float inv = 1.f / l;
                 const long long row = static_cast<long long>(it.q0 + i) * a.n_heads + it.h;
                 uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + row * D);
@@ -507,9 +615,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (a.lse_out && i < it.n) a.lse_out[row] = (r + log2f(l)) * 0.69314718055994531f;
             }
+            if (CL > 1) break;
             f += it.total;
-            have = items.advance(a, sh, true, &it);
+            have = items.advance<CL>(a, sh, true, &it);
         }
+        if constexpr (CL > 1) {
+            const bool part = have && ok && it.steps[t] > 0;
+            load_item<CL>(a, blockIdx, false, &it);
+            join_parts<D, CL>(a, it, base + C::Q_BYTES, to, part, r, l);
+        }
+    }
+    if (CL > 1 && warp >= 8) {  // the two barriers of join_parts
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     tc_fence_before();
     __syncwarp();
@@ -529,7 +648,9 @@ bool make_map(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+int row_pairs(const LatentPrefillArgs &a) { return (a.max_q_len + 2 * kRows - 1) / (2 * kRows); }
+
+template <int D, int CL>
 cudaError_t launch(const LatentPrefillArgs &a, cudaStream_t stream) {
     using C = Cfg<D>;
     const cuuint64_t H = a.n_heads;
@@ -548,18 +669,44 @@ cudaError_t launch(const LatentPrefillArgs &a, cudaStream_t stream) {
     if (!make_map(&mq, a.q, 3, dq, sq, bq) || !make_map(&mkv, a.kv, 3, dk, sk, bk) ||
         !make_map(&mr, a.k_rope, 2, dr, sr, br))
         return cudaErrorNotSupported;
-    auto kern = latent_prefill_kernel<D>;
+    auto kern = latent_prefill_kernel<D, CL>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t attr = allow_smem(kern, C::SMEM, done);
     if (attr != cudaSuccess) return attr;
-    const dim3 grid((a.max_q_len + 2 * kRows - 1) / (2 * kRows), a.n_heads, a.num_seqs);
-    return launch_pdl(kern, grid, dim3(kThreads), C::SMEM, stream, a, mq, mkv, mr);
+    const dim3 grid(CL * row_pairs(a), a.n_heads, a.num_seqs);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CL;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, mq, mkv, mr);
 }
 
 }  // namespace
 
-cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t stream) {
-    return a.head_dim == 128 ? launch<128>(a, stream) : launch<64>(a, stream);
+cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int sms, cudaStream_t stream) {
+    // Few items: the keys of each are split over a cluster, as long as all CTAs run at
+    // once (items at most: the lengths are on the device).  Resident CTAs, with 2 and
+    // with 4 a cluster, in us, 128-wide heads:
+    //    32 items, 512 rows behind 4000     64.4  40.3  26.9
+    //    32 items, 512 rows                 14.6  13.0  12.1
+    //    64 items, 2 x 512 rows behind 2000 41.7  29.3  38.4
+    //   128 items, 512 rows behind 2000     44.7  58.3  78.2
+    const long long items = static_cast<long long>(row_pairs(a)) * a.n_heads * a.num_seqs;
+    const int cl = 4 * items <= sms ? 4 : 2 * items <= sms ? 2 : 1;
+    if (a.head_dim == 128)
+        return cl == 4 ? launch<128, 4>(a, stream) : cl == 2 ? launch<128, 2>(a, stream)
+                                                             : launch<128, 1>(a, stream);
+    return cl == 4 ? launch<64, 4>(a, stream) : cl == 2 ? launch<64, 2>(a, stream)
+                                                        : launch<64, 1>(a, stream);
 }
 
 }  // namespace pkv

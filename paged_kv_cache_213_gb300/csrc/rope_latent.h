@@ -120,6 +120,6 @@ struct LatentPrefillArgs {
     float *lse_out;
     int32_t *err;
 };
-cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, cudaStream_t stream);
+cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int sms, cudaStream_t stream);
 
 }  // namespace pkv

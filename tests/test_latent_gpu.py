@@ -386,6 +386,20 @@ def test_prefill(nq, nk, H, d):
     _check_prefill(q, kv, kr, qs, ks, scale, got, "prefill")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("empty", [0, 20, 60, 500])
+def test_prefill_beside_empty_sequences(empty, d):
+    """The same sequences with ever more places in the batch that have none: few
+    places split each tile's keys over a cluster's CTAs, many do not."""
+    nq, nk = [200, 1, 129, 40], [420, 96, 129, 97]
+    q, kv, kr, qs, ks = _prefill_problem(nq, nk, 3, d, 71)
+    qs = np.concatenate([qs, np.full(empty, qs[-1])]).astype(np.int32)
+    ks = np.concatenate([ks, np.full(empty, ks[-1])]).astype(np.int32)
+    got = _prefill(q, kv, kr, qs, ks, 0.09, 200, 420)
+    assert got[2] == 0
+    _check_prefill(q, kv, kr, qs, ks, 0.09, got, f"{empty} empty")
+
+
 @pytest.mark.parametrize("factor", [0.0, 20.0, -1.0, -20.0])
 def test_prefill_flat_and_peaked(factor):
     q, kv, kr, qs, ks = _prefill_problem([300, 40], [300, 200], 2, 128, 5)
