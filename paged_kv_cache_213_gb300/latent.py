@@ -9,7 +9,7 @@ import functools
 import torch
 
 from .binding import _check, _need, library
-from .rope import _F16, _F32, _I32, _I64, _U8, _at, _at_strided, _current_device, _launch
+from .rope import _F16, _F32, _I32, _I64, _U8, _at, _at_strided, _current_device, _launch, _native
 
 _bound = None
 
@@ -65,6 +65,9 @@ def paged_latent_append(kv, weight, eps, cos_sin, positions, slot_mapping, cache
     With q_rope [T, H, P] the position part of the queries is rotated into
     q_out [T, H, P] (both with gaps between heads and tokens if need be, tokens
     outermost: q[..., d:] and absorbed[..., R:]; q_out may be q_rope)."""
+    if _native().latent_append(kv, weight, eps, cos_sin, positions, slot_mapping, cache, q_rope,
+                               q_out, interleaved, err_word):
+        return
     dev, cp, NB, bs, E = _cache(cache)
     kp = _at_strided(kv, "kv", _F16, dev)
     shape = kv.shape
@@ -134,6 +137,12 @@ def paged_latent_attention(q, cache, block_tables, context_lens, scale, latent_d
     sequence b owns the rows [query_start[b], query_start[b + 1]), its newest
     tokens (causal; max_q_len bounds their number); None: one token a sequence.
     Returns out [total_q, H, R] fp16: the weighted latents of every head."""
+    done = _native().latent_attention(q, cache, block_tables, context_lens, scale, latent_dim,
+                                      query_start, max_q_len,
+                                      0 if max_context_len is None else max_context_len, out,
+                                      workspace, lse, err_word)
+    if done is not None:
+        return done
     dev, cp, NB, bs, E = _cache(cache)
     qp = _at(q, "q", _F16, dev)
     tables = _at(block_tables, "block_tables", _I32, dev)
@@ -190,6 +199,10 @@ def paged_latent_gather(cache, block_tables, start, total, latent_dim, latents=N
     are the first tokens of sequence b.  cache [NB, bs, R + P] fp16,
     block_tables [B, MB] and start [B + 1] int32, total: rows of the results.
     Returns (latents [total, R], ropes [total, P]) fp16."""
+    done = _native().latent_gather(cache, block_tables, start, total, latent_dim, latents, ropes,
+                                   err_word)
+    if done is not None:
+        return done
     dev, cp, NB, bs, E = _cache(cache)
     tables = _at(block_tables, "block_tables", _I32, dev)
     first = _at(start, "start", _I32, dev)
@@ -225,6 +238,10 @@ def latent_prefill_attention(q, kv, k_rope, q_start, kv_start, scale, max_q_len,
     [total_kv, P], fp16; q_start, kv_start [B + 1] int32: each sequence's query
     rows and key rows (its queries are the newest tokens of its keys).
     max_q_len, max_kv_len: host bounds.  Returns out [total_q, H, d] fp16."""
+    done = _native().latent_prefill(q, kv, k_rope, q_start, kv_start, scale, max_q_len, max_kv_len,
+                                    out, lse, err_word)
+    if done is not None:
+        return done
     _need(q, "q", _F16)
     dev = q.device
     kp = _at(kv, "kv", _F16, dev)

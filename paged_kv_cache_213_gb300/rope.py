@@ -3,10 +3,12 @@ Marshalling only; the work is in the library's CUDA kernels."""
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 
 import torch
 
-from .binding import _check, _need, library
+from .binding import _check, _need, library, library_path
 
 PKV_ERRBIT_POSITION = 0x40
 
@@ -29,10 +31,31 @@ def _lib():
     return _bound
 
 
-# Small calls take as long as the host needs for them, so the marshalling below is
-# spare: each tensor is looked at once (the full checks of _need run where that look
-# fails, for the message), and device, stream and pointers are plain integers (the
-# wrapper objects of torch.cuda cost 2 us a call).
+_calls = None
+
+
+def _native():
+    """The module of ``native/calls.cpp``, which marshals the plain case of each call:
+    small calls take as long as the host needs for them, and this code needs 10 us more.
+    Its functions return None, having launched nothing, for what they do not take; the
+    code below then checks, and calls the library or raises."""
+    global _calls
+    if _calls is None:
+        library()
+        path = os.path.join(os.path.dirname(library_path()), "_pagedkv_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it first "
+                               "(python -m paged_kv_cache_213_gb300.build)")
+        spec = importlib.util.spec_from_file_location("_pagedkv_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _calls = module
+    return _calls
+
+
+# Each tensor is looked at once (the full checks of _need run where that look fails, for
+# the message), and device, stream and pointers are plain integers (the wrapper objects
+# of torch.cuda cost 2 us a call).
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 _F16, _F32, _I32, _I64, _U8 = (torch.float16, torch.float32, torch.int32, torch.int64,
@@ -157,6 +180,10 @@ def paged_qk_norm_rope_append(q, k, v, q_weight, k_weight, eps, cos_sin, positio
     slot_mapping [T] int64 (negative: padding, skipped); caches [NB, Hk, bs, d]
     fp16, in place.  Returns the queries [T, H, d] (q_out, which may be a
     contiguous q)."""
+    done = _native().qk_append(q, k, v, q_weight, k_weight, eps, cos_sin, positions, slot_mapping,
+                               k_cache, v_cache, interleaved, q_out, err_word)
+    if done is not None:
+        return done
     return _append(None, q, k, v, q_weight, k_weight, eps, cos_sin, positions, slot_mapping,
                    k_cache, v_cache, interleaved, q_out, err_word)
 
@@ -165,5 +192,10 @@ def paged_qk_norm_rope_append_fp8(q, k, v, q_weight, k_weight, eps, cos_sin, pos
                                   slot_mapping, k_cache, v_cache, k_scale, v_scale,
                                   interleaved=False, q_out=None, err_word=None):
     """paged_qk_norm_rope_append into E4M3 caches (uint8 codes of value / scale)."""
+    done = _native().qk_append_fp8(q, k, v, q_weight, k_weight, eps, cos_sin, positions,
+                                   slot_mapping, k_cache, v_cache, interleaved, q_out, err_word,
+                                   k_scale, v_scale)
+    if done is not None:
+        return done
     return _append((k_scale, v_scale), q, k, v, q_weight, k_weight, eps, cos_sin, positions,
                    slot_mapping, k_cache, v_cache, interleaved, q_out, err_word)

@@ -554,6 +554,102 @@ def test_copy_on_write_of_a_latent_block():
     assert torch.equal(c[1:], was[1:])
 
 
+class _Calls:
+    """The native marshalling, which has to take every call; or none of them."""
+
+    def __init__(self, real, native):
+        self.real, self.native, self.taken = real, native, 0
+
+    def __getattr__(self, name):
+        def call(*a):
+            if not self.native:
+                return None
+            r = getattr(self.real, name)(*a)
+            assert r is not None, name
+            self.taken += 1
+            return r
+        return call
+
+
+def _one_of_each_call():
+    """Results of every call, with and without what the caller may give."""
+    g = torch.Generator().manual_seed(5)
+
+    def rnd(*s):
+        return torch.randn(*s, generator=g).half().cuda()
+
+    i32 = dict(dtype=torch.int32, device="cuda")
+    T, H, Hk, d, R, P, bs = 5, 4, 2, 128, 512, 64, 16
+    cs, pos = torch.rand(50, P, generator=g).cuda(), torch.arange(T, **i32)
+    slots, err = torch.arange(T, device="cuda") + 3, _err()
+    q, k, v, w = rnd(T, H, d), rnd(T, Hk, d), rnd(T, Hk, d), rnd(d)
+    results = []
+    for out in (None, torch.empty_like(q)):
+        kc, vc = torch.zeros(2, 3, Hk, bs, d, dtype=torch.float16, device="cuda")
+        r = pkv.paged_qk_norm_rope_append(q, k, v, w, None, EPS, cs, pos, slots, kc, vc, q_out=out,
+                                          err_word=err)
+        assert out is None or r is out
+        k8, v8 = torch.zeros(2, 3, Hk, bs, d, dtype=torch.uint8, device="cuda")
+        r8 = pkv.paged_qk_norm_rope_append_fp8(q, k, v, None, w, EPS, None, None, slots, k8, v8, 0.02,
+                                               0.03, interleaved=True, q_out=out)
+        results += [kc, vc, k8, v8, r8.clone()] + ([r] if out is None else [])
+    cache, kv, lw = torch.zeros(4, bs, R + P, dtype=torch.float16, device="cuda"), rnd(40, R + P), rnd(R)
+    pos, slots = torch.arange(40, **i32), torch.arange(40, device="cuda")
+    qr, ab = rnd(40, H, P + 8), torch.zeros(40, H, R + P, dtype=torch.float16, device="cuda")
+    pkv.paged_latent_append(kv, lw, EPS, cs, pos, slots, cache, q_rope=qr[..., 8:], q_out=ab[..., R:])
+    pkv.paged_latent_append(kv[7:8], None, EPS, cs, pos[3:4], slots[:1] + 60, cache, interleaved=True,
+                            err_word=err)
+    results += [cache, ab]
+    bt, lens = torch.tensor([[0, 1, 2]], **i32), torch.tensor([40], **i32)
+    lse = torch.zeros(2, H, device="cuda")
+    ql = rnd(2, H, R + P)
+    ws = torch.empty(pkv.latent_plan(1, 2, 2, H, R, P, bs, 3, 40), dtype=torch.uint8, device="cuda")
+    results += [pkv.paged_latent_attention(ql, cache, bt, lens, 0.05, R, torch.tensor([0, 2], **i32), 2,
+                                           max_context_len=40, workspace=ws, lse=lse), lse]
+    out = torch.empty(1, H, R, dtype=torch.float16, device="cuda")
+    assert pkv.paged_latent_attention(ql[:1], cache, bt, lens, 1, R, out=out, err_word=err) is out
+    st = torch.tensor([0, 40], **i32)
+    lat, rop = pkv.paged_latent_gather(cache, bt, st, 40, R)
+    l2 = torch.empty_like(lat)
+    assert pkv.paged_latent_gather(cache, bt, st, 40, R, latents=l2, err_word=err)[0] is l2
+    ex, qp = rnd(40, H, 2 * d), rnd(40, H, d + P)
+    plse = torch.zeros(40, H, device="cuda")
+    results += [out, lat, rop, l2, pkv.latent_prefill_attention(qp, ex, rop, st, st, 0.07, 40, 40, lse=plse),
+                plse]
+    po = torch.empty_like(ex[..., :d])
+    assert pkv.latent_prefill_attention(qp, ex, rop, st, st, 0.07, 40, 40, out=po, err_word=err) is po
+    assert pkv.get_error(err) == 0
+    return [x.contiguous().cpu().numpy().tobytes() for x in results + [po]]
+
+
+def test_both_marshallings_make_the_same_calls(monkeypatch):
+    """Every call through the native marshalling and through the Python one: the same
+    bits."""
+    from paged_kv_cache_213_gb300 import rope
+    native, python = _Calls(rope._native(), True), _Calls(rope._native(), False)
+    monkeypatch.setattr(rope, "_calls", native)
+    one = _one_of_each_call()
+    monkeypatch.setattr(rope, "_calls", python)
+    other = _one_of_each_call()
+    assert native.taken == 12 and one == other
+
+
+def test_native_marshalling_leaves_the_rest():
+    """What the native marshalling does not take it leaves alone: it returns None."""
+    from paged_kv_cache_213_gb300 import rope
+    f = rope._native().latent_gather
+    c = torch.zeros(4, 16, 576, dtype=torch.float16, device="cuda")
+    bt = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+    st = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    plain = [c, bt, st, 40, 512, None, None, None]
+    assert f(*plain) is not None
+    for at, x in ((0, c.float()), (0, c.cpu()), (0, None), (0, "c"), (0, c[0]), (0, c.transpose(0, 1)),
+                  (1, bt.long()), (2, st[:1]), (3, 40.0), (3, 1 << 40), (3, -1), (4, 576), (4, None),
+                  (5, c), (6, torch.zeros(40, 64)), (7, c)):
+        assert f(*plain[:at], x, *plain[at + 1:]) is None, at
+    assert f(*plain[:-1]) is None and f(*plain, 1) is None and f() is None
+
+
 def test_python_calls_refuse_what_does_not_fit():
     """Types, shapes, strides and devices that the calls do not take."""
     p, q, qs, scale = _problem([20, 30], [1, 1], 4, 512, 16, 98)
