@@ -16,13 +16,14 @@
 //
 // A token's row is 1152 bytes at R = 512 and costs 2 (R + E) flops a row: with 128
 // rows the copy rate and the product rate of the SMs meet.  What bounds the kernel:
-//  few rows    the copies: 32 sequences of 128 .. 2048 tokens x 16 rows 20.8 us, of
+//  few rows    the copies: 32 sequences of 128 .. 2048 tokens x 16 rows 18.5 us, of
 //              which 6 are the bytes at the copy rate and the rest the start (every
-//              SM's first tiles at once, 4 us), one tile's chain and the join;
+//              SM's first tiles at once, 4 us), one tile's chain and the join; 64 of
+//              1000 .. 3000 35.6 us, 4.2 TB/s;
 //  64 rows     two tiles in flight: Q and a tile take 74 KB of shared memory each, and
 //              a tile lives 5500 cycles (copy 1100 .. 1800, scores 1200, softmax 1200,
 //              products 1000, release 700) for 1870 cycles of products.  64 sequences
-//              of 3000 .. 5000 tokens x 128 rows: 101 us, 3.1 TB/s, 708 TFLOP/s.
+//              of 3000 .. 5000 tokens x 128 rows: 96 us, 3.25 TB/s, 742 TFLOP/s.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
