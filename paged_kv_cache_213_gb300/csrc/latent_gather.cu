@@ -18,6 +18,7 @@ constexpr int kRows = 16;
 constexpr int kSteps = 5;  // pieces a thread has in flight: 16 rows of 576 entries in one go
 
 __global__ void __launch_bounds__(kThreads) latent_gather_kernel(const LatentGatherArgs a) {
+    grid_dependency_wait();
     allow_dependent_launch();
     __shared__ long long src[kRows];  // cache row, or -1
     const long long first = static_cast<long long>(blockIdx.x) * kRows;
@@ -74,8 +75,7 @@ __global__ void __launch_bounds__(kThreads) latent_gather_kernel(const LatentGat
 cudaError_t launch_latent_gather(const LatentGatherArgs &a, cudaStream_t stream) {
     const long long blocks = (a.total + kRows - 1) / kRows;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    latent_gather_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(latent_gather_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace pkv

@@ -175,6 +175,7 @@ __device__ __forceinline__ bool token_place(const int64_t *slots, const int32_t 
 // heads into E4M3 took 108 us).  D = 0 is any other size.
 template <bool F8, int U, int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) qk_append_kernel(const QkAppendArgs a) {
+    grid_dependency_wait();
     allow_dependent_launch();  // the attention kernel may get scheduled meanwhile
     const int width = D > 0 ? D / 8 : 1 << a.width_log2;
     const int lane = threadIdx.x & 31, j = lane & (width - 1);
@@ -272,6 +273,7 @@ constexpr int kHeadSteps = 8;  // 8003 tokens x 128 heads: 2 steps 62 us, 4 50.6
 constexpr int kMaxLatentSteps = 4;  // 1024 entries
 
 __global__ void __launch_bounds__(kThreads) latent_append_kernel(const LatentAppendArgs a) {
+    grid_dependency_wait();
     allow_dependent_launch();
     const unsigned job = (blockIdx.x * kThreads + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
@@ -385,11 +387,8 @@ cudaError_t launch_qk(QkAppendArgs a, cudaStream_t stream) {
     const long long threads = static_cast<long long>(a.num_tokens) * a.jobs * 32;
     if (threads > 0xffffffffLL - kThreads) return cudaErrorInvalidValue;
     const unsigned blocks = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
-    if (a.interleaved)
-        qk_append_kernel<F8, U, D, true><<<blocks, kThreads, 0, stream>>>(a);
-    else
-        qk_append_kernel<F8, U, D, false><<<blocks, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(a.interleaved ? qk_append_kernel<F8, U, D, true> : qk_append_kernel<F8, U, D, false>,
+                      dim3(blocks), dim3(kThreads), 0, stream, a);
 }
 
 template <bool F8, int U>
@@ -418,8 +417,7 @@ cudaError_t launch_latent_append(LatentAppendArgs a, cudaStream_t stream) {
     const long long threads = static_cast<long long>(a.num_tokens) * a.jobs * 32;
     const long long blocks = (threads + kThreads - 1) / kThreads;
     if (threads > 0xffffffffLL - kThreads) return cudaErrorInvalidValue;
-    latent_append_kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(latent_append_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace pkv
