@@ -400,6 +400,20 @@ def test_prefill_beside_empty_sequences(empty, d):
     _check_prefill(q, kv, kr, qs, ks, 0.09, got, f"{empty} empty")
 
 
+@pytest.mark.parametrize("factor", [1.0, 20.0, -20.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_single_tiles_among_others(d, factor):
+    """Sequences whose last (or only) rows fill no more than one tile, with an odd and
+    an even number of key steps, between others: 40 heads, so that CTAs take over
+    several in any order."""
+    nq, nk = [1, 128, 40, 129, 300, 7, 100, 384], [500, 128, 1000, 129, 395, 193, 290, 384]
+    q, kv, kr, qs, ks = _prefill_problem(nq, nk, 40, d, 81)
+    scale = factor / np.sqrt(d + 64)
+    got = _prefill(q, kv, kr, qs, ks, scale, 384, 1000)
+    assert got[2] == 0
+    _check_prefill(q, kv, kr, qs, ks, scale, got, "single tiles")
+
+
 @pytest.mark.parametrize("factor", [0.0, 20.0, -1.0, -20.0])
 def test_prefill_flat_and_peaked(factor):
     q, kv, kr, qs, ks = _prefill_problem([300, 40], [300, 200], 2, 128, 5)
