@@ -3,7 +3,7 @@
 // rows: one thread a row finds the row's sequence (binary search over start)
 // and its cache row, then all threads move 16-byte pieces, coalesced on both
 // sides (a row is one contiguous piece of the cache).  72000 rows of 576 entries:
-// 26.8 us, 6.2 TB/s read and written, 91 % of the copy rate (28.4 with
+// 26.7 us, 6.2 TB/s read and written, 92 % of the copy rate (28.4 with
 // the default cache policies: nothing here is used twice).
 #include "pagedkv_latent.h"
 #include "pkv_internal.h"

@@ -15,7 +15,7 @@
 // products.  Bound by the chain of one tile: products 1070 cycles (57 per 96-wide
 // score product: its operands' shared-memory reads, 64 per output product), signal
 // and wait 430, softmax 1100; a step of both tiles takes about 2500 cycles, of which
-// 2140 are products.  4096 tokens x 128 heads: 495 us, 1389 TFLOP/s (72 % of what a
+// 2140 are products.  4096 tokens x 128 heads: 500 us, 1375 TFLOP/s (71 % of what a
 // large bf16 matrix product reaches).
 //
 // Where there are few items, a cluster of two or four CTAs has one, each a part of its

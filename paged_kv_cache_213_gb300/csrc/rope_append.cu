@@ -9,8 +9,8 @@
 // the d/8 threads of a head reduce its sum of squares by shuffles, and the
 // partner of a split-half pair sits a fixed number of lanes away, so nothing
 // goes through shared memory and every input byte is read once.  8191 tokens x 80
-// heads of 128 into E4M3: 59 us, 5.4 TB/s (80 % of the copy rate); 8003 tokens x 128
-// query heads, latent: 47.5 us, 5.9 TB/s; up to some 64 tokens 2.5 us.
+// heads of 128 into E4M3: 60 us, 5.4 TB/s (79 % of the copy rate); 8003 tokens x 128
+// query heads, latent: 47 us, 6.0 TB/s; up to some 64 tokens 2.4 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
