@@ -203,7 +203,7 @@ __host__ __device__ inline Layout layout(int records, int workers, int cl, int r
 }
 
 struct Shared {
-    uint64_t full[4][3], empty[4][3], s_full[2], p_ready[2], pv_done, q_full, q_empty, o_full, o_free, drained[2];
+    uint64_t full[4][3], empty[4][3], s_full[2], p_ready[2], pv_done[2], q_full, q_empty, o_full, o_free, drained[2];
     uint32_t tmem;
     int stop;
     Split split;
@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         mbar_init(&sh.s_full[1], 1);
         mbar_init(&sh.p_ready[0], C::SW);
         mbar_init(&sh.p_ready[1], C::SW);
-        mbar_init(&sh.pv_done, 1);
+        mbar_init(&sh.pv_done[0], 1);
+        mbar_init(&sh.pv_done[1], 1);
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.o_full, 1);
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                                 mma_commit(&sh.empty[g % C::STAGES][part]);
                         }
                     }
-                    mma_commit(&sh.pv_done);
+                    mma_commit(&sh.pv_done[g & 1]);
                 }
                 if (ok) mma_commit(&sh.o_full);
                 ++k;
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     sync_softmax<kSoft>();
                     if (j > 0) {
                         // O^T's columns follow, after the products into it
-                        warp_wait_or_stop(&sh.pv_done, (g - 1) & 1, stop);
+                        warp_wait_or_stop(&sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, stop);
                         tc_fence_after();
 #pragma unroll 1
                         for (int v = 16 * group; v < C::VT * N; v += 16 * C::GROUPS) {
@@ -706,7 +707,14 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[g & 1]);
+                if (lane == 0) {
+                    // The products of two tiles before are done when these weights are
+                    // announced: a wait names its phase by parity alone, so no barrier
+                    // may get two phases ahead of who waits for it, or the softmax two
+                    // tiles ahead of the products (a ring of four stages has room for it).
+                    if (g > 1) wait_or_stop(&sh.pv_done[g & 1], ((g >> 1) & 1) ^ 1, stop);
+                    mbar_arrive(&sh.p_ready[g & 1]);
+                }
             }
             // the row sums, over the tokens of all threads
 #pragma unroll
