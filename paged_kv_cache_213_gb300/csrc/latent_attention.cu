@@ -12,7 +12,7 @@
 // second: with few rows (N = 16 .. 64) no tensor-core row is padding, O^T takes
 // only N TMEM columns a tile, and both operands of the second product are the
 // bytes already in shared memory, read along their other axis.  Above 64 rows two
-// CTAs of a cluster have 64 each and share every tile (multicast copies).
+// CTAs have 64 each; each copies every tile, the second one's from L2.
 //
 // A token's row is 1152 bytes at R = 512 and costs 2 (R + E) flops a row: with 128
 // rows the copy rate and the product rate of the SMs meet.  What bounds the kernel:
@@ -49,8 +49,7 @@ constexpr int kAhead = 2;  // tiles that the copies into L2 run ahead of those i
 // 2^kHead, and up to 2^(kHead + kLag) before r follows; fp16 ends at 2^16.
 constexpr float kHead = 6.f, kLag = 8.f;
 
-// CL: CTAs of a cluster, which share every token tile (each loads a part of it for
-// both) and have N query rows each.
+// CL: CTAs of a worker, which go through the same token tiles with N query rows each.
 template <int R, int N, int CL>
 struct Cfg {
     static constexpr int E = R + 64, PL = E / 64, VT = R / 128;
@@ -187,7 +186,7 @@ __device__ __forceinline__ bool next_piece(const LatentAttentionArgs &a, int row
 
 // Workspace: `records` x CL records {first output row, rows, first and last worker
 // of the segment; no rows: nothing to join}, then per piece slot (two a worker: 0
-// ends a segment or lies inside one, 1 starts one) and CTA of the cluster N pairs
+// ends a segment or lies inside one, 1 starts one) and CTA of the worker N pairs
 // (r, l) and N x R partial sums, four rows of a column together, then the columns.
 struct Layout {
     size_t ml, acc, total;
@@ -256,14 +255,14 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = a.n_q_heads;
     const int worker = blockIdx.x / CL;
-    const int rank = CL > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int rank = blockIdx.x % CL;
     int4 *records = static_cast<int4 *>(a.workspace);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             for (int x = 0; x < C::PARTS; ++x) {
                 mbar_init(&sh.full[s][x], 1);
-                mbar_init(&sh.empty[s][x], CL);
+                mbar_init(&sh.empty[s][x], 1);
             }
         }
         mbar_init(&sh.s_full[0], 1);
@@ -369,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         }
     }
     tc_fence_before();
-    if (CL > 1) cluster_sync(); else __syncthreads();
+    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
@@ -380,15 +379,13 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         if (threadIdx.x == 0 && !sp.by_segment) records[blockIdx.x] = make_int4(0, 0, 0, 0);
     } else if (warp == C::SW) {
         // --- copies ---
-        // a lane looks up `box` tokens of a tile, which one block holds; the cluster's
-        // CTAs share a tile's boxes
-        constexpr int kMost = kTile / CL / 16;  // boxes of this CTA, at most
-        const int box = min(a.block_size, kTile / CL), boxes = kTile / box, own = boxes / CL;
-        const bool mine = lane / own == rank;
+        // a lane looks up `box` tokens of a tile, which one block holds
+        constexpr int kMost = kTile / 16;  // boxes of a tile, at most
+        const int box = min(a.block_size, kTile), boxes = kTile / box;
         const char *cache = static_cast<const char *>(a.cache);
         const int block_log2 = 31 - __clz(a.block_size);
-        // a single CTA's tiles are read once: first to leave L2 (32 sequences x 16 heads
-        // 19.7 -> 18.8 us; with clusters it costs 2 %)
+        // a worker of one CTA reads its tiles once: first to leave L2 (32 sequences x 16
+        // heads 19.7 -> 18.8 us); the tiles of two stay for the other one
         const uint64_t policy = l2_policy_evict_first();
         int g = 0, k = 0;  // tiles, pieces so far
         int begun = 0;     // parts of tiles so far
@@ -410,8 +407,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 return (id << block_log2) + ((t * kTile + lane * box) & (a.block_size - 1));
             };
             auto to_l2 = [&](int row) {
-                if (mine && row >= 0)
-                    bulk_prefetch_l2(cache + static_cast<long long>(row) * (C::E * 2), box * C::E * 2);
+                const int part = box / CL;  // the worker's CTAs fetch a part of each box
+                if (row >= 0)
+                    bulk_prefetch_l2(cache + static_cast<long long>(row + rank * part) * (C::E * 2),
+                                     part * C::E * 2);
             };
             // entries are looked up an iteration before they are used (a lookup takes as
             // long as half a tile), and at the start all at once, before any is checked
@@ -435,15 +434,17 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                 int groups[kMost];  // of 8 cache rows, or -1
 #pragma unroll
                 for (int i = 0; i < kMost; ++i) {
-                    const int r = __shfl_sync(0xffffffffu, row, rank * own + i);
-                    groups[i] = i < own && r >= 0 ? r / 8 : -1;
+                    const int r = __shfl_sync(0xffffffffu, row, i);
+                    groups[i] = r >= 0 ? r / 8 : -1;
                 }
                 if (elect_one()) {
-                    unsigned char *dst = base + s * C::STAGE + rank * (kTile / 8 / CL) * C::GROUP;
+                    unsigned char *dst = base + s * C::STAGE;
 #pragma unroll 1
                     for (int x = 0; x < C::PARTS; ++x) {
                         ok = poll_or_stop(&sh.empty[s][x], ((g / C::STAGES) & 1) ^ 1, stop);
                         if (!ok) break;
+                        // only now: a part's bytes announced while its place still had
+                        // copies of the tile before in flight would count for those
                         uint64_t *full = &sh.full[s][x];
                         if (live > 0)
                             mbar_arrive_expect_tx(full, live * (box / 8) * C::GROUP);
@@ -454,8 +455,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                             if (groups[i] < 0) continue;
                             unsigned char *to = dst + x * C::PART + i * (box / 8) * C::GROUP;
                             if (CL > 1)
-                                tma_load_4d_multicast(to, &mc, 0, 0, x * C::PP, groups[i], full,
-                                                      (1 << CL) - 1);
+                                tma_load_4d(to, &mc, 0, 0, x * C::PP, groups[i], full);
                             else
                                 tma_load_4d(to, &mc, 0, 0, x * C::PP, groups[i], full, policy);
                         }
@@ -549,10 +549,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
 #pragma unroll
                         for (int part = 0; part < C::PARTS; ++part) {
                             if (C::last_reader(part) != v) continue;
-                            if (CL > 1)
-                                mma_commit_multicast(&sh.empty[g % C::STAGES][part], (1 << CL) - 1);
-                            else
-                                mma_commit(&sh.empty[g % C::STAGES][part]);
+                            mma_commit(&sh.empty[g % C::STAGES][part]);
                         }
                     }
                     mma_commit(&sh.pv_done[g & 1]);
@@ -796,8 +793,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
     }
     tc_fence_before();
     __syncwarp();
-    // a peer's copies and commits reach this CTA's memory until both are done
-    if (CL > 1) cluster_sync(); else __syncthreads();
+    __syncthreads();
     if (threadIdx.x == 0 && sh.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
     __syncwarp();
     if (warp == C::SW + 1) tmem_free(tmem, C::TMEM);
@@ -944,26 +940,14 @@ cudaError_t launch(const LatentAttentionArgs &a, const LatentSplit &sp, cudaStre
     CUtensorMap mq, mc;
     if (!make_map(&mq, a.q, static_cast<cuuint64_t>(a.total_q) * a.n_q_heads, C::E, C::PL, 0) ||
         !make_map(&mc, a.cache, static_cast<cuuint64_t>(a.num_blocks) * a.block_size, C::E, C::PP,
-                  (a.block_size < kTile / CL ? a.block_size : kTile / CL) / 8))
+                  (a.block_size < kTile ? a.block_size : kTile) / 8))
         return cudaErrorNotSupported;
     auto kern = latent_attention_kernel<R, N, CL>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t attr = allow_smem(kern, C::SMEM, done);
     if (attr != cudaSuccess) return attr;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(sp.workers * CL);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = CL;
-    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = CL > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, sp, mq, mc);
+    const cudaError_t e = launch_pdl(kern, dim3(sp.workers * CL), dim3(C::THREADS), C::SMEM, stream, a,
+                                     sp, mq, mc);
     if (e != cudaSuccess) return e;
     // more columns a thread where the rows are many: fewer, longer blocks
     constexpr int U = N == 64 ? R / 256 : 1;
@@ -977,12 +961,12 @@ bool latent_split(int num_seqs, int max_q_len, int heads, int latent_dim, int ma
                   LatentSplit *sp) {
     const long long rows = static_cast<long long>(max_q_len) * heads;
     sp->rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    sp->cluster = rows > 64 ? 2 : 1;
-    const int tile = sp->rows * sp->cluster;
+    sp->ctas = rows > 64 ? 2 : 1;
+    const int tile = sp->rows * sp->ctas;
     const long long tiles = (rows + tile - 1) / tile;
     const long long units = tiles * num_seqs * (max_len / kTile + 1);
     if (units >= (1LL << 31)) return false;
-    sp->workers = sms / sp->cluster;
+    sp->workers = sms / sp->ctas;
     // few segments: a record each; more than workers: one for what each worker starts
     sp->by_segment = tiles * num_seqs <= sp->workers;
     sp->records = sp->by_segment ? static_cast<int>(tiles * num_seqs) : sp->workers;
@@ -993,18 +977,18 @@ bool latent_split(int num_seqs, int max_q_len, int heads, int latent_dim, int ma
     const long long segments = tiles * num_seqs > 0 ? tiles * num_seqs : 1;
     const long long pieces = sp->workers / segments / (sp->rows == 64 ? 2 : 1);
     sp->join_threads = pieces >= 16 ? 8 : pieces >= 8 ? 4 : pieces >= 4 ? 2 : 1;
-    sp->ws_bytes = layout(sp->records, sp->workers, sp->cluster, sp->rows, latent_dim).total;
+    sp->ws_bytes = layout(sp->records, sp->workers, sp->ctas, sp->rows, latent_dim).total;
     return true;
 }
 
 cudaError_t launch_latent_attention(const LatentAttentionArgs &a, const LatentSplit &sp,
                                     cudaStream_t stream) {
     if (a.latent_dim == 512)
-        return sp.cluster == 2 ? launch<512, 64, 2>(a, sp, stream)
+        return sp.ctas == 2 ? launch<512, 64, 2>(a, sp, stream)
                : sp.rows == 16 ? launch<512, 16, 1>(a, sp, stream)
                : sp.rows == 32 ? launch<512, 32, 1>(a, sp, stream)
                                : launch<512, 64, 1>(a, sp, stream);
-    return sp.cluster == 2 ? launch<256, 64, 2>(a, sp, stream)
+    return sp.ctas == 2 ? launch<256, 64, 2>(a, sp, stream)
            : sp.rows == 16 ? launch<256, 16, 1>(a, sp, stream)
            : sp.rows == 32 ? launch<256, 32, 1>(a, sp, stream)
                            : launch<256, 64, 1>(a, sp, stream);

@@ -94,10 +94,10 @@ struct LatentAttentionArgs {
     float *lse_out;
     int32_t *err;
 };
-// How a call's work is split: `workers` clusters of `cluster` CTAs with `rows`
+// How a call's work is split: `workers` of `ctas` CTAs with `rows`
 // query rows each, one CTA per SM.
 struct LatentSplit {
-    int rows, cluster, workers;
+    int rows, ctas, workers;
     int by_segment;  // the join's records: one per segment (sequence and row tile), else one per worker
     int records;
     int join_threads;

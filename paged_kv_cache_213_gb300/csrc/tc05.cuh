@@ -198,15 +198,6 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
         : "memory");
 }
 
-// The same on the barrier at this offset in every CTA of the mask's cluster ranks.
-__device__ __forceinline__ void mma_commit_multicast(uint64_t *bar, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(smem_addr(bar)),
-        "h"(mask)
-        : "memory");
-}
-
 // --- clusters ---------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -234,7 +225,16 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 4-D tiled TMA load with an L2 eviction policy; x = innermost coordinate.
+// 4-D tiled TMA loads; x = innermost coordinate.  The second form has an L2 eviction
+// policy.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, int y, int z, int w,
                                             uint64_t *bar, uint64_t policy) {
     asm volatile(
@@ -242,17 +242,6 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, 
         ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)),
         "l"(policy)
-        : "memory");
-}
-// A 4-D load with the default policy, to this offset of every CTA of the mask, completion on the barrier at this
-// offset in each of them.
-__device__ __forceinline__ void tma_load_4d_multicast(void *dst, const void *tmap, int x, int y,
-                                                      int z, int w, uint64_t *bar, uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".multicast::cluster [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_addr(dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)),
-        "h"(mask)
         : "memory");
 }
 
