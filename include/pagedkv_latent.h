@@ -109,7 +109,8 @@ int paged_latent_append(const void *kv, int64_t kv_stride, const void *weight, f
  * PKV_ERRBIT_CONTEXT and its rows are left unwritten; a bad block id sets
  * PKV_ERRBIT_BLOCK_ID, and the results of the sequence that names it are
  * unspecified.  At most 4096 sequences and fewer than 2^31 cache rows
- * (PKV_ERR_UNSUPPORTED beyond).
+ * (PKV_ERR_UNSUPPORTED beyond).  After PKV_ERRBIT_TIMEOUT every result of the call is
+ * unspecified; the workspace needs nothing before the next one.
  */
 int paged_latent_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int latent_dim,
                       int rope_dim, int block_size, int max_blocks_per_seq, int max_context_len,
@@ -167,7 +168,8 @@ int paged_latent_gather(void *latents, void *ropes, const void *cache,
  *  head_dim       64 or 128;  rope_dim 64
  * Needs no workspace.  Rounding as for paged_latent_attention, and so with keys
  * and values that are not finite: rows of other sequences never reach a result,
- * those of the same sequence may within a tile of 128 queries.
+ * those of the same sequence may within a tile of 128 queries.  After
+ * PKV_ERRBIT_TIMEOUT every result of the call is unspecified.
  */
 int latent_prefill_attention(void *out, const void *q, const void *kv, const void *k_rope,
                              const int32_t *q_start, const int32_t *kv_start, int num_seqs,

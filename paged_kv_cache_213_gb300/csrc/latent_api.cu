@@ -302,6 +302,7 @@ int paged_latent_attention(void *out, const void *q, const void *cache,
     a.workspace = workspace;
     a.lse_out = lse_out;
     a.err = err_word;
+    a.first_wait_polls = pkv::test_wait_polls();
     return status_of(pkv::launch_latent_attention(a, plan.split, static_cast<cudaStream_t>(cuda_stream)));
 }
 
@@ -363,6 +364,7 @@ int latent_prefill_attention(void *out, const void *q, const void *kv, const voi
     a.rope_dim = rope_dim;
     a.lse_out = lse_out;
     a.err = err_word;
+    a.first_wait_polls = pkv::test_wait_polls();
     int sms = 0;
     if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
     return status_of(pkv::launch_latent_prefill(a, sms, static_cast<cudaStream_t>(cuda_stream)));

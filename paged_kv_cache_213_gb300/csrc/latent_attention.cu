@@ -205,6 +205,7 @@ struct Shared {
     uint64_t full[4][3], empty[4][3], s_full[2], p_ready[2], pv_done[2], q_full, q_empty, o_full, o_free, drained[2];
     uint32_t tmem;
     int stop;
+    int begun, asked;  // parts of tiles and query copies that were issued
     Split split;
     Walk walk;    // behind the first piece
     Piece first;
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         mbar_init(&sh.o_free, C::SW);
         mbar_init(&sh.drained[0], 1);
         mbar_init(&sh.drained[1], 1);
-        sh.stop = 0;
+        sh.stop = sh.begun = sh.asked = 0;
         sh.first.tiles = 0;
         fence_barrier_init();
     }
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const uint64_t policy = l2_policy_evict_first();
         int g = 0, k = 0;  // tiles, pieces so far
         int begun = 0;     // parts of tiles so far
+        int asked = 0;     // copies of queries so far
         bool ok = true;
         do {
             const int32_t *table = a.block_tables + static_cast<long long>(p.b) * a.max_blocks_per_seq;
@@ -420,6 +422,7 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             if (lane == 0) {
                 ok = wait_or_stop(&sh.q_empty, (k & 1) ^ 1, stop);
                 if (ok) {
+                    ++asked;
                     mbar_arrive_expect_tx(&sh.q_full, C::Q_BYTES);
                     const int row = p.s.q0 * H + p.rt * C::ROWS + rank * N;
                     for (int x = 0; x < N / 8; ++x)
@@ -475,13 +478,9 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             ok = __all_sync(0xffffffffu, ok);
         } while (ok && next_piece(a, C::ROWS, &w, &p));
         begun = __reduce_max_sync(0xffffffffu, begun);
-        if (!ok && lane == 0) {
-            // every copy in flight lands before the CTA gives its memory back
-            mbar_wait_bounded(&sh.q_full, (k - 1) & 1);
-            for (int i = max(0, begun - C::PARTS * C::STAGES); i < begun; ++i) {
-                const int t = i / C::PARTS;
-                mbar_wait_bounded(&sh.full[t % C::STAGES][i % C::PARTS], (t / C::STAGES) & 1);
-            }
+        if (lane == 0) {
+            sh.begun = begun;
+            sh.asked = asked;
         }
     } else if (warp == C::SW + 1) {
         // --- scores ---
@@ -492,9 +491,9 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
             const uint32_t kv = smem_addr(base);
             const uint64_t qd = smem_desc(smem_addr(q_smem), C::Q_GROUP, 0);
             int g = 0, k = 0;
-            bool ok = true;
+            bool ok = first_wait(&sh.full[0][0], 0, a.first_wait_polls, stop);
             do {
-                ok = wait_or_stop(&sh.q_full, k & 1, stop);
+                ok = ok && wait_or_stop(&sh.q_full, k & 1, stop);
 #pragma unroll 1
                 for (int j = 0; j < p.tiles && ok; ++j, ++g) {
                     // the scores' place is free when the weights before last are made
@@ -794,7 +793,16 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (threadIdx.x == 0 && sh.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+    if (threadIdx.x == 0 && sh.stop) {
+        flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+        // Every copy in flight lands before the CTA gives its memory back.  Not until here:
+        // the copy role may have issued its last one before another role gave up.
+        if (sh.asked > 0) mbar_wait_bounded(&sh.q_full, (sh.asked - 1) & 1);
+        for (int i = max(0, sh.begun - C::PARTS * C::STAGES); i < sh.begun; ++i) {
+            const int t = i / C::PARTS;
+            mbar_wait_bounded(&sh.full[t % C::STAGES][i % C::PARTS], (t / C::STAGES) & 1);
+        }
+    }
     __syncwarp();
     if (warp == C::SW + 1) tmem_free(tmem, C::TMEM);
 }

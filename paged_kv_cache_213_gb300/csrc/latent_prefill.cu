@@ -69,6 +69,9 @@ struct Shared {
     uint4 item[2];  // of the copy role, to the others: a CTA's coordinates, 1; or 0 at the end
     uint32_t tmem;
     int stop;
+    // what the copy role issued: pairs of keys and values, query tiles, and whether (and
+    // which) an answer of the hardware is still to come
+    int begun, queries[2], awaited, answers;
 };
 
 // One CTA's worth of work: two neighbouring tiles of query rows of one head and, in a
@@ -257,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.empty[s], 2);
         }
         mbar_init(&sh.answered, 1);
-        sh.stop = 0;
+        sh.stop = sh.begun = sh.queries[0] = sh.queries[1] = sh.awaited = 0;
         fence_barrier_init();
     }
     if (warp == 9) tmem_alloc(&sh.tmem, 512);
@@ -385,14 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (ok && f > 0) copy_pair(&last, last.total - 1, nullptr, 0);
-            if (!ok) {
-                // every copy in flight lands before the CTA gives its memory back
-                for (int t = 0; t < 2; ++t)
-                    if (q[t] > 0) mbar_wait_bounded(&sh.q_full[t], (q[t] - 1) & 1);
-                for (int i = max(0, f - C::STAGES); i < f; ++i)
-                    mbar_wait_bounded(&sh.full[i % C::STAGES], (i / C::STAGES) & 1);
-                if (open) mbar_wait_bounded(&sh.answered, answers & 1);
-            }
+            sh.begun = f;
+            sh.queries[0] = q[0];
+            sh.queries[1] = q[1];
+            sh.awaited = !ok && open;
+            sh.answers = answers;
         }
     } else if (warp < 11) {
         // --- matrix products ---
@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int f = 0;       // key steps so far
             int sc = 0, qc = 0;  // this tile's steps and items
             int turns = 0;
-            bool ok = true;
             bool more = items.advance<CL>(a, sh, false, &it);
+            bool ok = !more || first_wait(&sh.full[0], 0, a.first_wait_polls, stop);
             int steps = 0, total = 0;  // of the item at hand
             int j = -1;  // its step whose weights come next; -1: only the first scores
             while (ok) {
@@ -633,7 +633,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (threadIdx.x == 0 && sh.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+    if (threadIdx.x == 0 && sh.stop) {
+        flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+        // Every copy in flight lands before the CTA gives its memory back.  Not until here:
+        // the copy role may have issued its last one before another role gave up.
+        for (int t = 0; t < 2; ++t)
+            if (sh.queries[t] > 0) mbar_wait_bounded(&sh.q_full[t], (sh.queries[t] - 1) & 1);
+        for (int i = max(0, sh.begun - C::STAGES); i < sh.begun; ++i)
+            mbar_wait_bounded(&sh.full[i % C::STAGES], (i / C::STAGES) & 1);
+        if (sh.awaited) mbar_wait_bounded(&sh.answered, sh.answers & 1);
+    }
     __syncwarp();
     if (warp == 9) tmem_free(tmem, 512);
 }

@@ -93,6 +93,7 @@ struct LatentAttentionArgs {
     void *workspace;
     float *lse_out;
     int32_t *err;
+    int first_wait_polls;  // test hook, as in DecodeArgs: the first wait for a tile
 };
 // How a call's work is split: `workers` of `ctas` CTAs with `rows`
 // query rows each, one CTA per SM.
@@ -119,6 +120,7 @@ struct LatentPrefillArgs {
     int n_heads, head_dim, rope_dim;
     float *lse_out;
     int32_t *err;
+    int first_wait_polls;  // test hook, as in DecodeArgs: the first wait for keys
 };
 cudaError_t launch_latent_prefill(const LatentPrefillArgs &a, int sms, cudaStream_t stream);
 

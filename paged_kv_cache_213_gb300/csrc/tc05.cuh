@@ -44,7 +44,16 @@ __device__ __forceinline__ bool poll_or_stop(uint64_t *bar, uint32_t parity, vol
     return false;
 }
 
-// The same by all lanes of a warp: one answer for the whole warp.
+// The test hook in the place of a role's first wait: false after polls + 1 tests without
+// success, and every other role stops too.  polls < 0 (the hook is not set): no wait.
+__device__ __forceinline__ bool first_wait(uint64_t *bar, uint32_t parity, int polls,
+                                           volatile int *stop) {
+    if (polls < 0 || mbar_wait_polls(bar, parity, polls)) return true;
+    *stop = 1;
+    return false;
+}
+
+// wait_or_stop by all lanes of a warp: one answer for the whole warp.
 __device__ __forceinline__ bool warp_wait_or_stop(uint64_t *bar, uint32_t parity,
                                                   volatile int *stop) {
     return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop));
