@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -34,22 +35,43 @@ def _lib():
 _calls = None
 
 
+class _PythonOnly:
+    """In the place of the native module where it is missing: takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+def _load_calls():
+    from . import build as _build
+    path = os.path.join(os.path.dirname(library_path()), "_pagedkv_calls.so")
+    target, built = _build.calls_target(), _build.calls_built_for()
+    why = "missing" if built is None else f"built for {built}, not for {target}"
+    if built is not None and built == target:
+        try:
+            spec = importlib.util.spec_from_file_location("_pagedkv_calls", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            return module
+        except (ImportError, OSError) as e:
+            why = str(e)
+    warnings.warn(f"{path}: {why}; the calls are marshalled in Python, about 10 us slower each "
+                  "(build with python -m paged_kv_cache_213_gb300.build)", RuntimeWarning,
+                  stacklevel=4)
+    return _PythonOnly()
+
+
 def _native():
     """The module of ``native/calls.cpp``, which marshals the plain case of each call:
     small calls take as long as the host needs for them, and this code needs 10 us more.
     Its functions return None, having launched nothing, for what they do not take; the
-    code below then checks, and calls the library or raises."""
+    code below then checks, and calls the library or raises.  Where the module is
+    missing or was built for another torch, a warning says so once, and this code does
+    all of it."""
     global _calls
     if _calls is None:
         library()
-        path = os.path.join(os.path.dirname(library_path()), "_pagedkv_calls.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it first "
-                               "(python -m paged_kv_cache_213_gb300.build)")
-        spec = importlib.util.spec_from_file_location("_pagedkv_calls", path)
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        _calls = module
+        _calls = _load_calls()
     return _calls
 
 
