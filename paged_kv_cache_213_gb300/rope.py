@@ -78,8 +78,8 @@ def _native():
 # Each tensor is looked at once (the full checks of _need run where that look fails, for
 # the message), and device, stream and pointers are plain integers (the wrapper objects
 # of torch.cuda cost 2 us a call).
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # None: a torch without CUDA
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _F16, _F32, _I32, _I64, _U8 = (torch.float16, torch.float32, torch.int32, torch.int64,
                                torch.uint8)
 
