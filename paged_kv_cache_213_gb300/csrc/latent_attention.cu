@@ -707,8 +707,10 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
                     // The products of two tiles before are done when these weights are
                     // announced: a wait names its phase by parity alone, so no barrier
                     // may get two phases ahead of who waits for it, or the softmax two
-                    // tiles ahead of the products (a ring of four stages has room for it).
-                    if (g > 1) wait_or_stop(&sh.pv_done[g & 1], ((g >> 1) & 1) ^ 1, stop);
+                    // tiles ahead of the products.  A ring of two tiles has no room for
+                    // that (there the wait would cost 64 x 128 heads 1.7 %).
+                    if (C::STAGES > 2 && g > 1)
+                        wait_or_stop(&sh.pv_done[g & 1], ((g >> 1) & 1) ^ 1, stop);
                     mbar_arrive(&sh.p_ready[g & 1]);
                 }
             }

@@ -1,8 +1,8 @@
 """Model check of the absorbed latent attention kernel's barriers (host only).
 
 A CTA's roles (copies, scores, outputs' products, softmax) and its asynchronous
-work (tile copies and both warps' products, each in its own order) go through the
-tiles of a piece.  A wait names the phase of its barrier by parity alone, so it
+work (tile copies, both warps' products and what tells of their end, each in its own
+order) go through the tiles of a piece.  A wait names the phase of its barrier by parity alone, so it
 means what it says only while its barrier has completed that phase or is in it: a
 wait one phase further behind passes at once, and one whose phase is followed by
 another completed one never passes.  The model runs every interleaving and reports
@@ -19,7 +19,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SOURCE = os.path.join(ROOT, "paged_kv_cache_213_gb300", "csrc", "latent_attention.cu")
 
 
-def _roles(tiles, stages, ordered):
+def _roles(tiles, stages, halves, waits):
     """Per role a list of ("wait", barrier, phase), ("may", barrier, phase) for a wait
     that some tiles take (the softmax's, where the outputs follow a new reference),
     ("arrive", barrier) and ("issue", engine, barriers that its completion arrives on)."""
@@ -35,21 +35,21 @@ def _roles(tiles, stages, ordered):
         scores.append(("issue", "qk", (f"s_full{g & 1}",)))
         products.append(("wait", f"p_ready{g & 1}", g >> 1))
         # one barrier for all tiles, or one for the even and one for the odd ones
-        done = f"pv_done{g & 1}" if ordered else "pv_done"
-        products.append(("issue", "pv", (f"empty{s}", done)))
+        products.append(("issue", "pv", (f"empty{s}",)))
+        products.append(("issue", "pv", (f"pv_done{g & 1}" if halves else "pv_done",)))
         softmax.append(("wait", f"s_full{g & 1}", g >> 1))
         if g > 0:
-            softmax.append(("may", f"pv_done{(g - 1) & 1}", (g - 1) >> 1) if ordered else
+            softmax.append(("may", f"pv_done{(g - 1) & 1}", (g - 1) >> 1) if halves else
                            ("may", "pv_done", g - 1))
-        if ordered and g > 1:
+        if waits and g > 1:
             softmax.append(("wait", f"pv_done{g & 1}", (g >> 1) - 1))
         softmax.append(("arrive", f"p_ready{g & 1}"))
     return copies, scores, products, softmax
 
 
-def faults(tiles, stages, ordered):
+def faults(tiles, stages, halves, waits):
     """The waits (role, step) that some interleaving reaches too early or too late."""
-    roles = _roles(tiles, stages, ordered)
+    roles = _roles(tiles, stages, halves, waits)
     engines = ("tma", "qk", "pv")
     names = sorted({x for r in roles for step in r for x in
                     (step[2] if step[0] == "issue" else (step[1],))})
@@ -96,25 +96,31 @@ def faults(tiles, stages, ordered):
     return found
 
 
-def _kernel_is_ordered():
-    """Whether the kernel's softmax waits for the products of two tiles before ahead
-    of its arrival on p_ready."""
+def _kernel(stages):
+    """(halves, waits) of the kernel's form with this ring: whether even and odd tiles
+    have a barrier each for the end of their products, and whether the softmax waits for
+    the products of two tiles before ahead of its arrival on p_ready."""
     text = open(SOURCE).read()
     m = re.search(r"fence_proxy_async_smem\(\);\s*__syncwarp\(\);(.*?)"
                   r"mbar_arrive\(&sh\.p_ready\[g & 1\]\);", text, flags=re.S)
     assert m, "the arrival on p_ready is not where it was"
-    return "&sh.pv_done[g & 1]" in m.group(1)
+    wait = re.search(r"if \((C::STAGES > 2 && )?g > 1\)\s*wait_or_stop\(&sh\.pv_done\[g & 1\]",
+                     m.group(1))
+    return "pv_done[2]" in text, wait is not None and (stages > 2 or not wait.group(1))
 
 
 @pytest.mark.parametrize("stages", [2, 4])
 def test_every_wait_is_in_its_phase(stages):
-    assert faults(9, stages, _kernel_is_ordered()) == set()
+    assert faults(9, stages, *_kernel(stages)) == set()
 
 
 def test_the_model_finds_the_missing_wait():
     """Without the softmax's wait for earlier products a ring of four stages lets it
     run two tiles ahead of them: its own wait for them passes a phase early, and the
-    products' wait for weights can be two phases late.  A ring of two does not."""
+    products' wait for weights can be two phases late.  A ring of two does not, once
+    even and odd tiles have a barrier each."""
     softmax, products = 3, 2
-    assert {role for role, _ in faults(9, 4, False)} >= {softmax, products}
-    assert not faults(9, 2, False)
+    for halves in (False, True):
+        assert {role for role, _ in faults(9, 4, halves, False)} >= {softmax, products}
+    assert {role for role, _ in faults(9, 2, False, False)} == {softmax}
+    assert not faults(9, 2, True, False)
