@@ -81,7 +81,7 @@ int paged_latent_append(const void *kv, int64_t kv_stride, const void *weight, f
  *   out[i][h][:] = sum_t softmax_t(scale * q[i][h] . row_t) row_t[0:latent_dim]
  *
  * over the rows t of the token's sequence up to and including its own
- * position.  One kernel over an even split of the batch's (sequence, query
+ * position (the scaled logits within fp32's range).  One kernel over an even split of the batch's (sequence, query
  * rows, tokens) work, then one that joins the pieces by log-sum-exp.
  *
  *  q              device fp16 [total_q][n_q_heads][latent_dim + rope_dim]
@@ -92,7 +92,8 @@ int paged_latent_append(const void *kv, int64_t kv_stride, const void *weight, f
  *                 causal); NULL: one token a sequence (total_q == num_seqs,
  *                 max_q_len 1), where a context length of 0 gives out = 0 and
  *                 lse = -inf
- *  max_q_len      host upper bound of the tokens of one sequence
+ *  max_q_len      host upper bound of the tokens of one sequence; with 0, as with
+ *                 total_q 0, the call does nothing and flags nothing
  *  latent_dim     256 or 512;  rope_dim 64;  block_size 16, 32, 64, 128 or 256
  *  max_context_len, block_tables, context_lens, err_word, cuda_stream: as for
  *                 paged_decode_attention_multi
@@ -162,7 +163,9 @@ int paged_latent_gather(void *latents, void *ropes, const void *cache,
  *                 set PKV_ERRBIT_CONTEXT, and the sequence's rows are left
  *                 unwritten.
  *  max_q_len, max_kv_len   host upper bounds of n_b and m_b (a longer sequence
- *                 is flagged as out of bounds)
+ *                 is flagged as out of bounds; with max_q_len 0, as with total_q
+ *                 0, the call does nothing and flags nothing).  A sequence of
+ *                 more than 2^27 keys may run out a wait (PKV_ERRBIT_TIMEOUT).
  *  out            device fp16 [total_q][n_heads][head_dim];  lse_out fp32
  *                 [total_q][n_heads], may be NULL
  *  head_dim       64 or 128;  rope_dim 64

@@ -19,11 +19,17 @@
 //  few rows    the copies: 32 sequences of 128 .. 2048 tokens x 16 rows 18.5 us, of
 //              which 6 are the bytes at the copy rate and the rest the start (every
 //              SM's first tiles at once, 4 us), one tile's chain and the join; 64 of
-//              1000 .. 3000 35.6 us, 4.2 TB/s;
+//              1000 .. 3000 35.4 us, 4.2 TB/s;
 //  64 rows     two tiles in flight: Q and a tile take 74 KB of shared memory each, and
-//              a tile lives 5500 cycles (copy 1100 .. 1800, scores 1200, softmax 1200,
-//              products 1000, release 700) for 1870 cycles of products.  64 sequences
-//              of 3000 .. 5000 tokens x 128 rows: 96 us, 3.25 TB/s, 742 TFLOP/s.
+//              a tile lives about 5500 cycles (copy 1100 .. 1800, scores 1200, softmax
+//              1200, products 1000, release 700) for 1870 cycles of products, of which
+//              the scores' 1150 are the reads of their operands (4 KB for 16 cycles of
+//              arithmetic).  64 sequences of 3000 .. 5000 tokens x 128 rows: 95 us,
+//              3.3 TB/s, 750 TFLOP/s.
+// P^T is fp16 because the other operand of its product, the cached value, is: half a
+// step of each weight, 2^-11, as much as the result's own rounding.  The row sums take
+// the weights before that rounding; they, the references and O^T are fp32, in the pieces
+// and in the join too.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -385,8 +391,12 @@ __global__ void __launch_bounds__(Cfg<R, N, CL>::THREADS, 1)
         const int box = min(a.block_size, kTile), boxes = kTile / box;
         const char *cache = static_cast<const char *>(a.cache);
         const int block_log2 = 31 - __clz(a.block_size);
-        // a worker of one CTA reads its tiles once: first to leave L2 (32 sequences x 16
-        // heads 19.7 -> 18.8 us); the tiles of two stay for the other one
+        // a worker of one CTA reads its tiles once: first to leave L2.  Unshared blocks
+        // gain (32 x 128 .. 2048 tokens x 16 heads 20.2 -> 19.0 us, 64 x 1000 .. 3000
+        // 37.9 -> 37.4, the same with latents of 256 23.8 -> 21.8), a prefix that many
+        // sequences share loses (32 or 64 behind 2048 tokens nothing, 64 behind 8192
+        // 85.8 -> 89.5, 200 x 32 heads behind 4096 172 -> 184).  The tiles of a worker of
+        // two CTAs stay for the other one.
         const uint64_t policy = l2_policy_evict_first();
         int g = 0, k = 0;  // tiles, pieces so far
         int begun = 0;     // parts of tiles so far

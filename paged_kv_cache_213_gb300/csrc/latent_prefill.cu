@@ -15,8 +15,14 @@
 // products.  Bound by the chain of one tile: products 1070 cycles (57 per 96-wide
 // score product: its operands' shared-memory reads, 64 per output product), signal
 // and wait 430, softmax 1100; a step of both tiles takes about 2500 cycles, of which
-// 2140 are products.  4096 tokens x 128 heads: 500 us, 1375 TFLOP/s (71 % of what a
-// large bf16 matrix product reaches).
+// 2140 are products.  4096 tokens x 128 heads: 538 us in calls one after another, 1277
+// TFLOP/s (66 % of what a large bf16 matrix product reaches in a burst); 503 us behind
+// less work (six calls in a graph): the clock follows the power drawn before.
+//
+// P is fp16 because the values, the other operand of its product, are: half a step of
+// each weight, 2^-11, as much as the result's own rounding.  The row sums take the
+// weights before that rounding; they, the references and O are fp32, and so are the
+// parts that a cluster joins.
 //
 // Where there are few items, a cluster of two or four CTAs has one, each a part of its
 // keys, and joins the parts through shared memory.
@@ -45,7 +51,7 @@ namespace {
 constexpr int kP = 64;          // rotated entries
 constexpr int kRows = 128;      // query rows of a tile
 constexpr int kKeys = 96;       // key rows of a step
-constexpr int kThreads = 384;   // two softmax warpgroups; copy warp, MMA warp, two idle ones
+constexpr int kThreads = 384;   // two softmax warpgroups; copy warp, two MMA warps, an idle one
 // Registers move from the third warpgroup to the softmax: 8 x 32 x 208 + 4 x 32 x 88
 // is the 12 x 32 x 168 of the launch.
 constexpr int kQPlane = kRows * 128, kKPlane = kKeys * 128;  // 64 columns of a tile, bytes
