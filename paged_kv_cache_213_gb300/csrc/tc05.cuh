@@ -44,11 +44,12 @@ __device__ __forceinline__ bool poll_or_stop(uint64_t *bar, uint32_t parity, vol
     return false;
 }
 
-// The test hook in the place of a role's first wait: false after polls + 1 tests without
-// success, and every other role stops too.  polls < 0 (the hook is not set): no wait.
+// The test hook ahead of a role's first wait: false after that many tests without success
+// (0: at once, whatever has landed), and every other role stops too.  polls < 0 (the hook
+// is not set): true, and no wait.
 __device__ __forceinline__ bool first_wait(uint64_t *bar, uint32_t parity, int polls,
                                            volatile int *stop) {
-    if (polls < 0 || mbar_wait_polls(bar, parity, polls)) return true;
+    if (polls < 0 || (polls > 0 && mbar_wait_polls(bar, parity, polls - 1))) return true;
     *stop = 1;
     return false;
 }

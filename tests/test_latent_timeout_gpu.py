@@ -1,8 +1,8 @@
 """The give-up paths of the latent attention kernels, run on purpose without a fault.
 
 Every wait of theirs is bounded (about a second).  The test hook PKV_TEST_WAIT_POLLS=0
-makes the products' first wait for a tile give up at once, while its copies are in
-flight: the other roles stop, the copies land, and the call returns with
+makes the products' first wait for a tile give up at once, as a rule while its copies
+are in flight: the other roles stop, the copies land, and the call returns with
 PKV_ERRBIT_TIMEOUT.  The next call is right, with the workspace as it was left.  The
 batches leave the copies done with their part before the wait gives up (a tile or two
 in all) or in the middle of it (many)."""
