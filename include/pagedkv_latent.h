@@ -154,7 +154,8 @@ int paged_latent_gather(void *latents, void *ropes, const void *cache,
  *  kv             device fp16 [total_kv][n_heads][2 * head_dim]: the head's
  *                 key k, then its value v (the product of the latents with
  *                 the expansion's weights)
- *  k_rope         device fp16 [total_kv][rope_dim], shared by all heads
+ *  k_rope         device fp16 [total_kv][rope_dim], shared by all heads; with
+ *                 total_kv 0, kv and k_rope may be NULL
  *  q_start, kv_start   device int32 [num_seqs + 1]: sequence b owns the query
  *                 rows [q_start[b], q_start[b + 1]), n_b of them, and the
  *                 key/value rows [kv_start[b], kv_start[b + 1]), m_b of them;

@@ -340,7 +340,10 @@ int latent_prefill_attention(void *out, const void *q, const void *kv, const voi
         num_seqs > 65535)
         return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
-    if (!out || !q || !q_start || !kv_start || !kv || !k_rope) return PKV_ERR_INVALID_ARG;
+    if (!out || !q || !q_start || !kv_start) return PKV_ERR_INVALID_ARG;
+    // an empty tensor has no address; none of its rows is ever copied
+    if (total_kv == 0) kv = k_rope = q;
+    if (!kv || !k_rope) return PKV_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(kv, 16) || !aligned(k_rope, 16) ||
         !aligned(q_start, 4) || !aligned(kv_start, 4) || (lse_out && !aligned(lse_out, 4)) ||
         (err_word && !aligned(err_word, 4)))
