@@ -47,6 +47,13 @@ from .latent import (  # noqa: F401
     paged_latent_attention,
     paged_latent_gather,
 )
+from .q8 import (  # noqa: F401
+    paged_decode_attention_q8,
+    paged_kv_append_q8,
+    paged_kv_copy_blocks_q8,
+    paged_kv_gather_q8,
+    q8_plan,
+)
 from .rope import (  # noqa: F401
     PKV_ERRBIT_POSITION,
     paged_qk_norm_rope_append,

@@ -1,0 +1,81 @@
+// q8.h -- launch interfaces of the 8-bit caches with block scales
+// (include/pagedkv_q8.h), between q8_api.cu and the kernels.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "pagedkv_q8.h"
+
+namespace pkv {
+
+constexpr int kQ8MaxSeqs = 2048;
+
+struct Q8AppendArgs {
+    const void *k_new, *v_new;
+    long long k_stride, v_stride;  // elements between tokens
+    const int32_t *query_start;    // NULL: token b is sequence b's
+    const int32_t *block_tables, *context_lens;
+    int num_seqs, total, max_q_len, max_blocks_per_seq;
+    void *k_cache, *v_cache;
+    float *k_scales, *v_scales;
+    int n_kv_heads, head_dim, block_size;
+    long long num_blocks;
+    int32_t *err;
+};
+cudaError_t launch_q8_append(const Q8AppendArgs &a, int kind, cudaStream_t stream);
+
+struct Q8GatherArgs {
+    void *k, *v;
+    const void *k_cache, *v_cache;
+    const float *k_scales, *v_scales;
+    const int32_t *block_tables, *start;
+    int num_seqs;
+    long long total;
+    int max_blocks_per_seq;
+    long long num_blocks;
+    int n_kv_heads, head_dim, block_size;
+    int32_t *err;
+};
+cudaError_t launch_q8_gather(const Q8GatherArgs &a, int kind, cudaStream_t stream);
+
+struct Q8CopyArgs {
+    void *k_cache, *v_cache;
+    float *k_scales, *v_scales;
+    const int32_t *src, *dst, *tokens;
+    int num_copies, n_kv_heads, head_dim, block_size;
+    long long num_blocks;
+    int32_t *err;
+};
+cudaError_t launch_q8_copy(const Q8CopyArgs &a, cudaStream_t stream);
+
+struct Q8AttentionArgs {
+    void *out;
+    const void *q;
+    long long q_stride;  // elements between tokens
+    const void *k_cache, *v_cache;
+    const float *k_scales, *v_scales;
+    const int32_t *block_tables, *context_lens, *query_start;
+    int num_seqs, total_q, max_q_len, max_blocks_per_seq;
+    long long num_blocks;
+    float scale_log2;  // scale * log2(e), either sign
+    int n_q_heads, n_kv_heads, head_dim, block_size, max_context_len;
+    void *workspace;
+    float *lse_out;
+    int32_t *err;
+    int tables_ready;  // the kernel before writes no lengths, tables or query starts
+};
+// How a call's work is split: `ctas` CTAs of the kernel for `row_tiles` x 8 query rows.
+struct Q8Split {
+    int row_tiles;
+    int ctas;
+    size_t ws_bytes;
+};
+// false: more than 2^31 units of work.
+bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
+              int max_len, int sms, Q8Split *sp);
+cudaError_t launch_q8_attention(const Q8AttentionArgs &a, int kind, const Q8Split &sp,
+                                cudaStream_t stream);
+
+}  // namespace pkv

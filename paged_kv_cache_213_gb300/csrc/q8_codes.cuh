@@ -1,0 +1,46 @@
+// q8_codes.cuh -- codes of the 8-bit caches with block scales: fp32 to codes and
+// codes to fp16.  KIND is PKV_Q8_E4M3 or PKV_Q8_INT8.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+#include "pagedkv_q8.h"
+
+namespace pkv {
+
+template <int KIND>
+__device__ __forceinline__ constexpr float q8_limit() {
+    return KIND == PKV_Q8_E4M3 ? 448.f : 127.f;
+}
+
+// Two quotients to two codes, the first in the low byte: to nearest even,
+// saturated; NaN to the NaN code, or 0 for int8.
+template <int KIND>
+__device__ __forceinline__ uint32_t q8_encode2(float a, float b) {
+    if (KIND == PKV_Q8_E4M3)
+        return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    // cvt.rni of a NaN gives 0; the clamp is on the integers, which saturate
+    const int x = max(-127, min(127, __float2int_rn(a))), y = max(-127, min(127, __float2int_rn(b)));
+    return static_cast<uint32_t>(x & 255) | (static_cast<uint32_t>(y & 255) << 8);
+}
+
+// Codes 0, 1 (HI 0) or 2, 3 (HI 1) of four to fp16: exact.
+template <int KIND, int HI>
+__device__ __forceinline__ uint32_t q8_widen(uint32_t w) {
+    uint32_t r;
+    if (KIND == PKV_Q8_E4M3) {
+        const uint16_t s = static_cast<uint16_t>(HI ? w >> 16 : w);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(s));
+    } else {
+        // byte + 128 behind the exponent of 1024 is the fp16 number 1152 + code
+        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, HI ? 0x4342 : 0x4140);
+        const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&u), __floats2half2_rn(1152.f, 1152.f));
+        r = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return r;
+}
+
+}  // namespace pkv

@@ -1,4 +1,4 @@
-// calls.cpp -- the marshalling of rope.py's and latent.py's calls, natively.
+// calls.cpp -- the marshalling of rope.py's, latent.py's and q8.py's calls, natively.
 //
 // A call for a few tokens takes the GPU 2 to 9 us and took the host 15 to 20, nearly
 // all of it in Python: attributes of tensors, one wrapper object each, and the
@@ -21,6 +21,7 @@
 #include <initializer_list>
 
 #include "pagedkv_latent.h"
+#include "pagedkv_q8.h"
 #include "pagedkv_rope.h"
 
 namespace {
@@ -323,6 +324,123 @@ PyObject *latent_prefill(Args &a) {
     return out ? Py_NewRef(given) : THPVariable_Wrap(std::move(made));
 }
 
+// The 8-bit caches of a call: k_cache, v_cache, k_scales, v_scales.
+struct Q8 {
+    const Tensor *k, *v, *ks, *vs;
+    int kind = PKV_Q8_E4M3;
+    int64_t NB = 0, Hk = 0, bs = 0, d = 0;
+    bool ok = false;
+
+    explicit Q8(Args &a) {
+        at::ScalarType type = at::kByte;
+        if (a.left > 0 && THPVariable_Check(a.args[0]) &&
+            THPVariable_Unpack(a.args[0]).scalar_type() == at::kChar) {
+            type = at::kChar;
+            kind = PKV_Q8_INT8;
+        }
+        k = a.tensor(type);
+        v = a.tensor(type);
+        ks = a.tensor(at::kFloat);
+        vs = a.tensor(at::kFloat);
+        if (!a.ok || k->dim() != 4 || v->sizes() != k->sizes()) return;
+        NB = k->size(0), Hk = k->size(1), bs = k->size(2), d = k->size(3);
+        ok = Hk > 0 && is(ks, {NB, Hk}) && is(vs, {NB, Hk}) && fits({Hk, bs, d});
+    }
+    float *k_scales() const { return static_cast<float *>(ks->data_ptr()); }
+    float *v_scales() const { return static_cast<float *>(vs->data_ptr()); }
+};
+
+// k_new, v_new, the cache, block_tables, context_lens, query_start, max_q_len,
+// err_word; True
+PyObject *append_q8(Args &a) {
+    const Tensor *k = a.tensor(at::kHalf, false, true), *v = a.tensor(at::kHalf, false, true);
+    const Q8 c(a);
+    const Tensor *tables = a.tensor(at::kInt), *lens = a.tensor(at::kInt), *start = a.tensor(at::kInt, true);
+    const int most = a.int32();
+    const Tensor *err = a.tensor(at::kInt, true);
+    if (!a.plain() || !c.ok || k->dim() != 3 || tables->dim() != 2) Py_RETURN_NONE;
+    const int64_t T = k->size(0), B = tables->size(0), MB = tables->size(1);
+    if (!is(k, {T, c.Hk, c.d}) || !is(v, {T, c.Hk, c.d}) || !is(lens, {B}) || !is(start, {B + 1}) ||
+        (!start && (T != B || most != 1)) || !fits({T, B, MB}))
+        Py_RETURN_NONE;
+    const int64_t ks = token_stride(*k, T, c.Hk, c.d), vs = token_stride(*v, T, c.Hk, c.d);
+    if (ks < 0 || vs < 0) Py_RETURN_NONE;
+    const int rc = unlocked([&] { return paged_kv_append_q8(
+        k->data_ptr(), v->data_ptr(), ks, vs, static_cast<const int32_t *>(at_of(start)),
+        static_cast<const int32_t *>(at_of(tables)), static_cast<const int32_t *>(at_of(lens)),
+        static_cast<int>(B), static_cast<int>(T), most, static_cast<int>(MB), at_of(c.k), at_of(c.v),
+        c.k_scales(), c.v_scales(), c.kind, static_cast<int>(c.Hk), static_cast<int>(c.d),
+        static_cast<int>(c.bs), c.NB, static_cast<int32_t *>(at_of(err)), a.stream()); });
+    if (rc != PKV_OK) Py_RETURN_NONE;
+    Py_RETURN_TRUE;
+}
+
+// q, the cache, block_tables, context_lens, scale, query_start, max_q_len,
+// max_context_len, out, workspace, lse, err_word, flags
+PyObject *attention_q8(Args &a) {
+    const Tensor *q = a.tensor(at::kHalf, false, true);
+    const Q8 c(a);
+    const Tensor *tables = a.tensor(at::kInt), *lens = a.tensor(at::kInt);
+    const float scale = static_cast<float>(a.number());
+    const Tensor *start = a.tensor(at::kInt, true);
+    const int most = a.int32(), longest = a.int32();
+    PyObject *given = a.left > 0 ? a.args[0] : Py_None;
+    const Tensor *out = a.tensor(at::kHalf, true), *ws = a.tensor(at::kByte, true),
+                 *lse = a.tensor(at::kFloat, true), *err = a.tensor(at::kInt, true);
+    const uint32_t flags = static_cast<uint32_t>(a.integer(0, UINT_MAX));
+    // without a workspace one has to be zero-filled: the Python code does that
+    if (!a.plain() || !c.ok || !ws || q->dim() != 3 || tables->dim() != 2) Py_RETURN_NONE;
+    const int64_t TQ = q->size(0), H = q->size(1), B = tables->size(0), MB = tables->size(1);
+    if (q->size(2) != c.d || H % c.Hk != 0 || !is(lens, {B}) || !is(start, {B + 1}) ||
+        (!start && (TQ != B || most != 1)) || !is(out, {TQ, H, c.d}) || !is(lse, {TQ, H}) ||
+        !fits({TQ, H, B, MB}))
+        Py_RETURN_NONE;
+    const int64_t qs = token_stride(*q, TQ, H, c.d);
+    if (qs < 0) Py_RETURN_NONE;
+    Tensor made;
+    if (!out) made = a.make({TQ, H, c.d});
+    const int rc = unlocked([&] { return paged_decode_attention_q8(
+        out ? out->data_ptr() : made.data_ptr(), q->data_ptr(), qs, at_of(c.k), at_of(c.v), c.k_scales(),
+        c.v_scales(), c.kind, static_cast<const int32_t *>(at_of(tables)),
+        static_cast<const int32_t *>(at_of(lens)), static_cast<const int32_t *>(at_of(start)),
+        static_cast<int>(B), static_cast<int>(TQ), most, static_cast<int>(MB), c.NB, scale,
+        static_cast<int>(H), static_cast<int>(c.Hk), static_cast<int>(c.d), static_cast<int>(c.bs), longest,
+        at_of(ws), static_cast<size_t>(ws->numel()), static_cast<float *>(at_of(lse)),
+        static_cast<int32_t *>(at_of(err)), a.stream(), flags); });
+    if (rc != PKV_OK) Py_RETURN_NONE;
+    return out ? Py_NewRef(given) : THPVariable_Wrap(std::move(made));
+}
+
+// the cache, block_tables, start, total, k, v, err_word; a pair
+PyObject *gather_q8(Args &a) {
+    const Q8 c(a);
+    const Tensor *tables = a.tensor(at::kInt), *start = a.tensor(at::kInt);
+    const int64_t total = a.int32();
+    PyObject *gk = a.left > 0 ? a.args[0] : Py_None, *gv = a.left > 1 ? a.args[1] : Py_None;
+    const Tensor *k = a.tensor(at::kHalf, true), *v = a.tensor(at::kHalf, true), *err = a.tensor(at::kInt, true);
+    if (!a.plain() || !c.ok || tables->dim() != 2) Py_RETURN_NONE;
+    const int64_t B = tables->size(0), MB = tables->size(1);
+    if (total < 0 || !is(start, {B + 1}) || !is(k, {total, c.Hk, c.d}) || !is(v, {total, c.Hk, c.d}) ||
+        !fits({B, MB}))
+        Py_RETURN_NONE;
+    Tensor made_k, made_v;
+    if (!k) made_k = a.make({total, c.Hk, c.d});
+    if (!v) made_v = a.make({total, c.Hk, c.d});
+    const int rc = unlocked([&] { return paged_kv_gather_q8(
+        k ? k->data_ptr() : made_k.data_ptr(), v ? v->data_ptr() : made_v.data_ptr(), at_of(c.k), at_of(c.v),
+        c.k_scales(), c.v_scales(), c.kind, static_cast<const int32_t *>(at_of(tables)),
+        static_cast<const int32_t *>(at_of(start)), static_cast<int>(B), total, static_cast<int>(MB), c.NB,
+        static_cast<int>(c.Hk), static_cast<int>(c.d), static_cast<int>(c.bs),
+        static_cast<int32_t *>(at_of(err)), a.stream()); });
+    if (rc != PKV_OK) Py_RETURN_NONE;
+    PyObject *x = k ? Py_NewRef(gk) : THPVariable_Wrap(std::move(made_k));
+    PyObject *y = v ? Py_NewRef(gv) : THPVariable_Wrap(std::move(made_v));
+    PyObject *pair = x && y ? PyTuple_Pack(2, x, y) : nullptr;
+    Py_XDECREF(x);
+    Py_XDECREF(y);
+    return pair;
+}
+
 #define ENTRY(name, f) \
     {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&guarded<f>)), METH_FASTCALL, nullptr}
 
@@ -332,6 +450,9 @@ PyMethodDef methods[] = {ENTRY("qk_append", qk_append<false>),
                          ENTRY("latent_attention", latent_attention),
                          ENTRY("latent_gather", latent_gather),
                          ENTRY("latent_prefill", latent_prefill),
+                         ENTRY("append_q8", append_q8),
+                         ENTRY("attention_q8", attention_q8),
+                         ENTRY("gather_q8", gather_q8),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pagedkv_calls", nullptr, -1, methods,
