@@ -17,8 +17,8 @@
  * are finite and not negative (what the append writes is).
  *
  * Limits of every call: head_dim 64 or 128, block_size 16, 32, 64, 128 or 256,
- * at most 2048 sequences, fewer than 2^31 pieces of 16 rows x head in a cache
- * (PKV_ERR_UNSUPPORTED beyond).
+ * at most 2048 sequences, fewer than 2^31 rows of all blocks and heads in a
+ * cache (PKV_ERR_UNSUPPORTED beyond).
  */
 #ifndef PAGEDKV_Q8_H
 #define PAGEDKV_Q8_H

@@ -65,6 +65,7 @@ struct Q8AttentionArgs {
     float *lse_out;
     int32_t *err;
     int tables_ready;  // the kernel before writes no lengths, tables or query starts
+    int first_wait_polls;  // test hook, as in DecodeArgs
 };
 // How a call's work is split: `ctas` CTAs of the kernel for `row_tiles` x 8 query rows.
 struct Q8Split {

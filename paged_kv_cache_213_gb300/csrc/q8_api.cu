@@ -29,8 +29,8 @@ int check_cache(int kind, int n_kv_heads, int head_dim, int block_size, int64_t 
     if ((head_dim != 64 && head_dim != 128) || (block_size != 16 && block_size != 32 && block_size != 64 &&
                                                 block_size != 128 && block_size != 256))
         return PKV_ERR_UNSUPPORTED;
-    // 16-row pieces are numbered in 31 bits
-    if (num_blocks > INT32_MAX / n_kv_heads / (block_size / 16)) return PKV_ERR_UNSUPPORTED;
+    // rows (of all heads) are numbered in 31 bits
+    if (num_blocks > INT32_MAX / n_kv_heads / block_size) return PKV_ERR_UNSUPPORTED;
     return PKV_OK;
 }
 
@@ -200,6 +200,7 @@ int paged_decode_attention_q8(void *out, const void *q, int64_t q_stride, const 
     a.lse_out = lse_out;
     a.err = err_word;
     a.tables_ready = (flags & PKV_TABLES_READY) ? 1 : 0;
+    a.first_wait_polls = pkv::test_wait_polls();
     return status_of(pkv::launch_q8_attention(a, kind, plan.split, static_cast<cudaStream_t>(cuda_stream)));
 }
 

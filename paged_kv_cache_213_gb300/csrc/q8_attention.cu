@@ -14,12 +14,14 @@
 // is empty.  m moves only when a logit is 2^8 above it, w when v leaves [w / 64, 16 w]:
 // both are vote-and-branch, and p * (v / w) stays within fp16.
 //
-// Layout.  A lane copies what it will use itself, and nothing else, with 16-byte
-// cp.async into its own places of a ring: no barrier and no exchange between lanes,
-// and conflict-free reads.  The order of entries inside a product is free (K's columns
-// go with Q's, V's columns are rows of the result), so a lane's 16 contiguous bytes of a
-// row are its operand, and the result leaves in 16 contiguous entries a lane.  V's token
-// pairs are interleaved by one byte permute per four codes before they are widened.
+// Layout.  Each warp has a ring of tiles of its own, filled by TMA, one copy a tile of K
+// and one of V, swizzled.  The order of entries inside a product is free (K's columns go
+// with Q's, V's columns are rows of the result), so a lane's 16 contiguous bytes of a row
+// are its operand, every read is conflict-free, and the result leaves in 16 contiguous
+// entries a lane.  V's token pairs are interleaved by one byte permute per four codes
+// before they are widened.  (16-byte cp.async into places of the lane's own, without
+// swizzle or barrier, was bound by the cycle that each 32-byte sector takes on its way
+// into shared memory: 8 x 32k tokens 110 us.)
 //
 // Split.  The (sequence, head, row tile, 16-token tile) units are cut into equal ranges
 // for the warps of one CTA per SM.  Pieces of a segment (sequence, head, row tile) that
@@ -32,11 +34,18 @@
 #include "q8.h"
 #include "q8_codes.cuh"
 
+#ifndef Q8_W1
+#define Q8_W1 12
+#define Q8_S1 3
+#endif
+#ifndef Q8_W2
+#define Q8_W2 12
+#define Q8_S2 2
+#endif
 namespace pkv {
 namespace {
 
 constexpr int kTile = 16;   // tokens of a unit
-constexpr int kWarps = 8;
 constexpr float kMoveM = 8.f;            // a row's reference follows logits this far above it
 constexpr float kLn2 = 0.69314718055994531f;
 // Units a warp gets at least, where there are enough: a shorter range spends its time
@@ -45,22 +54,23 @@ constexpr int kMinUnits = 2;
 
 template <int D, int NT>
 struct Shape {
+    // registers: the sums take NT * D / 4 of a lane's
+    static constexpr int kWarps = NT == 1 ? Q8_W1 : NT == 2 ? Q8_W2 : 8;
+    static constexpr int kStages = NT == 1 ? Q8_S1 : NT == 2 ? Q8_S2 : NT == 3 ? 3 : 2;
     static constexpr int kRows = 8 * NT;
-    static constexpr int kKPieces = D / 32;             // 16-byte pieces of K a lane (2 rows)
+    static constexpr bool kQInRegs = NT == 1;           // else read from shared memory for each tile
     static constexpr int kVPiece = D / 8;               // bytes of a V row a lane takes
-    static constexpr int kQPieces = NT * D / 32;        // 16-byte pieces of Q a lane
-    static constexpr int kV = kKPieces * 512;           // offsets in a stage
-    static constexpr int kQ = kV + 4 * kVPiece * 32;
-    static constexpr int kS = kQ + kQPieces * 512;
-    static constexpr int kStage = kS + 256;
-    static constexpr int kStages = NT == 1 ? 3 : 2;
+    static constexpr int kV = kTile * D;                // of V in a stage
+    static constexpr int kStage = 2 * kTile * D;
+    // A warp's shared memory: the ring, then two places for Q: a segment's that is ahead,
+    // and one more ahead or the one in use, if that is not in registers.
+    static constexpr int kQ = kStages * kStage, kQBytes = NT * D * 16;
+    static constexpr int kQAhead = kQInRegs ? 2 : 1;
+    static constexpr int kWarpBytes = kQ + 2 * kQBytes;
     static constexpr int kRecord = kRows * D + 2 * kRows;  // floats: sums, then m and l a row
-    static constexpr int kRingBytes = kWarps * kStages * kStage;
-    static constexpr int kRecordBytes = kWarps * kRecord * 4;
-    static_assert(kRecord * 4 <= kStages * kStage, "a warp's ring holds its last piece's record");
-    static constexpr size_t smem(int seqs) {
-        return kRingBytes + kRecordBytes + (static_cast<size_t>(seqs) * 3 + 2) * 4 + kWarps * 64;
-    }
+    static_assert(kRecord * 4 <= kWarpBytes, "a warp's memory holds its last piece's record");
+    static_assert(kWarpBytes % 1024 == 0, "swizzled tiles lie on 1024 bytes");
+    static constexpr size_t smem(int seqs) { return kWarps * kWarpBytes + (static_cast<size_t>(seqs) * 3 + 2) * 4; }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -72,20 +82,8 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -141,8 +139,7 @@ struct Segment {
 
 // The cache tile (number of 16-row pieces) of unit u; bad blocks flag and become tile 0.
 __device__ __forceinline__ unsigned tile_of(const Batch &t, const Q8AttentionArgs &a, int rows, int group,
-                                            int bs16_log2, int u) {
-    Segment s;
+                                            int bs16_log2, int u, Segment &s) {
     s.find(t, a, rows, group, u);
     const int block = s.j >> bs16_log2;
     const int id = a.block_tables[static_cast<long long>(s.b) * a.max_blocks_per_seq + block];
@@ -151,27 +148,6 @@ __device__ __forceinline__ unsigned tile_of(const Batch &t, const Q8AttentionArg
         return 0;
     }
     return (static_cast<unsigned>(id) * a.n_kv_heads + s.h << bs16_log2) + (s.j & ((1 << bs16_log2) - 1));
-}
-
-// Sum over the CTA's warps of x (one value a thread), exclusive; *sum gets the whole.
-__device__ __forceinline__ int exclusive_sum(int x, int *warp_sums, int *sum) {
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    int y = x;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-        const int z = __shfl_up_sync(~0u, y, d);
-        if (lane >= d) y += z;
-    }
-    if (lane == 31) warp_sums[warp] = y;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += warp_sums[w];
-        all += warp_sums[w];
-    }
-    __syncthreads();
-    *sum = all;
-    return before + y - x;
 }
 
 // Where query row `row` of a segment's row tile lies, as a multiple of head_dim in out;
@@ -184,36 +160,86 @@ __device__ __forceinline__ long long row_at(const Batch &t, const Q8AttentionArg
     return static_cast<long long>(t.start[s.b] + i) * a.n_q_heads + s.h * group + (r - i * group);
 }
 
-// What a warp or a CTA leaves of a segment it holds a part of.
+// A row of a segment joined by 8 lanes: lane i of them holds the columns 32 k + 4 i on.
+template <int D>
+struct Row {
+    float4 sum[D / 32];
+    float top = -INFINITY, weight = 0.f;
+
+    __device__ Row() {
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) sum[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    // Another reference, at least the one there is.
+    __device__ void move(float to) {
+        const float g = top == -INFINITY ? 0.f : ex2(top - to);
+        top = to;
+        weight *= g;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            sum[k].x *= g;
+            sum[k].y *= g;
+            sum[k].z *= g;
+            sum[k].w *= g;
+        }
+    }
+    __device__ void add(float m, float l, const float4 (&x)[D / 32]) {
+        const float g = m == -INFINITY ? 0.f : ex2(m - top);
+        weight += g * l;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+            sum[k].x += g * x[k].x;
+            sum[k].y += g * x[k].y;
+            sum[k].z += g * x[k].z;
+            sum[k].w += g * x[k].w;
+        }
+    }
+    __device__ void write(const Q8AttentionArgs &a, long long row, int i) const {
+        const float z = 1.f / weight;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+            reinterpret_cast<uint2 *>(a.out)[row * (D / 4) + k * 8 + i] =
+                make_uint2(pack_half2(sum[k].x * z, sum[k].y * z), pack_half2(sum[k].z * z, sum[k].w * z));
+        if (a.lse_out && i == 0) a.lse_out[row] = (top + log2f(weight)) * kLn2;
+    }
+};
+
+// What a warp leaves of a segment that it holds a part of.
 struct Piece {
-    int first, end;  // the segment's units
-    int slot;        // -1: none; 0: the warp's record; 1: its ring
-    Segment at;
+    int first, end;   // the segment's units; first -1: none
+    int b, h, rt;
+    int in_ring;      // the record is in the warp's shared memory, else in the workspace
 };
 
 template <int KIND, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8AttentionArgs a) {
+__global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_kernel(
+    const Q8AttentionArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using S = Shape<D, NT>;
-    constexpr int kRows = S::kRows;
-    extern __shared__ __align__(128) unsigned char smem[];
-    float *records = reinterpret_cast<float *>(smem + S::kRingBytes);
-    int *cum = reinterpret_cast<int *>(smem + S::kRingBytes + S::kRecordBytes);
+    constexpr int kRows = S::kRows, kWarps = S::kWarps;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    int *cum = reinterpret_cast<int *>(smem + kWarps * S::kWarpBytes);
     int *len = cum + a.num_seqs + 1, *start = len + a.num_seqs;
     __shared__ int warp_sums[kWarps];
     __shared__ Piece pieces[kWarps * 2];
-    __shared__ int last_of[2];
+    __shared__ uint64_t landed[kWarps][S::kStages];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int r = lane / 4, c = lane % 4;  // the lane's row and column in a fragment
     const int group = a.n_q_heads / a.n_kv_heads;
     const int bs16_log2 = __ffs(a.block_size / kTile) - 1;
 
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&k_map);
+        prefetch_tmap(&v_map);
+    }
+    if (lane < S::kStages) mbar_init(&landed[warp][lane], 1);
+    fence_barrier_init();
     if (!a.tables_ready) {
         grid_dependency_wait();
         allow_dependent_launch();
     }
 
     // --- the batch's units
-    int at = 0;
+    int total = 0;
     for (int b0 = 0; b0 < a.num_seqs; b0 += kWarps * 32) {
         const int b = b0 + threadIdx.x;
         int units = 0;
@@ -233,15 +259,28 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
             start[b] = s;
             if (b == a.num_seqs - 1) start[b + 1] = s + n;
         }
-        int sum;
-        const int mine = exclusive_sum(units, warp_sums, &sum);
-        if (b < a.num_seqs) cum[b] = at + mine;
-        at += sum;
+        int upto = units;  // sum over the warp, this thread included
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int z = __shfl_up_sync(~0u, upto, d);
+            if (lane >= d) upto += z;
+        }
+        if (b0 > 0) __syncthreads();  // the sums of the round before are read
+        if (lane == 31) warp_sums[warp] = upto;
+        __syncthreads();
+        int before = total;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const int x = warp_sums[w];
+            if (w < warp) before += x;
+            total += x;
+        }
+        if (b < a.num_seqs) cum[b] = before + upto - units;
     }
-    if (threadIdx.x == 0) cum[a.num_seqs] = at;
+    if (threadIdx.x == 0) cum[a.num_seqs] = total;
+    if (lane < 2) pieces[2 * warp + lane].first = -1;
     __syncthreads();
-    const Batch t{cum, len, start, at};
-    const int total = at;
+    const Batch t{cum, len, start, total};
 
     // --- this warp's range
     const int ctas = min(static_cast<int>(gridDim.x), max(1, (total + kWarps * kMinUnits - 1) / (kWarps * kMinUnits)));
@@ -255,12 +294,79 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
     // --- what copies need: 32 units' tiles at a time, the next 32 under way
     int base = u0;
     unsigned tiles_now = 0, tiles_next = 0;
-    if (u0 + lane < u1) tiles_now = tile_of(t, a, kRows, group, bs16_log2, u0 + lane);
-    if (u0 + 32 + lane < u1) tiles_next = tile_of(t, a, kRows, group, bs16_log2, u0 + 32 + lane);
+    Segment seg{};  // of unit u0: lane 0's, for all
+    if (u0 + lane < u1) tiles_now = tile_of(t, a, kRows, group, bs16_log2, u0 + lane, seg);
+    seg.b = __shfl_sync(~0u, seg.b, 0);
+    seg.h = __shfl_sync(~0u, seg.h, 0);
+    seg.rt = __shfl_sync(~0u, seg.rt, 0);
+    seg.j = __shfl_sync(~0u, seg.j, 0);
+    seg.tiles = __shfl_sync(~0u, seg.tiles, 0);
+    seg.row_tiles = __shfl_sync(~0u, seg.row_tiles, 0);
     if (a.tables_ready) {
         grid_dependency_wait();
         allow_dependent_launch();
     }
+
+    unsigned char *mine = smem + warp * S::kWarpBytes;
+    uint64_t *full = landed[warp];
+    Segment ahead = seg;
+    int pu = u0;         // the next unit to copy
+    int pstage = 0, pq = 0, pending = 0;
+    bool pfirst = true;  // it starts a segment, or this range
+    bool alive = true;   // no wait has given up
+    float2 scales_prev = make_float2(0.f, 0.f), scales_now = scales_prev;
+    auto load_scales = [&] {
+        scales_prev = scales_now;
+        if (base + lane < u1) {
+            const unsigned cell = tiles_now >> bs16_log2;
+            scales_now = make_float2(__ldg(a.k_scales + cell), __ldg(a.v_scales + cell));
+        }
+    };
+
+    // Copies of the units before `to`, as far as there are places for their queries.
+    auto copy_ahead = [&](int to) {
+        while (pu < to && !(pfirst && pending == S::kQAhead) && alive) {
+            if (pu - base == 32) {
+                base += 32;
+                tiles_now = tiles_next;
+                load_scales();
+            }
+            const unsigned tile = __shfl_sync(~0u, tiles_now, pu - base);
+            if (lane == 0) {
+                unsigned char *dst = mine + pstage * S::kStage;
+                mbar_arrive_expect_tx(full + pstage, S::kStage);
+                tma_load_2d(dst, &k_map, 0, static_cast<int>(tile * kTile), full + pstage);
+                tma_load_2d(dst + S::kV, &v_map, 0, static_cast<int>(tile * kTile), full + pstage);
+            }
+            if (pu == base && base + 32 + lane < u1) {
+                Segment any;
+                tiles_next = tile_of(t, a, kRows, group, bs16_log2, base + 32 + lane, any);
+            }
+            if (pfirst) {
+                const uint32_t dst = smem_addr(mine) + S::kQ + pq * S::kQBytes + lane * 16;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    int token;
+                    const long long row = row_at(t, a, ahead, kRows, group, nt * 8 + r, &token);
+                    const int head = ahead.h * group + (ahead.rt * kRows + nt * 8 + r - token * group);
+                    const __half *q = static_cast<const __half *>(a.q) +
+                                      (row < 0 ? 0 : (t.start[ahead.b] + token) * a.q_stride + head * D) + c * (D / 4);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i)
+                        copy16(dst + (nt * (D / 32) + i) * 512, q + i * 8, row < 0 ? 0 : 16);
+                }
+                commit();
+                pq ^= 1;
+                ++pending;
+            }
+            ++pu;
+            pfirst = ahead.next(t, a, kRows, group);
+            pstage = pstage + 1 == S::kStages ? 0 : pstage + 1;
+        }
+    };
+
+    load_scales();
+    copy_ahead(min(u0 + S::kStages, u1));
     if (!a.query_start) {  // one token a sequence: an empty one has a result
         for (int b = cta; b < a.num_seqs; b += gridDim.x) {
             if (len[b] != 0) continue;
@@ -271,77 +377,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
                     a.lse_out[static_cast<long long>(b) * a.n_q_heads + i] = -INFINITY;
         }
     }
-
-    const uint32_t ring = smem_addr(smem) + warp * S::kStages * S::kStage;
-    unsigned char *ring_p = smem + warp * S::kStages * S::kStage;
-    const unsigned char *kc = static_cast<const unsigned char *>(a.k_cache) + r * D + c * 16;
-    const unsigned char *vc = static_cast<const unsigned char *>(a.v_cache) + 2 * c * D + r * S::kVPiece;
-    Segment ahead;
-    int pu = u0;       // the next unit to copy
-    int pstage = 0;
-    bool pfirst = true;  // it starts a segment, or this range
-    if (u0 < u1) ahead.find(t, a, kRows, group, u0);
-
-    auto copy_next = [&] {
-        if (pu < u1) {
-            if (pu - base == 32) {
-                base += 32;
-                tiles_now = tiles_next;
-                if (base + 32 + lane < u1) tiles_next = tile_of(t, a, kRows, group, bs16_log2, base + 32 + lane);
-            }
-            const unsigned tile = __shfl_sync(~0u, tiles_now, pu - base);
-            const uint32_t dst = ring + pstage * S::kStage;
-            const long long off = static_cast<long long>(tile) * (kTile * D);
-#pragma unroll
-            for (int i = 0; i < S::kKPieces; ++i) {
-                // rows r and r + 8; at D = 128 their two halves
-                const int row = i & 1, half = i >> 1;
-                copy16(dst + i * 512 + lane * 16, kc + off + row * 8 * D + half * 64);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
-                const unsigned char *src = vc + off + ((i & 1) + (i >> 1) * 8) * D;
-                if constexpr (D == 128)
-                    copy16(dst + S::kV + i * 512 + lane * 16, src);
-                else
-                    copy8(dst + S::kV + i * 256 + lane * 8, src);
-            }
-            const unsigned cell = tile >> bs16_log2;
-            copy4(dst + S::kS + lane * 8, a.k_scales + cell);
-            copy4(dst + S::kS + lane * 8 + 4, a.v_scales + cell);
-            if (pfirst) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    int token;
-                    const long long row = row_at(t, a, ahead, kRows, group, nt * 8 + r, &token);
-                    const int head = static_cast<int>(row % a.n_q_heads);
-                    const __half *q = static_cast<const __half *>(a.q) +
-                                      (row < 0 ? 0 : (t.start[ahead.b] + token) * a.q_stride + head * D) + c * 16;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i)
-                        copy16(dst + S::kQ + (nt * (D / 32) + i) * 512 + lane * 16, q + (i >> 1) * 64 + (i & 1) * 8,
-                               row < 0 ? 0 : 16);
-                }
-            }
-            ++pu;
-            pfirst = ahead.next(t, a, kRows, group);
-            pstage = pstage + 1 == S::kStages ? 0 : pstage + 1;
-        }
-        commit();
+    // records in the workspace: each CTA's warps', then its two parts of segments that
+    // other CTAs share
+    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+    float *records = reinterpret_cast<float *>(ws + kBalancedCounterBytes);
+    auto record_of = [&](int of_cta, int i) {
+        return records + (static_cast<long long>(of_cta) * (kWarps + 2) + i) * S::kRecord;
     };
 
-    if (lane == 0) pieces[2 * warp].slot = pieces[2 * warp + 1].slot = -1;
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) copy_next();
-
-    Segment seg;
-    if (u0 < u1) seg.find(t, a, kRows, group, u0);
-    int stage = 0;
+    // the lane's places in a tile: K rows r (and r + 8, 8 rows on), V rows 2c and 2c + 1 (and
+    // 8 rows on), by the TMA swizzle of D-byte rows
+    const int k0 = D == 128 ? r * D + (2 * c ^ r) * 16 : r * D + (c ^ (r >> 1)) * 16;
+    const int k1 = r * D + (2 * c + 1 ^ r) * 16;
+    const int v0 = S::kV + 2 * c * D + (D == 128 ? (r ^ 2 * c) * 16 : ((r >> 1) ^ c) * 16 + (r & 1) * 8);
+    const int v1 = S::kV + (2 * c + 1) * D + (D == 128 ? (r ^ 2 * c + 1) * 16 : ((r >> 1) ^ c) * 16 + (r & 1) * 8);
+    int stage = 0, parity = 0, qplace = 0;
+    int polls = a.first_wait_polls;  // test hook: the first wait gives up after so many
     for (int u = u0; u < u1;) {
         // --- a piece of a segment: units u to end
         const int seg_first = seg.first(u), seg_end = seg_first + seg.tiles, end = min(seg_end, u1);
         const int L = len[seg.b], n = start[seg.b + 1] - start[seg.b];
-        uint32_t q[NT][D / 16][2];
+        uint32_t q[S::kQInRegs ? NT : 1][D / 16][2];
         float o[NT][D / 16][4], l[NT][2], m[NT][2];
         int limit[NT][2];  // keys that a row attends
 #pragma unroll
@@ -359,53 +415,88 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
         }
         const int least = L - n + 1 + seg.rt * kRows / group;  // of the tile's first row
         float w = 0.f, inv_w = 0.f;
-        bool first = true;
-        for (; u < end; ++u) {
-            wait_copies<S::kStages - 2>();
-            copy_next();  // into the stage read last time
-            const unsigned char *p = ring_p + stage * S::kStage;
-            stage = stage + 1 == S::kStages ? 0 : stage + 1;
-            if (first) {
-                first = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(
-                            p + S::kQ + (nt * (D / 32) + i) * 512 + lane * 16);
-                        q[nt][2 * i][0] = x.x;
-                        q[nt][2 * i][1] = x.y;
-                        q[nt][2 * i + 1][0] = x.z;
-                        q[nt][2 * i + 1][1] = x.w;
-                    }
-            }
-            const int tok = (u - seg_first) * kTile;
-            const float2 scales = *reinterpret_cast<const float2 *>(p + S::kS + lane * 8);
-            const float f = scales.x * a.scale_log2;
-            // --- scores
-            float s[NT][4];
+        const unsigned char *qp = mine + S::kQ + qplace * S::kQBytes + lane * 16;
+        qplace ^= 1;
+        --pending;
+        wait_copies();
+        if constexpr (S::kQInRegs) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(qp + (nt * (D / 32) + i) * 512);
+                    q[nt][2 * i][0] = x.x;
+                    q[nt][2 * i][1] = x.y;
+                    q[nt][2 * i + 1][0] = x.z;
+                    q[nt][2 * i + 1][1] = x.w;
+                }
+        }
+        for (; u < end; ++u) {
+            if (alive) {
+                const bool ok = polls >= 0 ? mbar_wait_polls(full + stage, parity, polls)
+                                           : mbar_wait_bounded(full + stage, parity);
+                polls = -1;
+                if (!__all_sync(~0u, ok)) {
+                    // results are unspecified from here on, but every step of the split is made
+                    if (lane == 0) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+                    alive = false;
+                    for (int k = u, s = stage, y = parity; k < pu; ++k) {  // no copy outlives the warp
+                        mbar_wait_bounded(full + s, y);
+                        if (++s == S::kStages) s = 0, y ^= 1;
+                    }
+                    __syncwarp();
+                }
+            }
+            const unsigned char *p = mine + stage * S::kStage;
+            if (++stage == S::kStages) stage = 0, parity ^= 1;
+            const int tok = (u - seg_first) * kTile;
+            const bool past = u < base;
+            const float k_scale = __shfl_sync(~0u, past ? scales_prev.x : scales_now.x, (u - base) & 31);
+            const float v_scale = __shfl_sync(~0u, past ? scales_prev.y : scales_now.y, (u - base) & 31);
+            const float f = k_scale * a.scale_log2;
+            // --- scores, in two sums (half as long a chain)
+            float s[NT][4], s2[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[nt][i] = s2[nt][i] = 0.f;
 #pragma unroll
             for (int half = 0; half < D / 64; ++half) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(p + (2 * half) * 512 + lane * 16);
-                const uint4 y = *reinterpret_cast<const uint4 *>(p + (2 * half + 1) * 512 + lane * 16);
+                const uint4 x = *reinterpret_cast<const uint4 *>(p + (half ? k1 : k0));
+                const uint4 y = *reinterpret_cast<const uint4 *>(p + (half ? k1 : k0) + 8 * D);
                 const uint32_t wx[4] = {x.x, x.y, x.z, x.w}, wy[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t frag[4] = {q8_widen<KIND, 0>(wx[i]), q8_widen<KIND, 0>(wy[i]),
-                                              q8_widen<KIND, 1>(wx[i]), q8_widen<KIND, 1>(wy[i])};
+                for (int ii = 0; ii < 2; ++ii) {
+                    uint4 qx[NT];
+                    if constexpr (!S::kQInRegs) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma_16816(s[nt], frag, q[nt][half * 4 + i][0], q[nt][half * 4 + i][1]);
+                        for (int nt = 0; nt < NT; ++nt)
+                            qx[nt] = *reinterpret_cast<const uint4 *>(qp + (nt * (D / 32) + 2 * half + ii) * 512);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int i = 2 * ii + k;
+                        const uint32_t frag[4] = {q8_widen<KIND, 0>(wx[i]), q8_widen<KIND, 0>(wy[i]),
+                                                  q8_widen<KIND, 1>(wx[i]), q8_widen<KIND, 1>(wy[i])};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint32_t b0, b1;
+                            if constexpr (S::kQInRegs) {
+                                b0 = q[nt][half * 4 + i][0];
+                                b1 = q[nt][half * 4 + i][1];
+                            } else {
+                                b0 = k ? qx[nt].z : qx[nt].x;
+                                b1 = k ? qx[nt].w : qx[nt].y;
+                            }
+                            mma_16816(k ? s2[nt] : s[nt], frag, b0, b1);
+                        }
+                    }
                 }
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[nt][i] *= f;
+                for (int i = 0; i < 4; ++i) s[nt][i] = (s[nt][i] + s2[nt][i]) * f;
             if (tok + kTile > least) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -414,17 +505,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
                         if (tok + r + (i >> 1) * 8 >= limit[nt][i & 1]) s[nt][i] = -INFINITY;
             }
             // --- references
-            bool move = scales.y > 0.f && !(scales.y >= w * (1.f / 64.f) && scales.y <= w * 16.f);
+            bool move = v_scale > 0.f && !(v_scale >= w * (1.f / 64.f) && v_scale <= w * 16.f);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) move = move || s[nt][i] > m[nt][i & 1] + kMoveM;
             if (__any_sync(~0u, move)) {
                 float g = 1.f;
-                if (scales.y > 0.f && !(scales.y >= w * (1.f / 64.f) && scales.y <= w * 16.f)) {
-                    inv_w = __fdividef(1.f, scales.y);
+                if (v_scale > 0.f && !(v_scale >= w * (1.f / 64.f) && v_scale <= w * 16.f)) {
+                    inv_w = __fdividef(1.f, v_scale);
                     g = w * inv_w;
-                    w = scales.y;
+                    w = v_scale;
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -447,7 +538,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
                 }
             }
             // --- weights
-            const float fv = scales.y * inv_w;
+            const float fv = v_scale * inv_w;
             uint32_t pf[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -466,11 +557,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
             uint32_t v[4][S::kVPiece / 4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                const unsigned char *src = p + (i & 1 ? v1 : v0) + (i >> 1) * 8 * D;
                 if constexpr (D == 128) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(p + S::kV + i * 512 + lane * 16);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src);
                     v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
                 } else {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(p + S::kV + i * 256 + lane * 8);
+                    const uint2 x = *reinterpret_cast<const uint2 *>(src);
                     v[i][0] = x.x; v[i][1] = x.y;
                 }
             }
@@ -492,6 +584,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][2 * k + hi], frag, pf[nt][0], pf[nt][1]);
                 }
+            __syncwarp();  // every lane has read this stage
+            copy_ahead(min(u + 1 + S::kStages, u1));
         }
         // --- the piece's end: sums over the lanes of a row
 #pragma unroll
@@ -520,149 +614,132 @@ __global__ void __launch_bounds__(kWarps * 32, 1) q8_attention_kernel(const Q8At
                     if (a.lse_out && r == 0) a.lse_out[row] = (m[nt][i] + log2f(l[nt][i])) * kLn2;
                 }
         } else {
-            // the range's first piece has a record of its own; a later one is the last
-            // thing the warp does, and takes the ring
-            const int slot = seg_first < u0 ? 0 : 1;
-            if (slot == 1) wait_copies<0>();
+            // the last thing that the warp does takes its shared memory (no copy is in
+            // flight any more); what it goes on after goes to the workspace
+            const bool in_ring = end == u1;
             __syncwarp();
-            float *rec = slot ? reinterpret_cast<float *>(ring_p) : records + warp * S::kRecord;
+            float *rec = in_ring ? reinterpret_cast<float *>(mine) : record_of(cta, warp);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = nt * 8 + 2 * c + i;
 #pragma unroll
-                    for (int mt = 0; mt < D / 16; ++mt)
-                        *reinterpret_cast<float2 *>(rec + row * D + r * S::kVPiece + 2 * mt) =
-                            make_float2(o[nt][mt][i] * w, o[nt][mt][i + 2] * w);
+                    for (int k = 0; k < D / 32; ++k)
+                        *reinterpret_cast<float4 *>(rec + row * D + r * S::kVPiece + 4 * k) =
+                            make_float4(o[nt][2 * k][i] * w, o[nt][2 * k][i + 2] * w, o[nt][2 * k + 1][i] * w,
+                                        o[nt][2 * k + 1][i + 2] * w);
                     if (r == 0) {
                         rec[kRows * D + row] = m[nt][i];
                         rec[kRows * D + kRows + row] = l[nt][i];
                     }
                 }
-            if (lane == 0) pieces[2 * warp + slot] = Piece{seg_first, seg_end, slot, seg};
+            if (lane == 0)
+                pieces[2 * warp + (seg_first >= u0)] = Piece{seg_first, seg_end, seg.b, seg.h, seg.rt, in_ring};
         }
         if (u < u1) {
             seg.j = seg.tiles - 1;
             seg.next(t, a, kRows, group);
         }
     }
-    wait_copies<0>();
     __syncthreads();
 
-    // --- joins: runs of pieces of one segment, in the order of the warps
-    unsigned char *ws = static_cast<unsigned char *>(a.workspace);
-    int *counters = reinterpret_cast<int *>(ws);
-    float *parts = reinterpret_cast<float *>(ws + kBalancedCounterBytes);
-    Piece open[2];  // this CTA's parts of segments that other CTAs share
-    open[0].slot = open[1].slot = -1;
-    for (int i = 0; i < 2 * kWarps;) {
-        if (pieces[i].slot < 0) {
-            ++i;
+    // --- joins.  Lane i knows piece i; pieces of one segment are neighbours, in the order of
+    // the tokens.  A warp takes four rows of a segment, 8 lanes each.
+    static_assert(2 * kWarps <= 32, "a lane for each piece");
+    Piece piece;
+    piece.first = -1;
+    if (lane < 2 * kWarps) piece = pieces[lane];
+    const unsigned there = __ballot_sync(~0u, piece.first >= 0);
+    const unsigned lower = there & ((1u << lane) - 1);
+    const int prev = __shfl_sync(~0u, piece.first, lower ? 31 - __clz(lower) : 0);
+    const unsigned heads = __ballot_sync(~0u, piece.first >= 0 && (!lower || prev != piece.first));
+    const int segments = __popc(heads);
+    auto owner = [&](int u) { return static_cast<int>((static_cast<long long>(u + 1) * ctas - 1) / total); };
+    const int i8 = lane % 8;
+    for (int item = warp; item < segments * (kRows / 4); item += kWarps) {
+        const int quad = item / segments;
+        unsigned of = heads;
+        for (int k = item - quad * segments; k > 0; --k) of &= of - 1;
+        const int head = __ffs(of) - 1;
+        const unsigned rest = of & (of - 1);
+        unsigned members = there & (rest ? (1u << (__ffs(rest) - 1)) - 1 : ~0u) & ~((1u << head) - 1);
+        const Piece whole = pieces[head];
+        Segment at;
+        at.b = whole.b;
+        at.h = whole.h;
+        at.rt = whole.rt;
+        if (quad * 4 >= (start[at.b + 1] - start[at.b]) * group - at.rt * kRows) continue;  // no such rows
+        const int row = quad * 4 + lane / 8;
+        Row<D> sums;
+        for (; members; members &= members - 1) {
+            const int k = __ffs(members) - 1;
+            const float *rec = pieces[k].in_ring ? reinterpret_cast<const float *>(smem + k / 2 * S::kWarpBytes)
+                                                 : record_of(cta, k / 2);
+            float4 x[D / 32];
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) x[j] = reinterpret_cast<const float4 *>(rec + row * D)[j * 8 + i8];
+            const float m = rec[kRows * D + row], l = rec[kRows * D + kRows + row];
+            if (m > sums.top) sums.move(m);
+            sums.add(m, l, x);
+        }
+        int token;
+        const long long out_row = row_at(t, a, at, kRows, group, row, &token);
+        if (whole.first >= U0 && whole.end <= U1) {
+            if (out_row >= 0) sums.write(a, out_row, i8);
             continue;
         }
-        const Piece head = pieces[i];
-        int e = i + 1;
-        while (e < 2 * kWarps && (pieces[e].slot < 0 || pieces[e].first == head.first)) ++e;
-        const bool whole = head.first >= U0 && head.end <= U1;
-        const int side = head.first >= U0 ? 1 : 0;
-        float *part = parts + (static_cast<long long>(cta) * 2 + side) * S::kRecord;
-        if (!whole) open[side] = head;
-        for (int x = threadIdx.x; x < kRows * D / 4; x += kWarps * 32) {
-            const int row = x / (D / 4);
-            float top = -INFINITY;
-            for (int k = i; k < e; ++k)
-                if (pieces[k].slot >= 0) {
-                    const float *rec = pieces[k].slot ? reinterpret_cast<const float *>(smem + (k / 2) * S::kStages * S::kStage)
-                                                      : records + (k / 2) * S::kRecord;
-                    top = fmaxf(top, rec[kRows * D + row]);
-                }
-            const float ref = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i; k < e; ++k)
-                if (pieces[k].slot >= 0) {
-                    const float *rec = pieces[k].slot ? reinterpret_cast<const float *>(smem + (k / 2) * S::kStages * S::kStage)
-                                                      : records + (k / 2) * S::kRecord;
-                    const float g = ex2(rec[kRows * D + row] - ref);
-                    const float4 y = reinterpret_cast<const float4 *>(rec)[x];
-                    sum += g * rec[kRows * D + kRows + row];
-                    acc.x += g * y.x;
-                    acc.y += g * y.y;
-                    acc.z += g * y.z;
-                    acc.w += g * y.w;
-                }
-            if (whole) {
-                int token;
-                const long long at_row = row_at(t, a, head.at, kRows, group, row, &token);
-                if (at_row >= 0) {
-                    const float z = 1.f / sum;
-                    uint2 y = make_uint2(pack_half2(acc.x * z, acc.y * z), pack_half2(acc.z * z, acc.w * z));
-                    reinterpret_cast<uint2 *>(a.out)[at_row * (D / 4) + x % (D / 4)] = y;
-                    if (a.lse_out && x % (D / 4) == 0) a.lse_out[at_row] = (top + log2f(sum)) * kLn2;
-                }
-            } else {
-                reinterpret_cast<float4 *>(part)[x] = acc;
-                if (x % (D / 4) == 0) {
-                    part[kRows * D + row] = top;
-                    part[kRows * D + kRows + row] = sum;
-                }
-            }
+        // other CTAs share the segment: the last to arrive with these rows joins them, in
+        // the order of the CTAs
+        float *part = record_of(cta, kWarps + (whole.first >= U0));
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) __stcg(reinterpret_cast<float4 *>(part + row * D) + j * 8 + i8, sums.sum[j]);
+        if (i8 == 0) {
+            __stcg(part + kRows * D + row, sums.top);
+            __stcg(part + kRows * D + kRows + row, sums.weight);
         }
-        i = e;
-    }
-    // --- segments of several CTAs: the last to arrive joins
-    if (open[0].slot < 0 && open[1].slot < 0) return;
-    auto owner = [&](int u) { return static_cast<int>((static_cast<long long>(u + 1) * ctas - 1) / total); };
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x < 2) {
-        const int side = threadIdx.x;
-        last_of[side] = 0;
-        if (open[side].slot >= 0) {
-            const int from = owner(open[side].first), more = owner(open[side].end - 1) - from;
-            const int old = atomic_add_acq_rel_gpu(counters + from, 1);
+        __syncwarp();
+        const int from = owner(whole.first), more = owner(whole.end - 1) - from;
+        int last = 0;
+        if (lane == 0) {
+            int *counter = reinterpret_cast<int *>(ws) + from * (kRows / 4) + quad;
+            const int old = atomic_add_acq_rel_gpu(counter, 1);
             if (counter_not_zeroed(old, more)) {
                 flag_error(a.err, PKV_ERRBIT_WORKSPACE);
-                atomic_exch_relaxed_gpu(counters + from, kCounterPoison);
+                atomic_exch_relaxed_gpu(counter, kCounterPoison);
             } else if (old == more) {
-                last_of[side] = 1;
-                red_add_relaxed_gpu(counters + from, -(more + 1));
+                last = 1;
+                red_add_relaxed_gpu(counter, -(more + 1));
             }
         }
-    }
-    __syncthreads();
-    for (int side = 0; side < 2; ++side) {
-        if (!last_of[side]) continue;
-        __threadfence();
-        const Piece &head = open[side];
-        const int from = owner(head.first), to = owner(head.end - 1);
-        for (int x = threadIdx.x; x < kRows * D / 4; x += kWarps * 32) {
-            const int row = x / (D / 4);
-            int token;
-            const long long at_row = row_at(t, a, head.at, kRows, group, row, &token);
-            if (at_row < 0) continue;
-            float top = -INFINITY;
-            for (int k = from; k <= to; ++k)
-                top = fmaxf(top, __ldcg(parts + (2ll * k + (k == from)) * S::kRecord + kRows * D + row));
-            const float ref = top == -INFINITY ? 0.f : top;
-            float sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = from; k <= to; ++k) {
-                const float *rec = parts + (2ll * k + (k == from)) * S::kRecord;
-                const float g = ex2(__ldcg(rec + kRows * D + row) - ref);
-                const float4 y = __ldcg(reinterpret_cast<const float4 *>(rec) + x);
-                sum += g * __ldcg(rec + kRows * D + kRows + row);
-                acc.x += g * y.x;
-                acc.y += g * y.y;
-                acc.z += g * y.z;
-                acc.w += g * y.w;
+        if (!__shfl_sync(~0u, last, 0)) continue;
+        __syncwarp();
+        Row<D> joined;
+        constexpr int kAtOnce = 4;
+        for (int k0 = 0; k0 <= more; k0 += kAtOnce) {
+            float4 x[kAtOnce][D / 32];
+            float m[kAtOnce], l[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                m[k] = -INFINITY;
+                l[k] = 0.f;
+                if (k0 + k <= more) {  // the first CTA's part is its second
+                    const float *rec = record_of(from + k0 + k, kWarps + (k0 + k == 0));
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j)
+                        x[k][j] = __ldcg(reinterpret_cast<const float4 *>(rec + row * D) + j * 8 + i8);
+                    m[k] = __ldcg(rec + kRows * D + row);
+                    l[k] = __ldcg(rec + kRows * D + kRows + row);
+                }
             }
-            const float z = 1.f / sum;
-            uint2 y = make_uint2(pack_half2(acc.x * z, acc.y * z), pack_half2(acc.z * z, acc.w * z));
-            reinterpret_cast<uint2 *>(a.out)[at_row * (D / 4) + x % (D / 4)] = y;
-            if (a.lse_out && x % (D / 4) == 0) a.lse_out[at_row] = (top + log2f(sum)) * kLn2;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (k0 + k <= more) {
+                    if (m[k] > joined.top) joined.move(m[k]);
+                    joined.add(m[k], l[k], x[k]);
+                }
         }
+        if (out_row >= 0) joined.write(a, out_row, i8);
     }
 }
 
@@ -673,31 +750,46 @@ cudaError_t launch(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t str
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_pdl(q8_attention_kernel<KIND, D, NT>, dim3(sp.ctas), dim3(kWarps * 32), smem, stream, a);
+    CUtensorMap k_map, v_map;
+    const long long rows = a.num_blocks * a.n_kv_heads * a.block_size;
+    if (!make_cache_map_e4m3(&k_map, a.k_cache, rows, D) || !make_cache_map_e4m3(&v_map, a.v_cache, rows, D))
+        return cudaErrorNotSupported;
+    return launch_pdl(q8_attention_kernel<KIND, D, NT>, dim3(sp.ctas), dim3(Shape<D, NT>::kWarps * 32), smem,
+                      stream, a, k_map, v_map);
 }
 
 template <int KIND, int D>
 cudaError_t launch_rows(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t stream) {
-    return sp.row_tiles == 1 ? launch<KIND, D, 1>(a, sp, stream) : launch<KIND, D, 2>(a, sp, stream);
+    switch (sp.row_tiles) {
+        case 1: return launch<KIND, D, 1>(a, sp, stream);
+        case 2: return launch<KIND, D, 2>(a, sp, stream);
+        case 3: return launch<KIND, D, 3>(a, sp, stream);
+        default: return launch<KIND, D, 4>(a, sp, stream);
+    }
 }
 
-static_assert(Shape<128, 1>::smem(kQ8MaxSeqs) <= 227 * 1024 - 2048, "shared memory");
-static_assert(Shape<128, 2>::smem(kQ8MaxSeqs) <= 227 * 1024 - 2048, "shared memory");
+template <int NT>
+constexpr bool fits() {
+    return Shape<128, NT>::smem(kQ8MaxSeqs) <= 227 * 1024 - 1024;
+}
+static_assert(fits<1>() && fits<2>() && fits<3>() && fits<4>(), "shared memory");
 
 }  // namespace
 
 bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
               int sms, Q8Split *sp) {
     const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
-    sp->row_tiles = rows <= 8 ? 1 : 2;
+    sp->row_tiles = rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
     const long long height = 8 * sp->row_tiles;
     const long long tiles = (static_cast<long long>(max_len) + kTile - 1) / kTile;
     const double units = static_cast<double>(num_seqs) * n_kv_heads * tiles * ((rows + height - 1) / height);
     if (units >= 2147483648.0) return false;
     sp->ctas = sms;
-    if (static_cast<size_t>(sms) * 4 > kBalancedCounterBytes) sp->ctas = kBalancedCounterBytes / 4;
+    const int most = static_cast<int>(kBalancedCounterBytes / height);  // a counter for four rows of each CTA
+    if (sp->ctas > most) sp->ctas = most;
+    const int warps = sp->row_tiles == 1 ? Shape<128, 1>::kWarps : sp->row_tiles == 2 ? Shape<128, 2>::kWarps : Shape<128, 4>::kWarps;
     const size_t record = (height * head_dim + 2 * height) * 4;
-    sp->ws_bytes = kBalancedCounterBytes + static_cast<size_t>(sp->ctas) * 2 * record;
+    sp->ws_bytes = kBalancedCounterBytes + static_cast<size_t>(sp->ctas) * (warps + 2) * record;
     return true;
 }
 
