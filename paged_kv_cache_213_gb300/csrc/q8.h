@@ -50,6 +50,19 @@ struct Q8CopyArgs {
 };
 cudaError_t launch_q8_copy(const Q8CopyArgs &a, cudaStream_t stream);
 
+// Division of x < 2^31 by d as a product: with 2^(s - 1) < d <= 2^s and mul = ceil(2^(31 + s)
+// / d) = (2^(31 + s) + e) / d, 0 <= e < d, x * mul / 2^(31 + s) = x / d + x e / (d 2^(31 + s)),
+// and the last term is below 1 / d, too little to reach the next whole number.
+struct Q8Divide {
+    uint32_t mul;
+    int shift;
+};
+inline Q8Divide q8_divide_by(uint32_t d) {
+    int s = 0;
+    while ((1ull << s) < d) ++s;
+    return Q8Divide{static_cast<uint32_t>(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 struct Q8AttentionArgs {
     void *out;
     const void *q;
@@ -61,6 +74,8 @@ struct Q8AttentionArgs {
     long long num_blocks;
     float scale_log2;  // scale * log2(e), either sign
     int n_q_heads, n_kv_heads, head_dim, block_size, max_context_len;
+    Q8Divide by_group;  // query heads of a KV head
+    int record_rows;    // of Q8Split
     void *workspace;
     float *lse_out;
     int32_t *err;
@@ -71,6 +86,7 @@ struct Q8AttentionArgs {
 struct Q8Split {
     int row_tiles;
     int ctas;
+    int record_rows;  // query rows that a segment has at most
     size_t ws_bytes;
 };
 // false: more than 2^31 units of work.

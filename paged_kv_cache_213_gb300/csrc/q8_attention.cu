@@ -24,9 +24,9 @@
 // into shared memory: 8 x 32k tokens 110 us.)
 //
 // Split.  The (sequence, head, row tile, 16-token tile) units are cut into equal ranges
-// for the warps of one CTA per SM.  Pieces of a segment (sequence, head, row tile) that
-// several warps hold join in shared memory; those of several CTAs leave one record a
-// CTA, and the last CTA to arrive joins the records in order.
+// for the warps of one CTA per SM.  The parts of a segment (sequence, head, row tile)
+// that several warps of a CTA hold are joined there; CTAs that share a segment leave a
+// record each, and the last to arrive joins them, in the order of the tokens.
 #include <cuda_fp16.h>
 
 #include "pkv_internal.h"
@@ -34,14 +34,6 @@
 #include "q8.h"
 #include "q8_codes.cuh"
 
-#ifndef Q8_W1
-#define Q8_W1 12
-#define Q8_S1 3
-#endif
-#ifndef Q8_W2
-#define Q8_W2 12
-#define Q8_S2 2
-#endif
 namespace pkv {
 namespace {
 
@@ -52,23 +44,28 @@ constexpr float kLn2 = 0.69314718055994531f;
 // in the join.
 constexpr int kMinUnits = 2;
 
+// Floats of a record: sums and two numbers a row, whole 16-byte pieces.
+__host__ __device__ constexpr int q8_record_floats(int rows, int d) { return rows * d + (rows + 1) / 2 * 4; }
+
 template <int D, int NT>
 struct Shape {
-    // registers: the sums take NT * D / 4 of a lane's
-    static constexpr int kWarps = NT == 1 ? Q8_W1 : NT == 2 ? Q8_W2 : 8;
-    static constexpr int kStages = NT == 1 ? Q8_S1 : NT == 2 ? Q8_S2 : NT == 3 ? 3 : 2;
+    // Registers bound the warps: the sums take NT * D / 4 of a lane's.  At NT = 1 (32 x
+    // 128-2048 tokens; 8 x 32k; one of 700): 8 warps, 5 stages 21.6, 102, 8.1 us; 12 and 3:
+    // 21.0, 87.4, 9.2; 16 and 2: 20.9, 87.4, 10.9.
+    static constexpr int kWarps = NT <= 2 ? 12 : 8;
+    static constexpr int kStages = NT == 1 || NT == 3 ? 3 : 2;
     static constexpr int kRows = 8 * NT;
-    static constexpr bool kQInRegs = NT == 1;           // else read from shared memory for each tile
+    static constexpr bool kQInRegs = NT == 1;           // one tile of rows; else read from shared memory for each tile
     static constexpr int kVPiece = D / 8;               // bytes of a V row a lane takes
     static constexpr int kV = kTile * D;                // of V in a stage
     static constexpr int kStage = 2 * kTile * D;
     // A warp's shared memory: the ring, then two places for Q: a segment's that is ahead,
-    // and one more ahead or the one in use, if that is not in registers.
+    // and one more ahead or the one in use, if that is not in registers.  A warp's last
+    // record takes it all over.
     static constexpr int kQ = kStages * kStage, kQBytes = NT * D * 16;
     static constexpr int kQAhead = kQInRegs ? 2 : 1;
     static constexpr int kWarpBytes = kQ + 2 * kQBytes;
-    static constexpr int kRecord = kRows * D + 2 * kRows;  // floats: sums, then m and l a row
-    static_assert(kRecord * 4 <= kWarpBytes, "a warp's memory holds its last piece's record");
+    static_assert(q8_record_floats(kRows, D) * 4 <= kWarpBytes, "the last record's place");
     static_assert(kWarpBytes % 1024 == 0, "swizzled tiles lie on 1024 bytes");
     static constexpr size_t smem(int seqs) { return kWarps * kWarpBytes + (static_cast<size_t>(seqs) * 3 + 2) * 4; }
 };
@@ -83,12 +80,36 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+// All groups have landed but the `newer` (0 to 2) last ones.
+__device__ __forceinline__ void wait_copies(int newer) {
+    if (newer == 0)
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    else if (newer == 1)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
+
+// x / d for x < 2^31: the high part of a product (Divide's comment has the bound).
+__device__ __forceinline__ int divided(int x, const Q8Divide &d) {
+    return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(x)) * d.mul >> d.shift);
+}
+
+// `total` units in `n` ranges whose sizes differ by one at most, the larger first.
+struct Ranges {
+    int size, larger;  // of a smaller range; how many larger ones
+    __device__ Ranges(int total, int n) : size(total / n), larger(total - size * n) {}
+    __device__ int start(int i) const { return size * i + min(i, larger); }
+    __device__ int of(int x) const {  // the range that unit x lies in
+        const int split = larger * (size + 1);
+        return x < split ? x / (size + 1) : larger + (x - split) / max(size, 1);
+    }
+};
 
 // A batch's units: sequence b has those from cum[b] to cum[b + 1].
 struct Batch {
@@ -105,6 +126,7 @@ struct Segment {
     // The unit u of the batch.
     __device__ void find(const Batch &t, const Q8AttentionArgs &a, int rows, int group, int u) {
         int lo = 0, hi = a.num_seqs;  // cum[lo] <= u < cum[hi]
+#pragma unroll 1
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (t.cum[mid] <= u) lo = mid; else hi = mid;
@@ -117,7 +139,7 @@ struct Segment {
         h = q / row_tiles;
         rt = q - h * row_tiles;
     }
-    __device__ void sizes(const Batch &t, int rows, int group) {
+    __device__ __forceinline__ void sizes(const Batch &t, int rows, int group) {
         tiles = (t.len[b] + kTile - 1) / kTile;
         row_tiles = ((t.start[b + 1] - t.start[b]) * group + rows - 1) / rows;
     }
@@ -129,6 +151,7 @@ struct Segment {
         rt = 0;
         if (++h < a.n_kv_heads) return true;
         h = 0;
+#pragma unroll 1
         do ++b; while (b < a.num_seqs && t.cum[b + 1] == t.cum[b]);
         if (b < a.num_seqs) sizes(t, rows, group);
         return true;
@@ -154,7 +177,7 @@ __device__ __forceinline__ unsigned tile_of(const Batch &t, const Q8AttentionArg
 // -1: the tile's rows end before it.
 __device__ __forceinline__ long long row_at(const Batch &t, const Q8AttentionArgs &a, const Segment &s,
                                             int rows, int group, int row, int *token) {
-    const int r = s.rt * rows + row, i = r / group;
+    const int r = s.rt * rows + row, i = divided(r, a.by_group);
     *token = i;
     if (i >= t.start[s.b + 1] - t.start[s.b]) return -1;
     return static_cast<long long>(t.start[s.b] + i) * a.n_q_heads + s.h * group + (r - i * group);
@@ -172,7 +195,7 @@ struct Row {
     }
     // Another reference, at least the one there is.
     __device__ void move(float to) {
-        const float g = top == -INFINITY ? 0.f : ex2(top - to);
+        const float g = top == -INFINITY ? 0.f : ex2(top - to);  // 0 of nothing
         top = to;
         weight *= g;
 #pragma unroll
@@ -204,11 +227,24 @@ struct Row {
     }
 };
 
+// From shared memory or from L2, whatever the address says; never from L1.
+__device__ __forceinline__ float4 load_fresh4(const float *p) {
+    float4 x;
+    asm volatile("ld.volatile.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "l"(p) : "memory");
+    return x;
+}
+__device__ __forceinline__ float2 load_fresh2(const float *p) {
+    float2 x;
+    asm volatile("ld.volatile.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "l"(p) : "memory");
+    return x;
+}
+
 // What a warp leaves of a segment that it holds a part of.
 struct Piece {
-    int first, end;   // the segment's units; first -1: none
+    int first, end;  // the segment's units; first -1: none
     int b, h, rt;
-    int in_ring;      // the record is in the warp's shared memory, else in the workspace
+    int in_ring;     // the record is in the warp's shared memory, else in the workspace
 };
 
 template <int KIND, int D, int NT>
@@ -233,6 +269,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
     }
     if (lane < S::kStages) mbar_init(&landed[warp][lane], 1);
     fence_barrier_init();
+    // the block tables into L2, a line a thread of the grid (a prefetch reads nothing stale)
+    const long long line = static_cast<long long>(blockIdx.x) + static_cast<long long>(threadIdx.x) * gridDim.x;
+    if (line * 32 < static_cast<long long>(a.num_seqs) * a.max_blocks_per_seq) prefetch_l2(a.block_tables + line * 32);
     if (!a.tables_ready) {
         grid_dependency_wait();
         allow_dependent_launch();
@@ -240,6 +279,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
 
     // --- the batch's units
     int total = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < a.num_seqs; b0 += kWarps * 32) {
         const int b = b0 + threadIdx.x;
         int units = 0;
@@ -285,11 +325,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
     // --- this warp's range
     const int ctas = min(static_cast<int>(gridDim.x), max(1, (total + kWarps * kMinUnits - 1) / (kWarps * kMinUnits)));
     const int cta = blockIdx.x;
-    const bool works = cta < ctas;
-    auto cut = [&](int i) { return static_cast<int>(static_cast<long long>(total) * i / ctas); };
-    const int U0 = works ? cut(cta) : 0, U1 = works ? cut(cta + 1) : 0;
-    const int u0 = U0 + static_cast<int>(static_cast<long long>(U1 - U0) * warp / kWarps);
-    const int u1 = U0 + static_cast<int>(static_cast<long long>(U1 - U0) * (warp + 1) / kWarps);
+    const Ranges of_ctas(total, ctas);
+    const int U0 = cta < ctas ? of_ctas.start(cta) : 0, U1 = cta < ctas ? of_ctas.start(cta + 1) : 0;
+    const Ranges of_warps(U1 - U0, kWarps);
+    const int u0 = U0 + of_warps.start(warp), u1 = U0 + of_warps.start(warp + 1);
 
     // --- what copies need: 32 units' tiles at a time, the next 32 under way
     int base = u0;
@@ -323,8 +362,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
         }
     };
 
-    // Copies of the units before `to`, as far as there are places for their queries.
+    auto copy_tile = [&](bool does, unsigned tile, int to_stage) {
+        if (does) {
+            unsigned char *dst = mine + to_stage * S::kStage;
+            mbar_arrive_expect_tx(full + to_stage, S::kStage);
+            tma_load_2d(dst, &k_map, 0, static_cast<int>(tile * kTile), full + to_stage);
+            tma_load_2d(dst + S::kV, &v_map, 0, static_cast<int>(tile * kTile), full + to_stage);
+        }
+    };
+    // Copies of the units before `to`, as far as there are places for their queries; the
+    // first tile is under way.
     auto copy_ahead = [&](int to) {
+#pragma unroll 1
         while (pu < to && !(pfirst && pending == S::kQAhead) && alive) {
             if (pu - base == 32) {
                 base += 32;
@@ -332,12 +381,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                 load_scales();
             }
             const unsigned tile = __shfl_sync(~0u, tiles_now, pu - base);
-            if (lane == 0) {
-                unsigned char *dst = mine + pstage * S::kStage;
-                mbar_arrive_expect_tx(full + pstage, S::kStage);
-                tma_load_2d(dst, &k_map, 0, static_cast<int>(tile * kTile), full + pstage);
-                tma_load_2d(dst + S::kV, &v_map, 0, static_cast<int>(tile * kTile), full + pstage);
-            }
+            if (pu > u0) copy_tile(lane == 0, tile, pstage);
             if (pu == base && base + 32 + lane < u1) {
                 Segment any;
                 tiles_next = tile_of(t, a, kRows, group, bs16_log2, base + 32 + lane, any);
@@ -365,24 +409,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
         }
     };
 
+    // the first tile; its queries come before the next ones, or they would wait behind them
+    copy_tile(lane == 0 && u0 < u1, tiles_now, 0);
     load_scales();
-    copy_ahead(min(u0 + S::kStages, u1));
     if (!a.query_start) {  // one token a sequence: an empty one has a result
-        for (int b = cta; b < a.num_seqs; b += gridDim.x) {
+#pragma unroll 1
+        for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
             if (len[b] != 0) continue;
             uint4 *o = static_cast<uint4 *>(a.out) + static_cast<long long>(b) * a.n_q_heads * (D / 8);
+#pragma unroll 1
             for (int i = threadIdx.x; i < a.n_q_heads * (D / 8); i += kWarps * 32) o[i] = make_uint4(0, 0, 0, 0);
             if (a.lse_out)
-                for (int i = threadIdx.x; i < a.n_q_heads; i += kWarps * 32)
+    #pragma unroll 1
+            for (int i = threadIdx.x; i < a.n_q_heads; i += kWarps * 32)
                     a.lse_out[static_cast<long long>(b) * a.n_q_heads + i] = -INFINITY;
         }
     }
-    // records in the workspace: each CTA's warps', then its two parts of segments that
-    // other CTAs share
+    // Records, `record_rows` sums of D, then m and l of each row: of the CTA's warps that went
+    // on after it, then of the segment that began in a CTA before, and of the one that goes
+    // on in the next.
     unsigned char *ws = static_cast<unsigned char *>(a.workspace);
-    float *records = reinterpret_cast<float *>(ws + kBalancedCounterBytes);
     auto record_of = [&](int of_cta, int i) {
-        return records + (static_cast<long long>(of_cta) * (kWarps + 2) + i) * S::kRecord;
+        return reinterpret_cast<float *>(ws + kBalancedCounterBytes) +
+               ((kWarps + 2ll) * of_cta + i) * q8_record_floats(a.record_rows, D);
     };
 
     // the lane's places in a tile: K rows r (and r + 8, 8 rows on), V rows 2c and 2c + 1 (and
@@ -393,11 +442,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
     const int v1 = S::kV + (2 * c + 1) * D + (D == 128 ? (r ^ 2 * c + 1) * 16 : ((r >> 1) ^ c) * 16 + (r & 1) * 8);
     int stage = 0, parity = 0, qplace = 0;
     int polls = a.first_wait_polls;  // test hook: the first wait gives up after so many
+#pragma unroll 1
     for (int u = u0; u < u1;) {
         // --- a piece of a segment: units u to end
         const int seg_first = seg.first(u), seg_end = seg_first + seg.tiles, end = min(seg_end, u1);
         const int L = len[seg.b], n = start[seg.b + 1] - start[seg.b];
-        uint32_t q[S::kQInRegs ? NT : 1][D / 16][2];
+        uint32_t q[1][D / 16][2];
         float o[NT][D / 16][4], l[NT][2], m[NT][2];
         int limit[NT][2];  // keys that a row attends
 #pragma unroll
@@ -410,28 +460,32 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
             for (int i = 0; i < 2; ++i) {
                 l[nt][i] = 0.f;
                 m[nt][i] = -INFINITY;
-                limit[nt][i] = L - n + 1 + min((seg.rt * kRows + nt * 8 + 2 * c + i) / group, n - 1);
+                limit[nt][i] = L - n + 1 + min(divided(seg.rt * kRows + nt * 8 + 2 * c + i, a.by_group), n - 1);
             }
         }
-        const int least = L - n + 1 + seg.rt * kRows / group;  // of the tile's first row
+        const int least = L - n + 1 + divided(seg.rt * kRows, a.by_group);  // of the tile's first row
         float w = 0.f, inv_w = 0.f;
         const unsigned char *qp = mine + S::kQ + qplace * S::kQBytes + lane * 16;
         qplace ^= 1;
-        --pending;
-        wait_copies();
-        if constexpr (S::kQInRegs) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(qp + (nt * (D / 32) + i) * 512);
-                    q[nt][2 * i][0] = x.x;
-                    q[nt][2 * i][1] = x.y;
-                    q[nt][2 * i + 1][0] = x.z;
-                    q[nt][2 * i + 1][1] = x.w;
-                }
-        }
+        bool first = true;
+#pragma unroll 1
         for (; u < end; ++u) {
+            copy_ahead(min(u + S::kStages, u1));  // into the stage read last time
+            if (first) {
+                first = false;
+                --pending;
+                wait_copies(pending);
+                if constexpr (S::kQInRegs) {
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(qp + i * 512);
+                        q[0][2 * i][0] = x.x;
+                        q[0][2 * i][1] = x.y;
+                        q[0][2 * i + 1][0] = x.z;
+                        q[0][2 * i + 1][1] = x.w;
+                    }
+                }
+            }
             if (alive) {
                 const bool ok = polls >= 0 ? mbar_wait_polls(full + stage, parity, polls)
                                            : mbar_wait_bounded(full + stage, parity);
@@ -440,7 +494,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                     // results are unspecified from here on, but every step of the split is made
                     if (lane == 0) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
                     alive = false;
-                    for (int k = u, s = stage, y = parity; k < pu; ++k) {  // no copy outlives the warp
+                    const int sent = max(pu, min(u0 + 1, u1));
+#pragma unroll 1
+                    for (int k = u, s = stage, y = parity; k < sent; ++k) {  // no copy outlives the warp
                         mbar_wait_bounded(full + s, y);
                         if (++s == S::kStages) s = 0, y ^= 1;
                     }
@@ -585,7 +641,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                     for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][2 * k + hi], frag, pf[nt][0], pf[nt][1]);
                 }
             __syncwarp();  // every lane has read this stage
-            copy_ahead(min(u + 1 + S::kStages, u1));
         }
         // --- the piece's end: sums over the lanes of a row
 #pragma unroll
@@ -614,28 +669,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                     if (a.lse_out && r == 0) a.lse_out[row] = (m[nt][i] + log2f(l[nt][i])) * kLn2;
                 }
         } else {
-            // the last thing that the warp does takes its shared memory (no copy is in
-            // flight any more); what it goes on after goes to the workspace
-            const bool in_ring = end == u1;
+            // --- a part.  The last thing that the warp does takes its shared memory (no copy
+            // is in flight any more); what it goes on after goes to the workspace
+            const int valid = min(kRows, n * group - seg.rt * kRows);
             __syncwarp();
-            float *rec = in_ring ? reinterpret_cast<float *>(mine) : record_of(cta, warp);
+            float *rec = end == u1 ? reinterpret_cast<float *>(mine) : record_of(cta, warp);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int row = nt * 8 + 2 * c + i;
+                    if (row >= valid) continue;
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k)
                         *reinterpret_cast<float4 *>(rec + row * D + r * S::kVPiece + 4 * k) =
                             make_float4(o[nt][2 * k][i] * w, o[nt][2 * k][i + 2] * w, o[nt][2 * k + 1][i] * w,
                                         o[nt][2 * k + 1][i + 2] * w);
-                    if (r == 0) {
-                        rec[kRows * D + row] = m[nt][i];
-                        rec[kRows * D + kRows + row] = l[nt][i];
-                    }
+                    if (r == 0)
+                        *reinterpret_cast<float2 *>(rec + a.record_rows * D + 2 * row) = make_float2(m[nt][i], l[nt][i]);
                 }
             if (lane == 0)
-                pieces[2 * warp + (seg_first >= u0)] = Piece{seg_first, seg_end, seg.b, seg.h, seg.rt, in_ring};
+                pieces[2 * warp + (seg_first >= u0)] = Piece{seg_first, seg_end, seg.b, seg.h, seg.rt, end == u1};
         }
         if (u < u1) {
             seg.j = seg.tiles - 1;
@@ -647,99 +701,103 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
     // --- joins.  Lane i knows piece i; pieces of one segment are neighbours, in the order of
     // the tokens.  A warp takes four rows of a segment, 8 lanes each.
     static_assert(2 * kWarps <= 32, "a lane for each piece");
-    Piece piece;
-    piece.first = -1;
-    if (lane < 2 * kWarps) piece = pieces[lane];
-    const unsigned there = __ballot_sync(~0u, piece.first >= 0);
+    const int my_first = lane < 2 * kWarps ? pieces[lane].first : -1;
+    const unsigned there = __ballot_sync(~0u, my_first >= 0);
     const unsigned lower = there & ((1u << lane) - 1);
-    const int prev = __shfl_sync(~0u, piece.first, lower ? 31 - __clz(lower) : 0);
-    const unsigned heads = __ballot_sync(~0u, piece.first >= 0 && (!lower || prev != piece.first));
+    const int prev = __shfl_sync(~0u, my_first, lower ? 31 - __clz(lower) : 0);
+    const unsigned heads = __ballot_sync(~0u, my_first >= 0 && (!lower || prev != my_first));
     const int segments = __popc(heads);
-    auto owner = [&](int u) { return static_cast<int>((static_cast<long long>(u + 1) * ctas - 1) / total); };
-    const int i8 = lane % 8;
-    for (int item = warp; item < segments * (kRows / 4); item += kWarps) {
-        const int quad = item / segments;
+    constexpr int kQuads = kRows / 4;
+#pragma unroll 1
+    for (int item = warp; item < segments * kQuads; item += kWarps) {
         unsigned of = heads;
-        for (int k = item - quad * segments; k > 0; --k) of &= of - 1;
+        int quad = 0, nth = item;
+        while (nth >= segments) nth -= segments, quad += 4;
+        for (; nth > 0; --nth) of &= of - 1;
         const int head = __ffs(of) - 1;
         const unsigned rest = of & (of - 1);
-        unsigned members = there & (rest ? (1u << (__ffs(rest) - 1)) - 1 : ~0u) & ~((1u << head) - 1);
-        const Piece whole = pieces[head];
-        Segment at;
-        at.b = whole.b;
-        at.h = whole.h;
-        at.rt = whole.rt;
-        if (quad * 4 >= (start[at.b + 1] - start[at.b]) * group - at.rt * kRows) continue;  // no such rows
-        const int row = quad * 4 + lane / 8;
-        Row<D> sums;
-        for (; members; members &= members - 1) {
-            const int k = __ffs(members) - 1;
-            const float *rec = pieces[k].in_ring ? reinterpret_cast<const float *>(smem + k / 2 * S::kWarpBytes)
-                                                 : record_of(cta, k / 2);
-            float4 x[D / 32];
+        unsigned members = there & (rest ? (rest & -rest) - 1 : ~0u) & ~((1u << head) - 1);
+        const Piece at = pieces[head];
+        seg.b = at.b;
+        seg.h = at.h;
+        seg.rt = at.rt;
+        const int valid = min(kRows, (start[seg.b + 1] - start[seg.b]) * group - seg.rt * kRows);
+        if (quad >= valid) continue;
+        const int row = min(quad + lane / 8, valid - 1), i8 = lane % 8;
+        const int side = at.first >= U0;
+        bool whole = side && at.end <= U1;
+        int from = 0, parts = 0;  // of the CTAs', on the second round
+#pragma unroll 1
+        while (true) {
+            Row<D> y;
+            constexpr int kAtOnce = 4;  // loads go out for so many parts together
+#pragma unroll 1
+            for (int k0 = 0; parts ? k0 < parts : members != 0; k0 += kAtOnce) {
+                float4 x[kAtOnce][D / 32];
+                float2 ml[kAtOnce];
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) x[j] = reinterpret_cast<const float4 *>(rec + row * D)[j * 8 + i8];
-            const float m = rec[kRows * D + row], l = rec[kRows * D + kRows + row];
-            if (m > sums.top) sums.move(m);
-            sums.add(m, l, x);
-        }
-        int token;
-        const long long out_row = row_at(t, a, at, kRows, group, row, &token);
-        if (whole.first >= U0 && whole.end <= U1) {
-            if (out_row >= 0) sums.write(a, out_row, i8);
-            continue;
-        }
-        // other CTAs share the segment: the last to arrive with these rows joins them, in
-        // the order of the CTAs
-        float *part = record_of(cta, kWarps + (whole.first >= U0));
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const float *rec;
+                    bool there_is;
+                    if (parts) {
+                        there_is = k0 + k < parts;
+                        rec = record_of(from + k0 + k, kWarps + (k0 + k == 0));
+                    } else {
+                        there_is = members != 0;
+                        const int p = there_is ? __ffs(members) - 1 : head;
+                        members &= members - 1;
+                        rec = pieces[p].in_ring ? reinterpret_cast<const float *>(smem + p / 2 * S::kWarpBytes)
+                                                : static_cast<const float *>(record_of(cta, p / 2));
+                    }
+                    ml[k] = make_float2(-INFINITY, 0.f);
+                    if (there_is) {
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) __stcg(reinterpret_cast<float4 *>(part + row * D) + j * 8 + i8, sums.sum[j]);
-        if (i8 == 0) {
-            __stcg(part + kRows * D + row, sums.top);
-            __stcg(part + kRows * D + kRows + row, sums.weight);
-        }
-        __syncwarp();
-        const int from = owner(whole.first), more = owner(whole.end - 1) - from;
-        int last = 0;
-        if (lane == 0) {
-            int *counter = reinterpret_cast<int *>(ws) + from * (kRows / 4) + quad;
-            const int old = atomic_add_acq_rel_gpu(counter, 1);
-            if (counter_not_zeroed(old, more)) {
-                flag_error(a.err, PKV_ERRBIT_WORKSPACE);
-                atomic_exch_relaxed_gpu(counter, kCounterPoison);
-            } else if (old == more) {
-                last = 1;
-                red_add_relaxed_gpu(counter, -(more + 1));
+                        for (int j = 0; j < D / 32; ++j) x[k][j] = load_fresh4(rec + row * D + j * 32 + i8 * 4);
+                        ml[k] = load_fresh2(rec + a.record_rows * D + 2 * row);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < D / 32; ++j) x[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+                float top = y.top;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+                y.move(top);
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) y.add(ml[k].x, ml[k].y, x[k]);
             }
-        }
-        if (!__shfl_sync(~0u, last, 0)) continue;
-        __syncwarp();
-        Row<D> joined;
-        constexpr int kAtOnce = 4;
-        for (int k0 = 0; k0 <= more; k0 += kAtOnce) {
-            float4 x[kAtOnce][D / 32];
-            float m[kAtOnce], l[kAtOnce];
+            if (whole) {
+                int token;
+                const long long out_row = row_at(t, a, seg, kRows, group, row, &token);
+                if (quad + lane / 8 < valid) y.write(a, out_row, i8);
+                break;
+            }
+            // other CTAs share the segment: the last to arrive with these rows joins them
+            float *part = record_of(cta, kWarps + side);
+            if (quad + lane / 8 < valid) {
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                m[k] = -INFINITY;
-                l[k] = 0.f;
-                if (k0 + k <= more) {  // the first CTA's part is its second
-                    const float *rec = record_of(from + k0 + k, kWarps + (k0 + k == 0));
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j)
-                        x[k][j] = __ldcg(reinterpret_cast<const float4 *>(rec + row * D) + j * 8 + i8);
-                    m[k] = __ldcg(rec + kRows * D + row);
-                    l[k] = __ldcg(rec + kRows * D + kRows + row);
+                for (int j = 0; j < D / 32; ++j)
+                    __stcg(reinterpret_cast<float4 *>(part + row * D) + j * 8 + i8, y.sum[j]);
+                if (i8 == 0)
+                    __stcg(reinterpret_cast<float2 *>(part + a.record_rows * D) + row, make_float2(y.top, y.weight));
+            }
+            __syncwarp();
+            from = of_ctas.of(at.first);
+            parts = of_ctas.of(at.end - 1) - from + 1;
+            if (lane == 0) {
+                int *counter = reinterpret_cast<int *>(ws) + from * kQuads + quad / 4;
+                const int old = atomic_add_acq_rel_gpu(counter, 1);
+                if (counter_not_zeroed(old, parts - 1)) {
+                    flag_error(a.err, PKV_ERRBIT_WORKSPACE);
+                    atomic_exch_relaxed_gpu(counter, kCounterPoison);
+                } else if (old == parts - 1) {
+                    whole = true;
+                    red_add_relaxed_gpu(counter, -parts);
                 }
             }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-                if (k0 + k <= more) {
-                    if (m[k] > joined.top) joined.move(m[k]);
-                    joined.add(m[k], l[k], x[k]);
-                }
+            whole = __shfl_sync(~0u, whole, 0);
+            if (!whole) break;
         }
-        if (out_row >= 0) joined.write(a, out_row, i8);
     }
 }
 
@@ -785,11 +843,12 @@ bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int he
     const double units = static_cast<double>(num_seqs) * n_kv_heads * tiles * ((rows + height - 1) / height);
     if (units >= 2147483648.0) return false;
     sp->ctas = sms;
-    const int most = static_cast<int>(kBalancedCounterBytes / height);  // a counter for four rows of each CTA
-    if (sp->ctas > most) sp->ctas = most;
     const int warps = sp->row_tiles == 1 ? Shape<128, 1>::kWarps : sp->row_tiles == 2 ? Shape<128, 2>::kWarps : Shape<128, 4>::kWarps;
-    const size_t record = (height * head_dim + 2 * height) * 4;
-    sp->ws_bytes = kBalancedCounterBytes + static_cast<size_t>(sp->ctas) * (warps + 2) * record;
+    const int most = kBalancedMaxWorkers / (2 * sp->row_tiles);  // a counter for four rows of each
+    if (sp->ctas > most) sp->ctas = most;
+    sp->record_rows = static_cast<int>(rows < height ? rows : height);
+    sp->ws_bytes = kBalancedCounterBytes +
+                   static_cast<size_t>(sp->ctas) * (warps + 2) * q8_record_floats(sp->record_rows, head_dim) * sizeof(float);
     return true;
 }
 
