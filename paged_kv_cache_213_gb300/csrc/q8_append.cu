@@ -8,6 +8,7 @@
 // A token alone (decode) is a team of one row's lanes.
 #include <cuda_fp16.h>
 
+#include "f32x2.cuh"
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 #include "q8.h"
@@ -19,17 +20,39 @@ namespace {
 // Entries of the head that one lane takes: 16 bytes of fp16, 8 of codes.
 constexpr int kPiece = 8;
 
-// Largest finite |x| of 8 values.
-__device__ __forceinline__ float top_of(const uint4 &x) {
+// The largest of 8 sizes |x|, as fp16 bits in either half of the result, and of another
+// 8's.  fp16 sizes are ordered like their bits.
+__device__ __forceinline__ uint32_t top_bits(const uint4 &x, uint32_t other) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) other = __vmaxu2(other, w[i] & 0x7fff7fffu);
+    return other;
+}
+
+// The same over the finite values alone.
+__device__ __forceinline__ uint32_t finite_top_bits(const uint4 &x, uint32_t other) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        if (lo < 0x7c00u) m = max(m, lo);
-        if (hi < 0x7c00u) m = max(m, hi);
+        if (lo < 0x7c00u) other = __vmaxu2(other, lo);
+        if (hi < 0x7c00u) other = __vmaxu2(other, hi);
     }
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
+    return other;
+}
+
+// Largest finite |x| of N pieces.
+template <int N>
+__device__ __forceinline__ float top_of(const uint4 (&x)[N]) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) t = top_bits(x[i], t);
+    if ((t & 0xffffu) >= 0x7c00u || (t >> 16) >= 0x7c00u) {  // rare: infinities or NaN
+        t = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) t = finite_top_bits(x[i], t);
+    }
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(max(t & 0xffffu, t >> 16))));
 }
 
 // The scale after new tokens of largest entry `top`, and by how many powers of two
@@ -47,17 +70,25 @@ __device__ __forceinline__ float grown(float had, float top, int *power) {
     return ldexpf(had, k);
 }
 
+// What quantises by a scale: the divisor and its reciprocal (0: a scale that divide2 does
+// not take).
+struct Divisor {
+    float s, inv;
+    __device__ explicit Divisor(float scale) : s(scale > 0.f ? scale : 1.f) {
+        inv = s >= 8.7e-19f && s <= 1.1e18f ? __frcp_rn(s) : 0.f;  // 2^-60, 2^60
+    }
+};
+
 template <int KIND>
-__device__ __forceinline__ uint2 quantised(const uint4 &x, float scale) {
+__device__ __forceinline__ uint2 quantised(const uint4 &x, const Divisor &d) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&x);
-    const float s = scale > 0.f ? scale : 1.f;
-    uint32_t w[4];
+    float2 q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(h[i]);
-        w[i] = q8_encode2<KIND>(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+        q[i] = d.inv != 0.f ? divide2(f, d.s, d.inv) : make_float2(__fdiv_rn(f.x, d.s), __fdiv_rn(f.y, d.s));
     }
-    return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    return make_uint2(q8_encode4<KIND>(q[0], q[1]), q8_encode4<KIND>(q[2], q[3]));
 }
 
 // Codes of earlier tokens, whose scale grew by 2^power: code * 2^-power.
@@ -71,7 +102,7 @@ __device__ __forceinline__ uint2 shrunk(const uint2 &c, int power) {
         const uint32_t lo = q8_widen<KIND, 0>(w[i]), hi = q8_widen<KIND, 1>(w[i]);
         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
         const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        r[i] = q8_encode2<KIND>(a.x * f, a.y * f) | (q8_encode2<KIND>(b.x * f, b.y * f) << 16);
+        r[i] = q8_encode4<KIND>(make_float2(a.x * f, a.y * f), make_float2(b.x * f, b.y * f));
     }
     return make_uint2(r[0], r[1]);
 }
@@ -104,12 +135,12 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
         if (!ok && lane == 0 && h == 0 && side == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
         live = ok && n == 1;
     }
-    uint4 x = make_uint4(0, 0, 0, 0);
+    uint4 x[1] = {make_uint4(0, 0, 0, 0)};
     long long block = -1;
     int row = 0;
     if (live) {
         const uint4 *src = static_cast<const uint4 *>(side ? a.v_new : a.k_new);
-        x = __ldcs(src + (token * (side ? a.v_stride : a.k_stride) + h * D) / kPiece + lane);
+        x[0] = __ldcs(src + (token * (side ? a.v_stride : a.k_stride) + h * D) / kPiece + lane);
         const int j = (len - 1) / a.block_size;
         row = (len - 1) - j * a.block_size;
         block = a.block_tables[static_cast<long long>(b) * a.max_blocks_per_seq + j];
@@ -128,20 +159,20 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
     int power;
     const float scale = grown<KIND>(had, top, &power);
     uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * a.block_size * kTeam + lane;
-    rows[row * kTeam] = quantised<KIND>(x, scale);
+    rows[row * kTeam] = quantised<KIND>(x[0], Divisor(scale));
     if (power > 0)
         for (int r = 0; r < row; ++r) rows[r * kTeam] = shrunk<KIND>(rows[r * kTeam], power);
     if (lane == 0 && (row == 0 || scale != had)) scales[cell] = scale;
 }
 
-// Several tokens a sequence.  A CTA takes one block that a sequence touches and
-// 128 / block_size heads of it (one head from 128 rows on), eight warps of 16 rows
-// each (32 at 256 rows a block); the warps of a head exchange their largest entries.
+// Several tokens a sequence.  A CTA takes K or V of one block that a sequence touches, for
+// kWarps * 16 / block_size heads (one head from kWarps * 16 rows on), its warps 16 rows
+// each (32 or 64 at 128 or 256 rows a block); the warps of a head exchange their largest entries.
 //
 // Which block: the blocks of sequence b get the numbers from start[b] / bs + 2 b on.
 // A run of n tokens touches at most n / bs + 2 blocks (rounded down), so the ranges do
 // not meet, and a CTA finds its sequence without a sum over the ones before.
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
 template <int KIND, int D, int ROWS>  // rows of a warp
 __global__ void __launch_bounds__(kWarps * 32) q8_append_many_kernel(const Q8AppendArgs a) {
@@ -150,86 +181,83 @@ __global__ void __launch_bounds__(kWarps * 32) q8_append_many_kernel(const Q8App
     constexpr int kSteps = ROWS / kAt;
     grid_dependency_wait();
     allow_dependent_launch();
-    __shared__ int which;
-    __shared__ float tops[2][kWarps];
+    struct Found {
+        int b, start, n, len;
+    };
+    __shared__ Found found;
+    __shared__ float tops[kWarps];
     const long long v = blockIdx.x;
-    const int bs = a.block_size;
-    if (threadIdx.x == 0) which = -1;
+    const int bs = a.block_size, side = blockIdx.z;
+    const bool reports = blockIdx.y == 0 && side == 0 && threadIdx.x == 0;
+    if (threadIdx.x == 0) found.b = -1;
     __syncthreads();
     for (int b = threadIdx.x; b < a.num_seqs; b += kWarps * 32) {
-        const int s = a.query_start[b], e = a.query_start[b + 1];
+        const int s = a.query_start[b], e = a.query_start[b + 1], len = a.context_lens[b];
         if (s < 0 || e < s || e > a.total) {
-            if (v == 0 && blockIdx.y == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+            if (v == 0 && blockIdx.y == 0 && side == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
             continue;
         }
-        if (s / bs + 2ll * b <= v && v < e / bs + 2ll * (b + 1)) which = b;
+        if (s / bs + 2ll * b <= v && v < e / bs + 2ll * (b + 1)) found = Found{b, s, e - s, len};
     }
     __syncthreads();
-    const int b = which;
-    if (b < 0) return;
-    const int s = a.query_start[b], n = a.query_start[b + 1] - s, len = a.context_lens[b];
-    const int slot = static_cast<int>(v - (s / bs + 2ll * b));
-    if (n > a.max_q_len || n > len ||
-        len > static_cast<long long>(a.max_blocks_per_seq) * bs) {
-        if (threadIdx.x == 0 && slot == 0 && blockIdx.y == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+    const Found f = found;
+    if (f.b < 0 || f.n == 0) return;
+    const int slot = static_cast<int>(v - (f.start / bs + 2ll * f.b));
+    if (f.n > a.max_q_len || f.n > f.len || f.len > static_cast<long long>(a.max_blocks_per_seq) * bs) {
+        if (reports && slot == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
         return;
     }
-    const int first = len - n, j = first / bs + slot;
-    if (n == 0 || static_cast<long long>(j) * bs >= len) return;
-    const long long block = a.block_tables[static_cast<long long>(b) * a.max_blocks_per_seq + j];
-    if (block < 0 || block >= a.num_blocks) {
-        if (threadIdx.x == 0 && blockIdx.y == 0) flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
-        return;
-    }
-    const int low = max(first - j * bs, 0), high = min(len - j * bs, bs);  // the new rows
+    const int first = f.len - f.n, j = first / bs + slot;
+    if (static_cast<long long>(j) * bs >= f.len) return;
+    const long long block = a.block_tables[static_cast<long long>(f.b) * a.max_blocks_per_seq + j];
+    const int low = max(first - j * bs, 0), high = min(f.len - j * bs, bs);  // the new rows
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int per_head = bs / ROWS;          // warps of a head
     const int h = blockIdx.y * (kWarps / per_head) + warp / per_head;
     const int row0 = (warp % per_head) * ROWS + lane / kTeam;
     const bool live = h < a.n_kv_heads;
     const int hc = live ? h : 0;
-    const long long cell = block * a.n_kv_heads + hc;
-    const long long token0 = static_cast<long long>(s) - first + j * bs;  // token of row 0
+    // the tokens are read while the block's number is on its way
+    const uint4 *src = static_cast<const uint4 *>(side ? a.v_new : a.k_new) + hc * kTeam + lane % kTeam;
+    const long long stride = (side ? a.v_stride : a.k_stride) / kPiece;
+    const long long token0 = static_cast<long long>(f.start) - first + j * bs;  // token of row 0
+    uint4 x[kSteps];
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-        const uint4 *src = static_cast<const uint4 *>(side ? a.v_new : a.k_new);
-        const long long stride = (side ? a.v_stride : a.k_stride) / kPiece;
-        uint4 x[kSteps];
-        float top = 0.f;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int row = row0 + i * kAt;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (live && row >= low && row < high)
-                x[i] = __ldcs(src + (token0 + row) * stride + hc * kTeam + lane % kTeam);
-        }
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) top = fmaxf(top, top_of(x[i]));
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-        float *scales = side ? a.v_scales : a.k_scales;
-        const float had = live && low > 0 ? scales[cell] : 0.f;
-        if (per_head > 1) {
-            if (lane == 0) tops[side][warp] = top;
-            __syncthreads();  // and every warp has read the old scale
-            for (int w = 0; w < per_head; ++w) top = fmaxf(top, tops[side][warp / per_head * per_head + w]);
-        } else {
-            __syncwarp();
-        }
-        if (!live) continue;
-        int power;
-        const float scale = grown<KIND>(had, top, &power);
-        uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * bs * kTeam + lane % kTeam;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int row = row0 + i * kAt;
-            if (row >= low && row < high) rows[row * kTeam] = quantised<KIND>(x[i], scale);
-        }
-        if (power > 0)
-            for (int row = row0; row < min(low, row0 + ROWS); row += kAt)
-                rows[row * kTeam] = shrunk<KIND>(rows[row * kTeam], power);
-        if (warp % per_head == 0 && lane == 0 && (low == 0 || scale != had)) scales[cell] = scale;
+    for (int i = 0; i < kSteps; ++i) {
+        const int row = row0 + i * kAt;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (live && row >= low && row < high) x[i] = __ldcs(src + (token0 + row) * stride);
     }
+    if (block < 0 || block >= a.num_blocks) {
+        if (reports) flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
+        return;
+    }
+    const long long cell = block * a.n_kv_heads + hc;
+    float *scales = side ? a.v_scales : a.k_scales;
+    const float had = live && low > 0 ? scales[cell] : 0.f;
+    float top = top_of(x);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (per_head > 1) {
+        if (lane == 0) tops[warp] = top;
+        __syncthreads();  // and every warp has read the old scale
+        for (int w = 0; w < per_head; ++w) top = fmaxf(top, tops[warp / per_head * per_head + w]);
+    }
+    if (!live) return;
+    __syncwarp();
+    int power;
+    const float scale = grown<KIND>(had, top, &power);
+    const Divisor divisor(scale);
+    uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * bs * kTeam + lane % kTeam;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int row = row0 + i * kAt;
+        if (row >= low && row < high) rows[row * kTeam] = quantised<KIND>(x[i], divisor);
+    }
+    if (power > 0)
+        for (int row = row0; row < min(low, row0 - lane / kTeam + ROWS); row += kAt)
+            rows[row * kTeam] = shrunk<KIND>(rows[row * kTeam], power);
+    if (warp % per_head == 0 && lane == 0 && (low == 0 || scale != had)) scales[cell] = scale;
 }
 
 template <int KIND, int D>
@@ -241,51 +269,56 @@ cudaError_t launch_append(const Q8AppendArgs &a, cudaStream_t stream) {
         return launch_pdl(q8_append_one_kernel<KIND, D>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
                           stream, a);
     }
-    const int rows = a.block_size == 256 ? 32 : 16;
-    const int heads = kWarps / (a.block_size / rows);
+    const int rows = a.block_size <= kWarps * 16 ? 16 : a.block_size / kWarps;
+    const int heads = kWarps * rows / a.block_size;
     const long long slots = a.total / a.block_size + 2ll * a.num_seqs;
     const int groups = (a.n_kv_heads + heads - 1) / heads;
     if (slots > 0x7fffffffLL || groups > 65535) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(groups));
-    if (rows == 32)
-        return launch_pdl(q8_append_many_kernel<KIND, D, 32>, grid, dim3(kWarps * 32), 0, stream, a);
-    return launch_pdl(q8_append_many_kernel<KIND, D, 16>, grid, dim3(kWarps * 32), 0, stream, a);
+    const dim3 grid(static_cast<unsigned>(slots), static_cast<unsigned>(groups), 2), threads(kWarps * 32);
+    if (rows == 64) return launch_pdl(q8_append_many_kernel<KIND, D, 64>, grid, threads, 0, stream, a);
+    if (rows == 32) return launch_pdl(q8_append_many_kernel<KIND, D, 32>, grid, threads, 0, stream, a);
+    return launch_pdl(q8_append_many_kernel<KIND, D, 16>, grid, threads, 0, stream, a);
 }
 
 // --- read-back --------------------------------------------------------------
 
 constexpr int kGatherThreads = 256, kGatherRows = 16;
 
-// A CTA takes 16 output rows of every head: one thread a row finds its place in the
-// cache, then each thread turns 16 codes into 32 bytes, rows next to each other in
-// the block by neighbouring lanes.
+// A CTA takes 16 output rows of every head.  Each thread asks whether its sequences own
+// some of them (no search, whose steps would wait for one another), one thread a row
+// looks the row's block up, then each thread turns 16 codes into 32 bytes, rows next
+// to each other in the block by neighbouring lanes.
 template <int KIND, int D>
 __global__ void __launch_bounds__(kGatherThreads) q8_gather_kernel(const Q8GatherArgs a) {
     constexpr int kLanes = D / 16;
     grid_dependency_wait();
     allow_dependent_launch();
-    __shared__ int block_of[kGatherRows], row_of[kGatherRows];
+    __shared__ int seq_of[kGatherRows], block_of[kGatherRows], row_of[kGatherRows];
     const long long first = static_cast<long long>(blockIdx.x) * kGatherRows;
+    if (threadIdx.x < kGatherRows) seq_of[threadIdx.x] = -1;
+    __syncthreads();
+    for (int b = threadIdx.x; b < a.num_seqs; b += kGatherThreads) {
+        const long long s = a.start[b], e = a.start[b + 1];
+        if (s < 0) continue;
+        for (long long r = max(s, first); r < min(e, first + kGatherRows); ++r) {
+            seq_of[r - first] = b;
+            row_of[r - first] = static_cast<int>(r - s);
+        }
+    }
+    __syncthreads();
     if (threadIdx.x < kGatherRows) {
-        const long long r = first + threadIdx.x;
+        const int b = seq_of[threadIdx.x];
         int block = -1, row = 0;
-        if (r < a.total && r >= a.start[0] && r < a.start[a.num_seqs]) {
-            int lo = 0, hi = a.num_seqs;  // start[lo] <= r < start[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (a.start[mid] <= r) lo = mid; else hi = mid;
-            }
-            const long long t = r - a.start[lo];
-            const long long j = t / a.block_size;
-            if (t < 0 || j >= a.max_blocks_per_seq) {
+        if (b >= 0 && first + threadIdx.x < a.total) {
+            const int t = row_of[threadIdx.x], j = t / a.block_size;
+            if (j >= a.max_blocks_per_seq) {
                 flag_error(a.err, PKV_ERRBIT_CONTEXT);
             } else {
-                const int id = a.block_tables[static_cast<long long>(lo) * a.max_blocks_per_seq + j];
-                if (id < 0 || id >= a.num_blocks) {
+                block = a.block_tables[static_cast<long long>(b) * a.max_blocks_per_seq + j];
+                row = t - j * a.block_size;
+                if (block < 0 || block >= a.num_blocks) {
                     flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
-                } else {
-                    block = id;
-                    row = static_cast<int>(t - j * a.block_size);
+                    block = -1;
                 }
             }
         }
@@ -295,30 +328,42 @@ __global__ void __launch_bounds__(kGatherThreads) q8_gather_kernel(const Q8Gathe
     __syncthreads();
     const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes % kGatherRows;
     constexpr int kGroups = kGatherThreads / (kLanes * kGatherRows);  // (side, head) pairs at once
+    constexpr int kAtOnce = 4;                                        // and in flight a thread
     const int block = block_of[row];
     if (block < 0) return;
     const long long r = first + row;
-    for (int p = threadIdx.x / (kLanes * kGatherRows); p < 2 * a.n_kv_heads; p += kGroups) {
-        const int side = p / a.n_kv_heads, h = p - side * a.n_kv_heads;
-        const long long cell = static_cast<long long>(block) * a.n_kv_heads + h;
-        const uint4 c = __ldcs(static_cast<const uint4 *>(side ? a.v_cache : a.k_cache) +
-                               (cell * a.block_size + row_of[row]) * kLanes + lane);
-        const float scale = (side ? a.v_scales : a.k_scales)[cell];
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        uint32_t y[8];
+    for (int p0 = threadIdx.x / (kLanes * kGatherRows); p0 < 2 * a.n_kv_heads; p0 += kGroups * kAtOnce) {
+        uint4 c[kAtOnce];
+        float scale[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t u = i % 2 ? q8_widen<KIND, 1>(w[i / 2]) : q8_widen<KIND, 0>(w[i / 2]);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
-            // a NaN code stays NaN: the comparisons of the clamp are false for it
-            float p0 = f.x * scale, p1 = f.y * scale;
-            p0 = p0 > 65504.f ? 65504.f : p0 < -65504.f ? -65504.f : p0;
-            p1 = p1 > 65504.f ? 65504.f : p1 < -65504.f ? -65504.f : p1;
-            y[i] = pack_half2(p0, p1);
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int p = p0 + i * kGroups, side = p >= a.n_kv_heads, h = side ? p - a.n_kv_heads : p;
+            if (p >= 2 * a.n_kv_heads) continue;
+            const long long cell = static_cast<long long>(block) * a.n_kv_heads + h;
+            c[i] = __ldcs(static_cast<const uint4 *>(side ? a.v_cache : a.k_cache) +
+                          (cell * a.block_size + row_of[row]) * kLanes + lane);
+            scale[i] = __ldg((side ? a.v_scales : a.k_scales) + cell);
         }
-        uint4 *dst = static_cast<uint4 *>(side ? a.v : a.k) + ((r * a.n_kv_heads + h) * kLanes + lane) * 2;
-        __stcs(dst, make_uint4(y[0], y[1], y[2], y[3]));
-        __stcs(dst + 1, make_uint4(y[4], y[5], y[6], y[7]));
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int p = p0 + i * kGroups, side = p >= a.n_kv_heads, h = side ? p - a.n_kv_heads : p;
+            if (p >= 2 * a.n_kv_heads) continue;
+            const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+            uint32_t y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t u = k % 2 ? q8_widen<KIND, 1>(w[k / 2]) : q8_widen<KIND, 0>(w[k / 2]);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+                // a NaN code stays NaN: the comparisons of the clamp are false for it
+                float p0 = f.x * scale[i], p1 = f.y * scale[i];
+                p0 = p0 > 65504.f ? 65504.f : p0 < -65504.f ? -65504.f : p0;
+                p1 = p1 > 65504.f ? 65504.f : p1 < -65504.f ? -65504.f : p1;
+                y[k] = pack_half2(p0, p1);
+            }
+            uint4 *dst = static_cast<uint4 *>(side ? a.v : a.k) + ((r * a.n_kv_heads + h) * kLanes + lane) * 2;
+            __stcs(dst, make_uint4(y[0], y[1], y[2], y[3]));
+            __stcs(dst + 1, make_uint4(y[4], y[5], y[6], y[7]));
+        }
     }
 }
 

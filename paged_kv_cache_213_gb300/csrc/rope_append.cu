@@ -36,22 +36,6 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float2 (&f)[4]) {
     for (int i = 0; i < 4; ++i) f[i] = __half22float2(h[i]);
 }
 
-// x / scale, correctly rounded: the quotient by the reciprocal inv = RN(1 / scale),
-// then twice corrected by its exact residual (Markstein: with a correctly rounded
-// reciprocal and a quotient within one unit in the last place, one such correction
-// gives the rounded quotient; the first brings it there).  Exact where the residual is
-// a normal number, which holds for |x / scale| >= 2^-11 (smaller ones become code 0)
-// and scales in [2^-60, 2^60]; a quotient that is not finite stays as it is, and the
-// sign is that of x (a residual of 0 would turn -0 into 0).
-__device__ __forceinline__ float2 divide2(float2 x, float scale, float inv) {
-    const float2 s = make_float2(-scale, -scale), y = make_float2(inv, inv);
-    const float2 q0 = mul2(x, y);
-    const float2 q1 = fma2(fma2(s, q0, x), y, q0);
-    const float2 q2 = fma2(fma2(s, q1, x), y, q1);
-    return make_float2(fabsf(q0.x) < 1e30f ? copysignf(q2.x, q0.x) : q0.x,
-                       fabsf(q0.y) < 1e30f ? copysignf(q2.y, q0.y) : q0.y);
-}
-
 // 8 fp32 values to 8 E4M3 codes of y / scale, to the codes that paged_kv_append_fp8
 // stores.  inv = RN(1 / scale), or 0 for a scale that divide2 does not take.
 __device__ __forceinline__ uint2 quantize8(const float2 (&y)[4], float scale, float inv) {
