@@ -41,13 +41,14 @@ __device__ __forceinline__ uint32_t finite_top_bits(const uint4 &x, uint32_t oth
     return other;
 }
 
-// Largest finite |x| of N pieces.
+// Largest finite |x| of N pieces, and whether some are not finite.
 template <int N>
-__device__ __forceinline__ float top_of(const uint4 (&x)[N]) {
+__device__ __forceinline__ float top_of(const uint4 (&x)[N], bool *special) {
     uint32_t t = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) t = top_bits(x[i], t);
-    if ((t & 0xffffu) >= 0x7c00u || (t >> 16) >= 0x7c00u) {  // rare: infinities or NaN
+    *special = (t & 0xffffu) >= 0x7c00u || (t >> 16) >= 0x7c00u;
+    if (*special) {
         t = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) t = finite_top_bits(x[i], t);
@@ -79,16 +80,18 @@ struct Divisor {
     }
 };
 
-template <int KIND>
+// Codes of 8 values.  PLAIN: they are finite, no larger than what the scale covers, and
+// the divisor has a reciprocal.
+template <int KIND, bool PLAIN>
 __device__ __forceinline__ uint2 quantised(const uint4 &x, const Divisor &d) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&x);
     float2 q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(h[i]);
-        q[i] = d.inv != 0.f ? divide2(f, d.s, d.inv) : make_float2(__fdiv_rn(f.x, d.s), __fdiv_rn(f.y, d.s));
+        q[i] = PLAIN ? divide2_finite(f, d.s, d.inv) : make_float2(__fdiv_rn(f.x, d.s), __fdiv_rn(f.y, d.s));
     }
-    return make_uint2(q8_encode4<KIND>(q[0], q[1]), q8_encode4<KIND>(q[2], q[3]));
+    return make_uint2(q8_encode4<KIND, PLAIN>(q[0], q[1]), q8_encode4<KIND, PLAIN>(q[2], q[3]));
 }
 
 // Codes of earlier tokens, whose scale grew by 2^power: code * 2^-power.
@@ -149,7 +152,8 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
             live = false;
         }
     }
-    float top = top_of(x);
+    bool special;
+    float top = top_of(x, &special);
 #pragma unroll
     for (int d = kTeam / 2; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     if (!live) return;
@@ -159,7 +163,9 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
     int power;
     const float scale = grown<KIND>(had, top, &power);
     uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * a.block_size * kTeam + lane;
-    rows[row * kTeam] = quantised<KIND>(x[0], Divisor(scale));
+    const Divisor divisor(scale);
+    rows[row * kTeam] = special || divisor.inv == 0.f ? quantised<KIND, false>(x[0], divisor)
+                                                      : quantised<KIND, true>(x[0], divisor);
     if (power > 0)
         for (int r = 0; r < row; ++r) rows[r * kTeam] = shrunk<KIND>(rows[r * kTeam], power);
     if (lane == 0 && (row == 0 || scale != had)) scales[cell] = scale;
@@ -235,7 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32) q8_append_many_kernel(const Q8App
     const long long cell = block * a.n_kv_heads + hc;
     float *scales = side ? a.v_scales : a.k_scales;
     const float had = live && low > 0 ? scales[cell] : 0.f;
-    float top = top_of(x);
+    bool special;
+    float top = top_of(x, &special);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
     if (per_head > 1) {
@@ -249,10 +256,18 @@ __global__ void __launch_bounds__(kWarps * 32) q8_append_many_kernel(const Q8App
     const float scale = grown<KIND>(had, top, &power);
     const Divisor divisor(scale);
     uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * bs * kTeam + lane % kTeam;
+    if (!special && divisor.inv != 0.f) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int row = row0 + i * kAt;
-        if (row >= low && row < high) rows[row * kTeam] = quantised<KIND>(x[i], divisor);
+        for (int i = 0; i < kSteps; ++i) {
+            const int row = row0 + i * kAt;
+            if (row >= low && row < high) rows[row * kTeam] = quantised<KIND, true>(x[i], divisor);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            const int row = row0 + i * kAt;
+            if (row >= low && row < high) rows[row * kTeam] = quantised<KIND, false>(x[i], divisor);
+        }
     }
     if (power > 0)
         for (int row = row0; row < min(low, row0 - lane / kTeam + ROWS); row += kAt)
@@ -282,31 +297,33 @@ cudaError_t launch_append(const Q8AppendArgs &a, cudaStream_t stream) {
 
 // --- read-back --------------------------------------------------------------
 
-constexpr int kGatherThreads = 256, kGatherRows = 16;
+constexpr int kGatherThreads = 256;
 
-// A CTA takes 16 output rows of every head.  Each thread asks whether its sequences own
+// A CTA takes ROWS output rows of every head.  Each thread asks whether its sequences own
 // some of them (no search, whose steps would wait for one another), one thread a row
 // looks the row's block up, then each thread turns 16 codes into 32 bytes, rows next
 // to each other in the block by neighbouring lanes.
-template <int KIND, int D>
-__global__ void __launch_bounds__(kGatherThreads) q8_gather_kernel(const Q8GatherArgs a) {
+// (The bound of one CTA lets the compiler take 48 registers and keep both loads in flight; at the
+// 32 that it takes without, 72000 rows take 82.6 us.)
+template <int KIND, int D, int ROWS>
+__global__ void __launch_bounds__(kGatherThreads, 1) q8_gather_kernel(const Q8GatherArgs a) {
     constexpr int kLanes = D / 16;
     grid_dependency_wait();
     allow_dependent_launch();
-    __shared__ int seq_of[kGatherRows], block_of[kGatherRows], row_of[kGatherRows];
-    const long long first = static_cast<long long>(blockIdx.x) * kGatherRows;
-    if (threadIdx.x < kGatherRows) seq_of[threadIdx.x] = -1;
+    __shared__ int seq_of[ROWS], block_of[ROWS], row_of[ROWS];
+    const long long first = static_cast<long long>(blockIdx.x) * ROWS;
+    if (threadIdx.x < ROWS) seq_of[threadIdx.x] = -1;
     __syncthreads();
     for (int b = threadIdx.x; b < a.num_seqs; b += kGatherThreads) {
         const long long s = a.start[b], e = a.start[b + 1];
         if (s < 0) continue;
-        for (long long r = max(s, first); r < min(e, first + kGatherRows); ++r) {
+        for (long long r = max(s, first); r < min(e, first + ROWS); ++r) {
             seq_of[r - first] = b;
             row_of[r - first] = static_cast<int>(r - s);
         }
     }
     __syncthreads();
-    if (threadIdx.x < kGatherRows) {
+    if (threadIdx.x < ROWS) {
         const int b = seq_of[threadIdx.x];
         int block = -1, row = 0;
         if (b >= 0 && first + threadIdx.x < a.total) {
@@ -326,13 +343,13 @@ __global__ void __launch_bounds__(kGatherThreads) q8_gather_kernel(const Q8Gathe
         row_of[threadIdx.x] = row;
     }
     __syncthreads();
-    const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes % kGatherRows;
-    constexpr int kGroups = kGatherThreads / (kLanes * kGatherRows);  // (side, head) pairs at once
-    constexpr int kAtOnce = 4;                                        // and in flight a thread
+    const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes % ROWS;
+    constexpr int kGroups = kGatherThreads / (kLanes * ROWS);  // (side, head) pairs at once
+    constexpr int kAtOnce = 2;  // and in flight a thread (1: 73.4 us, 4: 87, with 8 x 2000-16000 tokens; this 70.1)
     const int block = block_of[row];
     if (block < 0) return;
     const long long r = first + row;
-    for (int p0 = threadIdx.x / (kLanes * kGatherRows); p0 < 2 * a.n_kv_heads; p0 += kGroups * kAtOnce) {
+    for (int p0 = threadIdx.x / (kLanes * ROWS); p0 < 2 * a.n_kv_heads; p0 += kGroups * kAtOnce) {
         uint4 c[kAtOnce];
         float scale[kAtOnce];
 #pragma unroll
@@ -403,17 +420,27 @@ cudaError_t launch_q8_append(const Q8AppendArgs &a, int kind, cudaStream_t strea
                                : launch_append<PKV_Q8_INT8, 64>(a, stream);
 }
 
-cudaError_t launch_q8_gather(const Q8GatherArgs &a, int kind, cudaStream_t stream) {
-    const long long blocks = (a.total + kGatherRows - 1) / kGatherRows;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+namespace {
+
+template <int KIND, int D>
+cudaError_t launch_gather(const Q8GatherArgs &a, cudaStream_t stream) {
+    // 16 rows a CTA, or 8 where those would leave SMs idle (1160 rows of 8 heads: 3.5 us, with
+    // 16 rows 5.1; 72000 rows: 73.8 us with 8 rows, 70.1 with 16)
+    const bool few = a.total <= 16 * 304;
+    const long long blocks = (a.total + (few ? 7 : 15)) / (few ? 8 : 16);
     const dim3 grid(static_cast<unsigned>(blocks)), threads(kGatherThreads);
+    return few ? launch_pdl(q8_gather_kernel<KIND, D, 8>, grid, threads, 0, stream, a)
+               : launch_pdl(q8_gather_kernel<KIND, D, 16>, grid, threads, 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_q8_gather(const Q8GatherArgs &a, int kind, cudaStream_t stream) {
     if (a.head_dim == 128)
-        return kind == PKV_Q8_E4M3
-                   ? launch_pdl(q8_gather_kernel<PKV_Q8_E4M3, 128>, grid, threads, 0, stream, a)
-                   : launch_pdl(q8_gather_kernel<PKV_Q8_INT8, 128>, grid, threads, 0, stream, a);
-    return kind == PKV_Q8_E4M3
-               ? launch_pdl(q8_gather_kernel<PKV_Q8_E4M3, 64>, grid, threads, 0, stream, a)
-               : launch_pdl(q8_gather_kernel<PKV_Q8_INT8, 64>, grid, threads, 0, stream, a);
+        return kind == PKV_Q8_E4M3 ? launch_gather<PKV_Q8_E4M3, 128>(a, stream)
+                                   : launch_gather<PKV_Q8_INT8, 128>(a, stream);
+    return kind == PKV_Q8_E4M3 ? launch_gather<PKV_Q8_E4M3, 64>(a, stream)
+                               : launch_gather<PKV_Q8_INT8, 64>(a, stream);
 }
 
 cudaError_t launch_q8_copy(const Q8CopyArgs &a, cudaStream_t stream) {

@@ -17,8 +17,9 @@ __device__ __forceinline__ constexpr float q8_limit() {
 }
 
 // Four quotients to four codes, the first in the low byte: to nearest even,
-// saturated; NaN to the NaN code, or 0 for int8.
-template <int KIND>
+// saturated; NaN to the NaN code, or 0 for int8.  PLAIN: all are numbers that need no
+// saturation (they round to a code).
+template <int KIND, bool PLAIN = false>
 __device__ __forceinline__ uint32_t q8_encode4(float2 a, float2 b) {
     if (KIND == PKV_Q8_E4M3)
         return __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3) |
@@ -26,7 +27,7 @@ __device__ __forceinline__ uint32_t q8_encode4(float2 a, float2 b) {
     // 1.5 * 2^23 leaves the whole number, rounded to even, in the sum's low byte (a
     // conversion instruction has a quarter of the additions' rate)
     auto low = [](float x) {
-        x = x == x ? fminf(fmaxf(x, -127.f), 127.f) : 0.f;
+        if (!PLAIN) x = x == x ? fminf(fmaxf(x, -127.f), 127.f) : 0.f;
         return __float_as_uint(x + 12582912.f);
     };
     return __byte_perm(__byte_perm(low(a.x), low(a.y), 0x0040), __byte_perm(low(b.x), low(b.y), 0x0040), 0x5410);
