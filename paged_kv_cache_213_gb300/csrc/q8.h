@@ -84,7 +84,7 @@ struct Q8AttentionArgs {
 };
 // How a call's work is split: `ctas` CTAs of the kernel for `row_tiles` x 8 query rows.
 struct Q8Split {
-    int row_tiles;
+    int row_tiles;  // 0: the kernel of q8_prefill.cu
     int ctas;
     int record_rows;  // query rows that a segment has at most
     size_t ws_bytes;
@@ -92,6 +92,10 @@ struct Q8Split {
 // false: more than 2^31 units of work.
 bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
               int max_len, int sms, Q8Split *sp);
+bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
+                      int max_len, int sms, Q8Split *sp);
+cudaError_t launch_q8_prefill(const Q8AttentionArgs &a, int kind, const Q8Split &sp,
+                              cudaStream_t stream);
 cudaError_t launch_q8_attention(const Q8AttentionArgs &a, int kind, const Q8Split &sp,
                                 cudaStream_t stream);
 

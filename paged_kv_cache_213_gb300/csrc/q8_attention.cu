@@ -34,6 +34,9 @@
 #include "q8.h"
 #include "q8_codes.cuh"
 
+#ifndef PFMIN
+#define PFMIN 24
+#endif
 namespace pkv {
 namespace {
 
@@ -837,6 +840,7 @@ static_assert(fits<1>() && fits<2>() && fits<3>() && fits<4>(), "shared memory")
 bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
               int sms, Q8Split *sp) {
     const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
+    if (rows > PFMIN) return q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, sp);
     sp->row_tiles = rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
     const long long height = 8 * sp->row_tiles;
     const long long tiles = (static_cast<long long>(max_len) + kTile - 1) / kTile;
@@ -854,6 +858,7 @@ bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int he
 
 cudaError_t launch_q8_attention(const Q8AttentionArgs &a, int kind, const Q8Split &sp,
                                 cudaStream_t stream) {
+    if (sp.row_tiles == 0) return launch_q8_prefill(a, kind, sp, stream);
     if (a.head_dim == 128)
         return kind == PKV_Q8_E4M3 ? launch_rows<PKV_Q8_E4M3, 128>(a, sp, stream)
                                    : launch_rows<PKV_Q8_INT8, 128>(a, sp, stream);

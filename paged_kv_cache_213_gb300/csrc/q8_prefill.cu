@@ -1,0 +1,727 @@
+// q8_prefill.cu -- attention over the 8-bit caches with block scales for many query rows
+// of a KV head: chunks of prompts, drafts to verify (paged_decode_attention_q8).
+//
+// An item is two tiles of 128 query rows (tokens x heads of a group) of one KV head.  For a
+// step of 128 keys, codes K, V widened to fp16 (exact) in shared memory:
+//   S [128 x 128] = Q K^T
+//   y = 2^(S f - r)          f: the key's block scale * scale * log2 e; r: the row's reference
+//   O += (y v / w) V         v: the key's block scale; w: the item's V reference
+// with S, O and P = y v / w in TMEM: P (fp16) takes the place of its own S and is the first
+// operand of the second product.  r moves only when a logit is 2^kLag above it, w when the
+// largest v of a step leaves [w / 64, 16 w]; O is then rescaled in TMEM by the thread that
+// owns the row.  The result is O w / l, l the sum of y before its rounding.
+//
+// Roles: two warpgroups of softmax, a tile each, a row a thread; one of converters, which
+// load codes into registers a step ahead, widen them and store them in the products'
+// layout; two warps of products, which take turns, so that one tile's softmax runs under
+// the other's products.
+//
+// Split.  The (sequence, head, pair of tiles, step) units are cut into equal ranges, one
+// per SM; items that several CTAs hold leave records, and the last to arrive joins them.
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "pkv_internal.h"
+#include "pkv_ptx.cuh"
+#include "q8.h"
+#include "q8_codes.cuh"
+#include "tc05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kRows = 128, kKeys = 128;  // of a tile, of a step
+constexpr int kPair = 2 * kRows;
+constexpr int kGroups = kKeys / 16;      // pieces of 16 keys, each of one block
+constexpr int kThreads = 512;  // 8 warps of softmax, 4 of converters, 2 of products and 2 idle ones
+// Registers: 256 x 176 + 128 x 96 + 128 x 64 is the 512 x 128 of the launch.
+constexpr int kPlane = 128 * 128;        // 128 rows of 64 fp16, swizzled
+constexpr float kLag = 8.f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr int kStages = 2;
+
+template <int D>
+struct Cfg {
+    static constexpr int kPlanes = D / 64;
+    static constexpr int kQ = kPlanes * kPlane;       // bytes of a tile's queries
+    static constexpr int kStage = 2 * kPlanes * kPlane;
+    static constexpr int kBytes = 2 * kQ + kStages * kStage;
+    static constexpr size_t smem(int seqs) { return 1024 + kBytes + (static_cast<size_t>(seqs) * 3 + 2) * 4; }
+};
+
+struct Roles {
+    uint64_t q_full[2], s_full[2], p_ready[2][2], o_done[2], turn[2], drained[2];
+    uint64_t full[kStages], empty[kStages], met;
+    float f[kStages][kGroups], v[kStages][kGroups];  // of a step's keys: logits' factor, V scale
+    uint32_t tmem;
+    int stop, last;
+    int sums[kThreads / 32];
+};
+
+struct Batch {
+    const int *cum, *len, *start;  // units before a sequence, its tokens, its first query row
+};
+
+// A place in the order of the units: sequence, KV head, pair of row tiles, step.
+struct Place {
+    int b, h, p, j;
+    int steps;  // of the pair
+
+    // Keys that the rows up to `row` of the sequence attend.
+    static __device__ int keys(const Batch &t, const Q8AttentionArgs &a, int b, int row) {
+        const int n = t.start[b + 1] - t.start[b];
+        return t.len[b] - n + 1 + min(divided(row, a.by_group), n - 1);
+    }
+    static __device__ int steps_of(const Batch &t, const Q8AttentionArgs &a, int b, int p) {
+        return (keys(t, a, b, p * kPair + kPair - 1) + kKeys - 1) / kKeys;
+    }
+    static __device__ int pairs(const Batch &t, const Q8AttentionArgs &a, int b) {
+        return ((t.start[b + 1] - t.start[b]) * (a.n_q_heads / a.n_kv_heads) + kPair - 1) / kPair;
+    }
+    static __device__ int divided(int x, const Q8Divide &d) {
+        return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(x)) * d.mul >> d.shift);
+    }
+    __device__ void find(const Batch &t, const Q8AttentionArgs &a, int u) {
+        int lo = 0, hi = a.num_seqs;  // cum[lo] <= u < cum[hi]
+#pragma unroll 1
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (t.cum[mid] <= u) lo = mid; else hi = mid;
+        }
+        b = lo;
+        const int of_head = (t.cum[b + 1] - t.cum[b]) / a.n_kv_heads;
+        j = u - t.cum[b];
+        h = j / of_head;
+        j -= h * of_head;
+        p = 0;
+#pragma unroll 1
+        while (j >= (steps = steps_of(t, a, b, p))) j -= steps, ++p;
+    }
+    // The first unit of the next pair.
+    __device__ void next(const Batch &t, const Q8AttentionArgs &a) {
+        j = 0;
+        if (++p == pairs(t, a, b)) {
+            p = 0;
+            if (++h == a.n_kv_heads) {
+                h = 0;
+#pragma unroll 1
+                do ++b; while (b < a.num_seqs && t.cum[b + 1] == t.cum[b]);
+                if (b >= a.num_seqs) return;
+            }
+        }
+        steps = steps_of(t, a, b, p);
+    }
+    // The steps of tile t of the pair; 0: it has no rows.
+    __device__ int steps_of_tile(const Batch &t, const Q8AttentionArgs &a, int tile) const {
+        const int row = p * kPair + tile * kRows;
+        if (row >= (t.start[b + 1] - t.start[b]) * (a.n_q_heads / a.n_kv_heads)) return 0;
+        return (keys(t, a, b, row + kRows - 1) + kKeys - 1) / kKeys;
+    }
+};
+
+// CTA c of n has the units [cut(c), cut(c + 1)).
+struct Ranges {
+    int size, larger;
+    __device__ Ranges(int total, int n) : size(total / n), larger(total - size * n) {}
+    __device__ int start(int i) const { return size * i + min(i, larger); }
+    __device__ int of(int x) const {
+        const int split = larger * (size + 1);
+        return x < split ? x / (size + 1) : larger + (x - split) / max(size, 1);
+    }
+};
+
+// A piece of 16 bytes in the products' layout: row `row` of a plane, piece q of 8.
+__device__ __forceinline__ int swizzled(int row, int q) { return row * 128 + ((q ^ (row & 7)) << 4); }
+
+template <int KIND, int D>
+__global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8AttentionArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(16) Roles sh;
+    unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    int *cum = reinterpret_cast<int *>(base + C::kBytes), *len = cum + a.num_seqs + 1, *start = len + a.num_seqs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = a.n_q_heads / a.n_kv_heads;
+
+    if (threadIdx.x == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&sh.q_full[t], 4);
+            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.p_ready[t][0], 4);
+            mbar_init(&sh.p_ready[t][1], 4);
+            mbar_init(&sh.o_done[t], 1);
+            mbar_init(&sh.turn[t], 1);
+            mbar_init(&sh.drained[t], 1);
+        }
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.full[s], 4);
+            mbar_init(&sh.empty[s], 2);
+        }
+        mbar_init(&sh.met, 8);
+        sh.stop = 0;
+        fence_barrier_init();
+    }
+    if (warp == 12) tmem_alloc(&sh.tmem, 512);
+    tc_fence_before();
+    grid_dependency_wait();
+    allow_dependent_launch();
+
+    // --- the batch's units
+    const Batch t{cum, len, start};
+    int total = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < a.num_seqs; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        int n = 0;
+        if (b < a.num_seqs) {
+            int l = a.context_lens[b], s = b;
+            n = 1;
+            if (a.query_start) {
+                s = a.query_start[b];
+                n = a.query_start[b + 1] - s;
+            } else if (l == 0) {
+                n = 0;
+            }
+            const bool ok = n >= 0 && n <= a.max_q_len && n <= l && s >= 0 && s + n <= a.total_q &&
+                            l <= a.max_context_len;
+            if (!ok && blockIdx.x == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+            len[b] = l;
+            start[b] = s;
+            if (b == a.num_seqs - 1) start[b + 1] = s + n;
+            if (!ok) n = 0;
+        }
+        __syncthreads();
+        int units = 0;
+        if (n > 0) {
+            const int pairs = (n * group + kPair - 1) / kPair;
+#pragma unroll 1
+            for (int p = 0; p < pairs; ++p)
+                units += (len[b] - n + kKeys + min(Place::divided(p * kPair + kPair - 1, a.by_group), n - 1)) / kKeys;
+            units *= a.n_kv_heads;
+        }
+        int upto = units;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int z = __shfl_up_sync(~0u, upto, d);
+            if (lane >= d) upto += z;
+        }
+        if (lane == 31) sh.sums[warp] = upto;
+        __syncthreads();
+        int before = total;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            const int x = sh.sums[w];
+            if (w < warp) before += x;
+            total += x;
+        }
+        if (b < a.num_seqs) cum[b] = before + upto - units;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) cum[a.num_seqs] = total;
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile int *stop = &sh.stop;
+    // TMEM columns: S of tile t at 128 t (P in its first half), O at 256 + 128 t
+
+    const int ctas = min(static_cast<int>(gridDim.x), max(1, total));
+    const Ranges ranges(total, ctas);
+    const int cta = blockIdx.x;
+    const int U0 = cta < ctas ? ranges.start(cta) : 0, U1 = cta < ctas ? ranges.start(cta + 1) : 0;
+    if (!a.query_start) {  // one token a sequence: an empty one has a result
+#pragma unroll 1
+        for (int b = cta; b < a.num_seqs; b += gridDim.x) {
+            if (len[b] != 0) continue;
+            uint4 *o = static_cast<uint4 *>(a.out) + static_cast<long long>(b) * a.n_q_heads * (D / 8);
+#pragma unroll 1
+            for (int i = threadIdx.x; i < a.n_q_heads * (D / 8); i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+            if (a.lse_out)
+#pragma unroll 1
+                for (int i = threadIdx.x; i < a.n_q_heads; i += kThreads)
+                    a.lse_out[static_cast<long long>(b) * a.n_q_heads + i] = -INFINITY;
+        }
+    }
+    Place at{};
+    if (U0 < U1) at.find(t, a, U0);
+
+    if (warp >= 12) {
+        // --- products ---
+        give_registers<64>();
+        if (warp < 14 && elect_one()) {
+            const int w = warp - 12;  // the tile
+            constexpr uint32_t ds = mma_desc(kRows, kKeys, false, false), dpv = mma_desc(kRows, D, false, true);
+            const uint32_t kv = smem_addr(base) + 2 * C::kQ, ts = tmem + 128 * w;
+            const uint64_t qd = smem_desc(smem_addr(base) + w * C::kQ, 1024, 0);
+            int f = 0, sc = 0, qc = 0, turns = 0;  // steps so far, this tile's, its pieces, turns
+            bool ok = U0 == U1 || first_wait(&sh.full[0], 0, a.first_wait_polls, stop);
+#pragma unroll 1
+            for (int u = U0; ok && u < U1; at.next(t, a)) {
+                const int n = min(at.steps - at.j, U1 - u);  // steps of this piece, and of its tile
+                const int mine = max(0, min(at.steps_of_tile(t, a, w) - at.j, n));
+                u += n;
+#pragma unroll 1
+                for (int j = -1; j < n; ++j) {  // between the softmax of step j and of the next
+                    const bool weights = j >= 0 && j < mine, scores = j + 1 < mine;
+                    if (j + 1 < n) {
+                        const int s = f + j + 1;
+                        ok = wait_or_stop(&sh.full[s % kStages], (s / kStages) & 1, stop);
+                    }
+                    if (ok && j < 0 && mine > 0) ok = wait_or_stop(&sh.q_full[w], qc++ & 1, stop);
+                    if (ok && weights) ok = wait_or_stop(&sh.p_ready[w][0], sc & 1, stop);
+                    ok = ok && wait_or_stop(&sh.turn[w], (turns & 1) ^ (w ^ 1), stop);
+                    if (!ok) break;
+                    ++turns;
+                    tc_fence_after();
+                    if (weights) {
+                        const uint64_t vd = smem_desc(
+                            kv + ((f + j) % kStages) * C::kStage + C::kPlanes * kPlane, 1024, kPlane);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
+                        ok = wait_or_stop(&sh.p_ready[w][1], sc & 1, stop);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 4; k < 8; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, true);
+                        ++sc;
+                        if (j + 1 == mine) mma_commit(&sh.o_done[w]);
+                    }
+                    if (scores) {
+                        const uint64_t kd = smem_desc(kv + ((f + j + 1) % kStages) * C::kStage, 1024, 0);
+#pragma unroll
+                        for (int k = 0; k < 4 * C::kPlanes; ++k)
+                            mma_ss(ts, qd + (k / 4) * (kPlane / 16) + (k % 4) * 2,
+                                   kd + (k / 4) * (kPlane / 16) + (k % 4) * 2, ds, k > 0);
+                        mma_commit(&sh.s_full[w]);
+                    }
+                    mbar_arrive(&sh.turn[w ^ 1]);
+                    if (j >= 0) mma_commit(&sh.empty[(f + j) % kStages]);
+                }
+                f += n;
+            }
+            // nothing of the tensor core is left in flight when TMEM is freed
+            mma_commit(&sh.drained[w]);
+            mbar_wait_bounded(&sh.drained[w], 0);
+        }
+    } else if (warp >= 8) {
+        // --- converters ---
+        give_registers<96>();
+        const int w = warp - 8;  // its pieces of 16 keys: 2 w and 2 w + 1
+        constexpr int kChunks = D / 16, kAt = 32 / kChunks, kLoads = 16 / kAt;  // lanes of a row, rows of a load
+        const int chunk = lane % kChunks, row0 = lane / kChunks;
+        const int bs16_log2 = __ffs(a.block_size / 16) - 1;
+        const uint4 *kc = static_cast<const uint4 *>(a.k_cache) + lane, *vc = static_cast<const uint4 *>(a.v_cache) + lane;
+        const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+        int f = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int u = U0; ok && u < U1; at.next(t, a)) {
+            const int n = min(at.steps - at.j, U1 - u);
+            u += n;
+            const int L = len[at.b];
+            const int *table = a.block_tables + static_cast<long long>(at.b) * a.max_blocks_per_seq;
+            // lane i knows the cache piece (of 16 rows) of step base + i / 2, the warp's
+            // group i % 2; a batch of 16 steps, and the one after it
+            auto pieces = [&](int from) {
+                const int g = (at.j + from + lane / 2) * kGroups + 2 * w + lane % 2;  // of the sequence
+                unsigned piece = 0;
+                if (from + lane / 2 < n && g * 16 < L) {
+                    const int id = table[g >> bs16_log2];
+                    if (id < 0 || id >= a.num_blocks)
+                        flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
+                    else
+                        piece = (static_cast<unsigned>(id) * a.n_kv_heads + at.h << bs16_log2) +
+                                (g & ((1 << bs16_log2) - 1));
+                }
+                return piece;
+            };
+            unsigned now = pieces(0), next = pieces(16);
+            uint4 x[2][2][kLoads];  // group, K or V: codes of the step at hand
+            float ks[2], vs[2];
+            auto load = [&](unsigned piece, int g, int side) {
+                const uint4 *src = (side ? vc : kc) + static_cast<long long>(piece) * (16 * kChunks);
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) x[g][side][i] = __ldg(src + i * 32);
+            };
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const unsigned piece = __shfl_sync(~0u, now, g);
+                load(piece, g, 0);
+                load(piece, g, 1);
+                ks[g] = __ldg(a.k_scales + (piece >> bs16_log2));
+                vs[g] = __ldg(a.v_scales + (piece >> bs16_log2));
+            }
+#pragma unroll 1
+            for (int j = 0; j < n; ++j, ++f) {
+                const int s = f % kStages;
+                ok = warp_wait_or_stop(&sh.empty[s], ((f / kStages) & 1) ^ 1, stop);
+                if (!ok) break;
+                unsigned char *st = base + 2 * C::kQ + s * C::kStage;
+                if (lane < 2) {  // pieces behind the sequence have no scale of their own
+                    const bool some = (at.j + j) * kKeys + (2 * w + lane) * 16 < L;
+                    sh.f[s][2 * w + lane] = some ? fmaxf((lane ? ks[1] : ks[0]) * scale, 1e-30f) : 1e-30f;
+                    sh.v[s][2 * w + lane] = some ? (lane ? vs[1] : vs[0]) : 0.f;
+                }
+                const int ahead = j + 1;
+                if ((ahead & 15) == 0) {
+                    now = next;
+                    next = pieces(ahead + 16);
+                }
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int key0 = (at.j + j) * kKeys + (2 * w + g) * 16;  // of the sequence
+                    const unsigned piece = __shfl_sync(~0u, now, (2 * ahead + g) & 31);
+#pragma unroll
+                    for (int side = 0; side < 2; ++side) {
+#pragma unroll
+                        for (int i = 0; i < kLoads; ++i) {
+                            const int in = i * kAt + row0, row = (2 * w + g) * 16 + in;
+                            uint4 c = x[g][side][i];
+                            // rows that hold no token may hold anything
+                            if (key0 + in >= L) c = make_uint4(0, 0, 0, 0);
+                            const uint4 lo = make_uint4(q8_widen<KIND, 0>(c.x), q8_widen<KIND, 1>(c.x),
+                                                        q8_widen<KIND, 0>(c.y), q8_widen<KIND, 1>(c.y));
+                            const uint4 hi = make_uint4(q8_widen<KIND, 0>(c.z), q8_widen<KIND, 1>(c.z),
+                                                        q8_widen<KIND, 0>(c.w), q8_widen<KIND, 1>(c.w));
+                            unsigned char *plane = st + (side * C::kPlanes + chunk / 4) * kPlane;
+                            // lanes of the second plane store their halves the other way
+                            // round: all 8 of a row then meet different banks
+                            const int q = chunk % 4 * 2, odd = chunk / 4;
+                            *reinterpret_cast<uint4 *>(plane + swizzled(row, q + odd)) = odd ? hi : lo;
+                            *reinterpret_cast<uint4 *>(plane + swizzled(row, q + 1 - odd)) = odd ? lo : hi;
+                        }
+                        if (ahead < n) load(piece, g, side);
+                    }
+                    if (ahead < n) {
+                        ks[g] = __ldg(a.k_scales + (piece >> bs16_log2));
+                        vs[g] = __ldg(a.v_scales + (piece >> bs16_log2));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.full[s]);
+            }
+        }
+    } else {
+        // --- softmax, results ---
+        take_registers<176>();
+        const int w = warp >> 2;  // the tile
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 * (warp % 4) << 16
+        const uint32_t ts = tmem + 128 * w + lanes, to = tmem + 256 + 128 * w + lanes;
+        const int row_in = w * kRows + (threadIdx.x & 127);  // of the pair
+        unsigned char *ws = static_cast<unsigned char *>(a.workspace);
+        // records: float4 [D / 4][record_rows], then reference and sum of each row
+        auto record_of = [&](int of_cta, int side) {
+            return reinterpret_cast<float4 *>(ws + kBalancedCounterBytes) +
+                   (2ll * of_cta + side) * (D / 4 + 1) * a.record_rows;
+        };
+        int f = 0, sc = 0, mine_so_far = 0, meetings = 0;
+        bool ok = true;
+#pragma unroll 1
+        for (int u = U0; ok && u < U1; at.next(t, a)) {
+            const int first = u - at.j, n = min(at.steps - at.j, U1 - u);
+            const int mine = max(0, min(at.steps_of_tile(t, a, w) - at.j, n));
+            u += n;
+            const int rows = (start[at.b + 1] - start[at.b]) * group - at.p * kPair;  // from the pair on
+            const int seen = Place::keys(t, a, at.b, at.p * kPair + row_in);
+            float r = 0.f, l = 0.f, wv = 0.f, inv_w = 0.f;
+            if (mine > 0) {
+                // the tile's queries: 16 lanes (8 at D = 64) a row
+                constexpr int kLanes = D / 8, kAt = 128 / kLanes;
+                const int piece = threadIdx.x % kLanes;
+#pragma unroll 4
+                for (int i = (threadIdx.x & 127) / kLanes; i < kRows; i += kAt) {
+                    const int r_of = at.p * kPair + w * kRows + i, tok = Place::divided(r_of, a.by_group);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (w * kRows + i < rows)
+                        x = __ldg(reinterpret_cast<const uint4 *>(
+                                      static_cast<const __half *>(a.q) + (start[at.b] + tok) * a.q_stride +
+                                      (at.h * group + r_of - tok * group) * D) + piece);
+                    *reinterpret_cast<uint4 *>(base + w * C::kQ + piece / 8 * kPlane + swizzled(i, piece % 8)) = x;
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_full[w]);
+            }
+#pragma unroll 1
+            for (int j = 0; j < mine; ++j, ++sc) {
+                const int s = (f + j) % kStages;
+                ok = warp_wait_or_stop(&sh.s_full[w], sc & 1, stop) &&
+                     warp_wait_or_stop(&sh.full[s], ((f + j) / kStages) & 1, stop);  // for the scales: long since
+                if (!ok) break;
+                tc_fence_after();
+                const float *fg = sh.f[s], *vg = sh.v[s];
+                const int left = seen - (at.j + j) * kKeys;
+                const bool masked = __any_sync(~0u, left < kKeys);
+                auto ready = [&](uint32_t (&x)[32], int c0) {  // logits' sign and mask
+                    if (a.scale_log2 < 0.f)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) x[c] ^= 0x80000000u;
+                    if (masked)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) x[c] = c0 + c < left ? x[c] : 0xff800000u;
+                };
+                auto top_of = [&](const uint32_t (&x)[32], float f0, float f1) {
+                    float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[16]);
+#pragma unroll
+                    for (int c = 1; c + 1 < 16; c += 2) {
+                        m0 = max3(m0, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
+                        m1 = max3(m1, __uint_as_float(x[16 + c]), __uint_as_float(x[16 + c + 1]));
+                    }
+                    m0 = fmaxf(m0, __uint_as_float(x[15]));
+                    m1 = fmaxf(m1, __uint_as_float(x[31]));
+                    return fmaxf(m0 * f0, m1 * f1);
+                };
+                // all logits once for the row's largest; the second half stays in registers
+                uint32_t x[2][32];
+                tmem_ld32(x[0], ts);
+                tmem_ld32(x[1], ts + 32);
+                tmem_wait_ld();
+                ready(x[0], 0);
+                ready(x[1], 32);
+                float top = fmaxf(top_of(x[0], fg[0], fg[1]), top_of(x[1], fg[2], fg[3]));
+                tmem_ld32(x[0], ts + 64);
+                tmem_ld32(x[1], ts + 96);
+                tmem_wait_ld();
+                ready(x[0], 64);
+                ready(x[1], 96);
+                top = fmaxf(top, fmaxf(top_of(x[0], fg[4], fg[5]), top_of(x[1], fg[6], fg[7])));
+                // --- references
+                float most = 0.f;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) most = fmaxf(most, vg[g]);
+                const bool far = most > 0.f && !(most >= wv * (1.f / 64.f) && most <= wv * 16.f);
+                float fac = 1.f;
+                if (far) {
+                    inv_w = __fdividef(1.f, most);
+                    fac = wv * inv_w;
+                    wv = most;
+                }
+                if (j == 0) {
+                    r = top > -INFINITY ? top : 0.f;
+                } else {
+                    const bool move = top - r > kLag;
+                    if (__any_sync(~0u, move || far)) {
+                        // S being full, every earlier product into O is done
+                        const float next = move ? top : r, g = ex2(r - next);
+                        r = next;
+                        l *= g;
+                        fac *= g;
+#pragma unroll
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(o, to + c);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fac);
+                            tmem_st16(to + c, o);
+                        }
+                    }
+                }
+                // --- weights
+                float2 sum = make_float2(0.f, 0.f);
+                auto weigh = [&](const uint32_t (&y)[32], int c0, const float (&ff)[2], const float (&vv)[2]) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const float2 e = fma2(make_float2(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])),
+                                              ff[c / 8], -r);
+                        const float2 z = make_float2(ex2(e.x), ex2(e.y));
+                        sum = add2(sum, z);
+                        const float2 q = mul2(z, make_float2(vv[c / 8], vv[c / 8]));
+                        p[c] = pack_half2(q.x, q.y);
+                    }
+                    tmem_st16(ts + c0 / 2, p);
+                };
+                auto announce = [&](int half) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_ready[w][half]);
+                };
+                uint32_t y[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    tmem_ld32(y, ts + 32 * q);
+                    tmem_wait_ld();
+                    ready(y, 32 * q);
+                    const float ff[2] = {fg[2 * q], fg[2 * q + 1]}, vv[2] = {vg[2 * q] * inv_w, vg[2 * q + 1] * inv_w};
+                    weigh(y, 32 * q, ff, vv);
+                }
+                announce(0);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float ff[2] = {fg[4 + 2 * q], fg[5 + 2 * q]}, vv[2] = {vg[4 + 2 * q] * inv_w, vg[5 + 2 * q] * inv_w};
+                    weigh(x[q], 64 + 32 * q, ff, vv);
+                }
+                announce(1);
+                l += sum.x + sum.y;
+            }
+            f += n;
+            if (!ok) break;
+            if (mine > 0) {
+                ok = warp_wait_or_stop(&sh.o_done[w], mine_so_far++ & 1, stop);
+                if (!ok) break;
+                tc_fence_after();
+            }
+            const bool whole = first >= U0 && first + at.steps <= U1;
+            const int tok = Place::divided(at.p * kPair + row_in, a.by_group);
+            const long long out_row = static_cast<long long>(start[at.b] + tok) * a.n_q_heads + at.h * group +
+                                      (at.p * kPair + row_in - tok * group);
+            const bool valid = row_in < rows;
+            if (whole) {
+                const float inv = wv / l;
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row * D);
+                if (mine > 0) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(o, to + c);
+                        tmem_wait_ld();
+                        if (valid)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t z[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    z[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                                      __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                                out[c / 8 + e] = make_uint4(z[0], z[1], z[2], z[3]);
+                            }
+                    }
+                    if (a.lse_out && valid) a.lse_out[out_row] = (r + log2f(l)) * kLn2;
+                }
+                continue;
+            }
+            // --- a part: its record, and the join by the last CTA to arrive
+            const int side = first >= U0;
+            float4 *rec = record_of(cta, side);
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                if (mine > 0) {
+                    tmem_ld32(o, to + c);
+                    tmem_wait_ld();
+                }
+                if (valid)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        __stcg(rec + (c / 4 + e) * a.record_rows + row_in,
+                               mine > 0 ? make_float4(__uint_as_float(o[4 * e]) * wv, __uint_as_float(o[4 * e + 1]) * wv,
+                                                      __uint_as_float(o[4 * e + 2]) * wv,
+                                                      __uint_as_float(o[4 * e + 3]) * wv)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f));
+            }
+            if (valid)
+                __stcg(rec + (D / 4) * a.record_rows + row_in,
+                       make_float4(mine > 0 && l != 0.f ? r : -INFINITY, mine > 0 ? l : 0.f, 0.f, 0.f));
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.met);
+            ok = warp_wait_or_stop(&sh.met, meetings++ & 1, stop);
+            if (!ok) break;
+            const int from = ranges.of(first), parts = ranges.of(first + at.steps - 1) - from + 1;
+            if (threadIdx.x == 0) {
+                int *counter = reinterpret_cast<int *>(ws) + from;
+                const int old = atomic_add_acq_rel_gpu(counter, 1);
+                sh.last = 0;
+                if (counter_not_zeroed(old, parts - 1)) {
+                    flag_error(a.err, PKV_ERRBIT_WORKSPACE);
+                    atomic_exch_relaxed_gpu(counter, kCounterPoison);
+                } else if (old == parts - 1) {
+                    sh.last = 1;
+                    red_add_relaxed_gpu(counter, -parts);
+                }
+                __threadfence();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.met);
+            ok = warp_wait_or_stop(&sh.met, meetings++ & 1, stop);
+            if (!ok) break;
+            if (!sh.last || !valid) continue;
+            __threadfence();
+            float high = -INFINITY, total_l = 0.f;
+#pragma unroll 1
+            for (int k = 0; k < parts; ++k)
+                high = fmaxf(high, __ldcg(&(record_of(from + k, k == 0) + (D / 4) * a.record_rows + row_in)->x));
+            if (high == -INFINITY) high = 0.f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 4; c0 += 8) {
+                float4 acc[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                total_l = 0.f;
+#pragma unroll 1
+                for (int k = 0; k < parts; ++k) {
+                    const float4 *part = record_of(from + k, k == 0) + row_in;
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + (D / 4) * a.record_rows));
+                    const float g = ex2(ml.x - high);
+                    total_l += g * ml.y;
+                    float4 z[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] = __ldcg(part + (c0 + e) * a.record_rows);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        acc[e].x += g * z[e].x;
+                        acc[e].y += g * z[e].y;
+                        acc[e].z += g * z[e].z;
+                        acc[e].w += g * z[e].w;
+                    }
+                }
+                const float inv = 1.f / total_l;
+                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row * D) + c0 / 2;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    out[e] = make_uint4(pack_half2(acc[2 * e].x * inv, acc[2 * e].y * inv),
+                                        pack_half2(acc[2 * e].z * inv, acc[2 * e].w * inv),
+                                        pack_half2(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
+                                        pack_half2(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
+            }
+            if (a.lse_out) a.lse_out[out_row] = (high + log2f(total_l)) * kLn2;
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+    if (warp == 12) tmem_free(tmem, 512);
+}
+
+template <int KIND, int D>
+cudaError_t launch(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t stream) {
+    auto kern = q8_prefill_kernel<KIND, D>;
+    const size_t smem = Cfg<D>::smem(a.num_seqs);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(sp.ctas), dim3(kThreads), smem, stream, a);
+}
+
+static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 1024, "shared memory");
+
+}  // namespace
+
+// The same plan as q8_split for the kernel of this file.
+bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
+                      int sms, Q8Split *sp) {
+    const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
+    const double steps = (static_cast<double>(max_len) + kKeys - 1) / kKeys + 1;
+    if (static_cast<double>(num_seqs) * n_kv_heads * ((rows + kPair - 1) / kPair) * steps >= 2147483648.0)
+        return false;
+    sp->row_tiles = 0;
+    sp->ctas = sms < kBalancedMaxWorkers ? sms : kBalancedMaxWorkers;
+    sp->record_rows = static_cast<int>(rows < kPair ? (rows + 31) / 32 * 32 : kPair);
+    sp->ws_bytes = kBalancedCounterBytes +
+                   static_cast<size_t>(sp->ctas) * 2 * (head_dim / 4 + 1) * sp->record_rows * sizeof(float4);
+    return true;
+}
+
+cudaError_t launch_q8_prefill(const Q8AttentionArgs &a, int kind, const Q8Split &sp, cudaStream_t stream) {
+    if (a.head_dim == 128)
+        return kind == PKV_Q8_E4M3 ? launch<PKV_Q8_E4M3, 128>(a, sp, stream)
+                                   : launch<PKV_Q8_INT8, 128>(a, sp, stream);
+    return kind == PKV_Q8_E4M3 ? launch<PKV_Q8_E4M3, 64>(a, sp, stream) : launch<PKV_Q8_INT8, 64>(a, sp, stream);
+}
+
+}  // namespace pkv
