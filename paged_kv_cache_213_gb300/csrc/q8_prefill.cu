@@ -45,17 +45,20 @@ template <int D>
 struct Cfg {
     static constexpr int kPlanes = D / 64;
     static constexpr int kQ = kPlanes * kPlane;       // bytes of a tile's queries
-    static constexpr int kStage = 2 * kPlanes * kPlane;
-    static constexpr int kBytes = 2 * kQ + kStages * kStage;
+    static constexpr int kHalf = kPlanes * kPlane;    // of a step's K or V
+    static constexpr int kBytes = 2 * kQ + 2 * kStages * kHalf;  // queries, K ring, V ring
     static constexpr size_t smem(int seqs) { return 1024 + kBytes + (static_cast<size_t>(seqs) * 3 + 2) * 4; }
 };
 
 struct Roles {
-    uint64_t q_full[2], s_full[2], p_ready[2][2], o_done[2], turn[2], drained[2];
-    uint64_t full[kStages], empty[kStages], met;
-    float f[kStages][kGroups], v[kStages][kGroups];  // of a step's keys: logits' factor, V scale
+    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_done[2], o_free[2], turn[2], drained[2];
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    // Of a step's keys: the logits' factor and the V scale.  A step's are written with its K,
+    // when the scores of two steps before are done, and read by its softmax, which is over
+    // when the scores of two steps behind are issued: three steps' lie side by side.
+    float f[4][kGroups], v[4][kGroups];
     uint32_t tmem;
-    int stop, last;
+    int stop;
     int sums[kThreads / 32];
 };
 
@@ -147,7 +150,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 4);
-            mbar_init(&sh.s_full[t], 1);
+            mbar_init(&sh.q_empty[t], 1);
+            mbar_init(&sh.s_full[t], 2);
+            mbar_init(&sh.o_free[t], 4);
             mbar_init(&sh.p_ready[t][0], 4);
             mbar_init(&sh.p_ready[t][1], 4);
             mbar_init(&sh.o_done[t], 1);
@@ -155,10 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             mbar_init(&sh.drained[t], 1);
         }
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sh.full[s], 4);
-            mbar_init(&sh.empty[s], 2);
+            mbar_init(&sh.k_full[s], 4);
+            mbar_init(&sh.k_empty[s], 2);
+            mbar_init(&sh.v_full[s], 4);
+            mbar_init(&sh.v_empty[s], 2);
         }
-        mbar_init(&sh.met, 8);
         sh.stop = 0;
         fence_barrier_init();
     }
@@ -253,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             constexpr uint32_t ds = mma_desc(kRows, kKeys, false, false), dpv = mma_desc(kRows, D, false, true);
             const uint32_t kv = smem_addr(base) + 2 * C::kQ, ts = tmem + 128 * w;
             const uint64_t qd = smem_desc(smem_addr(base) + w * C::kQ, 1024, 0);
-            int f = 0, sc = 0, qc = 0, turns = 0;  // steps so far, this tile's, its pieces, turns
-            bool ok = U0 == U1 || first_wait(&sh.full[0], 0, a.first_wait_polls, stop);
+            int f = 0, sc = 0, pc = 0, turns = 0;  // steps so far, this tile's, its pieces, turns
+            bool ok = U0 == U1 || first_wait(&sh.k_full[0], 0, a.first_wait_polls, stop);
 #pragma unroll 1
             for (int u = U0; ok && u < U1; at.next(t, a)) {
                 const int n = min(at.steps - at.j, U1 - u);  // steps of this piece, and of its tile
@@ -263,11 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
 #pragma unroll 1
                 for (int j = -1; j < n; ++j) {  // between the softmax of step j and of the next
                     const bool weights = j >= 0 && j < mine, scores = j + 1 < mine;
-                    if (j + 1 < n) {
-                        const int s = f + j + 1;
-                        ok = wait_or_stop(&sh.full[s % kStages], (s / kStages) & 1, stop);
-                    }
-                    if (ok && j < 0 && mine > 0) ok = wait_or_stop(&sh.q_full[w], qc++ & 1, stop);
+                    const int kf = f + j + 1, vf = f + j;
+                    if (j + 1 < n) ok = wait_or_stop(&sh.k_full[kf % kStages], (kf / kStages) & 1, stop);
+                    if (ok && j >= 0) ok = wait_or_stop(&sh.v_full[vf % kStages], (vf / kStages) & 1, stop);
+                    if (ok && j < 0 && mine > 0) ok = wait_or_stop(&sh.q_full[w], pc & 1, stop);
+                    if (ok && weights && j == 0 && pc > 0) ok = wait_or_stop(&sh.o_free[w], (pc - 1) & 1, stop);
                     if (ok && weights) ok = wait_or_stop(&sh.p_ready[w][0], sc & 1, stop);
                     ok = ok && wait_or_stop(&sh.turn[w], (turns & 1) ^ (w ^ 1), stop);
                     if (!ok) break;
@@ -275,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     tc_fence_after();
                     if (weights) {
                         const uint64_t vd = smem_desc(
-                            kv + ((f + j) % kStages) * C::kStage + C::kPlanes * kPlane, 1024, kPlane);
+                            kv + (kStages + vf % kStages) * C::kHalf, 1024, kPlane);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
                         ok = wait_or_stop(&sh.p_ready[w][1], sc & 1, stop);
@@ -287,17 +293,21 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                         if (j + 1 == mine) mma_commit(&sh.o_done[w]);
                     }
                     if (scores) {
-                        const uint64_t kd = smem_desc(kv + ((f + j + 1) % kStages) * C::kStage, 1024, 0);
+                        const uint64_t kd = smem_desc(kv + (kf % kStages) * C::kHalf, 1024, 0);
 #pragma unroll
                         for (int k = 0; k < 4 * C::kPlanes; ++k)
                             mma_ss(ts, qd + (k / 4) * (kPlane / 16) + (k % 4) * 2,
                                    kd + (k / 4) * (kPlane / 16) + (k % 4) * 2, ds, k > 0);
                         mma_commit(&sh.s_full[w]);
+                        mbar_arrive(&sh.s_full[w]);  // what this thread has seen (the scales) is seen there too
+                        if (j + 2 == mine) mma_commit(&sh.q_empty[w]);
                     }
                     mbar_arrive(&sh.turn[w ^ 1]);
-                    if (j >= 0) mma_commit(&sh.empty[(f + j) % kStages]);
+                    if (j >= 0) mma_commit(&sh.v_empty[vf % kStages]);
+                    if (j + 1 < n) mma_commit(&sh.k_empty[kf % kStages]);
                 }
                 f += n;
+                if (mine > 0) ++pc;
             }
             // nothing of the tensor core is left in flight when TMEM is freed
             mma_commit(&sh.drained[w]);
@@ -307,12 +317,24 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         // --- converters ---
         give_registers<96>();
         const int w = warp - 8;  // its pieces of 16 keys: 2 w and 2 w + 1
-        constexpr int kChunks = D / 16, kAt = 32 / kChunks, kLoads = 16 / kAt;  // lanes of a row, rows of a load
-        const int chunk = lane % kChunks, row0 = lane / kChunks;
+        constexpr int kAt = 32 / (4 * C::kPlanes), kLoads = 16 / kAt;  // rows of a load, loads of a piece
+        // A lane's 16 codes of a row become pieces 2 x and 2 x + 1 of a plane.  Eight lanes have
+        // two rows of one plane, whose swizzles differ in the lowest bit: no bank twice.
+        const int plane = lane / 16 * (C::kPlanes - 1), x4 = lane % 4;
+        const int row0 = C::kPlanes == 2 ? lane / 4 % 4 : lane / 4;
         const int bs16_log2 = __ffs(a.block_size / 16) - 1;
-        const uint4 *kc = static_cast<const uint4 *>(a.k_cache) + lane, *vc = static_cast<const uint4 *>(a.v_cache) + lane;
+        const int code_at = row0 * D + plane * 64 + x4 * 16;
+        const unsigned char *kc = static_cast<const unsigned char *>(a.k_cache) + code_at;
+        const unsigned char *vc = static_cast<const unsigned char *>(a.v_cache) + code_at;
+        // where the lane stores, for loads of even and odd number (the others lie 8 rows on)
+        int to[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                to[i][e] = plane * kPlane + swizzled(2 * w * 16 + (i * kAt & 7) + row0, 2 * x4 + e);
         const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
-        int f = 0;
+        int f = 0, pieces_of[2] = {0, 0};  // steps so far, pieces of a tile
         bool ok = true;
 #pragma unroll 1
         for (int u = U0; ok && u < U1; at.next(t, a)) {
@@ -320,8 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             u += n;
             const int L = len[at.b];
             const int *table = a.block_tables + static_cast<long long>(at.b) * a.max_blocks_per_seq;
-            // lane i knows the cache piece (of 16 rows) of step base + i / 2, the warp's
-            // group i % 2; a batch of 16 steps, and the one after it
+            // lane i knows the cache piece (of 16 rows) of step from + i / 2, the warp's
+            // group i % 2: of the step's batch of 16, and of the one after it
             auto pieces = [&](int from) {
                 const int g = (at.j + from + lane / 2) * kGroups + 2 * w + lane % 2;  // of the sequence
                 unsigned piece = 0;
@@ -335,72 +357,112 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 }
                 return piece;
             };
-            unsigned now = pieces(0), next = pieces(16);
-            uint4 x[2][2][kLoads];  // group, K or V: codes of the step at hand
+            unsigned before = 0, now = pieces(0), next = pieces(16);  // K runs a step ahead of V
+            uint4 xk[2][kLoads], xv[2][kLoads];  // codes on their way
             float ks[2], vs[2];
-            auto load = [&](unsigned piece, int g, int side) {
-                const uint4 *src = (side ? vc : kc) + static_cast<long long>(piece) * (16 * kChunks);
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) x[g][side][i] = __ldg(src + i * 32);
-            };
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const unsigned piece = __shfl_sync(~0u, now, g);
-                load(piece, g, 0);
-                load(piece, g, 1);
-                ks[g] = __ldg(a.k_scales + (piece >> bs16_log2));
-                vs[g] = __ldg(a.v_scales + (piece >> bs16_log2));
-            }
-#pragma unroll 1
-            for (int j = 0; j < n; ++j, ++f) {
-                const int s = f % kStages;
-                ok = warp_wait_or_stop(&sh.empty[s], ((f / kStages) & 1) ^ 1, stop);
-                if (!ok) break;
-                unsigned char *st = base + 2 * C::kQ + s * C::kStage;
-                if (lane < 2) {  // pieces behind the sequence have no scale of their own
-                    const bool some = (at.j + j) * kKeys + (2 * w + lane) * 16 < L;
-                    sh.f[s][2 * w + lane] = some ? fmaxf((lane ? ks[1] : ks[0]) * scale, 1e-30f) : 1e-30f;
-                    sh.v[s][2 * w + lane] = some ? (lane ? vs[1] : vs[0]) : 0.f;
-                }
-                const int ahead = j + 1;
-                if ((ahead & 15) == 0) {
-                    now = next;
-                    next = pieces(ahead + 16);
-                }
+            auto load = [&](uint4 (&x)[2][kLoads], const unsigned char *from, unsigned batch, int j) {
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const int key0 = (at.j + j) * kKeys + (2 * w + g) * 16;  // of the sequence
-                    const unsigned piece = __shfl_sync(~0u, now, (2 * ahead + g) & 31);
+                    const unsigned piece = __shfl_sync(~0u, batch, (2 * j + g) & 31);
+                    const unsigned char *src = from + static_cast<long long>(piece) * (16 * D);
 #pragma unroll
-                    for (int side = 0; side < 2; ++side) {
-#pragma unroll
-                        for (int i = 0; i < kLoads; ++i) {
-                            const int in = i * kAt + row0, row = (2 * w + g) * 16 + in;
-                            uint4 c = x[g][side][i];
-                            // rows that hold no token may hold anything
-                            if (key0 + in >= L) c = make_uint4(0, 0, 0, 0);
-                            const uint4 lo = make_uint4(q8_widen<KIND, 0>(c.x), q8_widen<KIND, 1>(c.x),
-                                                        q8_widen<KIND, 0>(c.y), q8_widen<KIND, 1>(c.y));
-                            const uint4 hi = make_uint4(q8_widen<KIND, 0>(c.z), q8_widen<KIND, 1>(c.z),
-                                                        q8_widen<KIND, 0>(c.w), q8_widen<KIND, 1>(c.w));
-                            unsigned char *plane = st + (side * C::kPlanes + chunk / 4) * kPlane;
-                            // lanes of the second plane store their halves the other way
-                            // round: all 8 of a row then meet different banks
-                            const int q = chunk % 4 * 2, odd = chunk / 4;
-                            *reinterpret_cast<uint4 *>(plane + swizzled(row, q + odd)) = odd ? hi : lo;
-                            *reinterpret_cast<uint4 *>(plane + swizzled(row, q + 1 - odd)) = odd ? lo : hi;
-                        }
-                        if (ahead < n) load(piece, g, side);
-                    }
-                    if (ahead < n) {
-                        ks[g] = __ldg(a.k_scales + (piece >> bs16_log2));
-                        vs[g] = __ldg(a.v_scales + (piece >> bs16_log2));
-                    }
+                    for (int i = 0; i < kLoads; ++i) x[g][i] = __ldg(reinterpret_cast<const uint4 *>(src + i * kAt * D));
                 }
+            };
+            auto load_scales = [&](int j) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const unsigned cell = __shfl_sync(~0u, now, (2 * j + g) & 31) >> bs16_log2;
+                    ks[g] = __ldg(a.k_scales + cell);
+                    vs[g] = __ldg(a.v_scales + cell);
+                }
+            };
+            // codes x of step j to `half` of the memory
+            auto widen = [&](const uint4 (&x)[2][kLoads], int j, unsigned char *half) {
+                const int key0 = (at.j + j) * kKeys + 2 * w * 16 + row0;  // of the sequence
+                const bool cut = key0 - row0 + 32 > L;
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+#pragma unroll
+                    for (int i = 0; i < kLoads; ++i) {
+                        uint4 c = x[g][i];
+                        // rows that hold no token may hold anything
+                        if (cut && key0 + g * 16 + i * kAt >= L) c = make_uint4(0, 0, 0, 0);
+                        unsigned char *dst = half + (g * 16 + (i * kAt & ~7)) * 128;
+                        *reinterpret_cast<uint4 *>(dst + to[kAt == 8 ? 0 : i & 1][0]) =
+                            make_uint4(q8_widen<KIND, 0>(c.x), q8_widen<KIND, 1>(c.x), q8_widen<KIND, 0>(c.y),
+                                       q8_widen<KIND, 1>(c.y));
+                        *reinterpret_cast<uint4 *>(dst + to[kAt == 8 ? 0 : i & 1][1]) =
+                            make_uint4(q8_widen<KIND, 0>(c.z), q8_widen<KIND, 1>(c.z), q8_widen<KIND, 0>(c.w),
+                                       q8_widen<KIND, 1>(c.w));
+                    }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.full[s]);
+            };
+            load(xk, kc, now, 0);
+            load_scales(0);
+            load(xv, vc, now, 0);
+            unsigned char *ring = base + 2 * C::kQ;
+#pragma unroll 1
+            for (int j = 0; j <= n; ++j) {  // K of step j, V of the step before
+                if (j < n) {
+                    const int kf = f + j, s = kf % kStages;
+                    ok = warp_wait_or_stop(&sh.k_empty[s], ((kf / kStages) & 1) ^ 1, stop);
+                    if (!ok) break;
+                    if (lane < 2) {  // pieces behind the sequence have no scale of their own
+                        const bool some = (at.j + j) * kKeys + (2 * w + lane) * 16 < L;
+                        sh.f[kf & 3][2 * w + lane] = some ? fmaxf((lane ? ks[1] : ks[0]) * scale, 1e-30f) : 1e-30f;
+                        sh.v[kf & 3][2 * w + lane] = some ? (lane ? vs[1] : vs[0]) : 0.f;
+                    }
+                    widen(xk, j, ring + s * C::kHalf);
+                    if (lane == 0) mbar_arrive(&sh.k_full[s]);
+                    if (((j + 1) & 15) == 0) {
+                        before = now;
+                        now = next;
+                        next = pieces(j + 17);
+                    }
+                    if (j + 1 < n) {
+                        load(xk, kc, now, j + 1);
+                        load_scales(j + 1);
+                    }
+                }
+                if (j == 0) {
+                    // the queries, 16 bytes a lane: their place is free when the scores of the
+                    // tile's piece before are done
+                    const int rows = (start[at.b + 1] - start[at.b]) * group - at.p * kPair;  // from the pair on
+                    constexpr int kLanes = D / 8, kQAt = 128 / kLanes;
+                    const int tid = threadIdx.x & 127, piece = tid % kLanes;
+#pragma unroll 1
+                    for (int tile = 0; tile < 2 && ok; ++tile) {
+                        if (min(at.steps_of_tile(t, a, tile) - at.j, n) <= 0) continue;
+                        ok = warp_wait_or_stop(&sh.q_empty[tile], (pieces_of[tile] & 1) ^ 1, stop);
+                        if (!ok) break;
+                        if (tile) ++pieces_of[1]; else ++pieces_of[0];
+#pragma unroll 4
+                        for (int i = tid / kLanes; i < kRows; i += kQAt) {
+                            const int r_of = at.p * kPair + tile * kRows + i, tok = Place::divided(r_of, a.by_group);
+                            uint4 x = make_uint4(0, 0, 0, 0);
+                            if (tile * kRows + i < rows)
+                                x = __ldg(reinterpret_cast<const uint4 *>(
+                                              static_cast<const __half *>(a.q) + (start[at.b] + tok) * a.q_stride +
+                                              (at.h * group + r_of - tok * group) * D) + piece);
+                            *reinterpret_cast<uint4 *>(base + tile * C::kQ + piece / 8 * kPlane + swizzled(i, piece % 8)) = x;
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.q_full[tile]);
+                    }
+                    if (!ok) break;
+                } else {
+                    const int vf = f + j - 1, s = vf % kStages;
+                    ok = warp_wait_or_stop(&sh.v_empty[s], ((vf / kStages) & 1) ^ 1, stop);
+                    if (!ok) break;
+                    widen(xv, j - 1, ring + (kStages + s) * C::kHalf);
+                    if (lane == 0) mbar_arrive(&sh.v_full[s]);
+                    if (j < n) load(xv, vc, ((j + 1) & 15) == 0 ? before : now, j);
+                }
             }
+            f += n;
         }
     } else {
         // --- softmax, results ---
@@ -415,7 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             return reinterpret_cast<float4 *>(ws + kBalancedCounterBytes) +
                    (2ll * of_cta + side) * (D / 4 + 1) * a.record_rows;
         };
-        int f = 0, sc = 0, mine_so_far = 0, meetings = 0;
+        auto out_row_of = [&](int b, int h, int p) {  // this thread's
+            const int row = p * kPair + row_in, tok = Place::divided(row, a.by_group);
+            return static_cast<long long>(start[b] + tok) * a.n_q_heads + h * group + (row - tok * group);
+        };
+        // a piece that other CTAs share, to be joined if this warp was the last to arrive with its rows
+        struct Share {
+            int out_b, h, p, from, parts, before;
+        } todo[2];
+        todo[0].parts = todo[1].parts = 0;
+        int f = 0, sc = 0, mine_so_far = 0;
         bool ok = true;
 #pragma unroll 1
         for (int u = U0; ok && u < U1; at.next(t, a)) {
@@ -425,30 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             const int rows = (start[at.b + 1] - start[at.b]) * group - at.p * kPair;  // from the pair on
             const int seen = Place::keys(t, a, at.b, at.p * kPair + row_in);
             float r = 0.f, l = 0.f, wv = 0.f, inv_w = 0.f;
-            if (mine > 0) {
-                // the tile's queries: 16 lanes (8 at D = 64) a row
-                constexpr int kLanes = D / 8, kAt = 128 / kLanes;
-                const int piece = threadIdx.x % kLanes;
-#pragma unroll 4
-                for (int i = (threadIdx.x & 127) / kLanes; i < kRows; i += kAt) {
-                    const int r_of = at.p * kPair + w * kRows + i, tok = Place::divided(r_of, a.by_group);
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (w * kRows + i < rows)
-                        x = __ldg(reinterpret_cast<const uint4 *>(
-                                      static_cast<const __half *>(a.q) + (start[at.b] + tok) * a.q_stride +
-                                      (at.h * group + r_of - tok * group) * D) + piece);
-                    *reinterpret_cast<uint4 *>(base + w * C::kQ + piece / 8 * kPlane + swizzled(i, piece % 8)) = x;
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.q_full[w]);
-            }
 #pragma unroll 1
             for (int j = 0; j < mine; ++j, ++sc) {
-                const int s = (f + j) % kStages;
-                ok = warp_wait_or_stop(&sh.s_full[w], sc & 1, stop) &&
-                     warp_wait_or_stop(&sh.full[s], ((f + j) / kStages) & 1, stop);  // for the scales: long since
+                const int s = (f + j) & 3;
+                ok = warp_wait_or_stop(&sh.s_full[w], sc & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
                 const float *fg = sh.f[s], *vg = sh.v[s];
@@ -565,102 +616,101 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 if (!ok) break;
                 tc_fence_after();
             }
-            const bool whole = first >= U0 && first + at.steps <= U1;
-            const int tok = Place::divided(at.p * kPair + row_in, a.by_group);
-            const long long out_row = static_cast<long long>(start[at.b] + tok) * a.n_q_heads + at.h * group +
-                                      (at.p * kPair + row_in - tok * group);
-            const bool valid = row_in < rows;
-            if (whole) {
-                const float inv = wv / l;
-                uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row * D);
-                if (mine > 0) {
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32(o, to + c);
-                        tmem_wait_ld();
-                        if (valid)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t z[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    z[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                                      __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-                                out[c / 8 + e] = make_uint4(z[0], z[1], z[2], z[3]);
-                            }
-                    }
-                    if (a.lse_out && valid) a.lse_out[out_row] = (r + log2f(l)) * kLn2;
-                }
-                continue;
-            }
-            // --- a part: its record, and the join by the last CTA to arrive
-            const int side = first >= U0;
-            float4 *rec = record_of(cta, side);
+            const bool whole = first >= U0 && first + at.steps <= U1, valid = row_in < rows;
+            const float inv = wv / l;
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row_of(at.b, at.h, at.p) * D);
+            float4 *rec = record_of(cta, first >= U0) + row_in;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
                 if (mine > 0) {
                     tmem_ld32(o, to + c);
                     tmem_wait_ld();
+                    if (c + 32 == D) {  // the next piece's products may write O
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.o_free[w]);
+                    }
                 }
-                if (valid)
+                if (!valid) continue;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t z[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            z[k] = pack_half2(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                              __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                        out[c / 8 + e] = make_uint4(z[0], z[1], z[2], z[3]);
+                    }
+                } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        __stcg(rec + (c / 4 + e) * a.record_rows + row_in,
+                        __stcg(rec + (c / 4 + e) * a.record_rows,
                                mine > 0 ? make_float4(__uint_as_float(o[4 * e]) * wv, __uint_as_float(o[4 * e + 1]) * wv,
                                                       __uint_as_float(o[4 * e + 2]) * wv,
                                                       __uint_as_float(o[4 * e + 3]) * wv)
                                         : make_float4(0.f, 0.f, 0.f, 0.f));
+                }
             }
+            if (whole) {
+                if (a.lse_out && valid)
+                    a.lse_out[out_row_of(at.b, at.h, at.p)] = (r + log2f(l)) * kLn2;
+                continue;
+            }
+            if (row_in - lane >= rows) continue;  // none of the warp's rows is one
             if (valid)
-                __stcg(rec + (D / 4) * a.record_rows + row_in,
+                __stcg(rec + (D / 4) * a.record_rows,
                        make_float4(mine > 0 && l != 0.f ? r : -INFINITY, mine > 0 ? l : 0.f, 0.f, 0.f));
-            __threadfence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.met);
-            ok = warp_wait_or_stop(&sh.met, meetings++ & 1, stop);
-            if (!ok) break;
-            const int from = ranges.of(first), parts = ranges.of(first + at.steps - 1) - from + 1;
-            if (threadIdx.x == 0) {
-                int *counter = reinterpret_cast<int *>(ws) + from;
-                const int old = atomic_add_acq_rel_gpu(counter, 1);
-                sh.last = 0;
-                if (counter_not_zeroed(old, parts - 1)) {
+            const int from = ranges.of(first);
+            todo[1] = todo[0];
+            todo[0] = Share{at.b, at.h, at.p, from, ranges.of(first + at.steps - 1) - from + 1, 0};
+            if (lane == 0)
+                todo[0].before = atomic_add_acq_rel_gpu(reinterpret_cast<int *>(ws) + from * 8 + warp, 1);
+        }
+        // --- joins, by the last warp to arrive with these rows
+#pragma unroll 1
+        for (int i = 0; i < 2 && ok; ++i) {
+            const Share of = todo[0];
+            todo[0] = todo[1];
+            todo[1].parts = 0;
+            if (of.parts == 0) continue;
+            int last = 0;
+            if (lane == 0) {
+                int *counter = reinterpret_cast<int *>(ws) + of.from * 8 + warp;
+                if (counter_not_zeroed(of.before, of.parts - 1)) {
                     flag_error(a.err, PKV_ERRBIT_WORKSPACE);
                     atomic_exch_relaxed_gpu(counter, kCounterPoison);
-                } else if (old == parts - 1) {
-                    sh.last = 1;
-                    red_add_relaxed_gpu(counter, -parts);
+                } else if (of.before == of.parts - 1) {
+                    last = 1;
+                    red_add_relaxed_gpu(counter, -of.parts);
                 }
-                __threadfence();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.met);
-            ok = warp_wait_or_stop(&sh.met, meetings++ & 1, stop);
-            if (!ok) break;
-            if (!sh.last || !valid) continue;
-            __threadfence();
-            float high = -INFINITY, total_l = 0.f;
+            if (!__shfl_sync(~0u, last, 0)) continue;
+            if (row_in >= (start[of.out_b + 1] - start[of.out_b]) * group - of.p * kPair) continue;
+            float high = -INFINITY;
 #pragma unroll 1
-            for (int k = 0; k < parts; ++k)
-                high = fmaxf(high, __ldcg(&(record_of(from + k, k == 0) + (D / 4) * a.record_rows + row_in)->x));
+            for (int k = 0; k < of.parts; ++k)
+                high = fmaxf(high, __ldcg(&(record_of(of.from + k, k == 0) + (D / 4) * a.record_rows + row_in)->x));
             if (high == -INFINITY) high = 0.f;
+            const long long out_row = out_row_of(of.out_b, of.h, of.p);
+            float sum = 0.f;
 #pragma unroll 1
             for (int c0 = 0; c0 < D / 4; c0 += 8) {
                 float4 acc[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                total_l = 0.f;
+                sum = 0.f;
 #pragma unroll 1
-                for (int k = 0; k < parts; ++k) {
-                    const float4 *part = record_of(from + k, k == 0) + row_in;
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + (D / 4) * a.record_rows));
-                    const float g = ex2(ml.x - high);
-                    total_l += g * ml.y;
+                for (int k = 0; k < of.parts; ++k) {
+                    const float4 *part = record_of(of.from + k, k == 0) + row_in;
                     float4 z[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) z[e] = __ldcg(part + (c0 + e) * a.record_rows);
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + (D / 4) * a.record_rows));
+                    const float g = ex2(ml.x - high);
+                    sum += g * ml.y;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         acc[e].x += g * z[e].x;
@@ -669,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                         acc[e].w += g * z[e].w;
                     }
                 }
-                const float inv = 1.f / total_l;
+                const float inv = 1.f / sum;
                 uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row * D) + c0 / 2;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -678,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                                         pack_half2(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
                                         pack_half2(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
             }
-            if (a.lse_out) a.lse_out[out_row] = (high + log2f(total_l)) * kLn2;
+            if (a.lse_out) a.lse_out[out_row] = (high + log2f(sum)) * kLn2;
         }
     }
     tc_fence_before();
@@ -710,7 +760,7 @@ bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads
     if (static_cast<double>(num_seqs) * n_kv_heads * ((rows + kPair - 1) / kPair) * steps >= 2147483648.0)
         return false;
     sp->row_tiles = 0;
-    sp->ctas = sms < kBalancedMaxWorkers ? sms : kBalancedMaxWorkers;
+    sp->ctas = sms < kBalancedMaxWorkers / 8 ? sms : kBalancedMaxWorkers / 8;  // a counter for each warp of rows
     sp->record_rows = static_cast<int>(rows < kPair ? (rows + 31) / 32 * 32 : kPair);
     sp->ws_bytes = kBalancedCounterBytes +
                    static_cast<size_t>(sp->ctas) * 2 * (head_dim / 4 + 1) * sp->record_rows * sizeof(float4);
