@@ -35,7 +35,6 @@ constexpr int kRows = 128, kKeys = 128;  // of a tile, of a step
 constexpr int kPair = 2 * kRows;
 constexpr int kGroups = kKeys / 16;      // pieces of 16 keys, each of one block
 constexpr int kThreads = 512;  // 8 warps of softmax, 4 of converters, 2 of products and 2 idle ones
-// Registers: 256 x 176 + 128 x 96 + 128 x 64 is the 512 x 128 of the launch.
 constexpr int kPlane = 128 * 128;        // 128 rows of 64 fp16, swizzled
 constexpr float kLag = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -253,7 +252,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
 
     if (warp >= 12) {
         // --- products ---
-        give_registers<64>();
         if (warp < 14 && elect_one()) {
             const int w = warp - 12;  // the tile
             constexpr uint32_t ds = mma_desc(kRows, kKeys, false, false), dpv = mma_desc(kRows, D, false, true);
@@ -282,19 +280,19 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     if (weights) {
                         const uint64_t vd = smem_desc(
                             kv + (kStages + vf % kStages) * C::kHalf, 1024, kPlane);
-#pragma unroll
+#pragma unroll 2
                         for (int k = 0; k < 4; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
                         ok = wait_or_stop(&sh.p_ready[w][1], sc & 1, stop);
                         if (!ok) break;
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 2
                         for (int k = 4; k < 8; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, true);
                         ++sc;
                         if (j + 1 == mine) mma_commit(&sh.o_done[w]);
                     }
                     if (scores) {
                         const uint64_t kd = smem_desc(kv + (kf % kStages) * C::kHalf, 1024, 0);
-#pragma unroll
+#pragma unroll 2
                         for (int k = 0; k < 4 * C::kPlanes; ++k)
                             mma_ss(ts, qd + (k / 4) * (kPlane / 16) + (k % 4) * 2,
                                    kd + (k / 4) * (kPlane / 16) + (k % 4) * 2, ds, k > 0);
@@ -315,7 +313,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         }
     } else if (warp >= 8) {
         // --- converters ---
-        give_registers<96>();
         const int w = warp - 8;  // its pieces of 16 keys: 2 w and 2 w + 1
         constexpr int kAt = 32 / (4 * C::kPlanes), kLoads = 16 / kAt;  // rows of a load, loads of a piece
         // A lane's 16 codes of a row become pieces 2 x and 2 x + 1 of a plane.  Eight lanes have
@@ -466,7 +463,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         }
     } else {
         // --- softmax, results ---
-        take_registers<176>();
         const int w = warp >> 2;  // the tile
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 * (warp % 4) << 16
         const uint32_t ts = tmem + 128 * w + lanes, to = tmem + 256 + 128 * w + lanes;
@@ -524,20 +520,20 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     m1 = fmaxf(m1, __uint_as_float(x[31]));
                     return fmaxf(m0 * f0, m1 * f1);
                 };
-                // all logits once for the row's largest; the second half stays in registers
-                uint32_t x[2][32];
-                tmem_ld32(x[0], ts);
-                tmem_ld32(x[1], ts + 32);
-                tmem_wait_ld();
-                ready(x[0], 0);
-                ready(x[1], 32);
-                float top = fmaxf(top_of(x[0], fg[0], fg[1]), top_of(x[1], fg[2], fg[3]));
-                tmem_ld32(x[0], ts + 64);
-                tmem_ld32(x[1], ts + 96);
-                tmem_wait_ld();
-                ready(x[0], 64);
-                ready(x[1], 96);
-                top = fmaxf(top, fmaxf(top_of(x[0], fg[4], fg[5]), top_of(x[1], fg[6], fg[7])));
+                // (The logits are read twice: kept, they would take a third of the registers.)
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t x[2][32];
+                    tmem_ld32(x[0], ts + 64 * half);
+                    tmem_ld32(x[1], ts + 64 * half + 32);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        ready(x[q], 64 * half + 32 * q);
+                        top = fmaxf(top, top_of(x[q], fg[4 * half + 2 * q], fg[4 * half + 2 * q + 1]));
+                    }
+                }
                 // --- references
                 float most = 0.f;
 #pragma unroll
@@ -572,41 +568,29 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 }
                 // --- weights
                 float2 sum = make_float2(0.f, 0.f);
-                auto weigh = [&](const uint32_t (&y)[32], int c0, const float (&ff)[2], const float (&vv)[2]) {
-                    uint32_t p[16];
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t x[32], p[16];
+                    tmem_ld32(x, ts + 32 * q);
+                    tmem_wait_ld();
+                    ready(x, 32 * q);
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float2 e = fma2(make_float2(__uint_as_float(y[2 * c]), __uint_as_float(y[2 * c + 1])),
-                                              ff[c / 8], -r);
+                        const float f = fg[2 * q + c / 8], v = vg[2 * q + c / 8] * inv_w;
+                        const float2 e = fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), f, -r);
                         const float2 z = make_float2(ex2(e.x), ex2(e.y));
                         sum = add2(sum, z);
-                        const float2 q = mul2(z, make_float2(vv[c / 8], vv[c / 8]));
-                        p[c] = pack_half2(q.x, q.y);
+                        const float2 y = mul2(z, make_float2(v, v));
+                        p[c] = pack_half2(y.x, y.y);
                     }
-                    tmem_st16(ts + c0 / 2, p);
-                };
-                auto announce = [&](int half) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sh.p_ready[w][half]);
-                };
-                uint32_t y[32];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    tmem_ld32(y, ts + 32 * q);
-                    tmem_wait_ld();
-                    ready(y, 32 * q);
-                    const float ff[2] = {fg[2 * q], fg[2 * q + 1]}, vv[2] = {vg[2 * q] * inv_w, vg[2 * q + 1] * inv_w};
-                    weigh(y, 32 * q, ff, vv);
+                    tmem_st16(ts + 16 * q, p);  // over logits that have been read: half as many columns
+                    if (q & 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.p_ready[w][q >> 1]);
+                    }
                 }
-                announce(0);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float ff[2] = {fg[4 + 2 * q], fg[5 + 2 * q]}, vv[2] = {vg[4 + 2 * q] * inv_w, vg[5 + 2 * q] * inv_w};
-                    weigh(x[q], 64 + 32 * q, ff, vv);
-                }
-                announce(1);
                 l += sum.x + sum.y;
             }
             f += n;
