@@ -2,8 +2,8 @@
 // of a KV head: chunks of prompts, drafts to verify (paged_decode_attention_q8).
 //
 // An item is two tiles of 128 query rows (tokens x heads of a group) of one KV head.  For a
-// step of 128 keys, codes K, V widened to fp16 (exact) in shared memory:
-//   S [128 x 128] = Q K^T
+// step of 64 keys, codes K, V widened to fp16 (exact) in shared memory:
+//   S [128 x 64] = Q K^T
 //   y = 2^(S f - r)          f: the key's block scale * scale * log2 e; r: the row's reference
 //   O += (y v / w) V         v: the key's block scale; w: the item's V reference
 // with S, O and P = y v / w in TMEM: P (fp16) takes the place of its own S and is the first
@@ -12,9 +12,10 @@
 // owns the row.  The result is O w / l, l the sum of y before its rounding.
 //
 // Roles: two warpgroups of softmax, a tile each, a row a thread; one of converters, which
-// load codes into registers a step ahead, widen them and store them in the products'
-// layout; two warps of products, which take turns, so that one tile's softmax runs under
-// the other's products.
+// load codes into registers two steps ahead, widen them and store them in the products'
+// layout; a warp of products for each tile.  A tile has two places for S, so the scores of
+// the next step are there when the softmax of one is done.  (With one place, and steps of
+// 128 keys, softmax and products of a tile took turns: 113 us for the chunks below.)
 //
 // Split.  The (sequence, head, pair of tiles, step) units are cut into equal ranges, one
 // per SM; items that several CTAs hold leave records, and the last to arrive joins them.
@@ -31,31 +32,39 @@
 namespace pkv {
 namespace {
 
-constexpr int kRows = 128, kKeys = 128;  // of a tile, of a step
+constexpr int kRows = 128, kKeys = 64;  // of a tile, of a step
 constexpr int kPair = 2 * kRows;
 constexpr int kGroups = kKeys / 16;      // pieces of 16 keys, each of one block
 constexpr int kThreads = 512;  // 8 warps of softmax, 4 of converters, 2 of products and 2 idle ones
-constexpr int kPlane = 128 * 128;        // 128 rows of 64 fp16, swizzled
+constexpr int kQPlane = kRows * 128, kPlane = kKeys * 128;  // rows of 64 fp16, swizzled
 constexpr float kLag = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kStages = 2;
+constexpr int kStages = 4;  // of the rings of K and of V
+constexpr int kSlots = 8;   // of a step's scales
 
 template <int D>
 struct Cfg {
     static constexpr int kPlanes = D / 64;
-    static constexpr int kQ = kPlanes * kPlane;       // bytes of a tile's queries
+    static constexpr int kQ = kPlanes * kQPlane;      // bytes of a tile's queries
     static constexpr int kHalf = kPlanes * kPlane;    // of a step's K or V
     static constexpr int kBytes = 2 * kQ + 2 * kStages * kHalf;  // queries, K ring, V ring
-    static constexpr size_t smem(int seqs) { return 1024 + kBytes + (static_cast<size_t>(seqs) * 3 + 2) * 4; }
+    static constexpr size_t smem(int seqs) { return kBytes + (static_cast<size_t>(seqs) * 3 + 2) * 4; }
+};
+
+// A piece that other CTAs share, to be joined if this warp was the last to arrive with its rows.
+struct Share {
+    int b, h, p;
+    int from, parts, before;  // CTAs from, parts of them; how many had arrived
 };
 
 struct Roles {
-    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], o_done[2], o_free[2], turn[2], drained[2];
+    Share todo[8][2];
+    uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2], pv_done[2], o_free[2], drained[2];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    // Of a step's keys: the logits' factor and the V scale.  A step's are written with its K,
-    // when the scores of two steps before are done, and read by its softmax, which is over
-    // when the scores of two steps behind are issued: three steps' lie side by side.
-    float f[4][kGroups], v[4][kGroups];
+    // Of a step's keys: the logits' factor and the V scale.  They are written with its K, and
+    // read by its softmax.  Step j + 8's K waits for the scores of step j + 4, which come
+    // behind the softmax of step j + 2: no slot is written while it is read.
+    float f[kSlots][kGroups], v[kSlots][kGroups];
     uint32_t tmem;
     int stop;
     int sums[kThreads / 32];
@@ -139,9 +148,8 @@ __device__ __forceinline__ int swizzled(int row, int q) { return row * 128 + ((q
 template <int KIND, int D>
 __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8AttentionArgs a) {
     using C = Cfg<D>;
-    extern __shared__ unsigned char raw[];
+    extern __shared__ __align__(1024) unsigned char base[];
     __shared__ __align__(16) Roles sh;
-    unsigned char *base = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     int *cum = reinterpret_cast<int *>(base + C::kBytes), *len = cum + a.num_seqs + 1, *start = len + a.num_seqs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = a.n_q_heads / a.n_kv_heads;
@@ -150,12 +158,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         for (int t = 0; t < 2; ++t) {
             mbar_init(&sh.q_full[t], 4);
             mbar_init(&sh.q_empty[t], 1);
-            mbar_init(&sh.s_full[t], 2);
+            mbar_init(&sh.s_full[t][0], 2);
+            mbar_init(&sh.s_full[t][1], 2);
             mbar_init(&sh.o_free[t], 4);
-            mbar_init(&sh.p_ready[t][0], 4);
-            mbar_init(&sh.p_ready[t][1], 4);
-            mbar_init(&sh.o_done[t], 1);
-            mbar_init(&sh.turn[t], 1);
+            mbar_init(&sh.p_ready[t], 4);
+            mbar_init(&sh.pv_done[t], 1);
             mbar_init(&sh.drained[t], 1);
         }
         for (int s = 0; s < kStages; ++s) {
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     volatile int *stop = &sh.stop;
-    // TMEM columns: S of tile t at 128 t (P in its first half), O at 256 + 128 t
+    // TMEM columns: S of tile t at 128 t and 128 t + 64 (P in its first half), O at 256 + 128 t
 
     const int ctas = min(static_cast<int>(gridDim.x), max(1, total));
     const Ranges ranges(total, ctas);
@@ -257,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             constexpr uint32_t ds = mma_desc(kRows, kKeys, false, false), dpv = mma_desc(kRows, D, false, true);
             const uint32_t kv = smem_addr(base) + 2 * C::kQ, ts = tmem + 128 * w;
             const uint64_t qd = smem_desc(smem_addr(base) + w * C::kQ, 1024, 0);
-            int f = 0, sc = 0, pc = 0, turns = 0;  // steps so far, this tile's, its pieces, turns
+            int f = 0, ss = 0, sc = 0, pc = 0;  // steps so far; this tile's scores, weights and pieces
             bool ok = U0 == U1 || first_wait(&sh.k_full[0], 0, a.first_wait_polls, stop);
 #pragma unroll 1
             for (int u = U0; ok && u < U1; at.next(t, a)) {
@@ -265,44 +272,46 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 const int mine = max(0, min(at.steps_of_tile(t, a, w) - at.j, n));
                 u += n;
 #pragma unroll 1
-                for (int j = -1; j < n; ++j) {  // between the softmax of step j and of the next
-                    const bool weights = j >= 0 && j < mine, scores = j + 1 < mine;
-                    const int kf = f + j + 1, vf = f + j;
-                    if (j + 1 < n) ok = wait_or_stop(&sh.k_full[kf % kStages], (kf / kStages) & 1, stop);
-                    if (ok && j >= 0) ok = wait_or_stop(&sh.v_full[vf % kStages], (vf / kStages) & 1, stop);
-                    if (ok && j < 0 && mine > 0) ok = wait_or_stop(&sh.q_full[w], pc & 1, stop);
-                    if (ok && weights && j == 0 && pc > 0) ok = wait_or_stop(&sh.o_free[w], (pc - 1) & 1, stop);
-                    if (ok && weights) ok = wait_or_stop(&sh.p_ready[w][0], sc & 1, stop);
-                    ok = ok && wait_or_stop(&sh.turn[w], (turns & 1) ^ (w ^ 1), stop);
-                    if (!ok) break;
-                    ++turns;
-                    tc_fence_after();
-                    if (weights) {
-                        const uint64_t vd = smem_desc(
-                            kv + (kStages + vf % kStages) * C::kHalf, 1024, kPlane);
-#pragma unroll 2
-                        for (int k = 0; k < 4; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
-                        ok = wait_or_stop(&sh.p_ready[w][1], sc & 1, stop);
+                for (int i = 0; i < n + 2; ++i) {  // outputs of step i - 2, scores of step i in their S's place
+                    if (i >= 2) {
+                        const int j = i - 2, vf = f + j;
+                        ok = wait_or_stop(&sh.v_full[vf % kStages], (vf / kStages) & 1, stop);
+                        if (ok && j < mine) {
+                            if (j == 0 && pc > 0) ok = wait_or_stop(&sh.o_free[w], (pc - 1) & 1, stop);
+                            ok = ok && wait_or_stop(&sh.p_ready[w], sc & 1, stop);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t vd = smem_desc(kv + (kStages + vf % kStages) * C::kHalf, 1024, kPlane);
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                mma_ts(ts + 256, ts + 64 * (sc & 1) + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
+                            mma_commit(&sh.pv_done[w]);
+                            ++sc;
+                        }
                         if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 2
-                        for (int k = 4; k < 8; ++k) mma_ts(ts + 256, ts + 8 * k, vd + k * 128, dpv, true);
-                        ++sc;
-                        if (j + 1 == mine) mma_commit(&sh.o_done[w]);
+                        mma_commit(&sh.v_empty[vf % kStages]);
                     }
-                    if (scores) {
-                        const uint64_t kd = smem_desc(kv + (kf % kStages) * C::kHalf, 1024, 0);
-#pragma unroll 2
-                        for (int k = 0; k < 4 * C::kPlanes; ++k)
-                            mma_ss(ts, qd + (k / 4) * (kPlane / 16) + (k % 4) * 2,
-                                   kd + (k / 4) * (kPlane / 16) + (k % 4) * 2, ds, k > 0);
-                        mma_commit(&sh.s_full[w]);
-                        mbar_arrive(&sh.s_full[w]);  // what this thread has seen (the scales) is seen there too
-                        if (j + 2 == mine) mma_commit(&sh.q_empty[w]);
+                    if (i < n) {
+                        const int kf = f + i;
+                        ok = wait_or_stop(&sh.k_full[kf % kStages], (kf / kStages) & 1, stop);
+                        if (ok && i < mine) {
+                            if (i == 0) ok = wait_or_stop(&sh.q_full[w], pc & 1, stop);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint64_t kd = smem_desc(kv + (kf % kStages) * C::kHalf, 1024, 0);
+#pragma unroll
+                            for (int k = 0; k < 4 * C::kPlanes; ++k)
+                                mma_ss(ts + 64 * (ss & 1), qd + (k / 4) * (kQPlane / 16) + (k % 4) * 2,
+                                       kd + (k / 4) * (kPlane / 16) + (k % 4) * 2, ds, k > 0);
+                            mma_commit(&sh.s_full[w][ss & 1]);
+                            // what this thread has seen (the scales) is seen there too
+                            mbar_arrive(&sh.s_full[w][ss & 1]);
+                            ++ss;
+                            if (i + 1 == mine) mma_commit(&sh.q_empty[w]);
+                        }
+                        if (!ok) break;
+                        mma_commit(&sh.k_empty[kf % kStages]);
                     }
-                    mbar_arrive(&sh.turn[w ^ 1]);
-                    if (j >= 0) mma_commit(&sh.v_empty[vf % kStages]);
-                    if (j + 1 < n) mma_commit(&sh.k_empty[kf % kStages]);
                 }
                 f += n;
                 if (mine > 0) ++pc;
@@ -313,8 +322,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         }
     } else if (warp >= 8) {
         // --- converters ---
-        const int w = warp - 8;  // its pieces of 16 keys: 2 w and 2 w + 1
-        constexpr int kAt = 32 / (4 * C::kPlanes), kLoads = 16 / kAt;  // rows of a load, loads of a piece
+        const int w = warp - 8;  // its 16 keys of a step
+        constexpr int kAt = 32 / (4 * C::kPlanes), kLoads = 16 / kAt;  // rows of a load, loads of 16 rows
         // A lane's 16 codes of a row become pieces 2 x and 2 x + 1 of a plane.  Eight lanes have
         // two rows of one plane, whose swizzles differ in the lowest bit: no bank twice.
         const int plane = lane / 16 * (C::kPlanes - 1), x4 = lane % 4;
@@ -329,8 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                to[i][e] = plane * kPlane + swizzled(2 * w * 16 + (i * kAt & 7) + row0, 2 * x4 + e);
+                to[i][e] = plane * kPlane + swizzled(w * 16 + (i * kAt & 7) + row0, 2 * x4 + e);
         const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
+        unsigned char *ring = base + 2 * C::kQ;
         int f = 0, pieces_of[2] = {0, 0};  // steps so far, pieces of a tile
         bool ok = true;
 #pragma unroll 1
@@ -339,12 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             u += n;
             const int L = len[at.b];
             const int *table = a.block_tables + static_cast<long long>(at.b) * a.max_blocks_per_seq;
-            // lane i knows the cache piece (of 16 rows) of step from + i / 2, the warp's
-            // group i % 2: of the step's batch of 16, and of the one after it
+            // lane i knows the cache piece (16 rows) of step from + i for this warp's keys; two
+            // batches of 32 steps
             auto pieces = [&](int from) {
-                const int g = (at.j + from + lane / 2) * kGroups + 2 * w + lane % 2;  // of the sequence
+                const int g = (at.j + from + lane) * kGroups + w;  // of the sequence
                 unsigned piece = 0;
-                if (from + lane / 2 < n && g * 16 < L) {
+                if (from + lane < n && g * 16 < L) {
                     const int id = table[g >> bs16_log2];
                     if (id < 0 || id >= a.num_blocks)
                         flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
@@ -354,113 +364,102 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 }
                 return piece;
             };
-            unsigned before = 0, now = pieces(0), next = pieces(16);  // K runs a step ahead of V
-            uint4 xk[2][kLoads], xv[2][kLoads];  // codes on their way
+            unsigned now = pieces(0), next = pieces(32);
+            uint4 xk[2][kLoads], xv[2][kLoads];  // codes of the next two steps, on their way
             float ks[2], vs[2];
-            auto load = [&](uint4 (&x)[2][kLoads], const unsigned char *from, unsigned batch, int j) {
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const unsigned piece = __shfl_sync(~0u, batch, (2 * j + g) & 31);
-                    const unsigned char *src = from + static_cast<long long>(piece) * (16 * D);
-#pragma unroll
-                    for (int i = 0; i < kLoads; ++i) x[g][i] = __ldg(reinterpret_cast<const uint4 *>(src + i * kAt * D));
+            auto load = [&](int e, int j) {  // step j, all in one go
+                if (j >= n) return;
+                if (j > 0 && (j & 31) == 0) {
+                    now = next;
+                    next = pieces(j + 32);
                 }
-            };
-            auto load_scales = [&](int j) {
+                const unsigned piece = __shfl_sync(~0u, now, j & 31);
+                const long long src = static_cast<long long>(piece) * (16 * D);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const unsigned cell = __shfl_sync(~0u, now, (2 * j + g) & 31) >> bs16_log2;
-                    ks[g] = __ldg(a.k_scales + cell);
-                    vs[g] = __ldg(a.v_scales + cell);
-                }
+                for (int i = 0; i < kLoads; ++i) xk[e][i] = __ldg(reinterpret_cast<const uint4 *>(kc + src + i * kAt * D));
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) xv[e][i] = __ldg(reinterpret_cast<const uint4 *>(vc + src + i * kAt * D));
+                ks[e] = __ldg(a.k_scales + (piece >> bs16_log2));
+                vs[e] = __ldg(a.v_scales + (piece >> bs16_log2));
             };
             // codes x of step j to `half` of the memory
-            auto widen = [&](const uint4 (&x)[2][kLoads], int j, unsigned char *half) {
-                const int key0 = (at.j + j) * kKeys + 2 * w * 16 + row0;  // of the sequence
-                const bool cut = key0 - row0 + 32 > L;
+            auto widen = [&](const uint4 (&x)[kLoads], int j, unsigned char *half) {
+                const int key0 = (at.j + j) * kKeys + w * 16 + row0;  // of the sequence
+                const bool cut = key0 - row0 + 16 > L;
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-#pragma unroll
-                    for (int i = 0; i < kLoads; ++i) {
-                        uint4 c = x[g][i];
-                        // rows that hold no token may hold anything
-                        if (cut && key0 + g * 16 + i * kAt >= L) c = make_uint4(0, 0, 0, 0);
-                        unsigned char *dst = half + (g * 16 + (i * kAt & ~7)) * 128;
-                        *reinterpret_cast<uint4 *>(dst + to[kAt == 8 ? 0 : i & 1][0]) =
-                            make_uint4(q8_widen<KIND, 0>(c.x), q8_widen<KIND, 1>(c.x), q8_widen<KIND, 0>(c.y),
-                                       q8_widen<KIND, 1>(c.y));
-                        *reinterpret_cast<uint4 *>(dst + to[kAt == 8 ? 0 : i & 1][1]) =
-                            make_uint4(q8_widen<KIND, 0>(c.z), q8_widen<KIND, 1>(c.z), q8_widen<KIND, 0>(c.w),
-                                       q8_widen<KIND, 1>(c.w));
-                    }
+                for (int i = 0; i < kLoads; ++i) {
+                    uint4 c = x[i];
+                    // rows that hold no token may hold anything
+                    if (cut && key0 + i * kAt >= L) c = make_uint4(0, 0, 0, 0);
+                    unsigned char *dst = half + (i * kAt & ~7) * 128;
+                    *reinterpret_cast<uint4 *>(dst + to[kAt == 8 ? 0 : i & 1][0]) =
+                        make_uint4(q8_widen<KIND, 0>(c.x), q8_widen<KIND, 1>(c.x), q8_widen<KIND, 0>(c.y),
+                                   q8_widen<KIND, 1>(c.y));
+                    *reinterpret_cast<uint4 *>(dst + to[kAt == 8 ? 0 : i & 1][1]) =
+                        make_uint4(q8_widen<KIND, 0>(c.z), q8_widen<KIND, 1>(c.z), q8_widen<KIND, 0>(c.w),
+                                   q8_widen<KIND, 1>(c.w));
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            load(xk, kc, now, 0);
-            load_scales(0);
-            load(xv, vc, now, 0);
-            unsigned char *ring = base + 2 * C::kQ;
+            load(0, 0);
+            load(1, 1);
+            // the queries, 16 bytes a lane: their place is free when the scores of the tile's
+            // piece before are done
+            const int rows = (start[at.b + 1] - start[at.b]) * group - at.p * kPair;  // from the pair on
 #pragma unroll 1
-            for (int j = 0; j <= n; ++j) {  // K of step j, V of the step before
-                if (j < n) {
-                    const int kf = f + j, s = kf % kStages;
+            for (int tile = 0; tile < 2 && ok; ++tile) {
+                if (min(at.steps_of_tile(t, a, tile) - at.j, n) <= 0) continue;
+                ok = warp_wait_or_stop(&sh.q_empty[tile], (pieces_of[tile] & 1) ^ 1, stop);
+                if (!ok) break;
+                if (tile) ++pieces_of[1]; else ++pieces_of[0];
+                constexpr int kLanes = D / 8, kQAt = 128 / kLanes;
+                const int tid = threadIdx.x & 127, piece = tid % kLanes;
+                const uint32_t dst = smem_addr(base) + tile * C::kQ + piece / 8 * kQPlane;
+#pragma unroll 1
+                for (int i = tid / kLanes; i < kRows; i += kQAt) {
+                    const int r_of = at.p * kPair + tile * kRows + i, tok = Place::divided(r_of, a.by_group);
+                    const bool some = tile * kRows + i < rows;
+                    const __half *q = static_cast<const __half *>(a.q) +
+                                      (some ? (start[at.b] + tok) * a.q_stride + (at.h * group + r_of - tok * group) * D : 0);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + swizzled(i, piece % 8)),
+                                 "l"(q + piece * 8), "r"(some ? 16 : 0) : "memory");
+                }
+            }
+            if (!ok) break;
+            bool queries = true;  // still to be announced
+#pragma unroll 1
+            for (int j0 = 0; j0 < n && ok; j0 += 2) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = j0 + e, kf = f + j, s = kf % kStages;
+                    if (j >= n || !ok) break;
                     ok = warp_wait_or_stop(&sh.k_empty[s], ((kf / kStages) & 1) ^ 1, stop);
                     if (!ok) break;
-                    if (lane < 2) {  // pieces behind the sequence have no scale of their own
-                        const bool some = (at.j + j) * kKeys + (2 * w + lane) * 16 < L;
-                        sh.f[kf & 3][2 * w + lane] = some ? fmaxf((lane ? ks[1] : ks[0]) * scale, 1e-30f) : 1e-30f;
-                        sh.v[kf & 3][2 * w + lane] = some ? (lane ? vs[1] : vs[0]) : 0.f;
+                    if (lane == 0) {  // keys behind the sequence have no scale of their own
+                        const bool some = (at.j + j) * kKeys + w * 16 < L;
+                        sh.f[kf % kSlots][w] = some ? fmaxf(ks[e] * scale, 1e-30f) : 1e-30f;
+                        sh.v[kf % kSlots][w] = some ? vs[e] : 0.f;
                     }
-                    widen(xk, j, ring + s * C::kHalf);
+                    widen(xk[e], j, ring + s * C::kHalf);
                     if (lane == 0) mbar_arrive(&sh.k_full[s]);
-                    if (((j + 1) & 15) == 0) {
-                        before = now;
-                        now = next;
-                        next = pieces(j + 17);
-                    }
-                    if (j + 1 < n) {
-                        load(xk, kc, now, j + 1);
-                        load_scales(j + 1);
-                    }
-                }
-                if (j == 0) {
-                    // the queries, 16 bytes a lane: their place is free when the scores of the
-                    // tile's piece before are done
-                    const int rows = (start[at.b + 1] - start[at.b]) * group - at.p * kPair;  // from the pair on
-                    constexpr int kLanes = D / 8, kQAt = 128 / kLanes;
-                    const int tid = threadIdx.x & 127, piece = tid % kLanes;
-#pragma unroll 1
-                    for (int tile = 0; tile < 2 && ok; ++tile) {
-                        if (min(at.steps_of_tile(t, a, tile) - at.j, n) <= 0) continue;
-                        ok = warp_wait_or_stop(&sh.q_empty[tile], (pieces_of[tile] & 1) ^ 1, stop);
-                        if (!ok) break;
-                        if (tile) ++pieces_of[1]; else ++pieces_of[0];
-#pragma unroll 4
-                        for (int i = tid / kLanes; i < kRows; i += kQAt) {
-                            const int r_of = at.p * kPair + tile * kRows + i, tok = Place::divided(r_of, a.by_group);
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (tile * kRows + i < rows)
-                                x = __ldg(reinterpret_cast<const uint4 *>(
-                                              static_cast<const __half *>(a.q) + (start[at.b] + tok) * a.q_stride +
-                                              (at.h * group + r_of - tok * group) * D) + piece);
-                            *reinterpret_cast<uint4 *>(base + tile * C::kQ + piece / 8 * kPlane + swizzled(i, piece % 8)) = x;
-                        }
+                    if (queries) {
+                        queries = false;
+                        asm volatile("cp.async.wait_all;" ::: "memory");
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.q_full[tile]);
+                        if (lane < 2 && min(at.steps_of_tile(t, a, lane) - at.j, n) > 0) mbar_arrive(&sh.q_full[lane]);
                     }
+                    ok = warp_wait_or_stop(&sh.v_empty[s], ((kf / kStages) & 1) ^ 1, stop);
                     if (!ok) break;
-                } else {
-                    const int vf = f + j - 1, s = vf % kStages;
-                    ok = warp_wait_or_stop(&sh.v_empty[s], ((vf / kStages) & 1) ^ 1, stop);
-                    if (!ok) break;
-                    widen(xv, j - 1, ring + (kStages + s) * C::kHalf);
+                    widen(xv[e], j, ring + (kStages + s) * C::kHalf);
                     if (lane == 0) mbar_arrive(&sh.v_full[s]);
-                    if (j < n) load(xv, vc, ((j + 1) & 15) == 0 ? before : now, j);
+                    load(e, j + 2);
                 }
             }
             f += n;
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // --- softmax, results ---
         const int w = warp >> 2;  // the tile
@@ -477,12 +476,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             const int row = p * kPair + row_in, tok = Place::divided(row, a.by_group);
             return static_cast<long long>(start[b] + tok) * a.n_q_heads + h * group + (row - tok * group);
         };
-        // a piece that other CTAs share, to be joined if this warp was the last to arrive with its rows
-        struct Share {
-            int out_b, h, p, from, parts, before;
-        } todo[2];
-        todo[0].parts = todo[1].parts = 0;
-        int f = 0, sc = 0, mine_so_far = 0;
+        int shares = 0;
+        int f = 0, sc = 0;
         bool ok = true;
 #pragma unroll 1
         for (int u = U0; ok && u < U1; at.next(t, a)) {
@@ -494,50 +489,40 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             float r = 0.f, l = 0.f, wv = 0.f, inv_w = 0.f;
 #pragma unroll 1
             for (int j = 0; j < mine; ++j, ++sc) {
-                const int s = (f + j) & 3;
-                ok = warp_wait_or_stop(&sh.s_full[w], sc & 1, stop);
+                const int slot = (f + j) % kSlots;
+                const uint32_t here = ts + 64 * (sc & 1);
+                ok = warp_wait_or_stop(&sh.s_full[w][sc & 1], (sc >> 1) & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
-                const float *fg = sh.f[s], *vg = sh.v[s];
-                const int left = seen - (at.j + j) * kKeys;
-                const bool masked = __any_sync(~0u, left < kKeys);
-                auto ready = [&](uint32_t (&x)[32], int c0) {  // logits' sign and mask
-                    if (a.scale_log2 < 0.f)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) x[c] ^= 0x80000000u;
-                    if (masked)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) x[c] = c0 + c < left ? x[c] : 0xff800000u;
-                };
-                auto top_of = [&](const uint32_t (&x)[32], float f0, float f1) {
-                    float m0 = __uint_as_float(x[0]), m1 = __uint_as_float(x[16]);
-#pragma unroll
-                    for (int c = 1; c + 1 < 16; c += 2) {
-                        m0 = max3(m0, __uint_as_float(x[c]), __uint_as_float(x[c + 1]));
-                        m1 = max3(m1, __uint_as_float(x[16 + c]), __uint_as_float(x[16 + c + 1]));
-                    }
-                    m0 = fmaxf(m0, __uint_as_float(x[15]));
-                    m1 = fmaxf(m1, __uint_as_float(x[31]));
-                    return fmaxf(m0 * f0, m1 * f1);
-                };
-                // (The logits are read twice: kept, they would take a third of the registers.)
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t x[2][32];
-                    tmem_ld32(x[0], ts + 64 * half);
-                    tmem_ld32(x[1], ts + 64 * half + 32);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        ready(x[q], 64 * half + 32 * q);
-                        top = fmaxf(top, top_of(x[q], fg[4 * half + 2 * q], fg[4 * half + 2 * q + 1]));
-                    }
-                }
-                // --- references
+                uint32_t x[2][32];
+                tmem_ld32(x[0], here);
+                tmem_ld32(x[1], here + 32);
+                const float *fg = sh.f[slot], *vg = sh.v[slot];
                 float most = 0.f;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) most = fmaxf(most, vg[g]);
+                const int left = seen - (at.j + j) * kKeys;
+                tmem_wait_ld();
+                if (a.scale_log2 < 0.f)
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c / 32][c % 32] ^= 0x80000000u;
+                if (__any_sync(~0u, left < kKeys))
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) x[c / 32][c % 32] = c < left ? x[c / 32][c % 32] : 0xff800000u;
+                // --- references
+                float top = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    const uint32_t *z = &x[g / 2][g % 2 * 16];
+                    float m0 = __uint_as_float(z[0]), m1 = __uint_as_float(z[1]);
+#pragma unroll
+                    for (int c = 2; c + 3 < 16; c += 4) {
+                        m0 = max3(m0, __uint_as_float(z[c]), __uint_as_float(z[c + 1]));
+                        m1 = max3(m1, __uint_as_float(z[c + 2]), __uint_as_float(z[c + 3]));
+                    }
+                    m0 = max3(m0, __uint_as_float(z[14]), __uint_as_float(z[15]));
+                    top = fmaxf(top, fmaxf(m0, m1) * fg[g]);
+                }
                 const bool far = most > 0.f && !(most >= wv * (1.f / 64.f) && most <= wv * 16.f);
                 float fac = 1.f;
                 if (far) {
@@ -550,12 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 } else {
                     const bool move = top - r > kLag;
                     if (__any_sync(~0u, move || far)) {
-                        // S being full, every earlier product into O is done
                         const float next = move ? top : r, g = ex2(r - next);
                         r = next;
                         l *= g;
                         fac *= g;
-#pragma unroll
+                        ok = warp_wait_or_stop(&sh.pv_done[w], (sc - 1) & 1, stop);  // the outputs so far
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
                         for (int c = 0; c < D; c += 16) {
                             uint32_t o[16];
                             tmem_ld16(o, to + c);
@@ -568,35 +555,31 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 }
                 // --- weights
                 float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t x[32], p[16];
-                    tmem_ld32(x, ts + 32 * q);
-                    tmem_wait_ld();
-                    ready(x, 32 * q);
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const float f = fg[2 * q + c / 8], v = vg[2 * q + c / 8] * inv_w;
-                        const float2 e = fma2(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), f, -r);
-                        const float2 z = make_float2(ex2(e.x), ex2(e.y));
-                        sum = add2(sum, z);
-                        const float2 y = mul2(z, make_float2(v, v));
-                        p[c] = pack_half2(y.x, y.y);
+                for (int g = 0; g < kGroups; ++g) {
+                    uint32_t p[8];
+                    const float fc = fg[g], v = vg[g] * inv_w;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        const uint32_t *z = &x[g / 2][g % 2 * 16 + 2 * c];
+                        const float2 e = fma2(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), fc, -r);
+                        const float2 y = make_float2(ex2(e.x), ex2(e.y));
+                        sum = add2(sum, y);
+                        const float2 m = mul2(y, make_float2(v, v));
+                        p[c] = pack_half2(m.x, m.y);
                     }
-                    tmem_st16(ts + 16 * q, p);  // over logits that have been read: half as many columns
-                    if (q & 1) {
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.p_ready[w][q >> 1]);
-                    }
+                    tmem_st8(here + 8 * g, p);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_ready[w]);
                 l += sum.x + sum.y;
             }
             f += n;
             if (!ok) break;
             if (mine > 0) {
-                ok = warp_wait_or_stop(&sh.o_done[w], mine_so_far++ & 1, stop);
+                ok = warp_wait_or_stop(&sh.pv_done[w], (sc - 1) & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -648,18 +631,17 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                        make_float4(mine > 0 && l != 0.f ? r : -INFINITY, mine > 0 ? l : 0.f, 0.f, 0.f));
             __syncwarp();
             const int from = ranges.of(first);
-            todo[1] = todo[0];
-            todo[0] = Share{at.b, at.h, at.p, from, ranges.of(first + at.steps - 1) - from + 1, 0};
             if (lane == 0)
-                todo[0].before = atomic_add_acq_rel_gpu(reinterpret_cast<int *>(ws) + from * 8 + warp, 1);
+                sh.todo[warp][shares] = Share{
+                    at.b, at.h, at.p, from, ranges.of(first + at.steps - 1) - from + 1,
+                    atomic_add_acq_rel_gpu(reinterpret_cast<int *>(ws) + from * 8 + warp, 1)};
+            ++shares;
         }
         // --- joins, by the last warp to arrive with these rows
 #pragma unroll 1
-        for (int i = 0; i < 2 && ok; ++i) {
-            const Share of = todo[0];
-            todo[0] = todo[1];
-            todo[1].parts = 0;
-            if (of.parts == 0) continue;
+        for (int i = 0; i < shares && ok; ++i) {
+            __syncwarp();
+            const Share of = sh.todo[warp][i];
             int last = 0;
             if (lane == 0) {
                 int *counter = reinterpret_cast<int *>(ws) + of.from * 8 + warp;
@@ -672,13 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 }
             }
             if (!__shfl_sync(~0u, last, 0)) continue;
-            if (row_in >= (start[of.out_b + 1] - start[of.out_b]) * group - of.p * kPair) continue;
+            if (row_in >= (start[of.b + 1] - start[of.b]) * group - of.p * kPair) continue;
             float high = -INFINITY;
 #pragma unroll 1
             for (int k = 0; k < of.parts; ++k)
                 high = fmaxf(high, __ldcg(&(record_of(of.from + k, k == 0) + (D / 4) * a.record_rows + row_in)->x));
             if (high == -INFINITY) high = 0.f;
-            const long long out_row = out_row_of(of.out_b, of.h, of.p);
+            const long long out_row = out_row_of(of.b, of.h, of.p);
             float sum = 0.f;
 #pragma unroll 1
             for (int c0 = 0; c0 < D / 4; c0 += 8) {
