@@ -39,8 +39,7 @@ constexpr int kThreads = 512;  // 8 warps of softmax, 4 of converters, 2 of prod
 constexpr int kQPlane = kRows * 128, kPlane = kKeys * 128;  // rows of 64 fp16, swizzled
 constexpr float kLag = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kStages = 4;  // of the rings of K and of V
-constexpr int kSlots = 8;   // of a step's scales
+constexpr int kStages = 4;  // of the ring of K and V
 
 template <int D>
 struct Cfg {
@@ -60,11 +59,10 @@ struct Share {
 struct Roles {
     Share todo[8][2];
     uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2], pv_done[2], o_free[2], drained[2];
-    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    // Of a step's keys: the logits' factor and the V scale.  They are written with its K, and
-    // read by its softmax.  Step j + 8's K waits for the scores of step j + 4, which come
-    // behind the softmax of step j + 2: no slot is written while it is read.
-    float f[kSlots][kGroups], v[kSlots][kGroups];
+    uint64_t full[kStages], empty[kStages];
+    // Of a step's keys: the logits' factor and the V scale; a stage is written again when the
+    // outputs of its step are done, and so its softmax.
+    float f[kStages][kGroups], v[kStages][kGroups];
     uint32_t tmem;
     int stop;
     int sums[kThreads / 32];
@@ -166,10 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             mbar_init(&sh.drained[t], 1);
         }
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sh.k_full[s], 4);
-            mbar_init(&sh.k_empty[s], 2);
-            mbar_init(&sh.v_full[s], 4);
-            mbar_init(&sh.v_empty[s], 2);
+            mbar_init(&sh.full[s], 4);
+            mbar_init(&sh.empty[s], 2);
         }
         sh.stop = 0;
         fence_barrier_init();
@@ -265,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             const uint32_t kv = smem_addr(base) + 2 * C::kQ, ts = tmem + 128 * w;
             const uint64_t qd = smem_desc(smem_addr(base) + w * C::kQ, 1024, 0);
             int f = 0, ss = 0, sc = 0, pc = 0;  // steps so far; this tile's scores, weights and pieces
-            bool ok = U0 == U1 || first_wait(&sh.k_full[0], 0, a.first_wait_polls, stop);
+            bool ok = U0 == U1 || first_wait(&sh.full[0], 0, a.first_wait_polls, stop);
 #pragma unroll 1
             for (int u = U0; ok && u < U1; at.next(t, a)) {
                 const int n = min(at.steps - at.j, U1 - u);  // steps of this piece, and of its tile
@@ -275,30 +271,28 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 for (int i = 0; i < n + 2; ++i) {  // outputs of step i - 2, scores of step i in their S's place
                     if (i >= 2) {
                         const int j = i - 2, vf = f + j;
-                        ok = wait_or_stop(&sh.v_full[vf % kStages], (vf / kStages) & 1, stop);
-                        if (ok && j < mine) {
+                        if (j < mine) {
                             if (j == 0 && pc > 0) ok = wait_or_stop(&sh.o_free[w], (pc - 1) & 1, stop);
                             ok = ok && wait_or_stop(&sh.p_ready[w], sc & 1, stop);
                             if (!ok) break;
                             tc_fence_after();
-                            const uint64_t vd = smem_desc(kv + (kStages + vf % kStages) * C::kHalf, 1024, kPlane);
+                            const uint64_t vd = smem_desc(kv + (2 * (vf % kStages) + 1) * C::kHalf, 1024, kPlane);
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; ++k)
                                 mma_ts(ts + 256, ts + 64 * (sc & 1) + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
                             mma_commit(&sh.pv_done[w]);
                             ++sc;
                         }
-                        if (!ok) break;
-                        mma_commit(&sh.v_empty[vf % kStages]);
+                        mma_commit(&sh.empty[vf % kStages]);
                     }
                     if (i < n) {
                         const int kf = f + i;
-                        ok = wait_or_stop(&sh.k_full[kf % kStages], (kf / kStages) & 1, stop);
+                        ok = wait_or_stop(&sh.full[kf % kStages], (kf / kStages) & 1, stop);
                         if (ok && i < mine) {
                             if (i == 0) ok = wait_or_stop(&sh.q_full[w], pc & 1, stop);
                             if (!ok) break;
                             tc_fence_after();
-                            const uint64_t kd = smem_desc(kv + (kf % kStages) * C::kHalf, 1024, 0);
+                            const uint64_t kd = smem_desc(kv + 2 * (kf % kStages) * C::kHalf, 1024, 0);
 #pragma unroll
                             for (int k = 0; k < 4 * C::kPlanes; ++k)
                                 mma_ss(ts + 64 * (ss & 1), qd + (k / 4) * (kQPlane / 16) + (k % 4) * 2,
@@ -310,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                             if (i + 1 == mine) mma_commit(&sh.q_empty[w]);
                         }
                         if (!ok) break;
-                        mma_commit(&sh.k_empty[kf % kStages]);
                     }
                 }
                 f += n;
@@ -399,8 +392,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                         make_uint4(q8_widen<KIND, 0>(c.z), q8_widen<KIND, 1>(c.z), q8_widen<KIND, 0>(c.w),
                                    q8_widen<KIND, 1>(c.w));
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
             };
             load(0, 0);
             load(1, 1);
@@ -416,14 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 constexpr int kLanes = D / 8, kQAt = 128 / kLanes;
                 const int tid = threadIdx.x & 127, piece = tid % kLanes;
                 const uint32_t dst = smem_addr(base) + tile * C::kQ + piece / 8 * kQPlane;
-#pragma unroll 1
+                const __half *q = static_cast<const __half *>(a.q) + start[at.b] * a.q_stride +
+                                  at.h * group * D + piece * 8;
+                const int row_at = at.p * kPair + tile * kRows, left = rows - tile * kRows;
+#pragma unroll 8
                 for (int i = tid / kLanes; i < kRows; i += kQAt) {
-                    const int r_of = at.p * kPair + tile * kRows + i, tok = Place::divided(r_of, a.by_group);
-                    const bool some = tile * kRows + i < rows;
-                    const __half *q = static_cast<const __half *>(a.q) +
-                                      (some ? (start[at.b] + tok) * a.q_stride + (at.h * group + r_of - tok * group) * D : 0);
+                    const int tok = Place::divided(row_at + i, a.by_group);
+                    const long long from = i < left ? tok * a.q_stride + (row_at + i - tok * group) * D : 0;
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + swizzled(i, piece % 8)),
-                                 "l"(q + piece * 8), "r"(some ? 16 : 0) : "memory");
+                                 "l"(q + from), "r"(i < left ? 16 : 0) : "memory");
                 }
             }
             if (!ok) break;
@@ -434,26 +426,23 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 for (int e = 0; e < 2; ++e) {
                     const int j = j0 + e, kf = f + j, s = kf % kStages;
                     if (j >= n || !ok) break;
-                    ok = warp_wait_or_stop(&sh.k_empty[s], ((kf / kStages) & 1) ^ 1, stop);
+                    ok = warp_wait_or_stop(&sh.empty[s], ((kf / kStages) & 1) ^ 1, stop);
                     if (!ok) break;
                     if (lane == 0) {  // keys behind the sequence have no scale of their own
                         const bool some = (at.j + j) * kKeys + w * 16 < L;
-                        sh.f[kf % kSlots][w] = some ? fmaxf(ks[e] * scale, 1e-30f) : 1e-30f;
-                        sh.v[kf % kSlots][w] = some ? vs[e] : 0.f;
+                        sh.f[s][w] = some ? fmaxf(ks[e] * scale, 1e-30f) : 1e-30f;
+                        sh.v[s][w] = some ? vs[e] : 0.f;
                     }
-                    widen(xk[e], j, ring + s * C::kHalf);
-                    if (lane == 0) mbar_arrive(&sh.k_full[s]);
+                    widen(xk[e], j, ring + 2 * s * C::kHalf);
+                    widen(xv[e], j, ring + (2 * s + 1) * C::kHalf);
+                    if (queries) asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.full[s]);
                     if (queries) {
                         queries = false;
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        fence_proxy_async_smem();
-                        __syncwarp();
                         if (lane < 2 && min(at.steps_of_tile(t, a, lane) - at.j, n) > 0) mbar_arrive(&sh.q_full[lane]);
                     }
-                    ok = warp_wait_or_stop(&sh.v_empty[s], ((kf / kStages) & 1) ^ 1, stop);
-                    if (!ok) break;
-                    widen(xv[e], j, ring + (kStages + s) * C::kHalf);
-                    if (lane == 0) mbar_arrive(&sh.v_full[s]);
                     load(e, j + 2);
                 }
             }
@@ -489,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             float r = 0.f, l = 0.f, wv = 0.f, inv_w = 0.f;
 #pragma unroll 1
             for (int j = 0; j < mine; ++j, ++sc) {
-                const int slot = (f + j) % kSlots;
+                const int slot = (f + j) % kStages;
                 const uint32_t here = ts + 64 * (sc & 1);
                 ok = warp_wait_or_stop(&sh.s_full[w][sc & 1], (sc >> 1) & 1, stop);
                 if (!ok) break;
