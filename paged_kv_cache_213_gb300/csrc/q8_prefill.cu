@@ -58,7 +58,12 @@ struct Share {
 
 struct Roles {
     Share todo[8][2];
-    uint64_t q_full[2], q_empty[2], s_full[2][2], p_ready[2], pv_done[2], o_free[2], drained[2];
+    uint64_t q_full[2], q_empty[2], o_free[2], drained[2];
+    // Of a tile's even and odd steps.  With the scores two steps ahead, a warp of softmax may be
+    // a step ahead of the others, whose arrivals it must not make up for, and done with a
+    // step when the outputs of the one before are not: a wait that names its phase by
+    // parity alone would take them for the step's own.
+    uint64_t s_full[2][2], p_ready[2][2], pv_done[2][2];
     uint64_t full[kStages], empty[kStages];
     // Of a step's keys: the logits' factor and the V scale; a stage is written again when the
     // outputs of its step are done, and so its softmax.
@@ -159,8 +164,10 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             mbar_init(&sh.s_full[t][0], 2);
             mbar_init(&sh.s_full[t][1], 2);
             mbar_init(&sh.o_free[t], 4);
-            mbar_init(&sh.p_ready[t], 4);
-            mbar_init(&sh.pv_done[t], 1);
+            mbar_init(&sh.p_ready[t][0], 4);
+            mbar_init(&sh.p_ready[t][1], 4);
+            mbar_init(&sh.pv_done[t][0], 1);
+            mbar_init(&sh.pv_done[t][1], 1);
             mbar_init(&sh.drained[t], 1);
         }
         for (int s = 0; s < kStages; ++s) {
@@ -273,14 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                         const int j = i - 2, vf = f + j;
                         if (j < mine) {
                             if (j == 0 && pc > 0) ok = wait_or_stop(&sh.o_free[w], (pc - 1) & 1, stop);
-                            ok = ok && wait_or_stop(&sh.p_ready[w], sc & 1, stop);
+                            ok = ok && wait_or_stop(&sh.p_ready[w][sc & 1], (sc >> 1) & 1, stop);
                             if (!ok) break;
                             tc_fence_after();
                             const uint64_t vd = smem_desc(kv + (2 * (vf % kStages) + 1) * C::kHalf, 1024, kPlane);
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; ++k)
                                 mma_ts(ts + 256, ts + 64 * (sc & 1) + 8 * k, vd + k * 128, dpv, j > 0 || k > 0);
-                            mma_commit(&sh.pv_done[w]);
+                            mma_commit(&sh.pv_done[w][sc & 1]);
                             ++sc;
                         }
                         mma_commit(&sh.empty[vf % kStages]);
@@ -528,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                         r = next;
                         l *= g;
                         fac *= g;
-                        ok = warp_wait_or_stop(&sh.pv_done[w], (sc - 1) & 1, stop);  // the outputs so far
+                        ok = warp_wait_or_stop(&sh.pv_done[w][(sc - 1) & 1], ((sc - 1) >> 1) & 1, stop);  // the outputs so far
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -562,13 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[w]);
+                if (lane == 0) mbar_arrive(&sh.p_ready[w][sc & 1]);
                 l += sum.x + sum.y;
             }
             f += n;
             if (!ok) break;
             if (mine > 0) {
-                ok = warp_wait_or_stop(&sh.pv_done[w], (sc - 1) & 1, stop);
+                ok = warp_wait_or_stop(&sh.pv_done[w][(sc - 1) & 1], ((sc - 1) >> 1) & 1, stop);
                 if (!ok) break;
                 tc_fence_after();
             }
@@ -588,8 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                         if (lane == 0) mbar_arrive(&sh.o_free[w]);
                     }
                 }
-                if (!valid) continue;
-                if (whole) {
+                if (valid && whole) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         uint32_t z[4];
@@ -599,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                                               __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
                         out[c / 8 + e] = make_uint4(z[0], z[1], z[2], z[3]);
                     }
-                } else {
+                } else if (valid) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         __stcg(rec + (c / 4 + e) * a.record_rows,
@@ -608,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                                                       __uint_as_float(o[4 * e + 3]) * wv)
                                         : make_float4(0.f, 0.f, 0.f, 0.f));
                 }
+                __syncwarp();  // the next load is the whole warp's
             }
             if (whole) {
                 if (a.lse_out && valid)
