@@ -75,7 +75,7 @@ struct Q8AttentionArgs {
     float scale_log2;  // scale * log2(e), either sign
     int n_q_heads, n_kv_heads, head_dim, block_size, max_context_len;
     Q8Divide by_group;  // query heads of a KV head
-    int record_rows;    // of Q8Split
+    int record_rows, tile_tokens;  // of Q8Split
     void *workspace;
     float *lse_out;
     int32_t *err;
@@ -87,6 +87,7 @@ struct Q8Split {
     int row_tiles;  // 0: the kernel of q8_prefill.cu
     int ctas;
     int record_rows;  // query rows that a segment has at most
+    int tile_tokens;  // of q8_prefill.cu: tokens of a tile of 128 rows
     size_t ws_bytes;
 };
 // false: more than 2^31 units of work.

@@ -198,6 +198,7 @@ int paged_decode_attention_q8(void *out, const void *q, int64_t q_stride, const 
     a.max_context_len = plan.max_len;
     a.by_group = pkv::q8_divide_by(n_q_heads / n_kv_heads);
     a.record_rows = plan.split.record_rows;
+    a.tile_tokens = plan.split.tile_tokens;
     a.workspace = workspace;
     a.lse_out = lse_out;
     a.err = err_word;

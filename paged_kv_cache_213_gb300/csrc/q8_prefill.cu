@@ -19,9 +19,9 @@
 //
 // Split.  The (sequence, head, pair of tiles, step) units are cut into equal ranges, one
 // per SM; items that several CTAs hold leave records, and the last to arrive joins them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
-
-#include <atomic>
 
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
@@ -30,12 +30,15 @@
 #include "tc05.cuh"
 
 namespace pkv {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
 namespace {
 
 constexpr int kRows = 128, kKeys = 64;  // of a tile, of a step
 constexpr int kPair = 2 * kRows;
 constexpr int kGroups = kKeys / 16;      // pieces of 16 keys, each of one block
-constexpr int kThreads = 512;  // 8 warps of softmax, 4 of converters, 2 of products and 2 idle ones
+constexpr int kThreads = 512;  // 8 warps of softmax, 4 of converters, 2 of products, 1 of queries, an idle one
 constexpr int kQPlane = kRows * 128, kPlane = kKeys * 128;  // rows of 64 fp16, swizzled
 constexpr float kLag = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -69,6 +72,7 @@ struct Roles {
     // outputs of its step are done, and so its softmax.
     float f[kStages][kGroups], v[kStages][kGroups];
     uint32_t tmem;
+    int queries[2];  // tiles of queries copied
     int stop;
     int sums[kThreads / 32];
 };
@@ -82,19 +86,16 @@ struct Place {
     int b, h, p, j;
     int steps;  // of the pair
 
-    // Keys that the rows up to `row` of the sequence attend.
-    static __device__ int keys(const Batch &t, const Q8AttentionArgs &a, int b, int row) {
+    // Keys that the tokens of the sequence up to number `tok` attend.
+    static __device__ int keys(const Batch &t, int b, int tok) {
         const int n = t.start[b + 1] - t.start[b];
-        return t.len[b] - n + 1 + min(divided(row, a.by_group), n - 1);
+        return t.len[b] - n + 1 + min(tok, n - 1);
     }
     static __device__ int steps_of(const Batch &t, const Q8AttentionArgs &a, int b, int p) {
-        return (keys(t, a, b, p * kPair + kPair - 1) + kKeys - 1) / kKeys;
+        return (keys(t, b, 2 * (p + 1) * a.tile_tokens - 1) + kKeys - 1) / kKeys;
     }
     static __device__ int pairs(const Batch &t, const Q8AttentionArgs &a, int b) {
-        return ((t.start[b + 1] - t.start[b]) * (a.n_q_heads / a.n_kv_heads) + kPair - 1) / kPair;
-    }
-    static __device__ int divided(int x, const Q8Divide &d) {
-        return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(x)) * d.mul >> d.shift);
+        return (t.start[b + 1] - t.start[b] + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
     }
     __device__ void find(const Batch &t, const Q8AttentionArgs &a, int u) {
         int lo = 0, hi = a.num_seqs;  // cum[lo] <= u < cum[hi]
@@ -128,9 +129,9 @@ struct Place {
     }
     // The steps of tile t of the pair; 0: it has no rows.
     __device__ int steps_of_tile(const Batch &t, const Q8AttentionArgs &a, int tile) const {
-        const int row = p * kPair + tile * kRows;
-        if (row >= (t.start[b + 1] - t.start[b]) * (a.n_q_heads / a.n_kv_heads)) return 0;
-        return (keys(t, a, b, row + kRows - 1) + kKeys - 1) / kKeys;
+        const int tok = (2 * p + tile) * a.tile_tokens;
+        if (tok >= t.start[b + 1] - t.start[b]) return 0;
+        return (keys(t, b, tok + a.tile_tokens - 1) + kKeys - 1) / kKeys;
     }
 };
 
@@ -145,11 +146,16 @@ struct Ranges {
     }
 };
 
+__device__ __forceinline__ int divided(int x, const Q8Divide &d) {
+    return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(x)) * d.mul >> d.shift);
+}
+
 // A piece of 16 bytes in the products' layout: row `row` of a plane, piece q of 8.
 __device__ __forceinline__ int swizzled(int row, int q) { return row * 128 + ((q ^ (row & 7)) << 4); }
 
 template <int KIND, int D>
-__global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8AttentionArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8AttentionArgs a,
+                                                                const __grid_constant__ CUtensorMap q_map) {
     using C = Cfg<D>;
     extern __shared__ __align__(1024) unsigned char base[];
     __shared__ __align__(16) Roles sh;
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
 
     if (threadIdx.x == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&sh.q_full[t], 4);
+            mbar_init(&sh.q_full[t], 1);
             mbar_init(&sh.q_empty[t], 1);
             mbar_init(&sh.s_full[t][0], 2);
             mbar_init(&sh.s_full[t][1], 2);
@@ -174,10 +180,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             mbar_init(&sh.full[s], 4);
             mbar_init(&sh.empty[s], 2);
         }
-        sh.stop = 0;
+        sh.stop = sh.queries[0] = sh.queries[1] = 0;
         fence_barrier_init();
     }
     if (warp == 12) tmem_alloc(&sh.tmem, 512);
+    if (threadIdx.x == 0) prefetch_tmap(&q_map);
     tc_fence_before();
     grid_dependency_wait();
     allow_dependent_launch();
@@ -209,10 +216,9 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         __syncthreads();
         int units = 0;
         if (n > 0) {
-            const int pairs = (n * group + kPair - 1) / kPair;
 #pragma unroll 1
-            for (int p = 0; p < pairs; ++p)
-                units += (len[b] - n + kKeys + min(Place::divided(p * kPair + kPair - 1, a.by_group), n - 1)) / kKeys;
+            for (int tok = 0; tok < n; tok += 2 * a.tile_tokens)
+                units += (len[b] - n + kKeys + min(tok + 2 * a.tile_tokens, n) - 1) / kKeys;
             units *= a.n_kv_heads;
         }
         int upto = units;
@@ -260,7 +266,34 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
     Place at{};
     if (U0 < U1) at.find(t, a, U0);
 
-    if (warp >= 12) {
+    if (warp == 14) {
+        // --- queries: a box of a tile's tokens and heads for each 64 columns.  Their place is
+        // free when the scores of the tile's piece before are done
+        if (elect_one()) {
+            const int tokens = a.tile_tokens, bytes = C::kPlanes * tokens * group * 128;
+            int pc[2] = {0, 0};
+            bool ok = true;
+#pragma unroll 1
+            for (int u = U0; ok && u < U1; at.next(t, a)) {
+                const int n = min(at.steps - at.j, U1 - u);
+                u += n;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (!ok || min(at.steps_of_tile(t, a, w) - at.j, n) <= 0) continue;
+                    ok = wait_or_stop(&sh.q_empty[w], (pc[w] & 1) ^ 1, stop);
+                    if (!ok) break;
+                    ++pc[w];
+                    mbar_arrive_expect_tx(&sh.q_full[w], bytes);
+#pragma unroll
+                    for (int p = 0; p < C::kPlanes; ++p)
+                        tma_load_3d(base + w * C::kQ + p * kQPlane, &q_map, 64 * p, at.h * group,
+                                    start[at.b] + (2 * at.p + w) * tokens, &sh.q_full[w]);
+                }
+            }
+            sh.queries[0] = pc[0];
+            sh.queries[1] = pc[1];
+        }
+    } else if (warp >= 12) {
         // --- products ---
         if (warp < 14 && elect_one()) {
             const int w = warp - 12;  // the tile
@@ -341,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 to[i][e] = plane * kPlane + swizzled(w * 16 + (i * kAt & 7) + row0, 2 * x4 + e);
         const float scale = fmaxf(fabsf(a.scale_log2), 1e-30f);
         unsigned char *ring = base + 2 * C::kQ;
-        int f = 0, pieces_of[2] = {0, 0};  // steps so far, pieces of a tile
+        int f = 0;  // steps so far
         bool ok = true;
 #pragma unroll 1
         for (int u = U0; ok && u < U1; at.next(t, a)) {
@@ -402,31 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             };
             load(0, 0);
             load(1, 1);
-            // the queries, 16 bytes a lane: their place is free when the scores of the tile's
-            // piece before are done
-            const int rows = (start[at.b + 1] - start[at.b]) * group - at.p * kPair;  // from the pair on
-#pragma unroll 1
-            for (int tile = 0; tile < 2 && ok; ++tile) {
-                if (min(at.steps_of_tile(t, a, tile) - at.j, n) <= 0) continue;
-                ok = warp_wait_or_stop(&sh.q_empty[tile], (pieces_of[tile] & 1) ^ 1, stop);
-                if (!ok) break;
-                if (tile) ++pieces_of[1]; else ++pieces_of[0];
-                constexpr int kLanes = D / 8, kQAt = 128 / kLanes;
-                const int tid = threadIdx.x & 127, piece = tid % kLanes;
-                const uint32_t dst = smem_addr(base) + tile * C::kQ + piece / 8 * kQPlane;
-                const __half *q = static_cast<const __half *>(a.q) + start[at.b] * a.q_stride +
-                                  at.h * group * D + piece * 8;
-                const int row_at = at.p * kPair + tile * kRows, left = rows - tile * kRows;
-#pragma unroll 8
-                for (int i = tid / kLanes; i < kRows; i += kQAt) {
-                    const int tok = Place::divided(row_at + i, a.by_group);
-                    const long long from = i < left ? tok * a.q_stride + (row_at + i - tok * group) * D : 0;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + swizzled(i, piece % 8)),
-                                 "l"(q + from), "r"(i < left ? 16 : 0) : "memory");
-                }
-            }
-            if (!ok) break;
-            bool queries = true;  // still to be announced
 #pragma unroll 1
             for (int j0 = 0; j0 < n && ok; j0 += 2) {
 #pragma unroll
@@ -442,26 +450,24 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     }
                     widen(xk[e], j, ring + 2 * s * C::kHalf);
                     widen(xv[e], j, ring + (2 * s + 1) * C::kHalf);
-                    if (queries) asm volatile("cp.async.wait_all;" ::: "memory");
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.full[s]);
-                    if (queries) {
-                        queries = false;
-                        if (lane < 2 && min(at.steps_of_tile(t, a, lane) - at.j, n) > 0) mbar_arrive(&sh.q_full[lane]);
-                    }
                     load(e, j + 2);
                 }
             }
             f += n;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
         // --- softmax, results ---
         const int w = warp >> 2;  // the tile
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 * (warp % 4) << 16
         const uint32_t ts = tmem + 128 * w + lanes, to = tmem + 256 + 128 * w + lanes;
         const int row_in = w * kRows + (threadIdx.x & 127);  // of the pair
+        // its token among the pair's, and its head in the group; rows behind the tile's tokens
+        // (where the group does not divide 128) are no token's
+        const int tok_in = divided(threadIdx.x & 127, a.by_group), head_in = (threadIdx.x & 127) - tok_in * group;
+        const int row_tok = tok_in < a.tile_tokens ? w * a.tile_tokens + tok_in : 1 << 29;
         unsigned char *ws = static_cast<unsigned char *>(a.workspace);
         // records: float4 [D / 4][record_rows], then reference and sum of each row
         auto record_of = [&](int of_cta, int side) {
@@ -469,8 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                    (2ll * of_cta + side) * (D / 4 + 1) * a.record_rows;
         };
         auto out_row_of = [&](int b, int h, int p) {  // this thread's
-            const int row = p * kPair + row_in, tok = Place::divided(row, a.by_group);
-            return static_cast<long long>(start[b] + tok) * a.n_q_heads + h * group + (row - tok * group);
+            return static_cast<long long>(start[b] + 2 * p * a.tile_tokens + row_tok) * a.n_q_heads + h * group + head_in;
         };
         int shares = 0;
         int f = 0, sc = 0;
@@ -480,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             const int first = u - at.j, n = min(at.steps - at.j, U1 - u);
             const int mine = max(0, min(at.steps_of_tile(t, a, w) - at.j, n));
             u += n;
-            const int rows = (start[at.b + 1] - start[at.b]) * group - at.p * kPair;  // from the pair on
-            const int seen = Place::keys(t, a, at.b, at.p * kPair + row_in);
+            const int tokens = start[at.b + 1] - start[at.b] - 2 * at.p * a.tile_tokens;  // from the pair on
+            const int seen = Place::keys(t, at.b, 2 * at.p * a.tile_tokens + row_tok);
             float r = 0.f, l = 0.f, wv = 0.f, inv_w = 0.f;
 #pragma unroll 1
             for (int j = 0; j < mine; ++j, ++sc) {
@@ -579,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 if (!ok) break;
                 tc_fence_after();
             }
-            const bool whole = first >= U0 && first + at.steps <= U1, valid = row_in < rows;
+            const bool whole = first >= U0 && first + at.steps <= U1, valid = row_tok < tokens;
             const float inv = wv / l;
             uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row_of(at.b, at.h, at.p) * D);
             float4 *rec = record_of(cta, first >= U0) + row_in;
@@ -621,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     a.lse_out[out_row_of(at.b, at.h, at.p)] = (r + log2f(l)) * kLn2;
                 continue;
             }
-            if (row_in - lane >= rows) continue;  // none of the warp's rows is one
+            if (!__any_sync(~0u, valid)) continue;
             if (valid)
                 __stcg(rec + (D / 4) * a.record_rows,
                        make_float4(mine > 0 && l != 0.f ? r : -INFINITY, mine > 0 ? l : 0.f, 0.f, 0.f));
@@ -650,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 }
             }
             if (!__shfl_sync(~0u, last, 0)) continue;
-            if (row_in >= (start[of.b + 1] - start[of.b]) * group - of.p * kPair) continue;
+            if (row_tok >= start[of.b + 1] - start[of.b] - 2 * of.p * a.tile_tokens) continue;
             float high = -INFINITY;
 #pragma unroll 1
             for (int k = 0; k < of.parts; ++k)
@@ -665,20 +670,28 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
                 sum = 0.f;
 #pragma unroll 1
-                for (int k = 0; k < of.parts; ++k) {
-                    const float4 *part = record_of(of.from + k, k == 0) + row_in;
-                    float4 z[8];
+                for (int k0 = 0; k0 < of.parts; k0 += 2) {  // the loads of two parts go out together
+                    float4 z[2][8];
+                    float2 ml[2];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[e] = __ldcg(part + (c0 + e) * a.record_rows);
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part + (D / 4) * a.record_rows));
-                    const float g = ex2(ml.x - high);
-                    sum += g * ml.y;
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 *part = record_of(of.from + min(k0 + k, of.parts - 1), k0 + k == 0) + row_in;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        acc[e].x += g * z[e].x;
-                        acc[e].y += g * z[e].y;
-                        acc[e].z += g * z[e].z;
-                        acc[e].w += g * z[e].w;
+                        for (int e = 0; e < 8; ++e) z[k][e] = __ldcg(part + (c0 + e) * a.record_rows);
+                        ml[k] = __ldcg(reinterpret_cast<const float2 *>(part + (D / 4) * a.record_rows));
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (k0 + k >= of.parts) continue;
+                        const float g = ex2(ml[k].x - high);
+                        sum += g * ml[k].y;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            acc[e].x += g * z[k][e].x;
+                            acc[e].y += g * z[k][e].y;
+                            acc[e].z += g * z[k][e].z;
+                            acc[e].w += g * z[k][e].w;
+                        }
                     }
                 }
                 const float inv = 1.f / sum;
@@ -696,7 +709,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
     tc_fence_before();
     __syncwarp();
     __syncthreads();
-    if (threadIdx.x == 0 && sh.stop) flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+    if (threadIdx.x == 0 && sh.stop) {
+        flag_error(a.err, PKV_ERRBIT_TIMEOUT);
+        // every copy in flight lands before the CTA gives its memory back
+        for (int w = 0; w < 2; ++w)
+            if (sh.queries[w] > 0) mbar_wait_bounded(&sh.q_full[w], (sh.queries[w] - 1) & 1);
+    }
+    __syncwarp();
     if (warp == 12) tmem_free(tmem, 512);
 }
 
@@ -707,7 +726,18 @@ cudaError_t launch(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t str
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(sp.ctas), dim3(kThreads), smem, stream, a);
+    CUtensorMap q_map;
+    auto fn = encode_fn();
+    const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(a.n_q_heads), static_cast<cuuint64_t>(a.total_q)};
+    const cuuint64_t strides[2] = {D * 2, static_cast<cuuint64_t>(a.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.n_q_heads / a.n_kv_heads),
+                               static_cast<cuuint32_t>(a.tile_tokens)};
+    const cuuint32_t one[3] = {1, 1, 1};
+    if (!fn || fn(&q_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, one,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorNotSupported;
+    return launch_pdl(kern, dim3(sp.ctas), dim3(kThreads), smem, stream, a, q_map);
 }
 
 static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 1024, "shared memory");
@@ -717,13 +747,16 @@ static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 1024, "shared memory");
 // The same plan as q8_split for the kernel of this file.
 bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
                       int sms, Q8Split *sp) {
-    const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
+    const int group = n_q_heads / n_kv_heads;
+    if (group > kRows) return false;
+    sp->tile_tokens = kRows / group;
     const double steps = (static_cast<double>(max_len) + kKeys - 1) / kKeys + 1;
-    if (static_cast<double>(num_seqs) * n_kv_heads * ((rows + kPair - 1) / kPair) * steps >= 2147483648.0)
-        return false;
+    const double pairs = static_cast<double>(max_q_len) / (2 * sp->tile_tokens) + 1;
+    if (static_cast<double>(num_seqs) * n_kv_heads * pairs * steps >= 2147483648.0) return false;
     sp->row_tiles = 0;
     sp->ctas = sms < kBalancedMaxWorkers / 8 ? sms : kBalancedMaxWorkers / 8;  // a counter for each warp of rows
-    sp->record_rows = static_cast<int>(rows < kPair ? (rows + 31) / 32 * 32 : kPair);
+    // rows of a pair that may be some: those of one tile, or of both
+    sp->record_rows = max_q_len > sp->tile_tokens ? kPair : (max_q_len * group + 31) / 32 * 32;
     sp->ws_bytes = kBalancedCounterBytes +
                    static_cast<size_t>(sp->ctas) * 2 * (head_dim / 4 + 1) * sp->record_rows * sizeof(float4);
     return true;
