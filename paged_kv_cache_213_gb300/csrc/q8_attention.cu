@@ -1,5 +1,5 @@
-// q8_attention.cu -- attention over the 8-bit caches with block scales
-// (paged_decode_attention_q8).
+// q8_attention.cu -- attention over the 8-bit caches with block scales for up to 32 query
+// rows of a KV head: decode, few drafts (paged_decode_attention_q8).
 //
 // Mathematics.  For the query rows of one KV head (tokens x heads of its group) and a
 // tile of 16 cached tokens of one block, with codes K, V and the block's scales k, v:
@@ -23,10 +23,10 @@
 // swizzle or barrier, was bound by the cycle that each 32-byte sector takes on its way
 // into shared memory: 8 x 32k tokens 110 us.)
 //
-// Split.  The (sequence, head, row tile, 16-token tile) units are cut into equal ranges
-// for the warps of one CTA per SM.  The parts of a segment (sequence, head, row tile)
-// that several warps of a CTA hold are joined there; CTAs that share a segment leave a
-// record each, and the last to arrive joins them, in the order of the tokens.
+// Split.  The (sequence, head, 16-token tile) units are cut into equal ranges for the
+// warps of one CTA per SM.  The parts of a segment (sequence, head) that several warps of
+// a CTA hold are joined there; CTAs that share a segment leave a record each, and the
+// last to arrive joins them, in the order of the tokens.
 #include <cuda_fp16.h>
 
 #include "pkv_internal.h"
@@ -34,9 +34,6 @@
 #include "q8.h"
 #include "q8_codes.cuh"
 
-#ifndef PFMIN
-#define PFMIN 24
-#endif
 namespace pkv {
 namespace {
 
@@ -122,12 +119,12 @@ struct Batch {
 
 // One segment, with the warp's place in it.
 struct Segment {
-    int b, h, rt;          // sequence, KV head, row tile
-    int tiles, row_tiles;  // of the sequence
-    int j;                 // 16-token tile
+    int b, h;   // sequence, KV head
+    int tiles;  // of the sequence
+    int j;      // 16-token tile
 
     // The unit u of the batch.
-    __device__ void find(const Batch &t, const Q8AttentionArgs &a, int rows, int group, int u) {
+    __device__ void find(const Batch &t, const Q8AttentionArgs &a, int u) {
         int lo = 0, hi = a.num_seqs;  // cum[lo] <= u < cum[hi]
 #pragma unroll 1
         while (hi - lo > 1) {
@@ -135,28 +132,20 @@ struct Segment {
             if (t.cum[mid] <= u) lo = mid; else hi = mid;
         }
         b = lo;
-        sizes(t, rows, group);
-        int r = u - t.cum[b];
-        const int q = r / tiles;
-        j = r - q * tiles;
-        h = q / row_tiles;
-        rt = q - h * row_tiles;
-    }
-    __device__ __forceinline__ void sizes(const Batch &t, int rows, int group) {
         tiles = (t.len[b] + kTile - 1) / kTile;
-        row_tiles = ((t.start[b + 1] - t.start[b]) * group + rows - 1) / rows;
+        j = u - t.cum[b];
+        h = j / tiles;
+        j -= h * tiles;
     }
     // The next unit; true when it is another segment's first.
-    __device__ bool next(const Batch &t, const Q8AttentionArgs &a, int rows, int group) {
+    __device__ bool next(const Batch &t, const Q8AttentionArgs &a) {
         if (++j < tiles) return false;
         j = 0;
-        if (++rt < row_tiles) return true;
-        rt = 0;
         if (++h < a.n_kv_heads) return true;
         h = 0;
 #pragma unroll 1
         do ++b; while (b < a.num_seqs && t.cum[b + 1] == t.cum[b]);
-        if (b < a.num_seqs) sizes(t, rows, group);
+        if (b < a.num_seqs) tiles = (t.len[b] + kTile - 1) / kTile;
         return true;
     }
     // The unit at which the segment starts, given that u is its unit j.
@@ -164,9 +153,9 @@ struct Segment {
 };
 
 // The cache tile (number of 16-row pieces) of unit u; bad blocks flag and become tile 0.
-__device__ __forceinline__ unsigned tile_of(const Batch &t, const Q8AttentionArgs &a, int rows, int group,
-                                            int bs16_log2, int u, Segment &s) {
-    s.find(t, a, rows, group, u);
+__device__ __forceinline__ unsigned tile_of(const Batch &t, const Q8AttentionArgs &a, int bs16_log2, int u,
+                                            Segment &s) {
+    s.find(t, a, u);
     const int block = s.j >> bs16_log2;
     const int id = a.block_tables[static_cast<long long>(s.b) * a.max_blocks_per_seq + block];
     if (id < 0 || id >= a.num_blocks) {
@@ -176,14 +165,14 @@ __device__ __forceinline__ unsigned tile_of(const Batch &t, const Q8AttentionArg
     return (static_cast<unsigned>(id) * a.n_kv_heads + s.h << bs16_log2) + (s.j & ((1 << bs16_log2) - 1));
 }
 
-// Where query row `row` of a segment's row tile lies, as a multiple of head_dim in out;
-// -1: the tile's rows end before it.
-__device__ __forceinline__ long long row_at(const Batch &t, const Q8AttentionArgs &a, const Segment &s,
-                                            int rows, int group, int row, int *token) {
-    const int r = s.rt * rows + row, i = divided(r, a.by_group);
+// Where query row `row` of a segment lies, as a multiple of head_dim in out; -1: its rows end
+// before it.
+__device__ __forceinline__ long long row_at(const Batch &t, const Q8AttentionArgs &a, int b, int h, int group,
+                                            int row, int *token) {
+    const int i = divided(row, a.by_group);
     *token = i;
-    if (i >= t.start[s.b + 1] - t.start[s.b]) return -1;
-    return static_cast<long long>(t.start[s.b] + i) * a.n_q_heads + s.h * group + (r - i * group);
+    if (i >= t.start[b + 1] - t.start[b]) return -1;
+    return static_cast<long long>(t.start[b] + i) * a.n_q_heads + h * group + (row - i * group);
 }
 
 // A row of a segment joined by 8 lanes: lane i of them holds the columns 32 k + 4 i on.
@@ -246,7 +235,7 @@ __device__ __forceinline__ float2 load_fresh2(const float *p) {
 // What a warp leaves of a segment that it holds a part of.
 struct Piece {
     int first, end;  // the segment's units; first -1: none
-    int b, h, rt;
+    int b, h;
     int in_ring;     // the record is in the warp's shared memory, else in the workspace
 };
 
@@ -297,7 +286,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
             const bool ok = n >= 0 && n <= a.max_q_len && n <= l && s >= 0 && s + n <= a.total_q &&
                             l <= a.max_context_len;
             if (!ok && blockIdx.x == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
-            if (ok) units = (l + kTile - 1) / kTile * ((n * group + kRows - 1) / kRows) * a.n_kv_heads;
+            if (ok) units = n > 0 ? (l + kTile - 1) / kTile * a.n_kv_heads : 0;
             len[b] = l;
             start[b] = s;
             if (b == a.num_seqs - 1) start[b + 1] = s + n;
@@ -337,13 +326,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
     int base = u0;
     unsigned tiles_now = 0, tiles_next = 0;
     Segment seg{};  // of unit u0: lane 0's, for all
-    if (u0 + lane < u1) tiles_now = tile_of(t, a, kRows, group, bs16_log2, u0 + lane, seg);
+    if (u0 + lane < u1) tiles_now = tile_of(t, a, bs16_log2, u0 + lane, seg);
     seg.b = __shfl_sync(~0u, seg.b, 0);
     seg.h = __shfl_sync(~0u, seg.h, 0);
-    seg.rt = __shfl_sync(~0u, seg.rt, 0);
     seg.j = __shfl_sync(~0u, seg.j, 0);
     seg.tiles = __shfl_sync(~0u, seg.tiles, 0);
-    seg.row_tiles = __shfl_sync(~0u, seg.row_tiles, 0);
     if (a.tables_ready) {
         grid_dependency_wait();
         allow_dependent_launch();
@@ -387,15 +374,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
             if (pu > u0) copy_tile(lane == 0, tile, pstage);
             if (pu == base && base + 32 + lane < u1) {
                 Segment any;
-                tiles_next = tile_of(t, a, kRows, group, bs16_log2, base + 32 + lane, any);
+                tiles_next = tile_of(t, a, bs16_log2, base + 32 + lane, any);
             }
             if (pfirst) {
                 const uint32_t dst = smem_addr(mine) + S::kQ + pq * S::kQBytes + lane * 16;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     int token;
-                    const long long row = row_at(t, a, ahead, kRows, group, nt * 8 + r, &token);
-                    const int head = ahead.h * group + (ahead.rt * kRows + nt * 8 + r - token * group);
+                    const long long row = row_at(t, a, ahead.b, ahead.h, group, nt * 8 + r, &token);
+                    const int head = ahead.h * group + (nt * 8 + r - token * group);
                     const __half *q = static_cast<const __half *>(a.q) +
                                       (row < 0 ? 0 : (t.start[ahead.b] + token) * a.q_stride + head * D) + c * (D / 4);
 #pragma unroll
@@ -407,7 +394,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                 ++pending;
             }
             ++pu;
-            pfirst = ahead.next(t, a, kRows, group);
+            pfirst = ahead.next(t, a);
             pstage = pstage + 1 == S::kStages ? 0 : pstage + 1;
         }
     };
@@ -463,10 +450,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
             for (int i = 0; i < 2; ++i) {
                 l[nt][i] = 0.f;
                 m[nt][i] = -INFINITY;
-                limit[nt][i] = L - n + 1 + min(divided(seg.rt * kRows + nt * 8 + 2 * c + i, a.by_group), n - 1);
+                limit[nt][i] = L - n + 1 + min(divided(nt * 8 + 2 * c + i, a.by_group), n - 1);
             }
         }
-        const int least = L - n + 1 + divided(seg.rt * kRows, a.by_group);  // of the tile's first row
+        const int least = L - n + 1;  // of the first row
         float w = 0.f, inv_w = 0.f;
         const unsigned char *qp = mine + S::kQ + qplace * S::kQBytes + lane * 16;
         qplace ^= 1;
@@ -658,7 +645,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     int token;
-                    const long long row = row_at(t, a, seg, kRows, group, nt * 8 + 2 * c + i, &token);
+                    const long long row = row_at(t, a, seg.b, seg.h, group, nt * 8 + 2 * c + i, &token);
                     if (row < 0) continue;
                     const float z = w / l[nt][i];
                     __half *dst = static_cast<__half *>(a.out) + row * D + r * S::kVPiece;
@@ -674,7 +661,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
         } else {
             // --- a part.  The last thing that the warp does takes its shared memory (no copy
             // is in flight any more); what it goes on after goes to the workspace
-            const int valid = min(kRows, n * group - seg.rt * kRows);
+            const int valid = n * group;
             __syncwarp();
             float *rec = end == u1 ? reinterpret_cast<float *>(mine) : record_of(cta, warp);
 #pragma unroll
@@ -692,11 +679,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                         *reinterpret_cast<float2 *>(rec + a.record_rows * D + 2 * row) = make_float2(m[nt][i], l[nt][i]);
                 }
             if (lane == 0)
-                pieces[2 * warp + (seg_first >= u0)] = Piece{seg_first, seg_end, seg.b, seg.h, seg.rt, end == u1};
+                pieces[2 * warp + (seg_first >= u0)] = Piece{seg_first, seg_end, seg.b, seg.h, end == u1};
         }
         if (u < u1) {
             seg.j = seg.tiles - 1;
-            seg.next(t, a, kRows, group);
+            seg.next(t, a);
         }
     }
     __syncthreads();
@@ -721,10 +708,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
         const unsigned rest = of & (of - 1);
         unsigned members = there & (rest ? (rest & -rest) - 1 : ~0u) & ~((1u << head) - 1);
         const Piece at = pieces[head];
-        seg.b = at.b;
-        seg.h = at.h;
-        seg.rt = at.rt;
-        const int valid = min(kRows, (start[seg.b + 1] - start[seg.b]) * group - seg.rt * kRows);
+        const int valid = (start[at.b + 1] - start[at.b]) * group;
         if (quad >= valid) continue;
         const int row = min(quad + lane / 8, valid - 1), i8 = lane % 8;
         const int side = at.first >= U0;
@@ -771,7 +755,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
             }
             if (whole) {
                 int token;
-                const long long out_row = row_at(t, a, seg, kRows, group, row, &token);
+                const long long out_row = row_at(t, a, at.b, at.h, group, row, &token);
                 if (quad + lane / 8 < valid) y.write(a, out_row, i8);
                 break;
             }
@@ -840,17 +824,19 @@ static_assert(fits<1>() && fits<2>() && fits<3>() && fits<4>(), "shared memory")
 bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
               int sms, Q8Split *sp) {
     const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
-    if (rows > PFMIN) return q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, sp);
-    sp->row_tiles = rows <= 24 ? static_cast<int>((rows + 7) / 8) : 4;
-    const long long height = 8 * sp->row_tiles;
-    const long long tiles = (static_cast<long long>(max_len) + kTile - 1) / kTile;
-    const double units = static_cast<double>(num_seqs) * n_kv_heads * tiles * ((rows + height - 1) / height);
+    // Up to 32 rows here, more on tcgen05 (24 sequences of 200-2900 tokens, four heads a
+    // group; this kernel and that one, us): 12 rows 26.3, 55.0; 20 rows 35.7, 54.7; 32 rows
+    // 44.6, 53.7; 64 rows, twice 32, 55.1, 55.4
+    if (rows > 32) return q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, sp);
+    sp->row_tiles = static_cast<int>((rows + 7) / 8);
+    sp->tile_tokens = 0;
+    const double units = static_cast<double>(num_seqs) * n_kv_heads * ((static_cast<double>(max_len) + kTile - 1) / kTile);
     if (units >= 2147483648.0) return false;
     sp->ctas = sms;
     const int warps = sp->row_tiles == 1 ? Shape<128, 1>::kWarps : sp->row_tiles == 2 ? Shape<128, 2>::kWarps : Shape<128, 4>::kWarps;
     const int most = kBalancedMaxWorkers / (2 * sp->row_tiles);  // a counter for four rows of each
     if (sp->ctas > most) sp->ctas = most;
-    sp->record_rows = static_cast<int>(rows < height ? rows : height);
+    sp->record_rows = static_cast<int>(rows);
     sp->ws_bytes = kBalancedCounterBytes +
                    static_cast<size_t>(sp->ctas) * (warps + 2) * q8_record_floats(sp->record_rows, head_dim) * sizeof(float);
     return true;
