@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
         } else if (len == 0) {
             n = 0;
         }
-        const bool ok = n >= 0 && n <= 1 && n <= len && token >= 0 && token + n <= a.total &&
+        const bool ok = n >= 0 && n <= 1 && n <= len && token >= 0 && token <= a.total - n &&
                         len <= static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
         if (!ok && lane == 0 && h == 0 && side == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
         live = ok && n == 1;
@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32) q8_append_many_kernel(const Q8App
     const Found f = found;
     if (f.b < 0 || f.n == 0) return;
     const int slot = static_cast<int>(v - (f.start / bs + 2ll * f.b));
+    if (slot < 0) return;  // of starts that decrease, which are flagged
     if (f.n > a.max_q_len || f.n > f.len || f.len > static_cast<long long>(a.max_blocks_per_seq) * bs) {
         if (reports && slot == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
         return;

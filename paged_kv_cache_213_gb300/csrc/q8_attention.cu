@@ -29,10 +29,13 @@
 // last to arrive joins them, in the order of the tokens.
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 #include "q8.h"
 #include "q8_codes.cuh"
+#include "rope_latent.h"
 
 namespace pkv {
 namespace {
@@ -283,7 +286,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
             } else if (l == 0) {
                 n = 0;
             }
-            const bool ok = n >= 0 && n <= a.max_q_len && n <= l && s >= 0 && s + n <= a.total_q &&
+            const bool ok = n >= 0 && n <= a.max_q_len && n <= l && s >= 0 && s <= a.total_q - n &&
                             l <= a.max_context_len;
             if (!ok && blockIdx.x == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
             if (ok) units = n > 0 ? (l + kTile - 1) / kTile * a.n_kv_heads : 0;
@@ -410,8 +413,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
 #pragma unroll 1
             for (int i = threadIdx.x; i < a.n_q_heads * (D / 8); i += kWarps * 32) o[i] = make_uint4(0, 0, 0, 0);
             if (a.lse_out)
-    #pragma unroll 1
-            for (int i = threadIdx.x; i < a.n_q_heads; i += kWarps * 32)
+#pragma unroll 1
+                for (int i = threadIdx.x; i < a.n_q_heads; i += kWarps * 32)
                     a.lse_out[static_cast<long long>(b) * a.n_q_heads + i] = -INFINITY;
         }
     }
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
     const int v0 = S::kV + 2 * c * D + (D == 128 ? (r ^ 2 * c) * 16 : ((r >> 1) ^ c) * 16 + (r & 1) * 8);
     const int v1 = S::kV + (2 * c + 1) * D + (D == 128 ? (r ^ 2 * c + 1) * 16 : ((r >> 1) ^ c) * 16 + (r & 1) * 8);
     int stage = 0, parity = 0, qplace = 0;
-    int polls = a.first_wait_polls;  // test hook: the first wait gives up after so many
+    int polls = a.first_wait_polls;  // test hook: from 0 on, polls of the first wait before it gives up
 #pragma unroll 1
     for (int u = u0; u < u1;) {
         // --- a piece of a segment: units u to end
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                 }
             }
             if (alive) {
-                const bool ok = polls >= 0 ? mbar_wait_polls(full + stage, parity, polls)
+                const bool ok = polls >= 0 ? polls > 0 && mbar_wait_polls(full + stage, parity, polls - 1)
                                            : mbar_wait_bounded(full + stage, parity);
                 polls = -1;
                 if (!__all_sync(~0u, ok)) {
@@ -791,9 +794,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
 template <int KIND, int D, int NT>
 cudaError_t launch(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t stream) {
     const size_t smem = Shape<D, NT>::smem(a.num_seqs);
-    const cudaError_t e = cudaFuncSetAttribute(q8_attention_kernel<KIND, D, NT>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(q8_attention_kernel<KIND, D, NT>,
+                                     static_cast<int>(Shape<D, NT>::smem(kQ8MaxSeqs)), done);
     if (e != cudaSuccess) return e;
     CUtensorMap k_map, v_map;
     const long long rows = a.num_blocks * a.n_kv_heads * a.block_size;

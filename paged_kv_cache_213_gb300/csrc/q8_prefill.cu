@@ -23,10 +23,13 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "pkv_internal.h"
 #include "pkv_ptx.cuh"
 #include "q8.h"
 #include "q8_codes.cuh"
+#include "rope_latent.h"
 #include "tc05.cuh"
 
 namespace pkv {
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             } else if (l == 0) {
                 n = 0;
             }
-            const bool ok = n >= 0 && n <= a.max_q_len && n <= l && s >= 0 && s + n <= a.total_q &&
+            const bool ok = n >= 0 && n <= a.max_q_len && n <= l && s >= 0 && s <= a.total_q - n &&
                             l <= a.max_context_len;
             if (!ok && blockIdx.x == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
             len[b] = l;
@@ -481,15 +484,15 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         int f = 0, sc = 0;
         bool ok = true;
 #pragma unroll 1
-        for (int u = U0; ok && u < U1; at.next(t, a)) {
+        for (int u = U0; u < U1; at.next(t, a)) {
             const int first = u - at.j, n = min(at.steps - at.j, U1 - u);
-            const int mine = max(0, min(at.steps_of_tile(t, a, w) - at.j, n));
+            int mine = max(0, min(at.steps_of_tile(t, a, w) - at.j, n));
             u += n;
             const int tokens = start[at.b + 1] - start[at.b] - 2 * at.p * a.tile_tokens;  // from the pair on
             const int seen = Place::keys(t, at.b, 2 * at.p * a.tile_tokens + row_tok);
             float r = 0.f, l = 0.f, wv = 0.f, inv_w = 0.f;
 #pragma unroll 1
-            for (int j = 0; j < mine; ++j, ++sc) {
+            for (int j = 0; ok && j < mine; ++j, ++sc) {
                 const int slot = (f + j) % kStages;
                 const uint32_t here = ts + 64 * (sc & 1);
                 ok = warp_wait_or_stop(&sh.s_full[w][sc & 1], (sc >> 1) & 1, stop);
@@ -578,12 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 l += sum.x + sum.y;
             }
             f += n;
-            if (!ok) break;
-            if (mine > 0) {
+            if (ok && mine > 0) {
                 ok = warp_wait_or_stop(&sh.pv_done[w][(sc - 1) & 1], ((sc - 1) >> 1) & 1, stop);
-                if (!ok) break;
                 tc_fence_after();
             }
+            // after a wait that gave up results are unspecified, but each arrival is made
+            if (!ok) mine = 0;
             const bool whole = first >= U0 && first + at.steps <= U1, valid = row_tok < tokens;
             const float inv = wv / l;
             uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row_of(at.b, at.h, at.p) * D);
@@ -640,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         }
         // --- joins, by the last warp to arrive with these rows
 #pragma unroll 1
-        for (int i = 0; i < shares && ok; ++i) {
+        for (int i = 0; i < shares; ++i) {
             __syncwarp();
             const Share of = sh.todo[warp][i];
             int last = 0;
@@ -722,9 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
 template <int KIND, int D>
 cudaError_t launch(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t stream) {
     auto kern = q8_prefill_kernel<KIND, D>;
-    const size_t smem = Cfg<D>::smem(a.num_seqs);
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(kern, static_cast<int>(Cfg<D>::smem(kQ8MaxSeqs)), done);
     if (e != cudaSuccess) return e;
     CUtensorMap q_map;
     auto fn = encode_fn();
@@ -733,11 +735,12 @@ cudaError_t launch(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t str
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(a.n_q_heads / a.n_kv_heads),
                                static_cast<cuuint32_t>(a.tile_tokens)};
     const cuuint32_t one[3] = {1, 1, 1};
-    if (!fn || fn(&q_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, one,
+    if (!fn) return cudaErrorNotSupported;
+    if (fn(&q_map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, one,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorNotSupported;
-    return launch_pdl(kern, dim3(sp.ctas), dim3(kThreads), smem, stream, a, q_map);
+        return cudaErrorInvalidValue;  // a stride that the map does not take
+    return launch_pdl(kern, dim3(sp.ctas), dim3(kThreads), Cfg<D>::smem(a.num_seqs), stream, a, q_map);
 }
 
 static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 1024, "shared memory");

@@ -113,10 +113,19 @@ class Paged:
             self.scales[side][ids][..., None].astype(np.float64)
 
 
-def attend64(q, k, v, scale):
+    def spread_in_steps(self, b, n, keys):
+        """[n, Hk]: the largest V scale in a token's step of `keys` tokens over its own."""
+        bs = self.codes[0].shape[2]
+        own = self.scales[1][self.tables[b, np.arange(n) // bs]].astype(np.float64)
+        most = np.repeat(np.maximum.reduceat(own, np.arange(0, n, keys)), keys, axis=0)[:n]
+        return np.where(own > 0, most / np.where(own > 0, own, 1.0), 1.0)
+
+
+def attend64(q, k, v, scale, spread=None):
     """One sequence: q [n, H, d], k, v [m, Hk, d]; query i attends the first m - n +
     i + 1 keys.  Returns out, sum_t p_t |v_t|, lse, the largest scale * sum |q k|,
-    and sum |v_t| / l over the tokens whose weight is below 2^-8 of the largest."""
+    and sum |v_t| / l over the tokens whose weight is below 2^-8 of the largest.  spread
+    [m, Hk]: that sum is of spread |v_t|, over weights below 2^-8 spread."""
     n, H, d = q.shape
     m, Hk, _ = k.shape
     g = H // Hk
@@ -128,7 +137,9 @@ def attend64(q, k, v, scale):
     top = s.max(-1, keepdims=True)
     p = np.exp(s - top)
     l = p.sum(-1, keepdims=True)
-    small = np.einsum("nhgt,thc->nhgc", (p < 2.0 ** -8) & seen[:, None, None], np.abs(v)) / l
+    spread = np.ones((m, Hk)) if spread is None else spread
+    small = np.einsum("nhgt,thc->nhgc", (p < 2.0 ** -8 * spread.T[:, None]) & seen[:, None, None],
+                      spread[..., None] * np.abs(v)) / l
     p /= l
     out, mag = (np.einsum("nhgt,thc->nhgc", p, x) for x in (v, np.abs(v)))
     lse = (top + np.log(l))[..., 0]
@@ -143,7 +154,9 @@ def assert_attention(got, lse, ref, what):
       weights   half an fp16 step each; where the product with the scales' ratio is
                 below fp16's normal numbers, half a subnormal step.  The ratio is at
                 least 1/64 and a row's largest weight at least 1, so that takes a
-                weight below 2^-8 of the largest, and costs it 64 * TINY16 of |v|
+                weight below 2^-8 of the largest, and costs it 64 * TINY16 of |v|.  Where
+                keys of several blocks share a reference, that of the largest V scale
+                in the step, both are larger by what the key's scale is smaller
       result    half an fp16 step."""
     out, mag, ref_lse, size, small = ref
     got = np.asarray(got, np.float64)

@@ -33,7 +33,7 @@ class OnGpu:
     """A Paged problem's tensors."""
 
     def __init__(self, p):
-        self.p = p
+        self.p, self.keys = p, 16  # keys that share a V reference at least
         self.kv = [t(c) for c in p.codes] + [t(s) for s in p.scales]
         self.tables, self.lens = t(p.tables), t(p.lens.astype(np.int32))
         self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -50,6 +50,8 @@ class OnGpu:
 
     def check(self, q16, scale, news=None, **kw):
         out, lse = self.attend(t(q16), scale, news, **kw)
+        if max(news or [1]) * (q16.shape[1] // self.p.codes[0].shape[1]) > 32:
+            self.keys = 64
         at = starts([1] * len(self.p.lens) if news is None else news)
         for b in range(len(self.p.lens)):
             self.near(b, q16, out, lse, scale, at)
@@ -62,7 +64,8 @@ class OnGpu:
             assert np.all(out[rows] == 0) and np.all(np.isneginf(lse[rows]))
         elif at[b] < at[b + 1]:
             k, v = (self.p.tokens(side, b, L) for side in range(2))
-            assert_attention(out[rows], lse[rows], attend64(q16[rows], k, v, scale), f"sequence {b} of {L}")
+            spread = self.p.spread_in_steps(b, L, self.keys)
+            assert_attention(out[rows], lse[rows], attend64(q16[rows], k, v, scale, spread), f"sequence {b} of {L}")
 
 
 def queries(p, T, H, gain=1.0):
