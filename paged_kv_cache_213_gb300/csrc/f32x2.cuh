@@ -46,14 +46,18 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 // reciprocal and a quotient within one unit in the last place, one such correction
 // gives the rounded quotient; the first brings it there).  Exact where the residual is
 // a normal number, which holds for |x / scale| >= 2^-11 (smaller ones become code 0)
-// and scales in [2^-60, 2^60].  The sign is that of x (a residual of 0 would turn -0
-// into 0).  x has to be finite.
-__device__ __forceinline__ float2 divide2_finite(float2 x, float scale, float inv) {
+// and scales in [2^-60, 2^60].  x has to be finite.  A residual of 0 turns -0 into 0.
+__device__ __forceinline__ float2 divide2_unsigned_zero(float2 x, float scale, float inv) {
     const float2 s = make_float2(-scale, -scale), y = make_float2(inv, inv);
     const float2 q0 = mul2(x, y);
     const float2 q1 = fma2(fma2(s, q0, x), y, q0);
-    const float2 q2 = fma2(fma2(s, q1, x), y, q1);
-    return make_float2(copysignf(q2.x, x.x), copysignf(q2.y, x.y));
+    return fma2(fma2(s, q1, x), y, q1);
+}
+
+// The same with the sign of x.
+__device__ __forceinline__ float2 divide2_finite(float2 x, float scale, float inv) {
+    const float2 q = divide2_unsigned_zero(x, scale, inv);
+    return make_float2(copysignf(q.x, x.x), copysignf(q.y, x.y));
 }
 
 // The same for any x: a quotient that is not finite stays as it is.

@@ -21,15 +21,16 @@ namespace {
 constexpr int kPiece = 8;
 
 // The largest of 8 sizes |x|, as fp16 bits in either half of the result, and of another
-// 8's.  fp16 sizes are ordered like their bits.
+// 8's; a NaN's bits where there is one.
 __device__ __forceinline__ uint32_t top_bits(const uint4 &x, uint32_t other) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const __half2 *h = reinterpret_cast<const __half2 *>(&x);
+    __half2 top = *reinterpret_cast<const __half2 *>(&other);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) other = __vmaxu2(other, w[i] & 0x7fff7fffu);
-    return other;
+    for (int i = 0; i < 4; ++i) top = __hmax2_nan(top, __habs2(h[i]));
+    return *reinterpret_cast<const uint32_t *>(&top);
 }
 
-// The same over the finite values alone.
+// The same over the finite values alone (sizes are ordered like their bits).
 __device__ __forceinline__ uint32_t finite_top_bits(const uint4 &x, uint32_t other) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -89,9 +90,14 @@ __device__ __forceinline__ uint2 quantised(const uint4 &x, const Divisor &d) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 f = __half22float2(h[i]);
-        q[i] = PLAIN ? divide2_finite(f, d.s, d.inv) : make_float2(__fdiv_rn(f.x, d.s), __fdiv_rn(f.y, d.s));
+        q[i] = PLAIN ? divide2_unsigned_zero(f, d.s, d.inv) : make_float2(__fdiv_rn(f.x, d.s), __fdiv_rn(f.y, d.s));
     }
-    return make_uint2(q8_encode4<KIND, PLAIN>(q[0], q[1]), q8_encode4<KIND, PLAIN>(q[2], q[3]));
+    uint2 codes = make_uint2(q8_encode4<KIND, PLAIN>(q[0], q[1]), q8_encode4<KIND, PLAIN>(q[2], q[3]));
+    if (PLAIN && KIND == PKV_Q8_E4M3) {  // the sign of a zero, with those that are there already
+        codes.x |= __byte_perm(x.x, x.y, 0x7531) & 0x80808080u;
+        codes.y |= __byte_perm(x.z, x.w, 0x7531) & 0x80808080u;
+    }
+    return codes;
 }
 
 // Codes of earlier tokens, whose scale grew by 2^power: code * 2^-power.
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
 constexpr int kWarps = 4;
 
 template <int KIND, int D, int ROWS>  // rows of a warp
-__global__ void __launch_bounds__(kWarps * 32) q8_append_many_kernel(const Q8AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, ROWS == 16 ? 8 : 1) q8_append_many_kernel(const Q8AppendArgs a) {
     constexpr int kTeam = D / kPiece;        // lanes of a row
     constexpr int kAt = 32 / kTeam;          // rows of one load
     constexpr int kSteps = ROWS / kAt;
