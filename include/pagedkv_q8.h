@@ -14,7 +14,7 @@
  * Layout: codes [num_blocks][n_kv_heads][block_size][head_dim], one byte each,
  * as in pagedkv.h; k_scales and v_scales fp32 [num_blocks][n_kv_heads].  Block
  * tables, ownership, errors and the error word are those of pagedkv.h.  Scales
- * are finite and not negative (what the append writes is).
+ * are 0 or between 2^-100 and 2^100 (what the append writes is).
  *
  * Limits of every call: head_dim 64 or 128, block_size 16, 32, 64, 128 or 256,
  * at most 2048 sequences, fewer than 2^31 rows of all blocks and heads in a
@@ -86,7 +86,9 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  *
  * over the tokens t of the sequence up to and including the query's own
  * position; query head h reads KV head h / (n_q_heads / n_kv_heads), any
- * whole ratio.
+ * whole ratio up to 128 (PKV_ERR_UNSUPPORTED beyond).  Up to 32 query rows of
+ * a KV head (max_q_len times that ratio) are streamed through one kernel; more
+ * go in tiles of 128 rows to another, on tcgen05.  out and q do not overlap.
  *
  *  q              device fp16, token i's n_q_heads * head_dim entries at
  *                 element i * q_stride (a multiple of 8)
@@ -103,13 +105,18 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  *  workspace      device scratch of at least paged_decode_q8_plan's bytes,
  *                 256-byte aligned.  Its first PKV_WORKSPACE_COUNTER_BYTES
  *                 bytes hold arrival counters: zero before the first use, and
- *                 left at zero by every call.  After PKV_ERRBIT_WORKSPACE (a
+ *                 left at zero by every call, also by one that flags
+ *                 PKV_ERRBIT_TIMEOUT.  After PKV_ERRBIT_WORKSPACE (a
  *                 counter that did not start at zero) clear them with
  *                 paged_decode_workspace_clear.  Calls that overlap in time
  *                 need separate workspaces.
- *  flags          0 or PKV_TABLES_READY, which covers query_start too
- * Logits, softmax and sums in fp32; the weights (times their block's V scale)
- * are rounded to fp16 for the product with the codes, which are exact.  Rows
+ *  flags          0 or PKV_TABLES_READY, which covers query_start too (made
+ *                 use of up to 32 rows)
+ * Logits, softmax and sums in fp32; the weights times their block's V scale
+ * are rounded to fp16 for the product with the codes, which are exact: off by
+ * 2^-11 of themselves, or where that is more by 2^-19 of the block's V scale
+ * (with more than 32 rows: of the largest V scale among 64 tokens), the largest
+ * weight of the row being 1.  Rows
  * behind a sequence's length never reach a result, whatever they hold.  A
  * cached NaN makes the queries that attend it NaN; one of a sequence's newest
  * tokens may also reach that sequence's earlier queries.

@@ -10,7 +10,7 @@
 
 namespace pkv {
 
-constexpr int kQ8MaxSeqs = 2048;
+constexpr int kQ8MaxSeqs = 2048, kQ8MaxGroup = 128;  // a tile has 128 rows
 
 struct Q8AppendArgs {
     const void *k_new, *v_new;

@@ -68,7 +68,7 @@ int make_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int n_kv_
         return PKV_ERR_INVALID_ARG;
     const int rc = check_cache(PKV_Q8_E4M3, n_kv_heads, head_dim, block_size, 1);
     if (rc != PKV_OK) return rc;
-    if (num_seqs > pkv::kQ8MaxSeqs) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > pkv::kQ8MaxSeqs || n_q_heads / n_kv_heads > pkv::kQ8MaxGroup) return PKV_ERR_UNSUPPORTED;
     const long long cap = static_cast<long long>(max_blocks_per_seq) * block_size;
     if (cap > (1LL << 30)) return PKV_ERR_INVALID_ARG;
     if (static_cast<long long>(total_q) * n_q_heads > (1LL << 30) ||

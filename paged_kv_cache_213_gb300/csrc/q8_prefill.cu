@@ -39,6 +39,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 namespace {
 
 constexpr int kRows = 128, kKeys = 64;  // of a tile, of a step
+static_assert(kQ8MaxGroup <= kRows, "a token's rows are in one tile");
 constexpr int kPair = 2 * kRows;
 constexpr int kGroups = kKeys / 16;      // pieces of 16 keys, each of one block
 constexpr int kThreads = 512;  // 8 warps of softmax, 4 of converters, 2 of products, 1 of queries, an idle one
@@ -751,7 +752,6 @@ static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 1024, "shared memory");
 bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
                       int sms, Q8Split *sp) {
     const int group = n_q_heads / n_kv_heads;
-    if (group > kRows) return false;
     sp->tile_tokens = kRows / group;
     const double steps = (static_cast<double>(max_len) + kKeys - 1) / kKeys + 1;
     const double pairs = static_cast<double>(max_q_len) / (2 * sp->tile_tokens) + 1;

@@ -1,5 +1,6 @@
 """The 8-bit caches with block scales without a GPU: host refusals, and the plain
 statements of tests/q8_util.py against torch's E4M3 and against themselves."""
+import ctypes
 import os
 
 import numpy as np
@@ -70,8 +71,28 @@ def test_attention_refusals(lib):
         assert _call(fn, AT, **change) == INVALID, change
     for change, status in CACHE:
         assert _call(fn, AT, **{**change, "q_stride": 4096}) == status, change
-    for change in (dict(num_seqs=2049), dict(total_q=1 << 29), dict(max_q_len=1 << 29)):
+    for change in (dict(num_seqs=2049), dict(total_q=1 << 29), dict(max_q_len=1 << 29), dict(H=258)):
         assert _call(fn, AT, **change) == UNSUPPORTED, change
+
+
+PL = dict(num_seqs=0, total_q=0, max_q_len=1, H=4, Hk=2, d=64, bs=16, MB=8, mcl=100)
+
+
+def test_plan_refusals(lib):
+    size = ctypes.c_size_t(7)
+
+    def plan(**change):
+        return lib.paged_decode_q8_plan(*{**PL, **change}.values(), ctypes.byref(size))
+
+    assert plan() == 0 and size.value == 0 and plan(H=256) == 0
+    for change in (dict(num_seqs=-1), dict(total_q=-1), dict(max_q_len=-1), dict(H=0), dict(H=3), dict(Hk=0),
+                   dict(MB=0), dict(MB=1 << 27), dict(d=0), dict(bs=0)):
+        assert plan(**change) == INVALID, change
+    for change in (dict(num_seqs=2049), dict(H=258), dict(d=96), dict(bs=8), dict(max_q_len=1 << 29)):
+        assert plan(**change) == UNSUPPORTED, change
+    assert lib.paged_decode_q8_plan(*PL.values(), None) == 0  # the size is not asked for
+    with pytest.raises(pkv.PagedKVError):
+        pkv.q8_plan(2, 2, 1, 258, 2, 64, 16, 8)
 
 
 GA = dict(ko=P, vo=P, k=P, v=P, ks=P, vs=P, kind=0, tables=P, start=P, num_seqs=2, total=5, MB=8, NB=64, Hk=2, d=64,
