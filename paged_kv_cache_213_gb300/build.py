@@ -4,7 +4,7 @@
 Each translation unit compiles in its own process (in parallel), then nvcc
 links the first into one shared library exporting the C ABI of
 ``include/pagedkv.h``; the second is the Python module that marshals the calls
-of ``rope.py`` and ``latent.py`` and links that library.  Usable as
+of ``rope.py``, ``latent.py`` and ``q8.py`` and links that library.  Usable as
 ``python -m paged_kv_cache_213_gb300.build``.
 
 The library needs nvcc alone.  Where the module does not build (no torch with CUDA,
@@ -167,7 +167,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 _link_calls(calls.result(), target)
             except (RuntimeError, OSError) as e:
                 warnings.warn(f"{LIB_PATH} is built, the Python module beside it is not "
-                              f"(rope.py and latent.py marshal their calls in Python): {e}")
+                              f"(rope.py, latent.py and q8.py marshal their calls in Python): {e}")
     return LIB_PATH
 
 
