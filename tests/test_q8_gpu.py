@@ -602,3 +602,98 @@ def test_calls_with_nothing_to_do():
     pkv.paged_kv_copy_blocks_q8(*gpu.kv, lens, lens)
     for x, y in zip(before, gpu.kv):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+# --- sizes at the edges -----------------------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_one_token_or_none_by_query_start(kind, marshalled):
+    """max_q_len 1 with query_start: sequences with a token and without, cached or empty."""
+    held, news = [0, 31, 16, 0, 700, 5], [1, 1, 0, 0, 1, 0]
+    Hk, d, bs = 2, 128, 16
+    p = Paged([m + n for m, n in zip(held, news)], Hk, d, bs, kind, seed=12)
+    for b, (m, n) in enumerate(zip(held, news)):
+        if n:
+            for side in range(2):
+                p.codes[side][p.tables[b, m // bs], :, m % bs] = 127
+                if m % bs == 0:
+                    p.scales[side][p.tables[b, m // bs]] = np.nan
+    x = [p.rng.standard_normal((sum(news), Hk, d)).astype(np.float16) for _ in "kv"]
+    gpu = OnGpu(p)
+    run_append(p, gpu.kv, news, x)
+    for side in range(2):
+        append64(kind, x[side], starts(news), p.lens, p.tables, p.codes[side], p.scales[side])
+    same_state(p, gpu.kv)
+    at, q = starts(news), queries(p, sum(news), 8)
+    out, lse = gpu.attend(t(q), 0.1, news)
+    for b, n in enumerate(news):
+        if n:
+            gpu.near(b, q, out, lse, 0.1, at)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("most", [1, 3])
+def test_as_many_sequences_as_there_may_be(kind, most):
+    held = [5 * i % 37 for i in range(2048)]
+    news = [1 + i % most for i in range(2048)]
+    p = Paged([m + n for m, n in zip(held, news)], 1, 64, 16, kind, seed=most)
+    for b, (m, n) in enumerate(zip(held, news)):
+        for i in range(m, m + n):
+            for side in range(2):
+                p.codes[side][p.tables[b, i // 16], :, i % 16] = 127
+                if i % 16 == 0:
+                    p.scales[side][p.tables[b, i // 16]] = np.nan
+    x = [p.rng.standard_normal((sum(news), 1, 64)).astype(np.float16) for _ in "kv"]
+    gpu = OnGpu(p)
+    run_append(p, gpu.kv, None if most == 1 else news, x)
+    for side in range(2):
+        append64(kind, x[side], starts(news), p.lens, p.tables, p.codes[side], p.scales[side])
+    same_state(p, gpu.kv)
+    total = int(p.lens.sum())
+    got = pkv.paged_kv_gather_q8(*gpu.kv, gpu.tables, t(starts(p.lens)), total, err_word=gpu.err)
+    assert pkv.get_error(gpu.err) == 0
+    for side in range(2):
+        want = np.concatenate([p.tokens(side, b, int(n)) for b, n in enumerate(p.lens)])
+        assert np.array_equal(got[side].cpu().numpy(), want.astype(np.float32).astype(np.float16))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_pool_beyond_32_bits(kind):
+    """Blocks behind 4 GB of codes: what every call does there is, bit for bit, what it does
+    in a small pool."""
+    Hk, d, bs, lens, news = 8, 128, 16, [700, 90], [1, 1]
+    small = Paged(lens, Hk, d, bs, kind, seed=13)
+    NB = 290000
+    assert NB * Hk * bs * d > 2 ** 32
+    far = np.full(small.NB, -1, np.int32)  # block of the small pool -> of the large one
+    used = sorted({int(i) for b, n in enumerate(lens) for i in small.tables[b, :-(-n // bs)]})
+    far[used] = NB - 1 - 3 * np.arange(len(used))
+    tables = np.where((small.tables >= 0) & (small.tables < small.NB), far[np.clip(small.tables, 0, small.NB - 1)],
+                      NB + 7).astype(np.int32)
+    a = OnGpu(small)
+    large = [torch.empty(NB, *x.shape[1:], dtype=x.dtype, device="cuda") for x in a.kv]
+    to, frm = torch.from_numpy(far[used].astype(np.int64)).cuda(), torch.tensor(used, device="cuda")
+    for x, y in zip(large, a.kv):
+        x[to] = y[frm]
+    pools = ((a.kv, a.tables), (large, t(tables)))
+    q, many = queries(small, 2, 32), queries(small, 150, 32)
+    x = [queries(small, 2, Hk) for _ in "kv"]
+    y = [queries(small, 150, Hk) for _ in "kv"]
+    results = []
+    for kv, tb in pools:
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        cut = dict(query_start=t(starts([90, 60])), max_q_len=90)
+        pkv.paged_kv_append_q8(t(y[0]), t(y[1]), *kv, tb, a.lens, err_word=err, **cut)
+        pkv.paged_kv_append_q8(t(x[0]), t(x[1]), *kv, tb, a.lens, err_word=err)
+        one = pkv.paged_decode_attention_q8(t(q), *kv, tb, a.lens, 0.1, err_word=err)
+        chunk = pkv.paged_decode_attention_q8(t(many), *kv, tb, a.lens, 0.1, err_word=err, **cut)
+        k, v = pkv.paged_kv_gather_q8(*kv, tb, t(starts(lens)), sum(lens), err_word=err)
+        src = tb[0, :2].contiguous()
+        pkv.paged_kv_copy_blocks_q8(*kv, src, tb[0, 2:4].contiguous(), err_word=err)
+        kk, _ = pkv.paged_kv_gather_q8(*kv, tb, t(starts([64, 0])), 64, err_word=err)
+        assert pkv.get_error(err) == 0
+        assert torch.equal(kk[:32].view(torch.uint8), kk[32:].view(torch.uint8))
+        results.append([z.view(torch.uint8).cpu().numpy() for z in (one, chunk, k, v, kk)])
+    for got, want in zip(*results):
+        assert np.array_equal(got, want)
+    assert np.isfinite(results[0][0].view(np.float16)).all()
