@@ -116,7 +116,8 @@ __device__ __forceinline__ uint2 shrunk(const uint2 &c, int power) {
     return make_uint2(r[0], r[1]);
 }
 
-// One token a sequence: a team of D / 8 lanes for each (sequence, head, K or V).
+// One token a sequence: a team of D / 8 lanes for each (sequence, head, K or V).  A launch
+// and three loads in a row (length, block, scale): 32 x 8 heads of 128 2.1 us.
 template <int KIND, int D>
 __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a) {
     constexpr int kTeam = D / kPiece;
@@ -184,6 +185,11 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
 // Which block: the blocks of sequence b get the numbers from start[b] / bs + 2 b on.
 // A run of n tokens touches at most n / bs + 2 blocks (rounded down), so the ranges do
 // not meet, and a CTA finds its sequence without a sum over the ones before.
+//
+// 8 CTAs an SM, each with its rows on the way before it knows the scale.  5 prompts of 411
+// to 2903 tokens, 8 heads of 128 (51 MB): 13.0 us, 3.9 TB/s; by instructions (half of the issue
+// slots) and by starts and ends, which a transfer of 7.5 us does not hide.  2 or 8 warps a CTA,
+// 40 warps an SM: 12.9, 13.4, 12.9; 24 warps an SM 15.2.
 constexpr int kWarps = 4;
 
 template <int KIND, int D, int ROWS>  // rows of a warp
@@ -310,6 +316,7 @@ constexpr int kGatherThreads = 256;
 // some of them (no search, whose steps would wait for one another), one thread a row
 // looks the row's block up, then each thread turns 16 codes into 32 bytes, rows next
 // to each other in the block by neighbouring lanes.
+// 8 sequences of 2000 to 16000 tokens, 8 heads of 128 (442 MB): 70.1 us, 6.3 TB/s: memory.
 // (The bound of one CTA lets the compiler take 48 registers and keep both loads in flight; at the
 // 32 that it takes without, 72000 rows take 82.6 us.)
 template <int KIND, int D, int ROWS>
@@ -393,7 +400,8 @@ __global__ void __launch_bounds__(kGatherThreads, 1) q8_gather_kernel(const Q8Ga
 
 // --- block copy -------------------------------------------------------------
 
-// A CTA a copy: the block's codes in 16-byte pieces, then its scales.
+// A CTA a copy: the block's codes in 16-byte pieces, then its scales.  For the few copies of a
+// step's forks, where the launch is all there is.
 __global__ void __launch_bounds__(256) q8_copy_kernel(const Q8CopyArgs a) {
     grid_dependency_wait();
     allow_dependent_launch();
