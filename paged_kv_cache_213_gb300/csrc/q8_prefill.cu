@@ -67,8 +67,16 @@ struct Share {
     int from, parts, before;  // CTAs from, parts of them; how many had arrived
 };
 
+// What a softmax warp knows of its piece, here while it goes through the steps: that loop has
+// 64 logits in registers and is slower with each other one that it has to leave room for (69.3
+// us for the chunks above, 63.1 with this).
+struct Piece {
+    int u, first, n, f, mine, shares, b, h, p, steps;
+};
+
 struct Roles {
     Share todo[8][2];
+    Piece keep[8];
     uint64_t q_full[2], q_empty[2], o_free[2], drained[2];
     // Of a tile's even and odd steps.  With the scores two steps ahead, a warp of softmax may be
     // a step ahead of the others, whose arrivals it must not make up for, and done with a
@@ -157,6 +165,22 @@ struct Ranges {
 __device__ __forceinline__ int divided(int x, const Q8Divide &d) {
     return static_cast<int>(static_cast<unsigned long long>(static_cast<unsigned>(x)) * d.mul >> d.shift);
 }
+
+// A thread's row among the pair's: its token, and its head in the group.  Rows behind the
+// tile's tokens (where the group does not divide 128) are no token's.
+struct Row {
+    int in_pair, tok, head;
+    __device__ Row(const Q8AttentionArgs &a, int row) : in_pair(row) {
+        const int group = a.n_q_heads / a.n_kv_heads, t = row / kRows, i = row % kRows;
+        const int tok_in = divided(i, a.by_group);
+        head = i - tok_in * group;
+        tok = tok_in < a.tile_tokens ? t * a.tile_tokens + tok_in : 1 << 29;
+    }
+    __device__ long long out_row(const Batch &t, const Q8AttentionArgs &a, int b, int h, int p) const {
+        return static_cast<long long>(t.start[b] + 2 * p * a.tile_tokens + tok) * a.n_q_heads +
+               h * (a.n_q_heads / a.n_kv_heads) + head;
+    }
+};
 
 // A piece of 16 bytes in the products' layout: row `row` of a plane, piece q of 8.
 __device__ __forceinline__ int swizzled(int row, int q) { return row * 128 + ((q ^ (row & 7)) << 4); }
@@ -471,34 +495,39 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
         const int w = warp >> 2;  // the tile
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 * (warp % 4) << 16
         const uint32_t ts = tmem + 128 * w + lanes, to = tmem + 256 + 128 * w + lanes;
-        const int row_in = w * kRows + (threadIdx.x & 127);  // of the pair
-        // its token among the pair's, and its head in the group; rows behind the tile's tokens
-        // (where the group does not divide 128) are no token's
-        const int tok_in = divided(threadIdx.x & 127, a.by_group), head_in = (threadIdx.x & 127) - tok_in * group;
-        const int row_tok = tok_in < a.tile_tokens ? w * a.tile_tokens + tok_in : 1 << 29;
         unsigned char *ws = static_cast<unsigned char *>(a.workspace);
         // records: float4 [D / 4][record_rows], then reference and sum of each row
         auto record_of = [&](int of_cta, int side) {
             return reinterpret_cast<float4 *>(ws + kBalancedCounterBytes) +
                    (2ll * of_cta + side) * (D / 4 + 1) * a.record_rows;
         };
-        auto out_row_of = [&](int b, int h, int p) {  // this thread's
-            return static_cast<long long>(start[b] + 2 * p * a.tile_tokens + row_tok) * a.n_q_heads + h * group + head_in;
-        };
         int shares = 0;
         int f = 0, sc = 0;
         bool ok = true;
 #pragma unroll 1
         for (int u = U0; u < U1; at.next(t, a)) {
-            const int first = u - at.j, n = min(at.steps - at.j, U1 - u);
+            int first = u - at.j, n = min(at.steps - at.j, U1 - u);
             int mine = max(0, min(at.steps_of_tile(t, a, w) - at.j, n));
             u += n;
-            const int tokens = start[at.b + 1] - start[at.b] - 2 * at.p * a.tile_tokens;  // from the pair on
-            const int seen = Place::keys(t, at.b, 2 * at.p * a.tile_tokens + row_tok);
+            int left = Place::keys(t, at.b, 2 * at.p * a.tile_tokens + Row(a, threadIdx.x).tok) - at.j * kKeys;
+            volatile Piece *keep = &sh.keep[warp];
+            if (lane == 0) {
+                keep->u = u;
+                keep->first = first;
+                keep->n = n;
+                keep->f = f;
+                keep->mine = mine;
+                keep->shares = shares;
+                keep->b = at.b;
+                keep->h = at.h;
+                keep->p = at.p;
+                keep->steps = at.steps;
+            }
+            int slot = f % kStages;
+            bool fresh = true;
             float r = 0.f, l = 0.f, wv = 0.f, inv_w = 0.f;
 #pragma unroll 1
-            for (int j = 0; ok && j < mine; ++j, ++sc) {
-                const int slot = (f + j) % kStages;
+            for (; ok && mine > 0; --mine, ++sc, left -= kKeys, slot = (slot + 1) % kStages) {
                 const uint32_t here = ts + 64 * (sc & 1);
                 ok = warp_wait_or_stop(&sh.s_full[w][sc & 1], (sc >> 1) & 1, stop);
                 if (!ok) break;
@@ -510,7 +539,6 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 float most = 0.f;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) most = fmaxf(most, vg[g]);
-                const int left = seen - (at.j + j) * kKeys;
                 tmem_wait_ld();
                 if (a.scale_log2 < 0.f)
 #pragma unroll
@@ -539,7 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     fac = wv * inv_w;
                     wv = most;
                 }
-                if (j == 0) {
+                if (fresh) {
+                    fresh = false;
                     r = top > -INFINITY ? top : 0.f;
                 } else {
                     const bool move = top - r > kLag;
@@ -565,19 +594,20 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 // --- weights
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    uint32_t p[8];
-                    const float fc = fg[g], v = vg[g] * inv_w;
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const uint32_t *z = &x[g / 2][g % 2 * 16 + 2 * c];
+                    for (int c = 0; c < 16; ++c) {
+                        const int g = 2 * half + c / 8;
+                        const float fc = fg[g], v = vg[g] * inv_w;
+                        const uint32_t *z = &x[half][2 * c];
                         const float2 e = fma2(make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])), fc, -r);
                         const float2 y = make_float2(ex2(e.x), ex2(e.y));
                         sum = add2(sum, y);
                         const float2 m = mul2(y, make_float2(v, v));
                         p[c] = pack_half2(m.x, m.y);
                     }
-                    tmem_st8(here + 8 * g, p);
+                    tmem_st16(here + 16 * half, p);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -585,17 +615,31 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 if (lane == 0) mbar_arrive(&sh.p_ready[w][sc & 1]);
                 l += sum.x + sum.y;
             }
-            f += n;
+            __syncwarp();
+            u = keep->u;
+            first = keep->first;
+            n = keep->n;
+            f = keep->f + n;
+            mine = keep->mine;
+            shares = keep->shares;
+            at.b = keep->b;
+            at.h = keep->h;
+            at.p = keep->p;
+            at.steps = keep->steps;
+            int tid;
+            asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+            const Row row(a, tid);
+            const int tokens = start[at.b + 1] - start[at.b] - 2 * at.p * a.tile_tokens;  // from the pair on
             if (ok && mine > 0) {
                 ok = warp_wait_or_stop(&sh.pv_done[w][(sc - 1) & 1], ((sc - 1) >> 1) & 1, stop);
                 tc_fence_after();
             }
             // after a wait that gave up results are unspecified, but each arrival is made
             if (!ok) mine = 0;
-            const bool whole = first >= U0 && first + at.steps <= U1, valid = row_tok < tokens;
+            const bool whole = first >= U0 && first + at.steps <= U1, valid = row.tok < tokens;
             const float inv = wv / l;
-            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + out_row_of(at.b, at.h, at.p) * D);
-            float4 *rec = record_of(cta, first >= U0) + row_in;
+            uint4 *out = reinterpret_cast<uint4 *>(static_cast<__half *>(a.out) + row.out_row(t, a, at.b, at.h, at.p) * D);
+            float4 *rec = record_of(cta, first >= U0) + row.in_pair;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -631,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             }
             if (whole) {
                 if (a.lse_out && valid)
-                    a.lse_out[out_row_of(at.b, at.h, at.p)] = (r + log2f(l)) * kLn2;
+                    a.lse_out[row.out_row(t, a, at.b, at.h, at.p)] = (r + log2f(l)) * kLn2;
                 continue;
             }
             if (!__any_sync(~0u, valid)) continue;
@@ -647,6 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
             ++shares;
         }
         // --- joins, by the last warp to arrive with these rows
+        const Row row(a, threadIdx.x);
 #pragma unroll 1
         for (int i = 0; i < shares; ++i) {
             __syncwarp();
@@ -663,13 +708,13 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 }
             }
             if (!__shfl_sync(~0u, last, 0)) continue;
-            if (row_tok >= start[of.b + 1] - start[of.b] - 2 * of.p * a.tile_tokens) continue;
+            if (row.tok >= start[of.b + 1] - start[of.b] - 2 * of.p * a.tile_tokens) continue;
             float high = -INFINITY;
 #pragma unroll 1
             for (int k = 0; k < of.parts; ++k)
-                high = fmaxf(high, __ldcg(&(record_of(of.from + k, k == 0) + (D / 4) * a.record_rows + row_in)->x));
+                high = fmaxf(high, __ldcg(&(record_of(of.from + k, k == 0) + (D / 4) * a.record_rows + row.in_pair)->x));
             if (high == -INFINITY) high = 0.f;
-            const long long out_row = out_row_of(of.b, of.h, of.p);
+            const long long out_row = row.out_row(t, a, of.b, of.h, of.p);
             float sum = 0.f;
 #pragma unroll 1
             for (int c0 = 0; c0 < D / 4; c0 += 8) {
@@ -683,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     float2 ml[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float4 *part = record_of(of.from + min(k0 + k, of.parts - 1), k0 + k == 0) + row_in;
+                        const float4 *part = record_of(of.from + min(k0 + k, of.parts - 1), k0 + k == 0) + row.in_pair;
 #pragma unroll
                         for (int e = 0; e < 8; ++e) z[k][e] = __ldcg(part + (c0 + e) * a.record_rows);
                         ml[k] = __ldcg(reinterpret_cast<const float2 *>(part + (D / 4) * a.record_rows));
@@ -748,7 +793,7 @@ cudaError_t launch(const Q8AttentionArgs &a, const Q8Split &sp, cudaStream_t str
     return launch_pdl(kern, dim3(sp.ctas), dim3(kThreads), Cfg<D>::smem(a.num_seqs), stream, a, q_map);
 }
 
-static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 1024, "shared memory");
+static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 2048, "shared memory");
 
 }  // namespace
 
