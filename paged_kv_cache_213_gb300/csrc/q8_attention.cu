@@ -28,7 +28,7 @@
 // a CTA hold are joined there; CTAs that share a segment leave a record each, and the
 // last to arrive joins them, in the order of the tokens.
 //
-// Measured (32 query heads on 8 of 128, E4M3): 8 x 32k tokens 88.6 us, 6.1 TB/s, memory; 32 x
+// Measured (32 query heads on 8 of 128, E4M3): 8 x 32k tokens 87.5 us, 6.1 TB/s, memory; 32 x
 // 128 to 2048 tokens 21.0 us, 3.4 TB/s, of which 4 us pass before the first tile lands and 5 us in the
 // joins; 20 rows, 24 x 200 to 2900 tokens, 36.1 us, where a warp's chain of instructions bounds
 // it (255 registers a thread, two warps a scheduler).

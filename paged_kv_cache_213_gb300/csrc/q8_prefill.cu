@@ -21,8 +21,8 @@
 // per SM; items that several CTAs hold leave records, and the last to arrive joins them.
 //
 // Measured: 3 chunks of 150 to 700 tokens behind 1800 to 2500, 32 query heads on 8 of 128 (47
-// GFLOP): 69.3 us, 0.68 PFLOP/s.  A step takes about 2300 cycles, of which the tensor core is busy 1100:
-// the softmax of a row's 64 keys is the chain (load 420, maximum 650, weights 930).
+// GFLOP): 63.4 us, 0.75 PFLOP/s.  A step takes about 2100 cycles, of which the tensor core is busy
+// 1100: the softmax of a row's 64 keys is the chain.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
@@ -69,7 +69,7 @@ struct Share {
 
 // What a softmax warp knows of its piece, here while it goes through the steps: that loop has
 // 64 logits in registers and is slower with each other one that it has to leave room for (69.3
-// us for the chunks above, 63.1 with this).
+// us for the chunks above, 63.4 with this).
 struct Piece {
     int u, first, n, f, mine, shares, b, h, p, steps;
 };
