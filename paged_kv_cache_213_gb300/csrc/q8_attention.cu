@@ -841,7 +841,8 @@ bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int he
     const double units = static_cast<double>(num_seqs) * n_kv_heads * ((static_cast<double>(max_len) + kTile - 1) / kTile);
     if (units >= 2147483648.0) return false;
     sp->ctas = sms;
-    const int warps = sp->row_tiles == 1 ? Shape<128, 1>::kWarps : sp->row_tiles == 2 ? Shape<128, 2>::kWarps : Shape<128, 4>::kWarps;
+    const int warps = sp->row_tiles <= 2 ? Shape<128, 2>::kWarps : Shape<128, 4>::kWarps;
+    static_assert(Shape<128, 1>::kWarps == Shape<128, 2>::kWarps && Shape<128, 3>::kWarps == Shape<128, 4>::kWarps, "");
     const int most = kBalancedMaxWorkers / (2 * sp->row_tiles);  // a counter for four rows of each
     if (sp->ctas > most) sp->ctas = most;
     sp->record_rows = static_cast<int>(rows);

@@ -577,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                         r = next;
                         l *= g;
                         fac *= g;
-                        ok = warp_wait_or_stop(&sh.pv_done[w][(sc - 1) & 1], ((sc - 1) >> 1) & 1, stop);  // the outputs so far
+                        // the outputs so far
+                        ok = warp_wait_or_stop(&sh.pv_done[w][(sc - 1) & 1], ((sc - 1) >> 1) & 1, stop);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
