@@ -833,8 +833,8 @@ bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int he
               int sms, Q8Split *sp) {
     const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
     // Up to 32 rows here, more on tcgen05 (24 sequences of 200-2900 tokens, four heads a
-    // group; this kernel and that one, us): 12 rows 26.3, 55.0; 20 rows 35.7, 54.7; 32 rows
-    // 44.6, 53.7; 64 rows, twice 32, 55.1, 55.4
+    // group; this kernel and that one, us): 12 rows 26.1, 50.4; 20 rows 36.1, 49.4; 32 rows
+    // 46.4, 48.5; 64 rows, twice 32 here, 55.1, 49.3
     if (rows > 32) return q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, sp);
     sp->row_tiles = static_cast<int>((rows + 7) / 8);
     sp->tile_tokens = 0;
