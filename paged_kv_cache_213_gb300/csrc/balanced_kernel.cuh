@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(kW * 32, kW == kWSmall ? 3 : 1)
             const size_t row = static_cast<size_t>(pc.b) * Hk + pc.j;
             uint4 piece = make_uint4(0u, 0u, 0u, 0u);
             if (lane < 2 * kU8)
-                piece = __ldg(static_cast<const uint4 *>(lane < kU8 ? a.append_k : a.append_v) +
-                              row * kU8 + (lane % kU8));
+                piece = __ldcg(static_cast<const uint4 *>(lane < kU8 ? a.append_k : a.append_v) +
+                               row * kU8 + (lane % kU8));
             const long long sl = a.append_slots[pc.b];
 #pragma unroll
             for (int s = 0; s < kS; ++s)

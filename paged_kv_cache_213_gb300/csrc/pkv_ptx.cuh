@@ -208,6 +208,8 @@ namespace pkv {
 // stream-serialization attribute may start before the previous kernel in the
 // stream finishes; grid_dependency_wait() blocks until that kernel has
 // completed and its writes are visible (a no-op without the attribute).
+// What that kernel may write is read by coherent loads: the non-coherent path is for
+// memory that stays as it is while this kernel runs, and this one runs by then.
 __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kGatherThreads, 1) q8_gather_kernel(const Q8Ga
             const long long cell = static_cast<long long>(block) * a.n_kv_heads + h;
             c[i] = __ldcs(static_cast<const uint4 *>(side ? a.v_cache : a.k_cache) +
                           (cell * a.block_size + row_of[row]) * kLanes + lane);
-            scale[i] = __ldg((side ? a.v_scales : a.k_scales) + cell);
+            scale[i] = (side ? a.v_scales : a.k_scales)[cell];
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {

@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
         scales_prev = scales_now;
         if (base + lane < u1) {
             const unsigned cell = tiles_now >> bs16_log2;
-            scales_now = make_float2(__ldg(a.k_scales + cell), __ldg(a.v_scales + cell));
+            scales_now = make_float2(__ldcg(a.k_scales + cell), __ldcg(a.v_scales + cell));
         }
     };
 

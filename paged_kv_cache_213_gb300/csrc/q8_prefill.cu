@@ -441,11 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 const unsigned piece = __shfl_sync(~0u, now, j & 31);
                 const long long src = static_cast<long long>(piece) * (16 * D);
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) xk[e][i] = __ldg(reinterpret_cast<const uint4 *>(kc + src + i * kAt * D));
+                for (int i = 0; i < kLoads; ++i) xk[e][i] = __ldcg(reinterpret_cast<const uint4 *>(kc + src + i * kAt * D));
 #pragma unroll
-                for (int i = 0; i < kLoads; ++i) xv[e][i] = __ldg(reinterpret_cast<const uint4 *>(vc + src + i * kAt * D));
-                ks[e] = __ldg(a.k_scales + (piece >> bs16_log2));
-                vs[e] = __ldg(a.v_scales + (piece >> bs16_log2));
+                for (int i = 0; i < kLoads; ++i) xv[e][i] = __ldcg(reinterpret_cast<const uint4 *>(vc + src + i * kAt * D));
+                ks[e] = __ldcg(a.k_scales + (piece >> bs16_log2));
+                vs[e] = __ldcg(a.v_scales + (piece >> bs16_log2));
             };
             // codes x of step j to `half` of the memory
             auto widen = [&](const uint4 (&x)[kLoads], int j, unsigned char *half) {

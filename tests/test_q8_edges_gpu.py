@@ -6,8 +6,8 @@ import torch
 
 import paged_kv_cache_213_gb300 as pkv
 
-from q8_util import Paged
-from test_q8_gpu import OnGpu, queries, starts, t
+from q8_util import Paged, append64, assert_attention, attend64
+from test_q8_gpu import KINDS, OnGpu, queries, same_state, starts, t
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,69 @@ def test_a_nan_query_has_a_nan_lse(news, L):
     want[news - 1, 3] = True
     assert np.array_equal(np.isnan(lse), want)
     assert np.array_equal(np.isnan(out), want[..., None].repeat(128, 2))
+
+
+# --- steps without a wait between them ----------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("news,bs", [(1, 16), (1, 256), (3, 16), (3, 64), (12, 16), (12, 128)])
+def test_flagged_attention_right_behind_an_append_that_grows_scales(kind, news, bs):
+    """Steps of append (each with larger tokens than the blocks hold, so that scales grow
+    and held codes are written anew) and attention under PKV_TABLES_READY, one behind the
+    other in a stream and in a replayed graph: every step's results, and the cache in the
+    end, by the definitions."""
+    Hk, g, d, steps = 2, 4, 128, 8
+    held = [0, 3, 15, 100, 40, 700, 17, 250]
+    B = len(held)
+    p = Paged([m + news * steps for m in held], Hk, d, bs, kind, seed=news + bs)
+    first = [t(c) for c in p.codes] + [t(s) for s in p.scales]
+    kv = [x.clone() for x in first]
+    gain = 2.0 ** np.arange(steps)
+    x = [[(gain[i] * p.rng.standard_normal((B * news, Hk, d))).astype(np.float16) for _ in "kv"] for i in range(steps)]
+    q = [queries(p, B * news, Hk * g) for _ in range(steps)]
+    lens = [[m + news * (i + 1) for m in held] for i in range(steps)]
+    at = starts([news] * B)
+    many = {} if news == 1 else dict(query_start=t(at), max_q_len=news)
+    ws = torch.zeros(pkv.q8_plan(B, B * news, news, Hk * g, Hk, d, bs, p.MB), dtype=torch.uint8, device="cuda")
+    tables, err = t(p.tables), torch.zeros(1, dtype=torch.int32, device="cuda")
+    tx, tq = [[t(y) for y in pair] for pair in x], [t(y) for y in q]
+    tl = [t(np.array(y, np.int32)) for y in lens]
+    out = [torch.empty_like(y) for y in tq]
+    lse = [torch.empty(y.shape[:2], device="cuda") for y in tq]
+    scale = 0.002
+
+    def chain():
+        for i in range(steps):
+            pkv.paged_kv_append_q8(*tx[i], *kv, tables, tl[i], err_word=err, **many)
+            pkv.paged_decode_attention_q8(tq[i], *kv, tables, tl[i], scale, out=out[i], lse=lse[i], workspace=ws,
+                                          err_word=err, flags=pkv.PKV_TABLES_READY, **many)
+
+    def results():
+        torch.cuda.synchronize()
+        assert pkv.get_error(err) == 0
+        return [[y.view(torch.uint8).cpu().numpy() for y in group] for group in (out, lse, kv)]
+
+    chain()
+    eager = results()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        with torch.cuda.graph(graph, stream=stream):
+            chain()
+        for _ in range(3):
+            for a, b in zip(kv, first):
+                a.copy_(b)
+            graph.replay()
+            again = results()
+            for a, b in zip(eager, again):
+                assert all(np.array_equal(y, z) for y, z in zip(a, b))
+    keys = 64 if news * g > 32 else 16
+    for i in range(steps):
+        for side in range(2):
+            append64(kind, x[i][side], at, lens[i], p.tables, p.codes[side], p.scales[side])
+        o, e = out[i].cpu().numpy(), lse[i].cpu().numpy()
+        for b, L in enumerate(lens[i]):
+            rows = slice(at[b], at[b + 1])
+            k, v = (p.tokens(s, b, L) for s in range(2))
+            ref = attend64(q[i][rows], k, v, scale, p.spread_in_steps(b, L, keys))
+            assert_attention(o[rows], e[rows], ref, f"step {i}, sequence {b}")
+    same_state(p, kv)
