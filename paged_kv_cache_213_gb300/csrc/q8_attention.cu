@@ -791,6 +791,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
                 }
             }
             whole = __shfl_sync(~0u, whole, 0);
+            __syncwarp();  // lane 0's acquire before every lane's loads of the other CTAs' records
             if (!whole) break;
         }
     }

@@ -23,3 +23,17 @@ def test_no_load_takes_the_path_for_memory_that_never_changes():
         assert not re.search(r"__ldg\b|ld\.global\.nc", _code(path)), path
     for path in early:
         assert "__restrict__" not in _code(path), path
+
+
+def test_an_acquire_by_one_lane_comes_before_the_other_lanes_loads():
+    """One lane counts an arrival with acquire order; the warp reads the records of those who
+    came before.  A shuffle hands the count over but orders no memory: a __syncwarp() has
+    to stand between (in the few-row kernel before the loop that reads starts again, in the
+    many-row kernel at the head of the loop of joins)."""
+    few = _code(os.path.join(CSRC, "q8_attention.cu"))
+    after = few[few.index("atomic_add_acq_rel_gpu("):]
+    until_break = after[:after.index("if (!whole) break;")]
+    assert until_break.index("__shfl_sync(") < until_break.index("__syncwarp();")
+    many = _code(os.path.join(CSRC, "q8_prefill.cu"))
+    after = many[many.index("atomic_add_acq_rel_gpu("):]
+    assert after.index("__syncwarp();") < after.index("__ldcg(")
