@@ -159,14 +159,15 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
             live = false;
         }
     }
+    const long long cell = block * a.n_kv_heads + h;
+    float *scales = side ? a.v_scales : a.k_scales;
+    const float had = live && row > 0 ? scales[cell] : 0.f;
     bool special;
     float top = top_of(x, &special);
 #pragma unroll
     for (int d = kTeam / 2; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    __syncwarp();  // every lane has read the old scale, which one lane writes below
     if (!live) return;
-    const long long cell = block * a.n_kv_heads + h;
-    float *scales = side ? a.v_scales : a.k_scales;
-    const float had = row > 0 ? scales[cell] : 0.f;
     int power;
     const float scale = grown<KIND>(had, top, &power);
     uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * a.block_size * kTeam + lane;

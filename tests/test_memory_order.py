@@ -37,3 +37,13 @@ def test_an_acquire_by_one_lane_comes_before_the_other_lanes_loads():
     many = _code(os.path.join(CSRC, "q8_prefill.cu"))
     after = many[many.index("atomic_add_acq_rel_gpu("):]
     assert after.index("__syncwarp();") < after.index("__ldcg(")
+
+
+def test_a_scale_is_read_by_all_before_one_lane_writes_it():
+    """All lanes of a team quantise by the old scale that they read; one of them writes the
+    new one.  A barrier has to stand between, in both append kernels."""
+    text = _code(os.path.join(CSRC, "q8_append.cu"))
+    for kernel in ("q8_append_one_kernel", "q8_append_many_kernel"):
+        body = text[text.index(kernel + "(const Q8AppendArgs a)"):]
+        read, write = body.index("scales[cell] : 0.f"), body.index("scales[cell] = scale;")
+        assert read < body.index("__syncwarp();", read) < write, kernel
