@@ -185,16 +185,19 @@ __global__ void __launch_bounds__(128) q8_append_one_kernel(const Q8AppendArgs a
 //
 // Which block: the blocks of sequence b get the numbers from start[b] / bs + 2 b on.
 // A run of n tokens touches at most n / bs + 2 blocks (rounded down), so the ranges do
-// not meet, and a CTA finds its sequence without a sum over the ones before.
+// not meet, and a CTA finds its sequence without a sum over the ones before.  Where starts
+// decrease (flagged) they may: the CTA then takes those that are in bounds one by one.
 //
 // 8 CTAs an SM, each with its rows on the way before it knows the scale.  5 prompts of 411
-// to 2903 tokens, 8 heads of 128 (51 MB): 13.0 us, 3.9 TB/s; by instructions (half of the issue
+// to 2903 tokens, 8 heads of 128 (51 MB): 12.8 us, 4.0 TB/s; by instructions (half of the issue
 // slots) and by starts and ends, which a transfer of 7.5 us does not hide.  2 or 8 warps a CTA,
 // 40 warps an SM: 12.9, 13.4, 12.9; 24 warps an SM 15.2.
+// (At 32 and 64 rows a warp: the CTAs that its registers leave room for without spills.)
 constexpr int kWarps = 4;
 
 template <int KIND, int D, int ROWS>  // rows of a warp
-__global__ void __launch_bounds__(kWarps * 32, ROWS == 16 ? 8 : 1) q8_append_many_kernel(const Q8AppendArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, ROWS == 16 ? 8 : ROWS * D == 32 * 64 ? 5 : ROWS * D == 64 * 128 ? 2 : 4)
+    q8_append_many_kernel(const Q8AppendArgs a) {
     constexpr int kTeam = D / kPiece;        // lanes of a row
     constexpr int kAt = 32 / kTeam;          // rows of one load
     constexpr int kSteps = ROWS / kAt;
@@ -202,91 +205,117 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 16 ? 8 : 1) q8_append_man
     allow_dependent_launch();
     struct Found {
         int b, start, n, len;
+        int more;  // its finder found others too
     };
     __shared__ Found found;
+    __shared__ int owner;
     __shared__ float tops[kWarps];
-    const long long v = blockIdx.x;
-    const int bs = a.block_size, side = blockIdx.z;
+    const int v = blockIdx.x;  // at most total / 16 + 2 * 2048
+    const int bs = a.block_size, bs_log2 = __ffs(bs) - 1, side = blockIdx.z;
     const bool reports = blockIdx.y == 0 && side == 0 && threadIdx.x == 0;
-    if (threadIdx.x == 0) found.b = -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < a.num_seqs; b += kWarps * 32) {
-        const int s = a.query_start[b], e = a.query_start[b + 1], len = a.context_lens[b];
-        if (s < 0 || e < s || e > a.total) {
-            if (v == 0 && blockIdx.y == 0 && side == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
-            continue;
+
+    auto append = [&](const Found f) {
+        const int slot = v - ((f.start >> bs_log2) + 2 * f.b);
+        if (f.n > a.max_q_len || f.n > f.len || f.len > static_cast<long long>(a.max_blocks_per_seq) * bs) {
+            if (reports && slot == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+            return;
         }
-        if (s / bs + 2ll * b <= v && v < e / bs + 2ll * (b + 1)) found = Found{b, s, e - s, len};
-    }
-    __syncthreads();
-    const Found f = found;
-    if (f.b < 0 || f.n == 0) return;
-    const int slot = static_cast<int>(v - (f.start / bs + 2ll * f.b));
-    if (slot < 0) return;  // of starts that decrease, which are flagged
-    if (f.n > a.max_q_len || f.n > f.len || f.len > static_cast<long long>(a.max_blocks_per_seq) * bs) {
-        if (reports && slot == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
-        return;
-    }
-    const int first = f.len - f.n, j = first / bs + slot;
-    if (static_cast<long long>(j) * bs >= f.len) return;
-    const long long block = a.block_tables[static_cast<long long>(f.b) * a.max_blocks_per_seq + j];
-    const int low = max(first - j * bs, 0), high = min(f.len - j * bs, bs);  // the new rows
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int per_head = bs / ROWS;          // warps of a head
-    const int h = blockIdx.y * (kWarps / per_head) + warp / per_head;
-    const int row0 = (warp % per_head) * ROWS + lane / kTeam;
-    const bool live = h < a.n_kv_heads;
-    const int hc = live ? h : 0;
-    // the tokens are read while the block's number is on its way
-    const uint4 *src = static_cast<const uint4 *>(side ? a.v_new : a.k_new) + hc * kTeam + lane % kTeam;
-    const long long stride = (side ? a.v_stride : a.k_stride) / kPiece;
-    const long long token0 = static_cast<long long>(f.start) - first + j * bs;  // token of row 0
-    uint4 x[kSteps];
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int row = row0 + i * kAt;
-        x[i] = make_uint4(0, 0, 0, 0);
-        if (live && row >= low && row < high) x[i] = __ldcs(src + (token0 + row) * stride);
-    }
-    if (block < 0 || block >= a.num_blocks) {
-        if (reports) flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
-        return;
-    }
-    const long long cell = block * a.n_kv_heads + hc;
-    float *scales = side ? a.v_scales : a.k_scales;
-    const float had = live && low > 0 ? scales[cell] : 0.f;
-    bool special;
-    float top = top_of(x, &special);
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    if (per_head > 1) {
-        if (lane == 0) tops[warp] = top;
-        __syncthreads();  // and every warp has read the old scale
-        for (int w = 0; w < per_head; ++w) top = fmaxf(top, tops[warp / per_head * per_head + w]);
-    }
-    if (!live) return;
-    __syncwarp();
-    int power;
-    const float scale = grown<KIND>(had, top, &power);
-    const Divisor divisor(scale);
-    uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * bs * kTeam + lane % kTeam;
-    if (!special && divisor.inv != 0.f) {
+        const int first = f.len - f.n, j = (first >> bs_log2) + slot;
+        if (static_cast<long long>(j) * bs >= f.len) return;
+        const long long block = a.block_tables[static_cast<long long>(f.b) * a.max_blocks_per_seq + j];
+        const int low = max(first - j * bs, 0), high = min(f.len - j * bs, bs);  // the new rows
+        int tid;  // read anew: rows and addresses are not kept for a second sequence
+        asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+        const int warp = tid / 32, lane = tid % 32;
+        const int per_head = bs / ROWS;          // warps of a head
+        const int h = blockIdx.y * (kWarps / per_head) + warp / per_head;
+        const int row0 = (warp % per_head) * ROWS + lane / kTeam;
+        const bool live = h < a.n_kv_heads;
+        const int hc = live ? h : 0;
+        // the tokens are read while the block's number is on its way
+        const uint4 *src = static_cast<const uint4 *>(side ? a.v_new : a.k_new) + hc * kTeam + lane % kTeam;
+        const long long stride = (side ? a.v_stride : a.k_stride) / kPiece;
+        const long long token0 = static_cast<long long>(f.start) - first + j * bs;  // token of row 0
+        uint4 x[kSteps];
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             const int row = row0 + i * kAt;
-            if (row >= low && row < high) rows[row * kTeam] = quantised<KIND, true>(x[i], divisor);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (live && row >= low && row < high) x[i] = __ldcs(src + (token0 + row) * stride);
         }
-    } else {
+        if (block < 0 || block >= a.num_blocks) {
+            if (reports) flag_error(a.err, PKV_ERRBIT_BLOCK_ID);
+            return;
+        }
+        const long long cell = block * a.n_kv_heads + hc;
+        float *scales = side ? a.v_scales : a.k_scales;
+        const float had = live && low > 0 ? scales[cell] : 0.f;
+        bool special;
+        float top = top_of(x, &special);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int row = row0 + i * kAt;
-            if (row >= low && row < high) rows[row * kTeam] = quantised<KIND, false>(x[i], divisor);
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        if (per_head > 1) {
+            if (lane == 0) tops[warp] = top;
+            __syncthreads();  // and every warp has read the old scale
+            for (int w = 0; w < per_head; ++w) top = fmaxf(top, tops[warp / per_head * per_head + w]);
         }
+        if (!live) return;
+        __syncwarp();
+        int power;
+        const float scale = grown<KIND>(had, top, &power);
+        const Divisor divisor(scale);
+        uint2 *rows = static_cast<uint2 *>(side ? a.v_cache : a.k_cache) + cell * bs * kTeam + lane % kTeam;
+        if (!special && divisor.inv != 0.f) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int row = row0 + i * kAt;
+                if (row >= low && row < high) rows[row * kTeam] = quantised<KIND, true>(x[i], divisor);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int row = row0 + i * kAt;
+                if (row >= low && row < high) rows[row * kTeam] = quantised<KIND, false>(x[i], divisor);
+            }
+        }
+        if (power > 0)
+            for (int row = row0; row < min(low, row0 - lane / kTeam + ROWS); row += kAt)
+                rows[row * kTeam] = shrunk<KIND>(rows[row * kTeam], power);
+        if (warp % per_head == 0 && lane == 0 && (low == 0 || scale != had)) scales[cell] = scale;
+    };
+
+    for (int last = -1;;) {  // the sequences behind it that have this number: one, with starts in order
+        Found mine{-1, 0, 0, 0, 0};
+        for (int b = threadIdx.x; b < a.num_seqs; b += kWarps * 32) {
+            const int s = a.query_start[b], e = a.query_start[b + 1], len = a.context_lens[b];
+            if (s < 0 || e < s || e > a.total) {
+                if (v == 0 && blockIdx.y == 0 && side == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
+                continue;
+            }
+            const int low = (s >> bs_log2) + 2 * b, end = (e >> bs_log2) + 2 * (b + 1);
+            if (v < low || v >= end || b <= last || e == s) continue;
+            if (mine.b < 0)
+                mine = Found{b, s, e - s, len, 0};
+            else
+                mine.more = 1;
+        }
+        if (mine.b >= 0) found = mine;
+        const int finders = __syncthreads_count(mine.b >= 0);
+        if (finders == 0) return;
+        if (finders > 1) {  // what they wrote may be mixed: the first sequence's finder writes again
+            if (threadIdx.x == 0) owner = a.num_seqs;
+            __syncthreads();
+            if (mine.b >= 0) atomicMin(&owner, mine.b);
+            __syncthreads();
+            if (mine.b == owner) found = mine;
+            __syncthreads();
+        }
+        const Found f = found;
+        append(f);
+        if (finders == 1 && !f.more) return;
+        last = f.b;
+        __syncthreads();
     }
-    if (power > 0)
-        for (int row = row0; row < min(low, row0 - lane / kTeam + ROWS); row += kAt)
-            rows[row * kTeam] = shrunk<KIND>(rows[row * kTeam], power);
-    if (warp % per_head == 0 && lane == 0 && (low == 0 || scale != had)) scales[cell] = scale;
 }
 
 template <int KIND, int D>

@@ -115,3 +115,51 @@ def test_flagged_attention_right_behind_an_append_that_grows_scales(kind, news, 
             ref = attend64(q[i][rows], k, v, scale, p.spread_in_steps(b, L, keys))
             assert_attention(o[rows], e[rows], ref, f"step {i}, sequence {b}")
     same_state(p, kv)
+
+
+# --- starts that decrease -------------------------------------------------------
+
+def _append_with(p, start, total, most, kind):
+    """Appends with these starts to a copy of p's tensors (five times, each the same), and
+    to p by the definition: sequences in bounds alone."""
+    x = [p.rng.standard_normal((total, *p.codes[0].shape[1::2])).astype(np.float16) for _ in "kv"]
+    first = [t(c) for c in p.codes] + [t(s) for s in p.scales]
+    for side in range(2):
+        for b, (s, e) in enumerate(zip(start[:-1], start[1:])):
+            L = int(p.lens[b])
+            if 0 <= s <= e <= total and e - s <= min(most, L) and L <= p.MB * p.codes[0].shape[2]:
+                append64(kind, x[side], [s, e], [L], p.tables[b:b + 1], p.codes[side], p.scales[side])
+    for _ in range(5):
+        kv, err = [y.clone() for y in first], torch.zeros(1, dtype=torch.int32, device="cuda")
+        pkv.paged_kv_append_q8(t(x[0]), t(x[1]), *kv, t(p.tables), t(p.lens.astype(np.int32)),
+                               query_start=t(np.array(start, np.int32)), max_q_len=most, err_word=err)
+        assert pkv.get_error(err) == pkv.PKV_ERRBIT_CONTEXT
+        same_state(p, kv)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bs,start", [
+    (16, [0, 200, 100, 200]),
+    (16, [0, 150, 40, 90, 10, 200, 200]),
+    (64, [50, 200, 0, 60, 300, 10]),
+    (128, [100, 0, 150, 20, 199, -1, 3]),
+    (256, [0, 200, 0, 200, 0, 200]),
+])
+def test_sequences_in_bounds_are_written_where_others_are_not(kind, bs, start):
+    """Starts that decrease, so that several sequences have rows in common, and entries that
+    are out of bounds: those sequences are flagged and nothing of them is written; all
+    others are, the same each time."""
+    p = Paged([230 + 7 * b for b in range(len(start) - 1)], 3, 64, bs, kind, seed=bs)
+    _append_with(p, start, 200, 200, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("most", [1, 2, 40])
+def test_many_sequences_in_no_order(kind, most):
+    rng = np.random.default_rng(most)
+    B, total = 400, 300
+    start = rng.integers(0, total, B + 1)
+    start[1::2] = np.minimum(start[::2][:B // 2] + rng.integers(0, most + 2, B // 2), total + 2)
+    p = Paged(rng.integers(1, 90, B), 2, 128, 16, kind, seed=most)
+    p.lens[::37] = 10 ** 6
+    _append_with(p, start, total, most, kind)
