@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(kWarps * 32, ROWS == 16 ? 8 : ROWS * D == 32 *
         Found mine{-1, 0, 0, 0, 0};
         for (int b = threadIdx.x; b < a.num_seqs; b += kWarps * 32) {
             const int s = a.query_start[b], e = a.query_start[b + 1], len = a.context_lens[b];
-            if (s < 0 || e < s || e > a.total) {
+            if (s < 0 || e < s || e > a.total ||
+                (e == s && (len < 0 || len > static_cast<long long>(a.max_blocks_per_seq) * bs))) {
                 if (v == 0 && blockIdx.y == 0 && side == 0) flag_error(a.err, PKV_ERRBIT_CONTEXT);
                 continue;
             }

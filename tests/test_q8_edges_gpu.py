@@ -163,3 +163,19 @@ def test_many_sequences_in_no_order(kind, most):
     p = Paged(rng.integers(1, 90, B), 2, 128, 16, kind, seed=most)
     p.lens[::37] = 10 ** 6
     _append_with(p, start, total, most, kind)
+
+
+@pytest.mark.parametrize("news", [[3, 0, 2], [1, 0, 1]])
+@pytest.mark.parametrize("length", [-1, 49, 10 ** 6])
+def test_a_length_out_of_bounds_is_flagged_without_new_tokens_too(news, length):
+    """In the kernel for single tokens and in the one for several; the others are written."""
+    p = Paged([40, 20, 41], 2, 64, 16, "int8", seed=5)
+    x = [p.rng.standard_normal((sum(news), 2, 64)).astype(np.float16) for _ in "kv"]
+    kv, lens = [t(c) for c in p.codes] + [t(s) for s in p.scales], np.array([40, length, 41], np.int32)
+    for side in range(2):
+        append64("int8", x[side], starts(news), p.lens, p.tables, p.codes[side], p.scales[side])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pkv.paged_kv_append_q8(t(x[0]), t(x[1]), *kv, t(p.tables), t(lens), query_start=t(starts(news)),
+                           max_q_len=max(news), err_word=err)
+    assert pkv.get_error(err) == pkv.PKV_ERRBIT_CONTEXT
+    same_state(p, kv)
