@@ -103,7 +103,10 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  *  max_context_len, block_tables, context_lens, err_word, cuda_stream: as for
  *                 paged_decode_attention_multi
  *  workspace      device scratch of at least paged_decode_q8_plan's bytes,
- *                 256-byte aligned.  Its first PKV_WORKSPACE_COUNTER_BYTES
+ *                 256-byte aligned.  A plan's bytes are enough for every call
+ *                 with the same n_kv_heads and head_dim whose other sizes are
+ *                 no larger: one for a loop's largest call serves the loop.
+ *                 Its first PKV_WORKSPACE_COUNTER_BYTES
  *                 bytes hold arrival counters: zero before the first use, and
  *                 left at zero by every call, also by one that flags
  *                 PKV_ERRBIT_TIMEOUT.  After PKV_ERRBIT_WORKSPACE (a

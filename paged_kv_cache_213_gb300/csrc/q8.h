@@ -93,6 +93,9 @@ struct Q8Split {
 // false: more than 2^31 units of work.
 bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
               int max_len, int sms, Q8Split *sp);
+// Workspace bytes that are enough for calls of these sizes and of smaller ones.
+size_t q8_plan_bytes(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
+                     int max_len, int sms);
 bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
                       int max_len, int sms, Q8Split *sp);
 cudaError_t launch_q8_prefill(const Q8AttentionArgs &a, int kind, const Q8Split &sp,

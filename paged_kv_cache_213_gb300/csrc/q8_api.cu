@@ -59,6 +59,7 @@ struct Plan {
     int max_len;
     bool empty;  // nothing to launch
     pkv::Q8Split split;
+    size_t bytes;  // for this call and smaller ones
 };
 
 int make_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
@@ -78,7 +79,7 @@ int make_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int n_kv_
     if (max_len > cap) max_len = cap;
     plan->max_len = static_cast<int>(max_len);
     plan->empty = num_seqs == 0 || total_q == 0 || max_q_len == 0;
-    plan->split.ws_bytes = 0;
+    plan->split.ws_bytes = plan->bytes = 0;
     if (plan->empty) return PKV_OK;
     int sms = 0;
     if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
@@ -86,6 +87,7 @@ int make_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int n_kv_
     const int most = max_q_len < total_q ? max_q_len : total_q;
     if (!pkv::q8_split(num_seqs, most, n_q_heads, n_kv_heads, head_dim, plan->max_len, sms, &plan->split))
         return PKV_ERR_UNSUPPORTED;
+    plan->bytes = pkv::q8_plan_bytes(num_seqs, most, n_q_heads, n_kv_heads, head_dim, plan->max_len, sms);
     return PKV_OK;
 }
 
@@ -142,7 +144,7 @@ int paged_decode_q8_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads
     Plan plan{};
     const int rc = make_plan(num_seqs, total_q, max_q_len, n_q_heads, n_kv_heads, head_dim, block_size,
                              max_blocks_per_seq, max_context_len, &plan);
-    if (rc == PKV_OK && workspace_bytes_out) *workspace_bytes_out = plan.split.ws_bytes;
+    if (rc == PKV_OK && workspace_bytes_out) *workspace_bytes_out = plan.bytes;
     return rc;
 }
 

@@ -34,6 +34,7 @@
 // it (255 registers a thread, two warps a scheduler).
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "pkv_internal.h"
@@ -830,26 +831,48 @@ static_assert(fits<1>() && fits<2>() && fits<3>() && fits<4>(), "shared memory")
 
 }  // namespace
 
+namespace {
+
+constexpr int kFewRows = 32;
+
+// The split of up to that many rows of a KV head.
+Q8Split split_of_rows(int rows, int head_dim, int sms) {
+    Q8Split sp{};
+    sp.row_tiles = (rows + 7) / 8;
+    const int warps = sp.row_tiles <= 2 ? Shape<128, 2>::kWarps : Shape<128, 4>::kWarps;
+    static_assert(Shape<128, 1>::kWarps == Shape<128, 2>::kWarps && Shape<128, 3>::kWarps == Shape<128, 4>::kWarps, "");
+    const int most = kBalancedMaxWorkers / (2 * sp.row_tiles);  // a counter for four rows of each
+    sp.ctas = std::min(sms, most);
+    sp.record_rows = rows;
+    sp.ws_bytes = kBalancedCounterBytes +
+                  static_cast<size_t>(sp.ctas) * (warps + 2) * q8_record_floats(rows, head_dim) * sizeof(float);
+    return sp;
+}
+
+}  // namespace
+
 bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
               int sms, Q8Split *sp) {
     const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
     // Up to 32 rows here, more on tcgen05 (24 sequences of 200-2900 tokens, four heads a
     // group; this kernel and that one, us): 12 rows 26.1, 50.4; 20 rows 36.1, 49.4; 32 rows
     // 46.4, 48.5; 64 rows, twice 32 here, 55.1, 49.3
-    if (rows > 32) return q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, sp);
-    sp->row_tiles = static_cast<int>((rows + 7) / 8);
-    sp->tile_tokens = 0;
+    if (rows > kFewRows) return q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, sp);
     const double units = static_cast<double>(num_seqs) * n_kv_heads * ((static_cast<double>(max_len) + kTile - 1) / kTile);
     if (units >= 2147483648.0) return false;
-    sp->ctas = sms;
-    const int warps = sp->row_tiles <= 2 ? Shape<128, 2>::kWarps : Shape<128, 4>::kWarps;
-    static_assert(Shape<128, 1>::kWarps == Shape<128, 2>::kWarps && Shape<128, 3>::kWarps == Shape<128, 4>::kWarps, "");
-    const int most = kBalancedMaxWorkers / (2 * sp->row_tiles);  // a counter for four rows of each
-    if (sp->ctas > most) sp->ctas = most;
-    sp->record_rows = static_cast<int>(rows);
-    sp->ws_bytes = kBalancedCounterBytes +
-                   static_cast<size_t>(sp->ctas) * (warps + 2) * q8_record_floats(sp->record_rows, head_dim) * sizeof(float);
+    *sp = split_of_rows(static_cast<int>(rows), head_dim, sms);
     return true;
+}
+
+size_t q8_plan_bytes(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len, int sms) {
+    const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
+    // fewer rows may take more: they have more warps, whose records are apart
+    size_t bytes = 0;
+    for (int r = 1; r <= kFewRows && r <= rows; ++r) bytes = std::max(bytes, split_of_rows(r, head_dim, sms).ws_bytes);
+    Q8Split sp{};
+    if (rows > kFewRows && q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, &sp))
+        bytes = std::max(bytes, sp.ws_bytes);
+    return bytes;
 }
 
 cudaError_t launch_q8_attention(const Q8AttentionArgs &a, int kind, const Q8Split &sp,

@@ -109,7 +109,8 @@ def paged_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block
 
 def q8_plan(num_seqs, total_q, max_q_len, n_q_heads, n_kv_heads, head_dim, block_size,
             max_blocks_per_seq, max_context_len=0):
-    """Workspace bytes of paged_decode_attention_q8 on the current device."""
+    """Workspace bytes of paged_decode_attention_q8 on the current device, for calls of
+    these sizes and of smaller ones."""
     W = ctypes.c_size_t(0)
     _check("paged_decode_q8_plan",
            _lib().paged_decode_q8_plan(num_seqs, total_q, max_q_len, n_q_heads, n_kv_heads,

@@ -179,3 +179,34 @@ def test_a_length_out_of_bounds_is_flagged_without_new_tokens_too(news, length):
                            max_q_len=max(news), err_word=err)
     assert pkv.get_error(err) == pkv.PKV_ERRBIT_CONTEXT
     same_state(p, kv)
+
+
+# --- plans ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_plan_never_falls_as_its_sizes_grow(d):
+    def plan(**change):
+        base = dict(num_seqs=9, total_q=300, max_q_len=1, n_q_heads=8, n_kv_heads=2, head_dim=d, block_size=16,
+                    max_blocks_per_seq=500, max_context_len=700)
+        return pkv.q8_plan(**{**base, **change})
+
+    for name, values in (("max_q_len", range(1, 301)), ("total_q", range(1, 301)), ("num_seqs", range(1, 60)),
+                         ("max_context_len", range(1, 8000, 61)), ("n_q_heads", range(2, 257, 2))):
+        for other in ({}, dict(max_q_len=5), dict(max_q_len=40)):
+            if name == "total_q":
+                other = dict(max_q_len=300)
+            got = [plan(**{**other, name: v}) for v in values]
+            assert got == sorted(got), (name, other)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("g,most", [(4, 5), (4, 8), (1, 17), (8, 16), (2, 33)])
+def test_a_workspace_for_the_largest_call_serves_smaller_ones(kind, g, most):
+    Hk, d = 2, 128
+    p = Paged([700, 90, 333], Hk, d, 16, kind, seed=most)
+    gpu = OnGpu(p)
+    ws = torch.zeros(pkv.q8_plan(3, 3 * most, most, Hk * g, Hk, d, 16, p.MB), dtype=torch.uint8, device="cuda")
+    for n in range(1, most + 1):
+        gpu.check(queries(p, 3 * n, Hk * g), 0.1, [n] * 3, workspace=ws)
+        if n == 1:
+            gpu.check(queries(p, 3, Hk * g), 0.1, workspace=ws)
