@@ -18,7 +18,8 @@
  *
  * Limits of every call: head_dim 64 or 128, block_size 16, 32, 64, 128 or 256,
  * at most 2048 sequences, fewer than 2^31 rows of all blocks and heads in a
- * cache (PKV_ERR_UNSUPPORTED beyond).
+ * cache, for attention about 2^31 tiles of 16 tokens and KV head by
+ * max_context_len (PKV_ERR_UNSUPPORTED beyond).
  */
 #ifndef PAGEDKV_Q8_H
 #define PAGEDKV_Q8_H

@@ -90,14 +90,15 @@ struct Q8Split {
     int tile_tokens;  // of q8_prefill.cu: tokens of a tile of 128 rows
     size_t ws_bytes;
 };
-// false: more than 2^31 units of work.
-bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
-              int max_len, int sms, Q8Split *sp);
+// Units of work that a call may have: they are counted in ints, some thousands ahead.
+constexpr double kQ8MaxUnits = 2147483648.0 - 65536.0;
+bool q8_fits(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int max_len);
+bool q8_prefill_fits(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int max_len);
+// Of sizes that fit.
+Q8Split q8_split(int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int sms);
+Q8Split q8_prefill_split(int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int sms);
 // Workspace bytes that are enough for calls of these sizes and of smaller ones.
-size_t q8_plan_bytes(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
-                     int max_len, int sms);
-bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
-                      int max_len, int sms, Q8Split *sp);
+size_t q8_plan_bytes(int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int sms);
 cudaError_t launch_q8_prefill(const Q8AttentionArgs &a, int kind, const Q8Split &sp,
                               cudaStream_t stream);
 cudaError_t launch_q8_attention(const Q8AttentionArgs &a, int kind, const Q8Split &sp,

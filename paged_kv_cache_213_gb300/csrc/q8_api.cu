@@ -81,13 +81,13 @@ int make_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int n_kv_
     plan->empty = num_seqs == 0 || total_q == 0 || max_q_len == 0;
     plan->split.ws_bytes = plan->bytes = 0;
     if (plan->empty) return PKV_OK;
-    int sms = 0;
-    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
     // no sequence has more new tokens than there are
     const int most = max_q_len < total_q ? max_q_len : total_q;
-    if (!pkv::q8_split(num_seqs, most, n_q_heads, n_kv_heads, head_dim, plan->max_len, sms, &plan->split))
-        return PKV_ERR_UNSUPPORTED;
-    plan->bytes = pkv::q8_plan_bytes(num_seqs, most, n_q_heads, n_kv_heads, head_dim, plan->max_len, sms);
+    if (!pkv::q8_fits(num_seqs, most, n_q_heads, n_kv_heads, plan->max_len)) return PKV_ERR_UNSUPPORTED;
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    plan->split = pkv::q8_split(most, n_q_heads, n_kv_heads, head_dim, sms);
+    plan->bytes = pkv::q8_plan_bytes(most, n_q_heads, n_kv_heads, head_dim, sms);
     return PKV_OK;
 }
 

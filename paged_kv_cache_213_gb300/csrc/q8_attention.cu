@@ -849,29 +849,32 @@ Q8Split split_of_rows(int rows, int head_dim, int sms) {
     return sp;
 }
 
-}  // namespace
-
-bool q8_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
-              int sms, Q8Split *sp) {
-    const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
-    // Up to 32 rows here, more on tcgen05 (24 sequences of 200-2900 tokens, four heads a
-    // group; this kernel and that one, us): 12 rows 26.1, 50.4; 20 rows 36.1, 49.4; 32 rows
-    // 46.4, 48.5; 64 rows, twice 32 here, 55.1, 49.3
-    if (rows > kFewRows) return q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, sp);
-    const double units = static_cast<double>(num_seqs) * n_kv_heads * ((static_cast<double>(max_len) + kTile - 1) / kTile);
-    if (units >= 2147483648.0) return false;
-    *sp = split_of_rows(static_cast<int>(rows), head_dim, sms);
-    return true;
+// Up to 32 rows here, more on tcgen05 (24 sequences of 200-2900 tokens, four heads a
+// group; this kernel and that one, us): 12 rows 26.1, 50.4; 20 rows 36.1, 49.4; 32 rows
+// 46.4, 48.5; 64 rows, twice 32 here, 55.1, 49.3
+long long rows_of(int max_q_len, int n_q_heads, int n_kv_heads) {
+    return static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
 }
 
-size_t q8_plan_bytes(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len, int sms) {
-    const long long rows = static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
+}  // namespace
+
+bool q8_fits(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int max_len) {
+    if (rows_of(max_q_len, n_q_heads, n_kv_heads) > kFewRows)
+        return q8_prefill_fits(num_seqs, max_q_len, n_q_heads, n_kv_heads, max_len);
+    return static_cast<double>(num_seqs) * n_kv_heads * ((static_cast<double>(max_len) + kTile - 1) / kTile) <= kQ8MaxUnits;
+}
+
+Q8Split q8_split(int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int sms) {
+    const long long rows = rows_of(max_q_len, n_q_heads, n_kv_heads);
+    return rows > kFewRows ? q8_prefill_split(max_q_len, n_q_heads, n_kv_heads, head_dim, sms)
+                           : split_of_rows(static_cast<int>(rows), head_dim, sms);
+}
+
+size_t q8_plan_bytes(int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int sms) {
+    const long long rows = rows_of(max_q_len, n_q_heads, n_kv_heads);
     // fewer rows may take more: they have more warps, whose records are apart
-    size_t bytes = 0;
+    size_t bytes = rows > kFewRows ? q8_prefill_split(max_q_len, n_q_heads, n_kv_heads, head_dim, sms).ws_bytes : 0;
     for (int r = 1; r <= kFewRows && r <= rows; ++r) bytes = std::max(bytes, split_of_rows(r, head_dim, sms).ws_bytes);
-    Q8Split sp{};
-    if (rows > kFewRows && q8_prefill_split(num_seqs, max_q_len, n_q_heads, n_kv_heads, head_dim, max_len, sms, &sp))
-        bytes = std::max(bytes, sp.ws_bytes);
     return bytes;
 }
 

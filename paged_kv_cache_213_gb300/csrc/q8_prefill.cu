@@ -798,21 +798,24 @@ static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 2048, "shared memory");
 
 }  // namespace
 
-// The same plan as q8_split for the kernel of this file.
-bool q8_prefill_split(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int max_len,
-                      int sms, Q8Split *sp) {
-    const int group = n_q_heads / n_kv_heads;
-    sp->tile_tokens = kRows / group;
+bool q8_prefill_fits(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int max_len) {
+    const int tile_tokens = kRows / (n_q_heads / n_kv_heads);
     const double steps = (static_cast<double>(max_len) + kKeys - 1) / kKeys + 1;
-    const double pairs = static_cast<double>(max_q_len) / (2 * sp->tile_tokens) + 1;
-    if (static_cast<double>(num_seqs) * n_kv_heads * pairs * steps >= 2147483648.0) return false;
-    sp->row_tiles = 0;
-    sp->ctas = sms < kBalancedMaxWorkers / 8 ? sms : kBalancedMaxWorkers / 8;  // a counter for each warp of rows
+    const double pairs = static_cast<double>(max_q_len) / (2 * tile_tokens) + 1;
+    return static_cast<double>(num_seqs) * n_kv_heads * pairs * steps <= kQ8MaxUnits;
+}
+
+// q8_split for the kernel of this file.
+Q8Split q8_prefill_split(int max_q_len, int n_q_heads, int n_kv_heads, int head_dim, int sms) {
+    const int group = n_q_heads / n_kv_heads;
+    Q8Split sp{};
+    sp.tile_tokens = kRows / group;
+    sp.ctas = sms < kBalancedMaxWorkers / 8 ? sms : kBalancedMaxWorkers / 8;  // a counter for each warp of rows
     // rows of a pair that may be some: those of one tile, or of both
-    sp->record_rows = max_q_len > sp->tile_tokens ? kPair : (max_q_len * group + 31) / 32 * 32;
-    sp->ws_bytes = kBalancedCounterBytes +
-                   static_cast<size_t>(sp->ctas) * 2 * (head_dim / 4 + 1) * sp->record_rows * sizeof(float4);
-    return true;
+    sp.record_rows = max_q_len > sp.tile_tokens ? kPair : (max_q_len * group + 31) / 32 * 32;
+    sp.ws_bytes = kBalancedCounterBytes +
+                  static_cast<size_t>(sp.ctas) * 2 * (head_dim / 4 + 1) * sp.record_rows * sizeof(float4);
+    return sp;
 }
 
 cudaError_t launch_q8_prefill(const Q8AttentionArgs &a, int kind, const Q8Split &sp, cudaStream_t stream) {
