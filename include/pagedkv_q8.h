@@ -89,7 +89,8 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  * position; query head h reads KV head h / (n_q_heads / n_kv_heads), any
  * whole ratio up to 128 (PKV_ERR_UNSUPPORTED beyond).  Up to 32 query rows of
  * a KV head (max_q_len times that ratio) are streamed through one kernel; more
- * go in tiles of 128 rows to another, on tcgen05.  out and q do not overlap.
+ * go in tiles of 128 rows to another, on tcgen05 (max_context_len up to 2^25
+ * there, PKV_ERR_UNSUPPORTED beyond).  out and q do not overlap.
  *
  *  q              device fp16, token i's n_q_heads * head_dim entries at
  *                 element i * q_stride (a multiple of 8)

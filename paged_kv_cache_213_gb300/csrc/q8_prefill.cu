@@ -51,6 +51,10 @@ constexpr int kQPlane = kRows * 128, kPlane = kKeys * 128;  // rows of 64 fp16, 
 constexpr float kLag = 8.f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kStages = 4;  // of the ring of K and V
+// Most waits last a step, two a piece: a tile's queries wait for the scores of the piece before, and
+// the softmax of a tile without rows for the next piece's.  2^25 tokens are 0.6 s at 1.1 us a
+// step, within what a wait may take.
+constexpr int kMaxTokens = 1 << 25;
 
 template <int D>
 struct Cfg {
@@ -799,6 +803,7 @@ static_assert(Cfg<128>::smem(kQ8MaxSeqs) <= 227 * 1024 - 2048, "shared memory");
 }  // namespace
 
 bool q8_prefill_fits(int num_seqs, int max_q_len, int n_q_heads, int n_kv_heads, int max_len) {
+    if (max_len > kMaxTokens) return false;
     const int tile_tokens = kRows / (n_q_heads / n_kv_heads);
     const double steps = (static_cast<double>(max_len) + kKeys - 1) / kKeys + 1;
     const double pairs = static_cast<double>(max_q_len) / (2 * tile_tokens) + 1;

@@ -26,3 +26,11 @@ def test_units_stay_within_their_counters(plan):
     assert plan(1, 1, 127, 127, 16909320 * 16) == UNSUPPORTED
     assert plan(2047, 1, 1, 1, 1049088 * 16) == UNSUPPORTED  # 2^31 - 512
     assert plan(1, 1, 127, 127, 16908800 * 16) != UNSUPPORTED  # 2^31 - 66048
+
+
+def test_no_wait_of_the_kernel_for_many_rows_lasts_a_second(plan):
+    """Some of its waits last a piece, all keys of a pair of tiles."""
+    assert plan(1, 33, 1, 1, (1 << 25) + 1) == UNSUPPORTED
+    assert plan(1, 5, 8, 1, 1 << 26) == UNSUPPORTED
+    assert plan(1, 33, 1, 1, 1 << 25) != UNSUPPORTED
+    assert plan(1, 32, 1, 1, 1 << 26) != UNSUPPORTED
