@@ -14,7 +14,8 @@
  * Layout: codes [num_blocks][n_kv_heads][block_size][head_dim], one byte each,
  * as in pagedkv.h; k_scales and v_scales fp32 [num_blocks][n_kv_heads].  Block
  * tables, ownership, errors and the error word are those of pagedkv.h.  Scales
- * are 0 or between 2^-100 and 2^100 (what the append writes is).
+ * are 0 or between 2^-100 and 2^64 (the append writes 2^-33 to 2^11 from fp16
+ * where it finds none).
  *
  * Limits of every call: head_dim 64 or 128, block_size 16, 32, 64, 128 or 256,
  * at most 2048 sequences, fewer than 2^31 rows of all blocks and heads in a
@@ -120,8 +121,8 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  * Logits, softmax and sums in fp32; the weights times their block's V scale
  * are rounded to fp16 for the product with the codes, which are exact: off by
  * 2^-11 of themselves, or where that is more by 2^-19 of the block's V scale
- * (with more than 32 rows: of the largest V scale among 64 tokens), the largest
- * weight of the row being 1.  Rows
+ * (with more than 32 rows: of the largest V scale among 64 tokens; of 2^-26 at
+ * least), the largest weight of the row being 1.  Rows
  * behind a sequence's length never reach a result, whatever they hold.  A
  * cached NaN makes the queries that attend it NaN; one of a sequence's newest
  * tokens may also reach that sequence's earlier queries.

@@ -568,9 +568,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kWarps * 32, 1) q8_attention_ker
             if (__any_sync(~0u, move)) {
                 float g = 1.f;
                 if (v_scale > 0.f && !(v_scale >= w * (1.f / 64.f) && v_scale <= w * 16.f)) {
-                    inv_w = __fdividef(1.f, v_scale);
+                    const float to = fmaxf(v_scale, kQ8LeastReference);
+                    inv_w = __fdividef(1.f, to);
                     g = w * inv_w;
-                    w = v_scale;
+                    w = to;
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {

@@ -49,4 +49,11 @@ __device__ __forceinline__ uint32_t q8_widen(uint32_t w) {
     return r;
 }
 
+// The least reference of sums of values, whose scales go up to 2^64.  A weight's rounding (half a
+// subnormal step of fp16, 2^-25, times the code) is below 2^-41 there, nothing in an fp16
+// result, and so is what smaller scales lose.  The sums' factor from one reference to the next
+// is between 2^-90 and 2^90: finite, so that a sum of 0 stays 0, and exact enough where it is
+// small.  A sum that overflows by it is one of values above 2^102.
+constexpr float kQ8LeastReference = 0x1p-26f;
+
 }  // namespace pkv

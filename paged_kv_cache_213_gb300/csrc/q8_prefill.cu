@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                 tmem_ld32(x[0], here);
                 tmem_ld32(x[1], here + 32);
                 const float *fg = sh.f[slot], *vg = sh.v[slot];
-                float most = 0.f;
+                float most = kQ8LeastReference;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) most = fmaxf(most, vg[g]);
                 tmem_wait_ld();
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) q8_prefill_kernel(const Q8Attenti
                     m0 = max3(m0, __uint_as_float(z[14]), __uint_as_float(z[15]));
                     top = fmaxf(top, fmaxf(m0, m1) * fg[g]);
                 }
-                const bool far = most > 0.f && !(most >= wv * (1.f / 64.f) && most <= wv * 16.f);
+                const bool far = !(most >= wv * (1.f / 64.f) && most <= wv * 16.f);
                 float fac = 1.f;
                 if (far) {
                     inv_w = __fdividef(1.f, most);

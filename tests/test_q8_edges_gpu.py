@@ -210,3 +210,54 @@ def test_a_workspace_for_the_largest_call_serves_smaller_ones(kind, g, most):
         gpu.check(queries(p, 3 * n, Hk * g), 0.1, [n] * 3, workspace=ws)
         if n == 1:
             gpu.check(queries(p, 3, Hk * g), 0.1, workspace=ws)
+
+
+# --- scales at the ends of their range ---------------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("news", [1, 5, 40])
+@pytest.mark.parametrize("large", ["zeros", "values"])
+def test_v_scales_from_the_least_to_the_largest(kind, d, news, large):
+    """Blocks of 64 tokens (a step of the kernel for many rows) of V scale 2^64 and 2^-100 next
+    to ordinary ones, in many orders.  Where the large ones hold zeros the result is that
+    of the others; where they hold numbers it is infinite and of the right sign."""
+    Hk, g, bs, n = 2, 4, 64, 12
+    p = Paged([n * bs] * 8 + [50 * bs], Hk, d, bs, kind, seed=d + news)
+    tiny, huge = np.float32(2.0 ** -100), np.float32(2.0 ** 64)
+    for b in range(9):
+        for j in range(n):
+            ids = p.tables[b, j]
+            pick = p.rng.integers(0, 4)
+            if pick == 0:
+                p.scales[1][ids] = tiny
+            elif pick == 1:
+                p.scales[1][ids] *= np.float32(2.0 ** -12)
+            elif pick == 2 and large == "zeros":
+                p.scales[1][ids] = huge
+                p.codes[1][ids] = 0
+    if large == "values":  # one block: sums of one sign or the other in each column
+        for b in range(8):
+            p.scales[1][p.tables[b, b]] = huge
+            p.codes[1][p.tables[b, b]] = np.abs(p.codes[1][p.tables[b, b]].astype(np.int16) % 100) + 1
+            if kind == "e4m3":
+                p.codes[1][p.tables[b, b], :, :, ::2] |= 128
+            else:
+                p.codes[1][p.tables[b, b], :, :, ::2] *= -1
+    times = 40  # the same sequences again and again, so that a warp goes through several blocks
+    p.tables, p.lens = np.tile(p.tables, (times, 1)), np.tile(p.lens, times)
+    gpu = OnGpu(p)
+    B = len(p.lens)
+    q, at = queries(p, B * news, Hk * g), starts([news] * B)
+    out, lse = gpu.attend(t(q), 0.1, None if news == 1 else [news] * B)
+    gpu.keys = 64 if news * g > 32 else 16
+    for b in range(0, B, 7 if news == 1 else 31):
+        if large == "zeros" or b % 9 == 8:
+            gpu.near(b, q, out, lse, 0.1, at)
+    if large == "values":
+        want = np.full((news, Hk * g, d), np.inf)
+        want[..., ::2] = -np.inf
+        for b in range(B):
+            if b % 9 < 8:
+                assert np.array_equal(out[at[b]:at[b + 1]].astype(np.float64), want), b
+        assert np.isfinite(lse).all()
