@@ -116,8 +116,9 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  *                 counter that did not start at zero) clear them with
  *                 paged_decode_workspace_clear.  Calls that overlap in time
  *                 need separate workspaces.
- *  flags          0 or PKV_TABLES_READY, which covers query_start too (made
- *                 use of up to 32 rows)
+ *  flags          0 or PKV_TABLES_READY, which covers query_start too, and
+ *                 err_word where the kernel before clears it (made use of up
+ *                 to 32 rows)
  * Logits, softmax and sums in fp32; the weights times their block's V scale
  * are rounded to fp16 for the product with the codes, which are exact: off by
  * 2^-11 of themselves, or where that is more by 2^-19 of the block's V scale
@@ -145,8 +146,10 @@ int paged_decode_attention_q8(void *out, const void *q, int64_t q_stride, const 
 
 /*
  * Cached tokens back in fp16, in token order: row start[b] + j of k and v is
- * token j of sequence b, j < start[b + 1] - start[b], value = code * scale to
- * nearest even, at most 65504 in size.
+ * token j of sequence b, j < start[b + 1] - start[b], value = code * scale
+ * rounded to fp32 and that to fp16, each to nearest even, at most 65504 in size
+ * (one product in some 20000 has more bits than fp32 and lands next to a tie of
+ * fp16: there the two roundings differ from one).
  *  start          device int32 [num_seqs + 1], non-decreasing, start[0] >= 0
  *  total          rows of the outputs; rows outside [start[0],
  *                 start[num_seqs]) are left as they were

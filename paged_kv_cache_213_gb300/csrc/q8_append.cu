@@ -416,7 +416,9 @@ __global__ void __launch_bounds__(kGatherThreads, 1) q8_gather_kernel(const Q8Ga
             for (int k = 0; k < 8; ++k) {
                 const uint32_t u = k % 2 ? q8_widen<KIND, 1>(w[k / 2]) : q8_widen<KIND, 0>(w[k / 2]);
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u));
-                // a NaN code stays NaN: the comparisons of the clamp are false for it
+                // rounded to fp32 here and to fp16 below (a product has 28 or 31 bits: one rounding alone
+                // would take its residual as well, for one entry in 20000).  A NaN code stays NaN: the
+                // comparisons of the clamp are false for it
                 float p0 = f.x * scale[i], p1 = f.y * scale[i];
                 p0 = p0 > 65504.f ? 65504.f : p0 < -65504.f ? -65504.f : p0;
                 p1 = p1 > 65504.f ? 65504.f : p1 < -65504.f ? -65504.f : p1;

@@ -6,7 +6,7 @@ import torch
 
 import paged_kv_cache_213_gb300 as pkv
 
-from q8_util import Paged, append64, assert_attention, attend64
+from q8_util import Paged, append64, assert_attention, attend64, values
 from test_q8_gpu import KINDS, OnGpu, queries, same_state, starts, t
 
 pytestmark = pytest.mark.gpu
@@ -261,3 +261,25 @@ def test_v_scales_from_the_least_to_the_largest(kind, d, news, large):
             if b % 9 < 8:
                 assert np.array_equal(out[at[b]:at[b + 1]].astype(np.float64), want), b
         assert np.isfinite(lse).all()
+
+
+# --- the read-back's roundings ------------------------------------------------------
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_read_back_rounds_to_fp32_and_then_to_fp16(kind):
+    """Every code at scales for some of whose products the two roundings end elsewhere than
+    one would, and at others."""
+    d, bs, n = 64, 16, 40
+    p = Paged([n * bs], 1, d, bs, kind, seed=1)
+    codes = np.array([c for c in range(256) if not (kind == "e4m3" and c & 127 == 127)]).astype(p.codes[0].dtype)
+    p.codes[0][:] = np.resize(codes, (bs, d))
+    some = np.exp2(p.rng.uniform(-20, 5, 200000)).astype(np.float32)
+    products = values(kind, codes) * some.astype(np.float64)[:, None]
+    apart = products.astype(np.float32).astype(np.float16) != products.astype(np.float16)
+    few = some[apart.any(1)][:n // 2]
+    p.scales[0][:] = p.rng.permutation(np.concatenate([few, some[:p.NB - len(few)]]))[:, None]
+    want = p.tokens(0, 0, n * bs)
+    twice, once = want.astype(np.float32).astype(np.float16), want.astype(np.float16)
+    assert (twice != once).sum() >= 10
+    k, _ = pkv.paged_kv_gather_q8(*OnGpu(p).kv, t(p.tables), t(starts([n * bs])), n * bs)
+    assert np.array_equal(k.cpu().numpy().view(np.uint16), twice.view(np.uint16))
