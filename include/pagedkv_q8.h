@@ -66,10 +66,12 @@ extern "C" {
  *                 token a sequence (total == num_seqs, max_q_len 1), where a
  *                 context length of 0 is a sequence without a token
  *  total          rows of k_new and v_new
- *  max_q_len      host upper bound of n_b
+ *  max_q_len      host upper bound of n_b; with 0, as with total 0, the call
+ *                 does nothing and flags nothing
  * A sequence with n_b outside [0, max_q_len], n_b > context_lens[b], rows
  * outside [0, total) or a length beyond max_blocks_per_seq * block_size sets
- * PKV_ERRBIT_CONTEXT and nothing of it is written; a bad block id sets
+ * PKV_ERRBIT_CONTEXT and nothing of it is written (the others are, also where
+ * starts decrease); a bad block id sets
  * PKV_ERRBIT_BLOCK_ID and that block is left out.  Two sequences that write to
  * one block in one call race (copy-on-write first: paged_kv_copy_blocks_q8).
  * Pointers 16-byte aligned (tables and lengths: 4).
@@ -91,7 +93,10 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  * whole ratio up to 128 (PKV_ERR_UNSUPPORTED beyond).  Up to 32 query rows of
  * a KV head (max_q_len times that ratio) are streamed through one kernel; more
  * go in tiles of 128 rows to another, on tcgen05 (max_context_len up to 2^25
- * there, PKV_ERR_UNSUPPORTED beyond).  out and q do not overlap.
+ * there, PKV_ERR_UNSUPPORTED beyond).  max_q_len decides for the whole call: a
+ * decode batch with a chunk in it is better given in two calls (64 sequences of
+ * one new token and one of 512: 125 us in one, 75 in two; next to a chunk each
+ * of those costs a tile of 128 rows).  out and q do not overlap.
  *
  *  q              device fp16, token i's n_q_heads * head_dim entries at
  *                 element i * q_stride (a multiple of 8)

@@ -6,6 +6,10 @@
 // of them: a team of lanes holds the rows in registers, reduces their largest
 // entry, and writes the codes from the same registers: one pass over memory.
 // A token alone (decode) is a team of one row's lanes.
+//
+// Where a scale grows, the same lanes rewrite the rows that the block holds, one after another.  32
+// tokens of 8 heads of 128, about half of a block's rows held (us): without growth 2.1 whatever the block;
+// one scale of 16 growing, 16 rows a block, 3.5; every scale, 16 rows 3.9, 64 rows 8.6, 256 rows 27.
 #include <cuda_fp16.h>
 
 #include "f32x2.cuh"
@@ -472,9 +476,9 @@ namespace {
 
 template <int KIND, int D>
 cudaError_t launch_gather(const Q8GatherArgs &a, cudaStream_t stream) {
-    // 16 rows a CTA, or 8 where those would leave SMs idle (1160 rows of 8 heads: 3.5 us, with
-    // 16 rows 5.1; 72000 rows: 73.8 us with 8 rows, 70.1 with 16)
-    const bool few = a.total <= 16 * 304;
+    // 16 rows a CTA, or 8 where those are less than two CTAs for each of 152 SMs (1160 rows of 8
+    // heads: 3.5 us, with 16 rows 5.1; 72000 rows: 73.8 us with 8 rows, 70.1 with 16)
+    const bool few = a.total <= 16 * 2 * 152;
     const long long blocks = (a.total + (few ? 7 : 15)) / (few ? 8 : 16);
     const dim3 grid(static_cast<unsigned>(blocks)), threads(kGatherThreads);
     return few ? launch_pdl(q8_gather_kernel<KIND, D, 8>, grid, threads, 0, stream, a)

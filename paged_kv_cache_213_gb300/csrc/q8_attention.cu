@@ -28,9 +28,9 @@
 // a CTA hold are joined there; CTAs that share a segment leave a record each, and the
 // last to arrive joins them, in the order of the tokens.
 //
-// Measured (32 query heads on 8 of 128, E4M3): 8 x 32k tokens 87.5 us, 6.1 TB/s, memory; 32 x
+// Measured (32 query heads on 8 of 128, E4M3): 8 x 32k tokens 87 us, 6.2 TB/s, memory; 32 x
 // 128 to 2048 tokens 21.0 us, 3.4 TB/s, of which 4 us pass before the first tile lands and 5 us in the
-// joins; 20 rows, 24 x 200 to 2900 tokens, 36.1 us, where a warp's chain of instructions bounds
+// joins; 20 rows, 24 x 200 to 2900 tokens, 36.2 us, where a warp's chain of instructions bounds
 // it (255 registers a thread, two warps a scheduler).
 #include <cuda_fp16.h>
 
@@ -850,9 +850,12 @@ Q8Split split_of_rows(int rows, int head_dim, int sms) {
     return sp;
 }
 
-// Up to 32 rows here, more on tcgen05 (24 sequences of 200-2900 tokens, four heads a
-// group; this kernel and that one, us): 12 rows 26.1, 50.4; 20 rows 36.1, 49.4; 32 rows
-// 46.4, 48.5; 64 rows, twice 32 here, 55.1, 49.3
+// Up to 32 rows here, more on tcgen05.  This kernel and that one, us, 8 KV heads, at 12, 20 and 32 rows:
+//   24 x 200-2900 tokens   E4M3, 128  25.9 49.3, 36.0 48.6, 46.5 47.7   int8, 64  21.1 42.2, 30.5 41.4, 36.1 41.1
+//   2 x 30000              E4M3, 128  35.7 68.7, 47.8 69.0, 57.3 64.4   int8, 64  29.4 55.6, 39.4 55.9, 43.6 52.8
+//   8 x 32000              E4M3, 128   102 178,   145 178,   178 177    int8, 64  85.7 157,   119 158,   134 157
+// (int8 of 128: 188 and 210 for the last, E4M3 of 64: 131 and 154.)  64 rows of the first, twice 32
+// here: 55.1, 49.3
 long long rows_of(int max_q_len, int n_q_heads, int n_kv_heads) {
     return static_cast<long long>(max_q_len) * (n_q_heads / n_kv_heads);
 }

@@ -21,8 +21,8 @@
 // per SM; items that several CTAs hold leave records, and the last to arrive joins them.
 //
 // Measured: 3 chunks of 150 to 700 tokens behind 1800 to 2500, 32 query heads on 8 of 128 (47
-// GFLOP): 63.4 us, 0.75 PFLOP/s.  A step takes about 2100 cycles, of which the tensor core is busy
-// 1100: the softmax of a row's 64 keys is the chain.
+// GFLOP): 63.1 us, 0.75 PFLOP/s.  A step takes about 2200 cycles, in which the tensor pipe is busy
+// 980: the softmax of a row's 64 keys is the chain.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
