@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(PipeCfg<D, G, HK>::THREADS, PipeCfg<D, G, HK>:
         }
         last_on = __shfl_sync(0xffffffffu, last_on, 1);
         if (!last_on) return true;
+        __syncwarp();  // lane 1's counts before the other lanes' fence
         // the other CTAs' records, visible after lane 1 saw their counts, are
         // read by bulk copies (the async proxy)
         __threadfence();

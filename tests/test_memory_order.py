@@ -37,6 +37,9 @@ def test_an_acquire_by_one_lane_comes_before_the_other_lanes_loads():
     many = _code(os.path.join(CSRC, "q8_prefill.cu"))
     after = many[many.index("atomic_add_acq_rel_gpu("):]
     assert after.index("__syncwarp();") < after.index("__ldcg(")
+    pipeline = _code(os.path.join(CSRC, "decode_pipeline.cu"))
+    after = pipeline[pipeline.index("atomic_add_relaxed_gpu("):]
+    assert after.index("__shfl_sync(") < after.index("__syncwarp();") < after.index("__threadfence();")
 
 
 def test_a_scale_is_read_by_all_before_one_lane_writes_it():
