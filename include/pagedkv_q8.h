@@ -92,8 +92,8 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  * position; query head h reads KV head h / (n_q_heads / n_kv_heads), any
  * whole ratio up to 128 (PKV_ERR_UNSUPPORTED beyond).  Up to 32 query rows of
  * a KV head (max_q_len times that ratio) are streamed through one kernel; more
- * go in tiles of 128 rows to another, on tcgen05 (max_context_len up to 2^25
- * there, PKV_ERR_UNSUPPORTED beyond).  max_q_len decides for the whole call: a
+ * go in tiles of 128 rows to another, on tcgen05 (max_context_len, or with 0
+ * the tables' tokens, up to 2^25 there, PKV_ERR_UNSUPPORTED beyond).  max_q_len decides for the whole call: a
  * decode batch with a chunk in it is better given in two calls (64 sequences of
  * one new token and one of 512: 125 us in one, 75 in two; next to a chunk each
  * of those costs a tile of 128 rows).  out and q do not overlap.
@@ -156,6 +156,7 @@ int paged_decode_attention_q8(void *out, const void *q, int64_t q_stride, const 
  * (one product in some 20000 has more bits than fp32 and lands next to a tie of
  * fp16: there the two roundings differ from one).
  *  start          device int32 [num_seqs + 1], non-decreasing, start[0] >= 0
+ *                 (rows that two sequences have in common are unspecified)
  *  total          rows of the outputs; rows outside [start[0],
  *                 start[num_seqs]) are left as they were
  *  k, v           device fp16 [total][n_kv_heads][head_dim]

@@ -58,8 +58,8 @@ int sm_count(int *out) {
 struct Plan {
     int max_len;
     bool empty;  // nothing to launch
+    int most, sms;  // tokens of a sequence that can be new; of the device
     pkv::Q8Split split;
-    size_t bytes;  // for this call and smaller ones
 };
 
 int make_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
@@ -79,15 +79,13 @@ int make_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads, int n_kv_
     if (max_len > cap) max_len = cap;
     plan->max_len = static_cast<int>(max_len);
     plan->empty = num_seqs == 0 || total_q == 0 || max_q_len == 0;
-    plan->split.ws_bytes = plan->bytes = 0;
+    plan->split.ws_bytes = 0;
     if (plan->empty) return PKV_OK;
     // no sequence has more new tokens than there are
-    const int most = max_q_len < total_q ? max_q_len : total_q;
-    if (!pkv::q8_fits(num_seqs, most, n_q_heads, n_kv_heads, plan->max_len)) return PKV_ERR_UNSUPPORTED;
-    int sms = 0;
-    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
-    plan->split = pkv::q8_split(most, n_q_heads, n_kv_heads, head_dim, sms);
-    plan->bytes = pkv::q8_plan_bytes(most, n_q_heads, n_kv_heads, head_dim, sms);
+    plan->most = max_q_len < total_q ? max_q_len : total_q;
+    if (!pkv::q8_fits(num_seqs, plan->most, n_q_heads, n_kv_heads, plan->max_len)) return PKV_ERR_UNSUPPORTED;
+    if (sm_count(&plan->sms) != PKV_OK) return PKV_ERR_CUDA;
+    plan->split = pkv::q8_split(plan->most, n_q_heads, n_kv_heads, head_dim, plan->sms);
     return PKV_OK;
 }
 
@@ -144,7 +142,8 @@ int paged_decode_q8_plan(int num_seqs, int total_q, int max_q_len, int n_q_heads
     Plan plan{};
     const int rc = make_plan(num_seqs, total_q, max_q_len, n_q_heads, n_kv_heads, head_dim, block_size,
                              max_blocks_per_seq, max_context_len, &plan);
-    if (rc == PKV_OK && workspace_bytes_out) *workspace_bytes_out = plan.bytes;
+    if (rc == PKV_OK && workspace_bytes_out)
+        *workspace_bytes_out = plan.empty ? 0 : pkv::q8_plan_bytes(plan.most, n_q_heads, n_kv_heads, head_dim, plan.sms);
     return rc;
 }
 
@@ -189,7 +188,7 @@ int paged_decode_attention_q8(void *out, const void *q, int64_t q_stride, const 
     a.query_start = query_start;
     a.num_seqs = num_seqs;
     a.total_q = total_q;
-    a.max_q_len = max_q_len < total_q ? max_q_len : total_q;
+    a.max_q_len = plan.most;
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.num_blocks = num_blocks;
     a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
