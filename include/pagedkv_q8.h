@@ -71,9 +71,9 @@ extern "C" {
  * A sequence with n_b outside [0, max_q_len], n_b > context_lens[b], rows
  * outside [0, total) or a length beyond max_blocks_per_seq * block_size sets
  * PKV_ERRBIT_CONTEXT and nothing of it is written (the others are, also where
- * starts decrease); a bad block id sets
- * PKV_ERRBIT_BLOCK_ID and that block is left out.  Two sequences that write to
- * one block in one call race (copy-on-write first: paged_kv_copy_blocks_q8).
+ * starts decrease); a bad block id sets PKV_ERRBIT_BLOCK_ID and that block is
+ * left out.  Two sequences that write to one block in one call race
+ * (copy-on-write first: paged_kv_copy_blocks_q8).
  * Pointers 16-byte aligned (tables and lengths: 4).
  */
 int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, int64_t v_stride,
@@ -93,10 +93,11 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  * whole ratio up to 128 (PKV_ERR_UNSUPPORTED beyond).  Up to 32 query rows of
  * a KV head (max_q_len times that ratio) are streamed through one kernel; more
  * go in tiles of 128 rows to another, on tcgen05 (max_context_len, or with 0
- * the tables' tokens, up to 2^25 there, PKV_ERR_UNSUPPORTED beyond).  max_q_len decides for the whole call: a
- * decode batch with a chunk in it is better given in two calls (64 sequences of
- * one new token and one of 512: 125 us in one, 75 in two; next to a chunk each
- * of those costs a tile of 128 rows).  out and q do not overlap.
+ * the tables' tokens, up to 2^25 there, PKV_ERR_UNSUPPORTED beyond).  max_q_len
+ * decides for the whole call: a decode batch with a chunk in it is better given
+ * in two calls (64 sequences of one new token and one of 512: 125 us in one, 75
+ * in two; next to a chunk each of those costs a tile of 128 rows).  out and q
+ * do not overlap.
  *
  *  q              device fp16, token i's n_q_heads * head_dim entries at
  *                 element i * q_stride (a multiple of 8)
@@ -114,9 +115,8 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  *                 256-byte aligned.  A plan's bytes are enough for every call
  *                 with the same n_kv_heads and head_dim whose other sizes are
  *                 no larger: one for a loop's largest call serves the loop.
- *                 Its first PKV_WORKSPACE_COUNTER_BYTES
- *                 bytes hold arrival counters: zero before the first use, and
- *                 left at zero by every call, also by one that flags
+ *                 Its first PKV_WORKSPACE_COUNTER_BYTES bytes hold arrival
+ *                 counters: zero before the first use, and left at zero by every call, also by one that flags
  *                 PKV_ERRBIT_TIMEOUT.  After PKV_ERRBIT_WORKSPACE (a
  *                 counter that did not start at zero) clear them with
  *                 paged_decode_workspace_clear.  Calls that overlap in time
