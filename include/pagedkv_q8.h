@@ -116,11 +116,11 @@ int paged_kv_append_q8(const void *k_new, const void *v_new, int64_t k_stride, i
  *                 with the same n_kv_heads and head_dim whose other sizes are
  *                 no larger: one for a loop's largest call serves the loop.
  *                 Its first PKV_WORKSPACE_COUNTER_BYTES bytes hold arrival
- *                 counters: zero before the first use, and left at zero by every call, also by one that flags
- *                 PKV_ERRBIT_TIMEOUT.  After PKV_ERRBIT_WORKSPACE (a
- *                 counter that did not start at zero) clear them with
- *                 paged_decode_workspace_clear.  Calls that overlap in time
- *                 need separate workspaces.
+ *                 counters: zero before the first use, and left at zero by
+ *                 every call, also by one that flags PKV_ERRBIT_TIMEOUT.  After
+ *                 PKV_ERRBIT_WORKSPACE (a counter that did not start at zero)
+ *                 clear them with paged_decode_workspace_clear.  Calls that
+ *                 overlap in time need separate workspaces.
  *  flags          0 or PKV_TABLES_READY, which covers query_start too, and
  *                 err_word where the kernel before clears it (made use of up
  *                 to 32 rows)
